@@ -69,6 +69,9 @@ extern "C" {
 
 #define PAGEDKV_HEAD_DIM 128
 #define PAGEDKV_BLOCK_SIZE 16
+#define PAGEDKV_LATENT_DIM 512       /* latent part of a latent-cache row */
+#define PAGEDKV_LATENT_ROPE_DIM 64   /* rotary key part of a latent-cache row */
+#define PAGEDKV_LATENT_MAX_HEADS 128
 
 typedef enum {
     KV_OK = 0,
@@ -401,6 +404,132 @@ PAGEDKV_API kv_status paged_attention_chunked_prefill(float *out, const void *q,
                                           size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Step tables: the block tables and slot numbers of one serving step, built on
+ * the device from request lengths in one launch (the counterpart, for lengths
+ * that live on the device, of filling the tables on the host).  Sequence s
+ * holds c_s = context_lens[s] tokens and gains n_s = new_lens[s] (0 allowed).
+ * Blocks c_s already needs are in its table row; the blocks it newly needs,
+ *   ceil((c_s + n_s)/16) - ceil(c_s/16),
+ * are taken from free_blocks in sequence order and written into its row.  The
+ * caller reserves that list beforehand (kv_block_alloc) and gives back what
+ * totals[1] leaves of it.
+ *
+ *  block_tables   device int32 [num_seqs][max_blocks_per_seq], in and out
+ *  context_lens, new_lens   device int32 [num_seqs]
+ *  free_blocks    device int32 [num_free], ids in the order they are handed out
+ *  num_blocks     blocks in the pool: no slot is given in a block outside it
+ *                 (the row's slot is then -1, flag 1)
+ *  cu_q_lens      out, device int32 [num_seqs + 1]: prefix sums of the rows
+ *  total_lens     out, device int32 [num_seqs]: c_s + n_s
+ *  slot_mapping   out, device int64 [max_tokens]: the slot of each row, -1 past
+ *                 the last
+ *  positions      out, device int32 [max_tokens]: the row's token position, 0
+ *                 past the last
+ *  totals         out, device int32 [2]: rows, free blocks taken
+ *  A sequence is refused -- no rows, no blocks, total_lens[s] = c_s -- if a
+ *  length is negative or c_s + n_s exceeds max_blocks_per_seq x 16 (flag 4), if
+ *  the rows of it and of all the valid sequences before it (refused ones
+ *  included) exceed max_tokens (flag 4), or if it needs blocks and those of it
+ *  and of all the valid sequences before it exceed num_free (flag 16).
+ *  No output may overlap an input or another output (KV_ERR_INVALID).
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API kv_status kv_build_step_tables(int32_t *block_tables, int32_t max_blocks_per_seq,
+                                           const int32_t *context_lens, const int32_t *new_lens, int32_t num_seqs,
+                                           const int32_t *free_blocks, int32_t num_free, int32_t num_blocks,
+                                           int32_t *cu_q_lens, int32_t *total_lens, int64_t *slot_mapping,
+                                           int32_t *positions, int32_t max_tokens, int32_t *totals, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: keys and values of all heads come from one vector a token,
+ * a latent of 512 values and a rotary key of 64.
+ *  Latent cache: [num_blocks][16][576] bf16, one row a token (latent, then
+ *  rotary key), in the same blocks and tables as the K/V cache.
+ *
+ * reshape_and_cache_latent writes new tokens' rows:
+ *  latent         device bf16, row t at latent + t x latent_stride, 512 values
+ *  rope           device bf16, row t at rope + t x rope_stride, 64 values
+ *                 (strides in elements, >= 0 and multiples of 8; the rows may be
+ *                 views of a wider tensor)
+ *  slot_mapping   device int64 [num_tokens], as for reshape_and_cache: negative
+ *                 skips the token, a slot outside the pool is skipped and
+ *                 flagged (flag 2).  A slot listed twice gets, for each 16 bytes
+ *                 of its row, one of the listed tokens' values.
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t latent_stride, const void *rope,
+                                               int64_t rope_stride, void *cache, const int64_t *slot_mapping,
+                                               int32_t num_tokens, int32_t num_blocks, void *stream);
+
+/* Attention over the paged latent cache, absorbed form: each head's query has
+ * been multiplied by that head's key expansion, so it is 576 wide (512 against
+ * the latent, 64 against the rotary key), and the output is the weighted sum of
+ * latents, to be multiplied by the head's value expansion:
+ *   out[r][h] = sum_t p_t x_t[0:512],  p = softmax_t(scale x q[r][h] . x_t).
+ * One call serves decode rows, drafts and prompt chunks: sequence s owns rows
+ * cu_q_lens[s] .. cu_q_lens[s+1]-1 at positions L-n .. L-1 (L = context_lens[s],
+ * n rows), and row i sees keys 0 .. L-n+i.
+ *
+ *  out            device bf16 [total_q_tokens][num_heads][512]
+ *  q              device bf16 [total_q_tokens][num_heads][576]
+ *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
+ *                 sequence (total_q_tokens = num_seqs)
+ *  context_lens   device int32 [num_seqs]; L = 0 (a padded entry): the
+ *                 sequence's rows are zeros.  A sequence with 0 < L < n, L < 0,
+ *                 L > max_blocks_per_seq x 16 or rows outside 0 ..
+ *                 total_q_tokens-1 is left out, its rows as they were (flag 4);
+ *                 so are rows that belong to no sequence (not flagged).
+ *  cache, block_tables, num_blocks   as above; the keys of a block outside the
+ *                 pool are not read, the sequence's output is then unspecified
+ *                 (flag 1)
+ *  num_heads      1 .. 128 (KV_ERR_UNSUPPORTED above)
+ *  scale          > 0 and finite
+ *  workspace      device scratch of paged_latent_attention_workspace_size()
+ *                 bytes, 256-byte aligned.  Calls that may overlap on the GPU
+ *                 (captured graphs replayed side by side among them) need one
+ *                 each.
+ * Scores, softmax statistics and sums are fp32; probabilities are rounded to
+ * bf16 for the second product, and the output once at the end.  Split points
+ * depend on the batch's lengths and sizes only, and no atomics touch the
+ * arithmetic: the same call gives the same bits. */
+PAGEDKV_API size_t paged_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
+                                                         int32_t num_heads, int32_t max_blocks_per_seq);
+PAGEDKV_API kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_lens,
+                                             const int32_t *context_lens, int32_t num_seqs,
+                                             int32_t total_q_tokens, const void *cache,
+                                             const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                             int32_t num_heads, int32_t num_blocks, float scale,
+                                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Attention over expanded latents, for prompts: head h's key of token t is
+ * kv[t][h][0:128] beside the shared rotary key k_rope[t], its value
+ * kv[t][h][128:256] (the output of the latent's expansion, as one product gives
+ * it; nothing is joined or repeated beforehand).  For the same weights it gives
+ * what the absorbed form gives after its output expansion, with 3.4 times fewer
+ * operations a key.
+ *   out[r][h] = sum_t p_t kv[t][h][128:256],
+ *   p = softmax_t(scale x (q[r][h][0:128] . kv[t][h][0:128] + q[r][h][128:192] . k_rope[t]))
+ * Sequence s owns rows cu_q_lens[s] .. and keys cu_k_lens[s] ..; row i of its
+ * nq rows sees the first nk-nq+i+1 of its nk keys (a row that sees none: zeros).
+ *
+ *  out            device bf16 [total_q_tokens][num_heads][128]
+ *  q              device bf16 [total_q_tokens][num_heads][192]
+ *  kv             device bf16 [total_k_tokens][num_heads][256]
+ *  k_rope         device bf16, row t at k_rope + t x k_rope_stride, 64 values
+ *                 (stride in elements, >= 64, a multiple of 8)
+ *  cu_q_lens, cu_k_lens   device int32 [num_seqs + 1], non-decreasing; a
+ *                 sequence whose rows or keys lie outside the tensors is left
+ *                 out, its rows as they were (flag 4); so are rows that belong
+ *                 to no sequence (not flagged)
+ *  num_heads, scale, workspace, rounding   as for paged_latent_attention */
+PAGEDKV_API size_t latent_prefill_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
+                                                           int32_t num_heads);
+PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const void *kv, const void *k_rope,
+                                               int64_t k_rope_stride, const int32_t *cu_q_lens,
+                                               const int32_t *cu_k_lens, int32_t num_seqs,
+                                               int32_t total_q_tokens, int32_t total_k_tokens,
+                                               int32_t num_heads, float scale, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Swap of KV blocks to host memory and back ([P2] "When it runs out anyway":
  * ship a preempted request's blocks over the host link and bring them back;
  * [P3] block management (f) preemption, swap out to CPU).
@@ -443,7 +572,8 @@ PAGEDKV_API kv_status kv_last_device_status(void *stream);
 
 /* Bit flags of the last non-OK device status (0 if none), for diagnostics:
  * 1 block id outside the pool, 2 slot outside the pool, 4 bad context length
- * or chunk, 8 a pipeline wait timed out.  Read together with
+ * or chunk, 8 a pipeline wait timed out, 16 the step's free-block list is too
+ * short.  Read together with
  * kv_last_device_status (which clears them). */
 PAGEDKV_API uint32_t kv_last_device_status_flags(void);
 

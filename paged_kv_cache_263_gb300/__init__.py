@@ -21,10 +21,15 @@ __all__ = [
     "kv_last_device_status", "kv_last_device_status_flags", "KV_BF16", "KV_FP8_E4M3",
     "HEAD_DIM", "BLOCK_SIZE", "library_path", "PrefixCache", "kv_swap_out", "kv_swap_in", "kv_waste_stats",
     "kv_trace_prefill", "kv_trace_prefill_kernel_ms", "kv_selftest_bounded_wait",
+    "kv_build_step_tables", "reshape_and_cache_latent", "paged_latent_attention",
+    "paged_latent_attention_workspace_size", "latent_prefill_attention",
+    "latent_prefill_attention_workspace_size", "LATENT_DIM", "LATENT_ROPE_DIM", "LATENT_MAX_HEADS",
 ]
 
 HEAD_DIM = 128
 BLOCK_SIZE = 16
+LATENT_DIM, LATENT_ROPE_DIM, LATENT_MAX_HEADS = 512, 64, 128
+_LATENT_ROW, _EXPANDED_QK = LATENT_DIM + LATENT_ROPE_DIM, HEAD_DIM + LATENT_ROPE_DIM
 KV_BF16, KV_FP8_E4M3 = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "out of blocks", 3: "unsupported",
            4: "CUDA error", 5: "device data out of range"}
@@ -99,6 +104,12 @@ def lib():
             "paged_attention_decode_static_scratch_bytes": (SZ, []),
             "paged_attention_decode_static_scratch": (c.c_int, [P, P, P, P, P, I, P, I, I, I, I, F, c.c_int, P,
                                                                 P, I, P]),
+            "kv_build_step_tables": (c.c_int, [P, I, P, P, I, P, I, I, P, P, P, P, I, P, P]),
+            "reshape_and_cache_latent": (c.c_int, [P, I64, P, I64, P, P, I, I, P]),
+            "paged_latent_attention_workspace_size": (SZ, [I, I, I, I]),
+            "paged_latent_attention": (c.c_int, [P, P, P, P, I, I, P, P, I, I, I, F, P, SZ, P]),
+            "latent_prefill_attention_workspace_size": (SZ, [I, I, I]),
+            "latent_prefill_attention": (c.c_int, [P, P, P, P, I64, P, P, I, I, I, I, F, P, SZ, P]),
             "kv_swap_out": (c.c_int, [P, P, I, I, c.c_int, P, I, P, P, P]),
             "kv_swap_in": (c.c_int, [P, P, I, I, c.c_int, P, I, P, P, P]),
             "kv_trace_prefill": (c.c_int, [I]),
@@ -422,6 +433,160 @@ def paged_attention_chunked_prefill(out, q, cu_q_lens, context_lens, max_q_len, 
         _ptr(v_cache), _ptr(block_tables), mb, hq, hkv, nb, float(scale), _cache_dtype(k_cache),
         _ptr(k_scale), _ptr(v_scale), int(num_splits), _ptr(workspace), ws_bytes, _stream(stream)),
         "paged_attention_chunked_prefill")
+    return out
+
+
+# ----------------------------------------------------------- latent attention
+def _on(name, t, device, dtype, shape):
+    """t is a contiguous CUDA tensor of this dtype and shape (None: any extent) on `device` (None: its own)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    have = t.shape
+    if len(have) != len(shape) or any(b is not None and a != b for a, b in zip(have, shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(have)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_on(name, t, device, width):
+    """Rows of `width` bf16 values whose first dimension may be strided; (pointer, row stride)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name} must be bf16 [tokens][{width}]")
+    row, one = t.stride()
+    # (without rows no stride means anything, and with one row its distance to the next does not)
+    if one != 1 and t.shape[0] > 0:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), row if t.shape[0] > 1 else width
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current: its current stream unless one is given."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, stream.cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream.cuda_stream)
+
+
+def _scratch(workspace, need, device, name):
+    """Pointer and size of the given workspace, or of a new one (returned too, to stay alive through the call)."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be a contiguous CUDA tensor on the other tensors' device")
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def kv_build_step_tables(block_tables, context_lens, new_lens, free_blocks, num_blocks, cu_q_lens, total_lens,
+                         slot_mapping, positions, totals, stream=None):
+    """Block tables and slot numbers of one step from request lengths, on the device.
+
+    Sequence s holds context_lens[s] tokens and gains new_lens[s]; the blocks it
+    newly needs come from free_blocks in sequence order and go into its row of
+    block_tables.  Outputs (int32; slot_mapping int64): cu_q_lens [B+1],
+    total_lens [B], slot_mapping and positions [max_tokens], totals [2] (rows,
+    free blocks taken).  Lengths that do not fit refuse the sequence and set the
+    device status (see kv_last_device_status)."""
+    i32 = torch.int32
+    tables = _on("block_tables", block_tables, None, i32, (None, None))
+    dev = block_tables.device
+    B, mb = block_tables.shape
+    args = (tables, mb, _on("context_lens", context_lens, dev, i32, (B,)), _on("new_lens", new_lens, dev, i32, (B,)),
+            B, _on("free_blocks", free_blocks, dev, i32, (None,)), free_blocks.shape[0], int(num_blocks),
+            _on("cu_q_lens", cu_q_lens, dev, i32, (B + 1,)), _on("total_lens", total_lens, dev, i32, (B,)),
+            _on("slot_mapping", slot_mapping, dev, torch.int64, (None,)),
+            _on("positions", positions, dev, i32, (slot_mapping.shape[0],)), slot_mapping.shape[0],
+            _on("totals", totals, dev, i32, (2,)))
+    _check(_call_on(dev, stream, lib().kv_build_step_tables, *args), "kv_build_step_tables")
+
+
+def reshape_and_cache_latent(latent, rope, cache, slot_mapping, stream=None):
+    """Write latent rows [T][512] and rotary keys [T][64] (bf16; rows may be views
+    of a wider tensor) into the paged latent cache [num_blocks][16][576]."""
+    bf = torch.bfloat16
+    c = _on("cache", cache, None, bf, (None, BLOCK_SIZE, _LATENT_ROW))
+    dev = cache.device
+    slots = _on("slot_mapping", slot_mapping, dev, torch.int64, (None,))
+    T = slot_mapping.shape[0]
+    lat, ls = _rows_on("latent", latent, dev, LATENT_DIM)
+    rp, rs = _rows_on("rope", rope, dev, LATENT_ROPE_DIM)
+    if latent.shape[0] != T or rope.shape[0] != T:
+        raise ValueError("latent, rope and slot_mapping must have the same number of tokens")
+    _check(_call_on(dev, stream, lib().reshape_and_cache_latent, lat, ls, rp, rs, c, slots, T, cache.shape[0]),
+           "reshape_and_cache_latent")
+
+
+def paged_latent_attention_workspace_size(num_seqs, total_q_tokens, num_heads, max_blocks_per_seq) -> int:
+    return int(lib().paged_latent_attention_workspace_size(num_seqs, total_q_tokens, num_heads, max_blocks_per_seq))
+
+
+def paged_latent_attention(out, q, cache, block_tables, context_lens, cu_q_lens=None, scale=None, workspace=None,
+                           stream=None):
+    """Attention over the paged latent cache, absorbed form: out[R][H][512] from
+    q[R][H][576] (bf16), one row a sequence, or cu_q_lens [B+1] rows.  scale
+    defaults to (128 + 64) ** -0.5, the expanded form's."""
+    bf, i32 = torch.bfloat16, torch.int32
+    qp = _on("q", q, None, bf, (None, None, _LATENT_ROW))
+    dev = q.device
+    R, h, _ = q.shape
+    B, mb = block_tables.shape if block_tables is not None else (None, None)
+    args = (_on("out", out, dev, bf, (R, h, LATENT_DIM)), qp,
+            None if cu_q_lens is None else _on("cu_q_lens", cu_q_lens, dev, i32, (B + 1,)),
+            _on("context_lens", context_lens, dev, i32, (B,)), B, R,
+            _on("cache", cache, dev, bf, (None, BLOCK_SIZE, _LATENT_ROW)),
+            _on("block_tables", block_tables, dev, i32, (B, mb)), mb, h, cache.shape[0],
+            _EXPANDED_QK ** -0.5 if scale is None else float(scale))
+    if cu_q_lens is None and R != B:
+        raise ValueError("without cu_q_lens, q must have one row a sequence")
+    L = lib()
+    need = 0 if workspace is not None else L.paged_latent_attention_workspace_size(B, R, h, mb)
+    ws, nbytes, _keep = _scratch(workspace, need, dev, "paged_latent_attention")
+    _check(_call_on(dev, stream, L.paged_latent_attention, *args, ws, nbytes), "paged_latent_attention")
+    return out
+
+
+def latent_prefill_attention_workspace_size(num_seqs, total_q_tokens, num_heads) -> int:
+    return int(lib().latent_prefill_attention_workspace_size(num_seqs, total_q_tokens, num_heads))
+
+
+def latent_prefill_attention(out, q, kv, k_rope, cu_q_lens, cu_k_lens, scale=None, workspace=None, stream=None):
+    """Prompt attention over expanded latents: out[Rq][H][128] from q[Rq][H][192],
+    kv[Rk][H][256] (key part, value) and the shared rotary keys k_rope[Rk][64]
+    (bf16; k_rope's rows may be views of a wider tensor), ragged by cu_q_lens and
+    cu_k_lens [B+1], causal from the end.  scale defaults to 192 ** -0.5."""
+    bf, i32 = torch.bfloat16, torch.int32
+    qp = _on("q", q, None, bf, (None, None, _EXPANDED_QK))
+    dev = q.device
+    R, h, _ = q.shape
+    kvp = _on("kv", kv, dev, bf, (None, h, 2 * HEAD_DIM))
+    rp, rs = _rows_on("k_rope", k_rope, dev, LATENT_ROPE_DIM)
+    if k_rope.shape[0] != kv.shape[0]:
+        raise ValueError("kv and k_rope must have the same number of tokens")
+    cu_q = _on("cu_q_lens", cu_q_lens, dev, i32, (None,))
+    B = cu_q_lens.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_q_lens must have at least one entry")
+    args = (_on("out", out, dev, bf, (R, h, HEAD_DIM)), qp, kvp, rp, rs, cu_q,
+            _on("cu_k_lens", cu_k_lens, dev, i32, (B + 1,)), B, R, kv.shape[0], h,
+            _EXPANDED_QK ** -0.5 if scale is None else float(scale))
+    L = lib()
+    need = 0 if workspace is not None else L.latent_prefill_attention_workspace_size(B, R, h)
+    ws, nbytes, _keep = _scratch(workspace, need, dev, "latent_prefill_attention")
+    _check(_call_on(dev, stream, L.latent_prefill_attention, *args, ws, nbytes), "latent_prefill_attention")
     return out
 
 

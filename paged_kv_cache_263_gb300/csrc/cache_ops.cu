@@ -77,6 +77,32 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Latent cache write: one thread per 16-byte piece of a token's row, 64 pieces
+// of the latent and 8 of the rotary key.  A plain copy of 1,152 bytes a token,
+// bound by memory; the two sources are read in place (their rows may be views of
+// a wider projection), so nothing is joined beforehand.
+constexpr int LROW = LKD / 8, LLAT = LAT / 8;   // 72 pieces a row, 64 of them latent
+__global__ void __launch_bounds__(256)
+    latent_write_kernel(const uint4 *__restrict__ lat, int64_t lat_stride, const uint4 *__restrict__ rope,
+                        int64_t rope_stride, uint4 *__restrict__ cache, const int64_t *__restrict__ slots,
+                        int64_t total, int64_t num_slots)
+{
+    griddep_launch_dependents();
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / LROW;
+        const int c = (int)(i - t * LROW);
+        const int64_t slot = __ldg(slots + t);
+        const uint4 x = __ldg(c < LLAT ? lat + t * lat_stride + c : rope + t * rope_stride + (c - LLAT));
+        if (slot < 0) continue;
+        if (slot >= num_slots) {
+            if (c == 0) atomicOr(&g_status, ST_BAD_SLOT);
+            continue;
+        }
+        cache[slot * LROW + c] = x;
+    }
+}
+
 // Copies every (head) tile of block src to block dst, K and V.
 __global__ void __launch_bounds__(256)
     block_copy_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc, int64_t src, int64_t dst,
@@ -114,6 +140,9 @@ __global__ void __launch_bounds__(32) bounded_wait_selftest_kernel(unsigned long
 namespace pkv_decode { uint32_t take_status(); }
 namespace pkv_prefill { uint32_t take_status(); }
 namespace pkv_swap { uint32_t take_status(); }
+namespace pkv_step { uint32_t take_status(); }
+namespace pkv_latent { uint32_t take_status(); }
+namespace pkv_latent_prefill { uint32_t take_status(); }
 
 static uint32_t take_status_cache()
 {
@@ -174,11 +203,34 @@ kv_status reshape_and_cache(const void *k, const void *v, void *k_cache, void *v
     return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
+kv_status reshape_and_cache_latent(const void *latent, int64_t latent_stride, const void *rope,
+                                   int64_t rope_stride, void *cache, const int64_t *slot_mapping,
+                                   int32_t num_tokens, int32_t num_blocks, void *stream)
+{
+    PKV_NVTX_RANGE("reshape_and_cache_latent");
+    if (num_tokens == 0) return KV_OK;
+    if (num_tokens < 0 || num_blocks < 1) return KV_ERR_INVALID;
+    if (!latent || !rope || !cache || !slot_mapping) return KV_ERR_INVALID;
+    // rows may be spaced apart (or, with stride 0, one row written to every slot), never backwards
+    if (latent_stride < 0 || rope_stride < 0 || latent_stride % 8 || rope_stride % 8) return KV_ERR_INVALID;
+    if (!pkv_host::aligned(latent, 16) || !pkv_host::aligned(rope, 16) || !pkv_host::aligned(cache, 16) ||
+        !pkv_host::aligned(slot_mapping, 8))
+        return KV_ERR_INVALID;
+    const int64_t total = (int64_t)num_tokens * LROW;
+    const int threads = 256;
+    const int blocks = static_cast<int>(std::min<int64_t>((total + threads - 1) / threads, 152 * 16));
+    latent_write_kernel<<<blocks, threads, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint4 *>(latent), latent_stride / 8, static_cast<const uint4 *>(rope), rope_stride / 8,
+        static_cast<uint4 *>(cache), slot_mapping, total, (int64_t)num_blocks * BS);
+    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
 kv_status kv_last_device_status(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KV_ERR_CUDA;
     uint32_t f = take_status_cache() | pkv_decode::take_status() | pkv_prefill::take_status() |
-                 pkv_swap::take_status();
+                 pkv_swap::take_status() | pkv_step::take_status() | pkv_latent::take_status() |
+                 pkv_latent_prefill::take_status();
     g_last_flags.store(f, std::memory_order_relaxed);
     return f ? KV_ERR_DEVICE_BOUNDS : KV_OK;
 }

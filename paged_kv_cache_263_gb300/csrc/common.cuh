@@ -21,6 +21,9 @@ namespace pkv {
 
 constexpr int D = PAGEDKV_HEAD_DIM;   // 128
 constexpr int BS = PAGEDKV_BLOCK_SIZE; // 16
+constexpr int LAT = PAGEDKV_LATENT_DIM;          // 512
+constexpr int ROPE = PAGEDKV_LATENT_ROPE_DIM;    // 64
+constexpr int LKD = LAT + ROPE;                  // 576: a latent-cache row
 
 // sticky device status bits (one word per translation unit, read by the host)
 enum : uint32_t {
@@ -28,6 +31,7 @@ enum : uint32_t {
     ST_BAD_SLOT = 2u,
     ST_BAD_LEN = 4u,
     ST_TIMEOUT = 8u,
+    ST_NO_BLOCKS = 16u,
 };
 
 // wait limit for every spin on an mbarrier: ~2 s of wall time
