@@ -1,10 +1,43 @@
 // latent_decode.cu -- attention over a paged latent cache, absorbed form
-// (sm_103a).
+// (sm_103a, 5th-generation tensor cores, thread-block clusters).
 //
 // A cached row x_t holds a token's latent (512) and rotary key (64); a head's
 // query, multiplied by that head's key expansion beforehand, is 576 wide, and
 //   out[r][h] = sum_t p_t x_t[0:512],  p = softmax_t(scale * q[r][h] . x_t)
 // over the keys t <= L - n + i that row i of a sequence's n rows sees.
+//
+// What bounds it.  A key is 1,152 bytes, read once for all heads; a (row, head)
+// costs 2 x (576 + 512) operations a key.  One token of 128 heads makes 242
+// operations a byte, just under the GPU's ratio (1,916 TFLOP/s : 6,789 GB/s =
+// 282), so decode is bound by memory as long as the products run on the tensor
+// cores with full tiles: 128 query rows = (tokens x heads) packed, padded with
+// zero rows when a sequence has fewer.
+//
+// Why a pair of CTAs.  The output of 128 rows is 128 x 512 fp32, all of one SM's
+// tensor memory, and the queries (144 KiB) and a key tile do not fit its shared
+// memory together.  A cluster of two CTAs therefore shares a tile by dims:
+// CTA c holds latent dims 256c .. 256c+255 and rotary dims 32c .. 32c+31 of the
+// queries and of every key, so that each byte is loaded by one CTA only.
+//  * S = Q K^T: each CTA multiplies its 288 dims, giving a partial S[128 x 64]
+//    of the 64-key tile; the partial sums (fp32) are exchanged through
+//    distributed shared memory (asynchronous stores that count on the receiver's
+//    mbarrier) and both CTAs add the two -- a + b is the same either way round,
+//    so both hold the same scores.
+//  * Each computes the softmax of all 128 rows, and O[128 x 256] += P V over its
+//    own 256 dims: the key tile in shared memory is the K-major B operand of the
+//    first product and the MN-major B operand of the second.
+//  * Tensor memory: Q 128 columns (the A operand of the first product; its
+//    rotary part is in shared memory), S 2 x 64 (P in bf16 is written over S and
+//    is the A operand of the second product), O 256: 512.
+//  * Warps 0-3: softmax, one query row a thread, and the epilogue.  Warps 4-7:
+//    send the partial scores, and load the next item's queries meanwhile.  Warp
+//    8: TMA producer, four stages of 64 keys (36 KiB).  Warp 9: MMA issuer.
+//
+// Work split.  The tiles of all (sequence, 128-row unit) pairs are laid end to
+// end and cut into equal ranges, one a cluster: the batch's ragged lengths
+// balance without a plan on the host, and one long context is split over all
+// SMs.  A unit that a cut falls into leaves fp32 partial sums in the workspace
+// (at most two a cluster), which latent_merge_kernel joins in cluster order.
 #include "common.cuh"
 #include "trace.h"
 
@@ -18,69 +51,731 @@ __device__ uint32_t g_status;
 using namespace pkv;
 
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr int TK = 64;                            // keys per tile
+constexpr int HALF = LAT / 2, RHALF = ROPE / 2;   // a CTA's latent and rotary dims
+constexpr int NCL = 76;                           // clusters: a pair of CTAs on each pair of the 152 SMs
+constexpr int MIN_TILES = 2;                      // tiles a cluster takes at least, if there are as many
+constexpr int STAGES = 4;
+constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys x 64 dims
+constexpr uint32_t ROPE_OFF = 4 * CHUNK_BYTES;    // within a stage
+constexpr uint32_t STAGE_BYTES = ROPE_OFF + TK * 64;
+constexpr uint32_t SQR = STAGES * STAGE_BYTES;    // the queries' rotary part, 128 rows x 64 bytes
+constexpr uint32_t SRECV = SQR + 128 * 64;        // the peer's partial scores, 2 x [16 column groups][128 rows] float4
+constexpr uint32_t RECV_BYTES = 128 * TK * 4;
+constexpr uint32_t SBAR = SRECV + 2 * RECV_BYTES;
+constexpr uint32_t LIST_OFF = 512;                // within the barrier area
+constexpr int LIST = 40;                          // sequences tabled in shared memory
+constexpr int SMEM_BYTES = SBAR + 1024 + 1024;    // + 1 KiB: aligned to 1 KiB at run time
+constexpr int THREADS = 320;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+
+enum {
+    B_KVF = 0,                  // + stage: the tile landed
+    B_KVE = B_KVF + STAGES,     // + stage: every MMA reading it is done
+    B_Q = B_KVE + STAGES,       // the item's queries are in place (128 arrivals)
+    B_S = B_Q + 1,              // + buffer: a partial S tile is in tensor memory
+    B_SENT = B_S + 2,           // + 4 x buffer + warp: its rows were read by the sending warp
+    B_RECV = B_SENT + 8,        // + 4 x buffer + warp: the peer's partial rows arrived
+    B_RFREE = B_RECV + 8,       // + 4 x buffer + warp: the peer has read what this CTA sent
+    B_P = B_RFREE + 8,          // + buffer: P is in tensor memory (128 arrivals)
+    B_PVD = B_P + 2,            // the latest PV product finished
+    B_DRAIN = B_PVD + 1,        // every MMA of the item finished
+    B_OFREE = B_DRAIN + 1,      // the item's O was read (128 arrivals)
+    NBAR = B_OFREE + 1
+};
+static_assert(NBAR * 8 + 64 <= LIST_OFF && LIST_OFF + LIST * 12 <= 1024, "barrier area");
+
+// instruction descriptors, kind::f16: bf16 A and B, fp32 accumulate, M = 128
+constexpr uint32_t idesc(int n, bool b_mn_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+constexpr uint32_t IDESC_S = idesc(TK, false);
+constexpr uint32_t IDESC_PV = idesc(HALF, true);
 
 struct LatentParams {
     uint16_t *out;
-    const uint16_t *q, *cache;
+    const uint16_t *q;
     const int32_t *cu, *lens, *tables;
-    int num_seqs, rows, heads, max_blocks, num_blocks;
+    int4 *desc;       // [NCL] the unit to merge whose first tiles cluster k holds: 1 (0: none), partials, rows, -
+    int64_t *desc2;   // [NCL] the unit's first (row, head)
+    float *part_o;    // [2 NCL][slot_rows][512]
+    float *part_ml;   // [2 NCL][slot_rows][2]
+    int slot_rows;    // rows of a unit, at most
+    int num_seqs, rows, heads, tpt, max_blocks, num_blocks;
     float scale_log2;
 };
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
 
-// One warp per (row, head): lane l holds dims l, l + 32, ... of q and of the sum.
-__global__ void __launch_bounds__(256) latent_simple_kernel(const LatentParams p)
+// bounded wait that also gives up once another warp of the CTA has
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w >= (long long)p.rows * p.heads) return;
-    const int row = (int)(w / p.heads), h = (int)(w % p.heads);
-    int s = row, a = row, n = 1;
-    if (p.cu) {
-        s = -1;
-        for (int i = 0; i < p.num_seqs; ++i)
-            if (p.cu[i] <= row && row < p.cu[i + 1]) {
-                s = i;
-                a = p.cu[i];
-                n = p.cu[i + 1] - a;
+    if constexpr (!CLUSTER) return mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    bool ok = try_wait<CLUSTER>(bar, parity);
+    if (!ok) {
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if (try_wait<CLUSTER>(bar, parity)) {
+                ok = true;
                 break;
             }
-        if (s < 0) return;
-    }
-    const int L = p.lens[s];
-    if (L < 0 || L > p.max_blocks * BS || (L < n && L != 0) || a < 0 || a + n > p.rows) {
-        if (lane == 0) flag(ST_BAD_LEN);
-        return;
-    }
-    const int last = L - n + (row - a);
-    float q[18], o[16], m = -INFINITY, l = 0.f;
-    const uint16_t *qr = p.q + w * LKD;
-    for (int k = 0; k < 18; ++k) q[k] = __uint_as_float((uint32_t)qr[lane + 32 * k] << 16);
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
-    for (int t = 0; t <= last && L > 0; ++t) {
-        const int id = p.tables[(size_t)s * p.max_blocks + t / BS];
-        if (id < 0 || id >= p.num_blocks) {
-            if (lane == 0) flag(ST_BAD_BLOCK);
-            continue;
+            if ((it & 63u) == 0) {
+                if (*abort_flag) break;
+                if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+                    *abort_flag = 1;
+                    flag(ST_TIMEOUT);
+                    break;
+                }
+            }
         }
-        const uint16_t *x = p.cache + ((size_t)id * BS + t % BS) * LKD;
-        float v[18], d = 0.f;
-        for (int k = 0; k < 18; ++k) {
-            v[k] = __uint_as_float((uint32_t)x[lane + 32 * k] << 16);
-            d += q[k] * v[k];
-        }
-        for (int b = 16; b > 0; b >>= 1) d += __shfl_xor_sync(0xffffffffu, d, b);
-        d *= p.scale_log2;
-        const float mn = fmaxf(m, d), c = ex2(m - mn), e = ex2(d - mn);
-        l = l * c + e;
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * c + e * v[k];
-        m = mn;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t *r = p.out + w * LAT;
-    for (int k = 0; k < 16; ++k) r[lane + 32 * k] = (uint16_t)(pack_bf16(o[k] * inv, 0.f) & 0xffffu);
+    return __all_sync(0xffffffffu, ok);   // the roles run warp-collective instructions: a warp leaves as a whole
 }
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes into the peer's shared memory, counted on the peer's mbarrier
+__device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, float c, float d, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr),
+                 "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_peer(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// 64-byte-swizzled K-major operand (rows of 64 bytes)
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_bytes)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;
+    return d;
+}
+
+// ------------------------------------------------------------------- the work
+// A sequence as the kernel sees it: n = 0 if it has no rows or was refused.
+struct Seq {
+    int a, n, L;
+};
+__device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagging)
+{
+    Seq q;
+    q.a = p.cu ? __ldg(p.cu + s) : s;
+    const int b = p.cu ? __ldg(p.cu + s + 1) : s + 1;
+    q.n = b - q.a;
+    q.L = __ldg(p.lens + s);
+    if (q.n == 0) return q;
+    if (q.a < 0 || b < q.a || b > p.rows || q.L < 0 || q.L > p.max_blocks * BS || (q.L != 0 && q.L < q.n)) {
+        if (flagging) flag(ST_BAD_LEN);
+        q.n = 0;
+    }
+    return q;
+}
+__device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK - 1) / TK); }
+// tiles of all its units: every unit is charged the whole context (the causal
+// end of a prompt chunk's earlier units leaves the rest of their charge empty)
+__device__ __forceinline__ long long seq_cost(const LatentParams &p, const Seq &q)
+{
+    return q.n > 0 ? (long long)((q.n + p.tpt - 1) / p.tpt) * seq_tiles(q) : 0;
+}
+
+struct Item {
+    Seq q;
+    int s, t0, toks;     // the unit's first token within the sequence, and its tokens
+    int j0, j1, kt;      // its tiles in this cluster's range, and all its tiles
+    long long g0;        // the place of its first tile
+    int KT;              // what it is charged
+};
+// Walks a cluster's range; every role keeps one and sees the same items.
+struct Walk {
+    int s;
+    long long base, pos, end;
+};
+__device__ __forceinline__ bool next_item(const LatentParams &p, const int *list, int s_first, Walk &w, Item &it)
+{
+    while (w.pos < w.end) {
+        Seq q;
+        long long cost;
+        for (;;) {
+            if (w.s >= p.num_seqs) return false;
+            const int i = w.s - s_first;
+            if (i < LIST) q = {list[3 * i], list[3 * i + 1], list[3 * i + 2]};
+            else q = read_seq(p, w.s, false);
+            cost = seq_cost(p, q);
+            if (w.pos < w.base + cost) break;
+            w.base += cost;
+            ++w.s;
+        }
+        const int KT = seq_tiles(q);
+        const long long rem = w.pos - w.base, u = rem / KT;
+        const int j0 = (int)(rem - u * KT);
+        const int jend = (int)min((long long)KT, j0 + (w.end - w.pos));
+        it.t0 = (int)u * p.tpt;
+        it.toks = min(p.tpt, q.n - it.t0);
+        it.kt = max(1, (q.L - q.n + it.t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
+        it.g0 = w.base + u * KT;
+        w.pos += jend - j0;
+        if (j0 >= it.kt) continue;
+        it.q = q;
+        it.s = w.s;
+        it.j0 = j0;
+        it.j1 = min(jend, it.kt);
+        it.KT = KT;
+        return true;
+    }
+    return false;
+}
+
+__global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
+                  const LatentParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SBAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_start = reinterpret_cast<int *>(tmem_slot + 2);        // the first sequence of the range
+    long long *s_work = reinterpret_cast<long long *>(bars + NBAR + 2);   // [0] total, [1] base of s_start
+    int *list = reinterpret_cast<int *>(smem + SBAR + LIST_OFF);
+    long long *scan = reinterpret_cast<long long *>(smem + SRECV);        // setup only
+    auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t c = cluster_rank(), peer = c ^ 1u;
+    const int k = blockIdx.x >> 1;                                // cluster
+    griddep_launch_dependents();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar(B_KVF + i), 1);
+            mbar_init(bar(B_KVE + i), 1);
+        }
+        mbar_init(bar(B_Q), 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + i), 128);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(bar(B_SENT + i), 1);
+            mbar_init(bar(B_RECV + i), 1);
+            mbar_init(bar(B_RFREE + i), 1);
+        }
+        mbar_init(bar(B_PVD), 1);
+        mbar_init(bar(B_DRAIN), 1);
+        mbar_init(bar(B_OFREE), 128);
+        *abort_flag = 0;
+        *s_start = p.num_seqs;
+        s_work[1] = 0;
+        fence_mbar_init();
+        prefetch_tmap(&lmap);
+        prefetch_tmap(&rmap);
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    griddep_wait();       // everything below reads what earlier kernels wrote
+    // ---- the cluster's range: prefix sums of the sequences' costs, a run of
+    // consecutive sequences a thread
+    const int per = (p.num_seqs + THREADS - 1) / THREADS;
+    const int sa = min(p.num_seqs, (int)threadIdx.x * per), sb = min(p.num_seqs, sa + per);
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += seq_cost(p, read_seq(p, s, blockIdx.x == 0));
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long before = 0, W = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+        const long long t = scan[i];
+        if (i < warp) before += t;
+        W += t;
+    }
+    const long long nc = max(1ll, min((long long)NCL, W / MIN_TILES));   // clusters with work
+    Walk walk;
+    walk.pos = k < nc ? W * k / nc : W;
+    walk.end = k < nc ? W * (k + 1) / nc : W;
+    {
+        long long b = before + incl - mine;
+        if (walk.pos < walk.end && b <= walk.pos && walk.pos < b + mine) {
+            int s = sa;
+            for (; s < sb; ++s) {
+                const long long cost = seq_cost(p, read_seq(p, s, false));
+                if (walk.pos < b + cost) break;
+                b += cost;
+            }
+            *s_start = s;
+            s_work[1] = b;
+        }
+    }
+    __syncthreads();
+    const int s_first = *s_start;
+    for (int i = threadIdx.x; i < LIST; i += THREADS) {
+        const Seq q = s_first + i < p.num_seqs ? read_seq(p, s_first + i, false) : Seq{0, 0, 0};
+        list[3 * i] = q.a;
+        list[3 * i + 1] = q.n;
+        list[3 * i + 2] = q.L;
+    }
+    walk.s = s_first;
+    walk.base = s_work[1];
+    __syncthreads();
+    cluster_sync_all();   // the peer's barriers exist before anything is sent; its scan area is free
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tQ = tmem, tO = tmem + 256;
+    auto tS = [&](int b) -> uint32_t { return tmem + 128 + b * TK; };
+
+    Item it;
+    if (warp == 8) {
+        // ======================= producer: lanes 0-15 one 2 KiB box each (block
+        // lane / 4, 64 dims lane % 4), lanes 16-19 a block's rotary box; each lane
+        // reads its block id of the next tile while it waits for the stage
+        const bool is_r = lane >= 16;
+        const int blk = is_r ? lane - 16 : lane >> 2, chunk = lane & 3;
+        int u = 0;
+        bool ok = true;
+        while (ok && next_item(p, list, s_first, walk, it)) {
+            const int32_t *bt = p.tables + (size_t)it.s * p.max_blocks;
+            const int nblk = (it.q.L + BS - 1) / BS;
+            auto block_id = [&](int j) -> int32_t {
+                const int b = j * (TK / BS) + blk;
+                return (lane < 20 && j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
+            };
+            int32_t next_id = block_id(it.j0);
+            for (int j = it.j0; j < it.j1; ++j, ++u) {
+                const int st = u % STAGES;
+                const int32_t id = next_id;
+                next_id = block_id(j + 1);
+                if (u >= STAGES && !wait_bar(bar(B_KVE + st), ((u - STAGES) / STAGES) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const bool in = lane < 20 && j * (TK / BS) + blk < nblk;
+                const bool valid = in && id >= 0 && id < p.num_blocks;
+                if (in && !valid) flag(ST_BAD_BLOCK);
+                const unsigned vm = __ballot_sync(0xffffffffu, valid);
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(bar(B_KVF + st), __popc(vm & 0xffffu) * 2048 + __popc(vm >> 16) * 1024);
+                }
+                __syncwarp();
+                if (valid) {
+                    const uint32_t stg = sbase + st * STAGE_BYTES;
+                    if (is_r) tma_load_2d(stg + ROPE_OFF + blk * 1024, &rmap, LAT + c * RHALF, id * BS, bar(B_KVF + st));
+                    else tma_load_2d(stg + chunk * CHUNK_BYTES + blk * 2048, &lmap, c * HALF + chunk * 64, id * BS, bar(B_KVF + st));
+                }
+            }
+        }
+        if (*abort_flag)      // loads in flight land before the CTA exits
+            for (int uu = max(0, u - STAGES); uu < u; ++uu)
+                (void)mbar_wait_bounded(bar(B_KVF + uu % STAGES), (uu / STAGES) & 1);
+    } else if (warp == 9) {
+        // ======================= MMA issuer
+        const uint64_t kdesc0 = sdesc_sw128(sbase, 16, 1024);
+        const uint64_t rdesc0 = sdesc_sw64(sbase + ROPE_OFF, 512);
+        const uint64_t qrdesc = sdesc_sw64(sbase + SQR, 512);
+        const uint64_t vdesc0 = sdesc_sw128(sbase, CHUNK_BYTES, 1024);
+        int u = 0, items = 0;
+        bool ok = true;
+        while (ok && next_item(p, list, s_first, walk, it)) {
+            const int T = it.j1 - it.j0;
+            // partial S of the item's tile jj (the CTA's tile u + jj) into buffer (u + jj) & 1
+            auto issue_s = [&](int jj) -> bool {
+                const int x = u + jj, st = x % STAGES;
+                if (!wait_bar(bar(B_KVF + st), (x / STAGES) & 1, abort_flag)) return false;
+                const int first = it.q.L - (it.j0 + jj) * TK;
+                if (first < TK) {
+                    // keys at or past the context's end may hold anything (never
+                    // written, or not loaded); P is 0 there, but 0 x NaN is NaN
+                    const uint32_t vb = sbase + st * STAGE_BYTES;
+                    for (int e = lane; e < (TK - first) * 32; e += 32)
+                        st_shared_v4(vb + ((e >> 3) & 3) * CHUNK_BYTES + (first + (e >> 5)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)((st * STAGE_BYTES) >> 4);
+                    const uint32_t ts = tS(x & 1);
+#pragma unroll
+                    for (int kk = 0; kk < 16; ++kk)
+                        umma_f16_ts(ts, tQ + kk * 8, kdesc0 + off + (uint64_t)(((kk >> 2) * CHUNK_BYTES + (kk & 3) * 32) >> 4),
+                                    IDESC_S, kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+                        umma_f16(ts, qrdesc + (uint64_t)((kk * 32) >> 4), rdesc0 + off + (uint64_t)((kk * 32) >> 4), IDESC_S, 1u);
+                    umma_commit(bar(B_S + (x & 1)));
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = wait_bar(bar(B_Q), items & 1, abort_flag);
+            for (int jj = 0; ok && jj < min(2, T); ++jj) ok = issue_s(jj);
+            for (int jj = 0; ok && jj < T; ++jj) {
+                const int x = u + jj, st = x % STAGES;
+                if (!wait_bar(bar(B_P + (x & 1)), (x >> 1) & 1, abort_flag)) { ok = false; break; }
+                // the item before: its O has been read
+                if (jj == 0 && items > 0 && !wait_bar(bar(B_OFREE), (items - 1) & 1, abort_flag)) { ok = false; break; }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t vd = vdesc0 + (uint64_t)((st * STAGE_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        umma_f16_ts(tO, tS(x & 1) + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), IDESC_PV, (jj > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(bar(B_PVD));
+                    umma_commit(bar(B_KVE + st));
+                    if (jj == T - 1) umma_commit(bar(B_DRAIN));
+                }
+                __syncwarp();
+                // in issue order: PV(jj) reads P from the buffer that S(jj + 2) overwrites
+                if (jj + 2 < T) ok = issue_s(jj + 2);
+            }
+            u += T;
+            ++items;
+        }
+        if (!ok) {      // given up inside an item: its products are waited for too
+            if (lane == 0) umma_commit(bar(B_DRAIN));
+            __syncwarp();
+            ++items;
+        }
+        // every MMA finished before tensor memory is released
+        if (items > 0) (void)mbar_wait_bounded(bar(B_DRAIN), (items - 1) & 1);
+    } else if (warp >= 4) {
+        // ======================= senders: thread = query row
+        const int w = warp & 3, r = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+        int x = 0;                            // tiles
+        // per buffer: whether this warp has sent in it, and the parity of its next
+        // release (a warp skips items that give it no real row)
+        uint32_t sent = 0u, fpar = 0u;
+        bool ok = true;
+        while (ok && next_item(p, list, s_first, walk, it)) {
+            const int rows = it.toks * p.heads;
+            // the queries: every first product of the item before has finished (this
+            // warp saw its last S), so they may be replaced
+            {
+                const uint16_t *src = p.q + ((size_t)(it.q.a + it.t0) * p.heads + r) * LKD;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint4 y = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + c * HALF) + h * 8 + e) : zero;
+                        v[4 * e] = y.x;
+                        v[4 * e + 1] = y.y;
+                        v[4 * e + 2] = y.z;
+                        v[4 * e + 3] = y.w;
+                    }
+                    tmem_st32u(tQ + lane_base + 32 * h, v);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 y = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + LAT + c * RHALF) + e) : zero;
+                    // (64-byte swizzle: 16-byte pieces permuted by the row's bits 1-2)
+                    st_shared_v4(sbase + SQR + r * 64 + ((e ^ ((r >> 1) & 3)) << 4), y.x, y.y, y.z, y.w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                fence_proxy_async_smem();
+                mbar_arrive(bar(B_Q));
+            }
+            const bool active = w * 32 < rows;    // warps without a real row exchange nothing
+            for (int j = it.j0; j < it.j1; ++j, ++x) {
+                const int b = x & 1, i = 4 * b + w;
+                if (!wait_bar(bar(B_S + b), (x >> 1) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                if (active) {
+                    float v[64];
+                    tmem_ld64(tS(b) + lane_base, v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SENT + i));
+                    if ((sent >> b) & 1) {
+                        if (!wait_bar<true>(bar(B_RFREE + i), (fpar >> b) & 1, abort_flag)) { ok = false; break; }
+                        fpar ^= 1u << b;
+                    }
+                    sent |= 1u << b;
+                    const uint32_t dst = peer_addr(sbase + SRECV + b * RECV_BYTES + r * 16, peer);
+                    const uint32_t rb = peer_addr(bar(B_RECV + i), peer);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        st_async_v4(dst + e * 2048, v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], rb);
+                } else {
+                    if (lane == 0) mbar_arrive(bar(B_SENT + i));
+                }
+            }
+        }
+    } else {
+        // ======================= softmax and epilogue: thread = query row = lane
+        const int r = threadIdx.x;
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        int x = 0, items = 0;
+        uint32_t rpar = 0u;      // per buffer: the parity of the next rows from the peer
+        const float sl = p.scale_log2;
+        bool ok = true, merges = false;
+        while (ok && next_item(p, list, s_first, walk, it)) {
+            const int rows = it.toks * p.heads;
+            const bool active = warp * 32 < rows;
+            const int tok = min(r, rows - 1) / p.heads;
+            const int first_pos = it.q.L - it.q.n + it.t0;
+            const int pos = it.q.L > 0 ? first_pos + tok : -1;    // the last key this row sees
+            const int pos_min = it.q.L > 0 ? first_pos : -1;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = it.j0; j < it.j1 && ok; ++j, ++x) {
+                const int b = x & 1, i = 4 * b + warp, t0 = j * TK;
+                if (!wait_bar(bar(B_SENT + i), (x >> 1) & 1, abort_flag)) { ok = false; break; }
+                if (active) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar(B_RECV + i), 32 * TK * 4);
+                    if (!wait_bar<true>(bar(B_RECV + i), (rpar >> b) & 1, abort_flag)) { ok = false; break; }
+                    rpar ^= 1u << b;
+                    tc_fence_after();
+                    float sv[TK];
+                    tmem_ld64(tS(b) + lane_base, sv);
+                    const uint32_t src = sbase + SRECV + b * RECV_BYTES + r * 16;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        uint32_t a0, a1, a2, a3;
+                        lds128(src + e * 2048, a0, a1, a2, a3);
+                        sv[4 * e] += __uint_as_float(a0);
+                        sv[4 * e + 1] += __uint_as_float(a1);
+                        sv[4 * e + 2] += __uint_as_float(a2);
+                        sv[4 * e + 3] += __uint_as_float(a3);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive_peer(peer_addr(bar(B_RFREE + i), peer));
+                    if (t0 + TK - 1 > pos_min) {
+#pragma unroll
+                        for (int e = 0; e < TK; ++e)
+                            if (t0 + e > pos) sv[e] = -INFINITY;
+                    }
+                    // raw scores; the scale (> 0) is applied inside the exponent's FFMA
+                    float mk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mk[e] = fmaxf(sv[e], sv[4 + e]);
+#pragma unroll
+                    for (int e = 8; e < TK; e += 8)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) mk[h] = max3(mk[h], sv[e + h], sv[e + 4 + h]);
+                    const float mx = max3(mk[0], mk[1], fmaxf(mk[2], mk[3])) * sl;
+                    // the reference moves only when the maximum has grown by 2^8 (P stays
+                    // finite in fp32 and bf16, whose relative precision does not depend on
+                    // its size): O is seldom rescaled
+                    float alpha = 1.f;
+                    if (mx > m_ref + RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
+                        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
+                        m_ref = mx;
+                    }
+                    const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
+                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                    uint32_t pw[TK / 2];
+#pragma unroll
+                    for (int e = 0; e < TK / 2; ++e) {
+                        float y0, y1;
+                        f2_unpack(f2_fma(f2_pack(sv[2 * e], sv[2 * e + 1]), sl2, mn2), y0, y1);
+                        const float p0 = ex2(y0), p1 = ex2(y1);
+                        acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+                        pw[e] = pack_bf16(p0, p1);   // the second product's operand type, beside bf16 values
+                    }
+                    float s0, s1;
+                    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+                    l = l * alpha + (s0 + s1);
+                    // O is rescaled once PV(j-1) has accumulated into it; PV(j) waits for P
+                    if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        if (!wait_bar(bar(B_PVD), (x - 1) & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int h = 0; h < HALF / 32; ++h) {
+                            float o[32];
+                            tmem_ld32(tO + lane_base + h * 32, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tmem_st32(tO + lane_base + h * 32, o);
+                        }
+                    }
+                    tmem_st32u(tS(b) + lane_base, pw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                mbar_arrive(bar(B_P + b));
+            }
+            if (!ok) break;
+            if (!wait_bar(bar(B_DRAIN), items & 1, abort_flag)) break;
+            tc_fence_after();
+            const bool whole = it.j0 == 0 && it.j1 == it.kt;
+            const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
+            if (active) {
+                const size_t row = (size_t)(it.q.a + it.t0) * p.heads + r;
+                const size_t pr = (size_t)slot * p.slot_rows + r;
+                const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int h = 0; h < HALF / 32; ++h) {
+                    float o[32];
+                    tmem_ld32(tO + lane_base + h * 32, o);
+                    if (r >= rows) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * LAT + c * HALF + h * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * LAT + c * HALF + h * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                if (!whole && r < rows && c == 0) {
+                    p.part_ml[2 * pr] = l > 0.f ? m_ref : -INFINITY;
+                    p.part_ml[2 * pr + 1] = l;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(B_OFREE));
+            if (!whole && it.j0 == 0 && threadIdx.x == 0 && c == 0) {
+                // this cluster holds the unit's first tiles: what there is to merge
+                const long long last = it.g0 + it.kt - 1;       // the place of its last tile
+                long long kl = last * nc / W;                    // the cluster that holds it
+                while (W * (kl + 1) / nc <= last) ++kl;
+                while (W * kl / nc > last) --kl;
+                p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
+                p.desc[k] = make_int4(1, (int)(kl - k + 1), rows, 0);
+                merges = true;
+            }
+            ++items;
+        }
+        // (the workspace starts with anything)
+        if (!merges && threadIdx.x == 0 && c == 0) p.desc[k] = make_int4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    cluster_sync_all();   // nothing is sent to a CTA that has left
+}
+
+// Joins the partial sums of the units that a cut fell into: a warp for each
+// (row, 128 dims), cluster by cluster, with weights 2^(m_i - max m).  The partial
+// sums are read once, from L2 as a rule.
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
+{
+    __shared__ int4 desc[NCL];
+    griddep_wait();
+    for (int i = threadIdx.x; i < NCL; i += blockDim.x) desc[i] = p.desc[i];
+    __syncthreads();
+    const int lane = threadIdx.x & 31, nw = gridDim.x * (blockDim.x >> 5);
+    const int per = p.slot_rows * 4;
+    for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < NCL * per; t += nw) {
+        const int k = t / per, row = (t % per) >> 2, q4 = t & 3;
+        const int4 d = desc[k];
+        if (d.x == 0 || row >= d.z) continue;
+        // partial i: the first is in its cluster's second slot, the others in their cluster's first
+        auto slot = [&](int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows + row; };
+        float M = -INFINITY;
+        for (int i = lane; i < d.y; i += 32) M = fmaxf(M, p.part_ml[2 * slot(i)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        if (M != -INFINITY) {
+            for (int i0 = 0; i0 < d.y; i0 += 32) {
+                float f = 0.f, fl = 0.f;
+                if (i0 + lane < d.y) {
+                    const float2 e = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(i0 + lane));
+                    f = ex2(e.x - M);
+                    fl = f * e.y;
+                }
+                l += fl;
+                const int n = min(32, d.y - i0);
+                for (int j0 = 0; j0 < n; j0 += 8) {
+                    float4 v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = j0 + j < n ? reinterpret_cast<const float4 *>(p.part_o + slot(i0 + j0 + j) * LAT + q4 * 128)[lane]
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+                        if (j0 + j < n) {
+                            acc.x += fj * v[j].x;
+                            acc.y += fj * v[j].y;
+                            acc.z += fj * v[j].z;
+                            acc.w += fj * v[j].w;
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<uint2 *>(p.out + (p.desc2[k] + row) * LAT + q4 * 128)[lane] =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+}
+
+int unit_tokens(int heads) { return 128 / heads; }
+
+// workspace: the merge list, then the partial maxima and sums, then the partial outputs
+struct Layout {
+    size_t desc2, ml, o, total;
+    int slot_rows;
+};
+Layout layout(int heads)
+{
+    Layout y;
+    y.slot_rows = unit_tokens(heads) * heads;
+    y.desc2 = NCL * sizeof(int4);
+    y.ml = 2048;
+    y.o = y.ml + (((size_t)2 * NCL * y.slot_rows * 8 + 255) & ~(size_t)255);
+    y.total = y.o + (size_t)2 * NCL * y.slot_rows * LAT * 4;
+    return y;
+}
+static_assert(NCL * (sizeof(int4) + 8) <= 2048, "merge list");
 
 }  // namespace
 
@@ -99,8 +794,10 @@ extern "C" {
 size_t paged_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t num_heads,
                                              int32_t max_blocks_per_seq)
 {
-    (void)num_seqs, (void)total_q_tokens, (void)num_heads, (void)max_blocks_per_seq;
-    return 0;
+    if (num_seqs < 1 || total_q_tokens < 1 || num_heads < 1 || num_heads > PAGEDKV_LATENT_MAX_HEADS ||
+        max_blocks_per_seq < 1)
+        return 0;
+    return layout(num_heads).total;
 }
 
 kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
@@ -125,13 +822,40 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     const size_t need =
         paged_latent_attention_workspace_size(num_seqs, total_q_tokens, num_heads, max_blocks_per_seq);
     if (need && (!workspace || workspace_bytes < need || !pkv_host::aligned(workspace, 256))) return KV_ERR_INVALID;
-    const LatentParams p = {static_cast<uint16_t *>(out), static_cast<const uint16_t *>(q),
-                            static_cast<const uint16_t *>(cache), cu_q_lens, context_lens, block_tables, num_seqs,
-                            total_q_tokens, num_heads, max_blocks_per_seq, num_blocks, scale * LOG2E};
-    const long long warps = (long long)total_q_tokens * num_heads;
-    if ((warps + 7) / 8 > INT32_MAX) return KV_ERR_UNSUPPORTED;
-    latent_simple_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    const Layout y = layout(num_heads);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    LatentParams p;
+    p.out = static_cast<uint16_t *>(out);
+    p.q = static_cast<const uint16_t *>(q);
+    p.cu = cu_q_lens;
+    p.lens = context_lens;
+    p.tables = block_tables;
+    p.desc = reinterpret_cast<int4 *>(ws);
+    p.desc2 = reinterpret_cast<int64_t *>(ws + y.desc2);
+    p.part_ml = reinterpret_cast<float *>(ws + y.ml);
+    p.part_o = reinterpret_cast<float *>(ws + y.o);
+    p.slot_rows = y.slot_rows;
+    p.num_seqs = num_seqs;
+    p.rows = total_q_tokens;
+    p.heads = num_heads;
+    p.tpt = unit_tokens(num_heads);
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * LOG2E;
+    // the cache as rows of 576: boxes of 16 rows (a block) x 64 latent or 32 rotary dims
+    CUtensorMap lmap, rmap;
+    const uint64_t rows = (uint64_t)num_blocks * BS;
+    if (!pkv_host::encode_tmap_2d(&lmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, 64, BS,
+                                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !pkv_host::encode_tmap_2d(&rmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, RHALF, BS,
+                                  CU_TENSOR_MAP_SWIZZLE_64B))
+        return KV_ERR_CUDA;
+    if (pkv_host::ensure_dynamic_smem<latent_kernel>(SMEM_BYTES) != cudaSuccess) return KV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pkv_host::launch_ex(latent_kernel, dim3(2 * NCL), dim3(THREADS), SMEM_BYTES, st, true, lmap, rmap, p) != cudaSuccess ||
+        pkv_host::launch_ex(latent_merge_kernel, dim3(2 * NCL), dim3(256), 0, st, true, p) != cudaSuccess)
+        return KV_ERR_CUDA;
+    return KV_OK;
 }
 
 }  // extern "C"
