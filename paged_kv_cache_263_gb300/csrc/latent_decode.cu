@@ -26,12 +26,22 @@
 //  * Each computes the softmax of all 128 rows, and O[128 x 256] += P V over its
 //    own 256 dims: the key tile in shared memory is the K-major B operand of the
 //    first product and the MN-major B operand of the second.
-//  * Tensor memory: Q 128 columns (the A operand of the first product; its
-//    rotary part is in shared memory), S 2 x 64 (P in bf16 is written over S and
-//    is the A operand of the second product), O 256: 512.
-//  * Warps 0-3: softmax, one query row a thread, and the epilogue.  Warps 4-7:
-//    send the partial scores, and load the next item's queries meanwhile.  Warp
-//    8: TMA producer, four stages of 64 keys (36 KiB).  Warp 9: MMA issuer.
+//  * Tensor memory, 512 columns: Q 96 (192 dims as the A operand of the first
+//    product; the other 64 and the rotary part are in shared memory), P 32 (bf16,
+//    the A operand of the second product), S 2 x 64, O 256.  P has its own
+//    columns so that an S buffer is free as soon as it has been read: the first
+//    products run ahead of the softmax.  With P written over S (and all of Q in
+//    tensor memory) a tile took 2,000-2,800 cycles, all of it the latency of the
+//    loop S -> exchange -> softmax -> PV -> next S over two buffers.
+//  * The exchange goes in slots of 32 columns (three of 16 KiB), each released
+//    as soon as it is added, so that three slots keep both directions busy.
+//  * Warps 0-7: exchange, softmax and epilogue, one query row a thread; warps 0-3
+//    take the even tiles (S buffer 0), warps 4-7 the odd ones, and hand the
+//    running maximum on through shared memory.  A tile costs its warps about
+//    2,000 cycles, nearly all latency, so one group alone set the pace.  The
+//    group that does not have an item's last tile loads the next item's queries.
+//    Warp 8: TMA producer, four stages of 64 keys (36 KiB).  Warps 9 and 10: MMA
+//    issuers.
 //
 // Work split.  The tiles of all (sequence, 128-row unit) pairs are laid end to
 // end and cut into equal ranges, one a cluster: the batch's ragged lengths
@@ -60,14 +70,18 @@ constexpr int STAGES = 4;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys x 64 dims
 constexpr uint32_t ROPE_OFF = 4 * CHUNK_BYTES;    // within a stage
 constexpr uint32_t STAGE_BYTES = ROPE_OFF + TK * 64;
-constexpr uint32_t SQR = STAGES * STAGE_BYTES;    // the queries' rotary part, 128 rows x 64 bytes
-constexpr uint32_t SRECV = SQR + 128 * 64;        // the peer's partial scores, 2 x [16 column groups][128 rows] float4
-constexpr uint32_t RECV_BYTES = 128 * TK * 4;
-constexpr uint32_t SBAR = SRECV + 2 * RECV_BYTES;
+constexpr int QT = 192;                           // a CTA's query dims in tensor memory; the other 64 are in shared
+constexpr uint32_t SQ = STAGES * STAGE_BYTES;     // query dims 192..255 of the CTA's 256, 128 rows x 128 bytes
+constexpr uint32_t SQR = SQ + 128 * 128;          // the queries' rotary part, 128 rows x 64 bytes
+constexpr int SLOTS = 3, SCOLS = 32;              // the peer's partial scores: slots of 32 columns,
+constexpr uint32_t SRECV = SQR + 128 * 64;        // [8 groups of 4 columns][128 rows] float4
+constexpr uint32_t SLOT_BYTES = 128 * SCOLS * 4;
+constexpr uint32_t SMAX = SRECV + SLOTS * SLOT_BYTES;   // running maxima [128]; at an item's end [item parity][group](sum, maximum)[128]
+constexpr uint32_t SBAR = SMAX + 9 * 128 * 4;
 constexpr uint32_t LIST_OFF = 512;                // within the barrier area
 constexpr int LIST = 40;                          // sequences tabled in shared memory
 constexpr int SMEM_BYTES = SBAR + 1024 + 1024;    // + 1 KiB: aligned to 1 KiB at run time
-constexpr int THREADS = 320;
+constexpr int W_PROD = 8, W_MMA = 9, THREADS = 32 * (W_MMA + 2);
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 
 enum {
@@ -75,15 +89,21 @@ enum {
     B_KVE = B_KVF + STAGES,     // + stage: every MMA reading it is done
     B_Q = B_KVE + STAGES,       // the item's queries are in place (128 arrivals)
     B_S = B_Q + 1,              // + buffer: a partial S tile is in tensor memory
-    B_SENT = B_S + 2,           // + 4 x buffer + warp: its rows were read by the sending warp
-    B_RECV = B_SENT + 8,        // + 4 x buffer + warp: the peer's partial rows arrived
-    B_RFREE = B_RECV + 8,       // + 4 x buffer + warp: the peer has read what this CTA sent
-    B_P = B_RFREE + 8,          // + buffer: P is in tensor memory (128 arrivals)
-    B_PVD = B_P + 2,            // the latest PV product finished
-    B_DRAIN = B_PVD + 1,        // every MMA of the item finished
-    B_OFREE = B_DRAIN + 1,      // the item's O was read (128 arrivals)
-    NBAR = B_OFREE + 1
+    B_SFREE = B_S + 2,          // + buffer: it has been read (a group's 4 warps)
+    B_RECV = B_SFREE + 2,       // + 4 x slot + row warp: the peer's partial rows arrived
+    B_RFREE = B_RECV + 4 * SLOTS,   // + 4 x slot + row warp: the peer has read what this CTA sent
+    B_SORD = B_RFREE + 4 * SLOTS,   // + row warp: the tile's partial rows have been sent
+    B_MAX = B_SORD + 4,         // + row warp: the peer's have been added, the running maxima are in shared memory
+    B_SUM = B_MAX + 4,          // + row warp: both groups' sums are in shared memory
+    B_P = B_SUM + 4,            // P is in tensor memory (128 arrivals)
+    B_PVD = B_P + 1,            // + tile parity: its PV product finished (one barrier each: a group waits for
+                                // every second tile's, and a parity must not be waited for two phases ahead)
+    B_DRAIN = B_PVD + 2,        // every MMA of the item finished
+    B_OFREE = B_DRAIN + 1,      // the item's O was read (256 arrivals)
+    B_END = B_OFREE + 1,        // + issuer: everything it issued finished
+    NBAR = B_END + 2
 };
+static_assert(QT == 192, "the loads of the queries");
 static_assert(NBAR * 8 + 64 <= LIST_OFF && LIST_OFF + LIST * 12 <= 1024, "barrier area");
 
 // instruction descriptors, kind::f16: bf16 A and B, fp32 accumulate, M = 128
@@ -111,28 +131,13 @@ struct LatentParams {
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
 
 // bounded wait that also gives up once another warp of the CTA has
-template <bool CLUSTER>
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
-{
-    if constexpr (!CLUSTER) return mbar_try_wait(bar, parity);
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    bool ok = try_wait<CLUSTER>(bar, parity);
+    bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
         const unsigned long long t0 = globaltimer();
         for (uint32_t it = 1;; ++it) {
-            if (try_wait<CLUSTER>(bar, parity)) {
+            if (mbar_try_wait(bar, parity)) {
                 ok = true;
                 break;
             }
@@ -172,9 +177,16 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, flo
                  "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void arrive_peer(uint32_t bar)
+// tells the peer that this warp has read what it sent.  Relaxed: a release at
+// cluster scope waits for all of the thread's memory traffic (about 2,000 cycles
+// here, measured, in every tile).  What must be done before is only this warp's
+// reads of the slot, and the caller arrives after a vote that depends on every
+// value read, so they are.
+__device__ __forceinline__ void arrive_peer(uint32_t bar, int vote)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("{\n\t.reg .b32 t;\n\tmov.b32 t, %1;\n\tmbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(vote)
+                 : "memory");
 }
 // 64-byte-swizzled K-major operand (rows of 64 bytes)
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_bytes)
@@ -186,6 +198,13 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_byte
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)4 << 61;
     return d;
+}
+
+// the peer's barrier expects `bytes` of what follows (relaxed: nothing before has to be seen)
+__device__ __forceinline__ void expect_peer(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
 }
 
 // ------------------------------------------------------------------- the work
@@ -208,59 +227,69 @@ __device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagg
     return q;
 }
 __device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK - 1) / TK); }
+// a / b for a >= 0, b > 0 (a 64-bit division costs several hundred cycles)
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // tiles of all its units: every unit is charged the whole context (the causal
 // end of a prompt chunk's earlier units leaves the rest of their charge empty)
 __device__ __forceinline__ long long seq_cost(const LatentParams &p, const Seq &q)
 {
-    return q.n > 0 ? (long long)((q.n + p.tpt - 1) / p.tpt) * seq_tiles(q) : 0;
+    if (q.n <= 0) return 0;
+    return (long long)(q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
 }
 
 struct Item {
     Seq q;
     int s, t0, toks;     // the unit's first token within the sequence, and its tokens
     int j0, j1, kt;      // its tiles in this cluster's range, and all its tiles
-    long long g0;        // the place of its first tile
-    int KT;              // what it is charged
+    int left;            // tiles of the range from its first one on
 };
-// Walks a cluster's range; every role keeps one and sees the same items.
+// Walks a cluster's range; every role keeps one and sees the same items.  (No
+// division and no memory but shared: it runs between two items of every role.)
 struct Walk {
-    int s;
-    long long base, pos, end;
+    int s, u, j, left;   // next: sequence, unit, tile; tiles left
 };
 __device__ __forceinline__ bool next_item(const LatentParams &p, const int *list, int s_first, Walk &w, Item &it)
 {
-    while (w.pos < w.end) {
+    while (w.left > 0 && w.s < p.num_seqs) {
+        const int i = w.s - s_first;
         Seq q;
-        long long cost;
-        for (;;) {
-            if (w.s >= p.num_seqs) return false;
-            const int i = w.s - s_first;
-            if (i < LIST) q = {list[3 * i], list[3 * i + 1], list[3 * i + 2]};
-            else q = read_seq(p, w.s, false);
-            cost = seq_cost(p, q);
-            if (w.pos < w.base + cost) break;
-            w.base += cost;
+        if (i < LIST) q = {list[3 * i], list[3 * i + 1], list[3 * i + 2]};
+        else q = read_seq(p, w.s, false);
+        const int t0 = w.u * p.tpt;
+        if (t0 >= q.n) {             // (a sequence without rows, too)
             ++w.s;
+            w.u = w.j = 0;
+            continue;
         }
-        const int KT = seq_tiles(q);
-        const long long rem = w.pos - w.base, u = rem / KT;
-        const int j0 = (int)(rem - u * KT);
-        const int jend = (int)min((long long)KT, j0 + (w.end - w.pos));
-        it.t0 = (int)u * p.tpt;
-        it.toks = min(p.tpt, q.n - it.t0);
-        it.kt = max(1, (q.L - q.n + it.t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
-        it.g0 = w.base + u * KT;
-        w.pos += jend - j0;
-        if (j0 >= it.kt) continue;
         it.q = q;
         it.s = w.s;
-        it.j0 = j0;
+        it.t0 = t0;
+        it.toks = min(p.tpt, q.n - t0);
+        it.j0 = w.j;
+        it.left = w.left;
+        const int jend = min(seq_tiles(q), w.j + w.left);
+        w.left -= jend - w.j;
+        ++w.u;
+        w.j = 0;
+        it.kt = max(1, (q.L - q.n + t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
         it.j1 = min(jend, it.kt);
-        it.KT = KT;
-        return true;
+        if (it.j0 < it.kt) return true;
     }
     return false;
 }
+
+// The range of cluster k of nc: W tiles in nc runs, the first W % nc one longer.
+struct Cut {
+    long long each, extra;
+    __device__ __forceinline__ long long begin(int k) const { return k * each + min((long long)k, extra); }
+    __device__ __forceinline__ int owner(long long pos) const
+    {
+        return (int)(pos < extra * (each + 1) ? quotient(pos, each + 1) : extra + quotient(pos - extra * (each + 1), each));
+    }
+};
 
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     latent_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
@@ -272,8 +301,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SBAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_start = reinterpret_cast<int *>(tmem_slot + 2);        // the first sequence of the range
-    long long *s_work = reinterpret_cast<long long *>(bars + NBAR + 2);   // [0] total, [1] base of s_start
+    int *s_start = reinterpret_cast<int *>(tmem_slot + 2);        // the range's first sequence, unit and tile
+    long long *s_work = reinterpret_cast<long long *>(bars + NBAR + 4);   // the cut: each, extra
     int *list = reinterpret_cast<int *>(smem + SBAR + LIST_OFF);
     long long *scan = reinterpret_cast<long long *>(smem + SRECV);        // setup only
     auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
@@ -290,19 +319,26 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         mbar_init(bar(B_Q), 128);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_S + i), 1);
-            mbar_init(bar(B_P + i), 128);
+            mbar_init(bar(B_SFREE + i), 4);
+            mbar_init(bar(B_END + i), 1);
         }
-        for (int i = 0; i < 8; ++i) {
-            mbar_init(bar(B_SENT + i), 1);
+        for (int i = 0; i < 4 * SLOTS; ++i) {
             mbar_init(bar(B_RECV + i), 1);
             mbar_init(bar(B_RFREE + i), 1);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(B_SORD + i), 1);
+            mbar_init(bar(B_MAX + i), 1);
+            mbar_init(bar(B_SUM + i), 2);
+        }
+        mbar_init(bar(B_P), 128);
         mbar_init(bar(B_PVD), 1);
+        mbar_init(bar(B_PVD + 1), 1);
         mbar_init(bar(B_DRAIN), 1);
-        mbar_init(bar(B_OFREE), 128);
+        mbar_init(bar(B_OFREE), 256);
         *abort_flag = 0;
-        *s_start = p.num_seqs;
-        s_work[1] = 0;
+        s_start[0] = p.num_seqs;
+        s_start[1] = s_start[2] = 0;
         fence_mbar_init();
         prefetch_tmap(&lmap);
         prefetch_tmap(&rmap);
@@ -334,41 +370,48 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         if (i < warp) before += t;
         W += t;
     }
-    const long long nc = max(1ll, min((long long)NCL, W / MIN_TILES));   // clusters with work
-    Walk walk;
-    walk.pos = k < nc ? W * k / nc : W;
-    walk.end = k < nc ? W * (k + 1) / nc : W;
+    // clusters with work, and this one's range
+    const int nc = (int)max(1ll, min((long long)NCL, W / MIN_TILES));
+    Cut cut;
+    cut.each = quotient(W, nc);
+    cut.extra = W - cut.each * nc;
+    const long long w0 = k < nc ? cut.begin(k) : W, w1 = k < nc ? cut.begin(k + 1) : W;
     {
         long long b = before + incl - mine;
-        if (walk.pos < walk.end && b <= walk.pos && walk.pos < b + mine) {
+        if (w0 < w1 && b <= w0 && w0 < b + mine) {
             int s = sa;
             for (; s < sb; ++s) {
                 const long long cost = seq_cost(p, read_seq(p, s, false));
-                if (walk.pos < b + cost) break;
+                if (w0 < b + cost) break;
                 b += cost;
             }
-            *s_start = s;
-            s_work[1] = b;
+            const int KT = seq_tiles(read_seq(p, s, false));
+            const long long u = quotient(w0 - b, KT);
+            s_start[0] = s;
+            s_start[1] = (int)u;
+            s_start[2] = (int)(w0 - b - u * KT);
+            s_work[0] = cut.each;
+            s_work[1] = cut.extra;
         }
     }
     __syncthreads();
-    const int s_first = *s_start;
+    const int s_first = s_start[0];
     for (int i = threadIdx.x; i < LIST; i += THREADS) {
         const Seq q = s_first + i < p.num_seqs ? read_seq(p, s_first + i, false) : Seq{0, 0, 0};
         list[3 * i] = q.a;
         list[3 * i + 1] = q.n;
         list[3 * i + 2] = q.L;
     }
-    walk.s = s_first;
-    walk.base = s_work[1];
+    const int range = (int)(w1 - w0);
+    Walk walk = {s_first, s_start[1], s_start[2], range};
     __syncthreads();
     cluster_sync_all();   // the peer's barriers exist before anything is sent; its scan area is free
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tQ = tmem, tO = tmem + 256;
+    const uint32_t tQ = tmem, tP = tmem + QT / 2, tO = tmem + 256;
     auto tS = [&](int b) -> uint32_t { return tmem + 128 + b * TK; };
 
     Item it;
-    if (warp == 8) {
+    if (warp == W_PROD) {
         // ======================= producer: lanes 0-15 one 2 KiB box each (block
         // lane / 4, 64 dims lane % 4), lanes 16-19 a block's rotary box; each lane
         // reads its block id of the next tile while it waits for the stage
@@ -379,6 +422,14 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         while (ok && next_item(p, list, s_first, walk, it)) {
             const int32_t *bt = p.tables + (size_t)it.s * p.max_blocks;
             const int nblk = (it.q.L + BS - 1) / BS;
+            // the item's queries, into L2 (this warp runs up to four tiles ahead)
+            for (int r = lane; r < it.toks * p.heads; r += 32) {
+                const uint16_t *src = p.q + ((size_t)(it.q.a + it.t0) * p.heads + r) * LKD;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c * HALF + e * 64));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src + LAT + c * RHALF));
+            }
+            __syncwarp();
             auto block_id = [&](int j) -> int32_t {
                 const int b = j * (TK / BS) + blk;
                 return (lane < 20 && j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
@@ -411,203 +462,235 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         if (*abort_flag)      // loads in flight land before the CTA exits
             for (int uu = max(0, u - STAGES); uu < u; ++uu)
                 (void)mbar_wait_bounded(bar(B_KVF + uu % STAGES), (uu / STAGES) & 1);
-    } else if (warp == 9) {
-        // ======================= MMA issuer
-        const uint64_t kdesc0 = sdesc_sw128(sbase, 16, 1024);
-        const uint64_t rdesc0 = sdesc_sw64(sbase + ROPE_OFF, 512);
-        const uint64_t qrdesc = sdesc_sw64(sbase + SQR, 512);
-        const uint64_t vdesc0 = sdesc_sw128(sbase, CHUNK_BYTES, 1024);
-        int u = 0, items = 0;
+    } else if (warp >= W_MMA) {
+        // ======================= MMA issuers: one warp the first product of every
+        // tile, the other the second, so that a second product never queues behind
+        // a first one whose tile has not landed.  One elected lane issues: with
+        // elect.sync the compiler keeps descriptors in uniform registers, and a
+        // 128 x 64 x 16 product leaves every 33 cycles (54 from a lane-0 branch,
+        // measured), which is its execution time.
+        int x = 0, items = 0;       // tiles and items done
         bool ok = true;
-        while (ok && next_item(p, list, s_first, walk, it)) {
-            const int T = it.j1 - it.j0;
-            // partial S of the item's tile jj (the CTA's tile u + jj) into buffer (u + jj) & 1
-            auto issue_s = [&](int jj) -> bool {
-                const int x = u + jj, st = x % STAGES;
-                if (!wait_bar(bar(B_KVF + st), (x / STAGES) & 1, abort_flag)) return false;
-                const int first = it.q.L - (it.j0 + jj) * TK;
-                if (first < TK) {
-                    // keys at or past the context's end may hold anything (never
-                    // written, or not loaded); P is 0 there, but 0 x NaN is NaN
-                    const uint32_t vb = sbase + st * STAGE_BYTES;
-                    for (int e = lane; e < (TK - first) * 32; e += 32)
-                        st_shared_v4(vb + ((e >> 3) & 3) * CHUNK_BYTES + (first + (e >> 5)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
+        if (warp == W_MMA) {
+            const uint64_t kdesc0 = sdesc_sw128(sbase, 16, 1024);
+            const uint64_t rdesc0 = sdesc_sw64(sbase + ROPE_OFF, 512);
+            const uint64_t qdesc = sdesc_sw128(sbase + SQ, 16, 1024), qrdesc = sdesc_sw64(sbase + SQR, 512);
+            for (; ok && next_item(p, list, s_first, walk, it); ++items) {
+                ok = wait_bar(bar(B_Q), items & 1, abort_flag);
+                for (int j = it.j0; ok && j < it.j1; ++j, ++x) {
+                    const int st = x % STAGES, b = x & 1;
+                    // S(x - 2) has been read
+                    if (x >= 2 && !wait_bar(bar(B_SFREE + b), ((x >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!wait_bar(bar(B_KVF + st), (x / STAGES) & 1, abort_flag)) { ok = false; break; }
+                    const int first = it.q.L - j * TK;
+                    if (first < TK) {
+                        // keys at or past the context's end may hold anything (never
+                        // written, or not loaded); P is 0 there, but 0 x NaN is NaN
+                        const uint32_t vb = sbase + st * STAGE_BYTES;
+                        for (int e = lane; e < (TK - first) * 32; e += 32)
+                            st_shared_v4(vb + ((e >> 3) & 3) * CHUNK_BYTES + (first + (e >> 5)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (elect_one()) {
+                        tc_fence_after();
+                        const uint64_t off = (uint64_t)((st * STAGE_BYTES) >> 4);
+                        const uint32_t ts = tS(b);
+#pragma unroll
+                        for (int kk = 0; kk < QT / 16; ++kk)
+                            umma_f16_ts(ts, tQ + kk * 8, kdesc0 + off + (uint64_t)(((kk >> 2) * CHUNK_BYTES + (kk & 3) * 32) >> 4),
+                                        IDESC_S, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(ts, qdesc + (uint64_t)((kk * 32) >> 4),
+                                     kdesc0 + off + (uint64_t)((3 * CHUNK_BYTES + kk * 32) >> 4), IDESC_S, 1u);
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+                            umma_f16(ts, qrdesc + (uint64_t)((kk * 32) >> 4), rdesc0 + off + (uint64_t)((kk * 32) >> 4), IDESC_S, 1u);
+                        umma_commit(bar(B_S + b));
+                    }
                     __syncwarp();
                 }
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint64_t off = (uint64_t)((st * STAGE_BYTES) >> 4);
-                    const uint32_t ts = tS(x & 1);
-#pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)
-                        umma_f16_ts(ts, tQ + kk * 8, kdesc0 + off + (uint64_t)(((kk >> 2) * CHUNK_BYTES + (kk & 3) * 32) >> 4),
-                                    IDESC_S, kk > 0);
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk)
-                        umma_f16(ts, qrdesc + (uint64_t)((kk * 32) >> 4), rdesc0 + off + (uint64_t)((kk * 32) >> 4), IDESC_S, 1u);
-                    umma_commit(bar(B_S + (x & 1)));
-                }
-                __syncwarp();
-                return true;
-            };
-            ok = wait_bar(bar(B_Q), items & 1, abort_flag);
-            for (int jj = 0; ok && jj < min(2, T); ++jj) ok = issue_s(jj);
-            for (int jj = 0; ok && jj < T; ++jj) {
-                const int x = u + jj, st = x % STAGES;
-                if (!wait_bar(bar(B_P + (x & 1)), (x >> 1) & 1, abort_flag)) { ok = false; break; }
-                // the item before: its O has been read
-                if (jj == 0 && items > 0 && !wait_bar(bar(B_OFREE), (items - 1) & 1, abort_flag)) { ok = false; break; }
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint64_t vd = vdesc0 + (uint64_t)((st * STAGE_BYTES) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < TK / 16; ++kk)
-                        umma_f16_ts(tO, tS(x & 1) + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), IDESC_PV, (jj > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit(bar(B_PVD));
-                    umma_commit(bar(B_KVE + st));
-                    if (jj == T - 1) umma_commit(bar(B_DRAIN));
-                }
-                __syncwarp();
-                // in issue order: PV(jj) reads P from the buffer that S(jj + 2) overwrites
-                if (jj + 2 < T) ok = issue_s(jj + 2);
             }
-            u += T;
-            ++items;
-        }
-        if (!ok) {      // given up inside an item: its products are waited for too
-            if (lane == 0) umma_commit(bar(B_DRAIN));
-            __syncwarp();
-            ++items;
-        }
-        // every MMA finished before tensor memory is released
-        if (items > 0) (void)mbar_wait_bounded(bar(B_DRAIN), (items - 1) & 1);
-    } else if (warp >= 4) {
-        // ======================= senders: thread = query row
-        const int w = warp & 3, r = threadIdx.x & 127;
-        const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-        int x = 0;                            // tiles
-        // per buffer: whether this warp has sent in it, and the parity of its next
-        // release (a warp skips items that give it no real row)
-        uint32_t sent = 0u, fpar = 0u;
-        bool ok = true;
-        while (ok && next_item(p, list, s_first, walk, it)) {
-            const int rows = it.toks * p.heads;
-            // the queries: every first product of the item before has finished (this
-            // warp saw its last S), so they may be replaced
-            {
-                const uint16_t *src = p.q + ((size_t)(it.q.a + it.t0) * p.heads + r) * LKD;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            const uint64_t vdesc0 = sdesc_sw128(sbase, CHUNK_BYTES, 1024);
+            for (; ok && next_item(p, list, s_first, walk, it); ++items) {
+                for (int j = it.j0; j < it.j1; ++j, ++x) {
+                    const int st = x % STAGES;
+                    // the item before: its O has been read
+                    if (j == it.j0 && items > 0 && !wait_bar(bar(B_OFREE), (items - 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!wait_bar(bar(B_P), x & 1, abort_flag)) { ok = false; break; }
+                    if (elect_one()) {
+                        tc_fence_after();
+                        const uint64_t vd = vdesc0 + (uint64_t)((st * STAGE_BYTES) >> 4);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint4 y = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + c * HALF) + h * 8 + e) : zero;
-                        v[4 * e] = y.x;
-                        v[4 * e + 1] = y.y;
-                        v[4 * e + 2] = y.z;
-                        v[4 * e + 3] = y.w;
+                        for (int kk = 0; kk < TK / 16; ++kk)
+                            umma_f16_ts(tO, tP + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), IDESC_PV, (j > it.j0 || kk > 0) ? 1u : 0u);
+                        umma_commit(bar(B_PVD + (x & 1)));
+                        umma_commit(bar(B_KVE + st));
+                        if (j == it.j1 - 1) umma_commit(bar(B_DRAIN));
                     }
-                    tmem_st32u(tQ + lane_base + 32 * h, v);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 y = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + LAT + c * RHALF) + e) : zero;
-                    // (64-byte swizzle: 16-byte pieces permuted by the row's bits 1-2)
-                    st_shared_v4(sbase + SQR + r * 64 + ((e ^ ((r >> 1) & 3)) << 4), y.x, y.y, y.z, y.w);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                fence_proxy_async_smem();
-                mbar_arrive(bar(B_Q));
-            }
-            const bool active = w * 32 < rows;    // warps without a real row exchange nothing
-            for (int j = it.j0; j < it.j1; ++j, ++x) {
-                const int b = x & 1, i = 4 * b + w;
-                if (!wait_bar(bar(B_S + b), (x >> 1) & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-                if (active) {
-                    float v[64];
-                    tmem_ld64(tS(b) + lane_base, v);
-                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_SENT + i));
-                    if ((sent >> b) & 1) {
-                        if (!wait_bar<true>(bar(B_RFREE + i), (fpar >> b) & 1, abort_flag)) { ok = false; break; }
-                        fpar ^= 1u << b;
-                    }
-                    sent |= 1u << b;
-                    const uint32_t dst = peer_addr(sbase + SRECV + b * RECV_BYTES + r * 16, peer);
-                    const uint32_t rb = peer_addr(bar(B_RECV + i), peer);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        st_async_v4(dst + e * 2048, v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3], rb);
-                } else {
-                    if (lane == 0) mbar_arrive(bar(B_SENT + i));
                 }
             }
         }
+        // everything issued has finished before tensor memory is released
+        if (elect_one()) umma_commit(bar(B_END + (warp - W_MMA)));
+        __syncwarp();
+        (void)mbar_wait_bounded(bar(B_END + (warp - W_MMA)), 0);
     } else {
-        // ======================= softmax and epilogue: thread = query row = lane
-        const int r = threadIdx.x;
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        int x = 0, items = 0;
-        uint32_t rpar = 0u;      // per buffer: the parity of the next rows from the peer
+        // ======================= exchange, softmax and epilogue: threads r (even
+        // tiles) and r + 128 (odd tiles) = query row r
+        const int r = threadIdx.x & 127, w = warp & 3, grp = warp >> 2;
+        const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+        volatile float *m_sh = reinterpret_cast<volatile float *>(smem + SMAX), *l_sh = m_sh + 128;
+        int x = 0, items = 0, hs = 0;         // tiles, items, slots of the exchange so far
+        int sums = 0;                         // items this warp had a real row in
         const float sl = p.scale_log2;
-        bool ok = true, merges = false;
-        while (ok && next_item(p, list, s_first, walk, it)) {
+        bool merges = false;
+        // an item's queries, into tensor and shared memory
+        auto load_queries = [&](const Item &q) {
+            const int rows = q.toks * p.heads;
+            const uint16_t *src = p.q + ((size_t)(q.q.a + q.t0) * p.heads + r) * LKD;
+            const uint4 *lat4 = reinterpret_cast<const uint4 *>(src + c * HALF), *rope4 = reinterpret_cast<const uint4 *>(src + LAT + c * RHALF);
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            // (the loads of a half are in flight together)
+            uint4 y[20];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = r < rows ? __ldg(lat4 + e) : zero;
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+                if (h == 2) {
+#pragma unroll
+                    for (int e = 0; e < 20; ++e) y[e] = r < rows ? __ldg(e < 16 ? lat4 + 16 + e : rope4 + (e - 16)) : zero;
+                }
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 t = y[h == 1 ? 8 + e : e];
+                    v[4 * e] = t.x;
+                    v[4 * e + 1] = t.y;
+                    v[4 * e + 2] = t.z;
+                    v[4 * e + 3] = t.w;
+                }
+                tmem_st32u(tQ + lane_base + 32 * h, v);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                // (128-byte swizzle: 16-byte pieces permuted by the row's bits 0-2)
+                st_shared_v4(sbase + SQ + r * 128 + ((e ^ (r & 7)) << 4), y[8 + e].x, y[8 + e].y, y[8 + e].z, y[8 + e].w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                // (64-byte swizzle: by the row's bits 1-2)
+                st_shared_v4(sbase + SQR + r * 64 + ((e ^ ((r >> 1) & 3)) << 4), y[16 + e].x, y[16 + e].y, y[16 + e].z, y[16 + e].w);
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            mbar_arrive(bar(B_Q));
+        };
+        Item nx;
+        bool ok = true, more = next_item(p, list, s_first, walk, nx);
+        if (more && grp == 1) load_queries(nx);
+        while (ok && more) {
+            it = nx;
+            more = next_item(p, list, s_first, walk, nx);
             const int rows = it.toks * p.heads;
-            const bool active = warp * 32 < rows;
+            const bool active = w * 32 < rows;
             const int tok = min(r, rows - 1) / p.heads;
             const int first_pos = it.q.L - it.q.n + it.t0;
             const int pos = it.q.L > 0 ? first_pos + tok : -1;    // the last key this row sees
             const int pos_min = it.q.L > 0 ? first_pos : -1;
-            float m_ref = -INFINITY, l = 0.f;
-            for (int j = it.j0; j < it.j1 && ok; ++j, ++x) {
-                const int b = x & 1, i = 4 * b + warp, t0 = j * TK;
-                if (!wait_bar(bar(B_SENT + i), (x >> 1) & 1, abort_flag)) { ok = false; break; }
+            float m_ref = -INFINITY, l = 0.f;                     // (l relative to m_ref)
+            for (int j = it.j0; j < it.j1; ++j, ++x, hs += active ? TK / SCOLS : 0) {
+                if ((x & 1) != grp) continue;
+                const int t0 = j * TK;
+                if (!wait_bar(bar(B_S + grp), (x >> 1) & 1, abort_flag)) { ok = false; break; }
+                float sv[TK];
                 if (active) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar(B_RECV + i), 32 * TK * 4);
-                    if (!wait_bar<true>(bar(B_RECV + i), (rpar >> b) & 1, abort_flag)) { ok = false; break; }
-                    rpar ^= 1u << b;
                     tc_fence_after();
-                    float sv[TK];
-                    tmem_ld64(tS(b) + lane_base, sv);
-                    const uint32_t src = sbase + SRECV + b * RECV_BYTES + r * 16;
+                    tmem_ld64(tS(grp) + lane_base, sv);
+                    tc_fence_before();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(bar(B_SFREE + grp));
+                // (the groups send, and add, their tiles in turn: a slot's phases would
+                // otherwise be waited for out of order, which a parity cannot tell)
+                if (x > 0 && !wait_bar(bar(B_SORD + w), (x - 1) & 1, abort_flag)) { ok = false; break; }
+                float mraw = -INFINITY;
+                if (active) {
+                    // this CTA's part of the sums to the peer, 32 columns at a time
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        uint32_t a0, a1, a2, a3;
-                        lds128(src + e * 2048, a0, a1, a2, a3);
-                        sv[4 * e] += __uint_as_float(a0);
-                        sv[4 * e + 1] += __uint_as_float(a1);
-                        sv[4 * e + 2] += __uint_as_float(a2);
-                        sv[4 * e + 3] += __uint_as_float(a3);
+                    for (int h = 0; h < TK / SCOLS; ++h) {
+                        const int slot = (hs + h) % SLOTS, i = 4 * slot + w;
+                        if (hs + h >= SLOTS && !wait_bar(bar(B_RFREE + i), ((hs + h) / SLOTS - 1) & 1, abort_flag)) ok = false;
+                        const uint32_t dst = peer_addr(sbase + SRECV + slot * SLOT_BYTES + r * 16, peer);
+                        const uint32_t rb = peer_addr(bar(B_RECV + i), peer);
+                        if (ok) {
+                            if (lane == 0) expect_peer(rb, 32 * SCOLS * 4);
+#pragma unroll
+                            for (int e = 0; e < SCOLS; e += 4)
+                                st_async_v4(dst + e * 512, sv[h * SCOLS + e], sv[h * SCOLS + e + 1], sv[h * SCOLS + e + 2],
+                                            sv[h * SCOLS + e + 3], rb);
+                        }
                     }
                     __syncwarp();
-                    if (lane == 0) arrive_peer(peer_addr(bar(B_RFREE + i), peer));
-                    if (t0 + TK - 1 > pos_min) {
+                }
+                if (lane == 0) mbar_arrive(bar(B_SORD + w));
+                // the running maximum after the tile before
+                if (x > 0 && !wait_bar(bar(B_MAX + w), (x - 1) & 1, abort_flag)) ok = false;
+                if (!ok) break;
+                if (active) {
+                    // the peer's part
 #pragma unroll
-                        for (int e = 0; e < TK; ++e)
-                            if (t0 + e > pos) sv[e] = -INFINITY;
+                    for (int h = 0; h < TK / SCOLS; ++h) {
+                        const int slot = (hs + h) % SLOTS, i = 4 * slot + w;
+                        if (!wait_bar(bar(B_RECV + i), ((hs + h) / SLOTS) & 1, abort_flag)) ok = false;
+                        const uint32_t src = sbase + SRECV + slot * SLOT_BYTES + r * 16;
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < SCOLS / 4; ++e) {
+                            uint32_t a[4];
+                            lds128(src + e * 2048, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) sv[h * SCOLS + 4 * e + f] += __uint_as_float(a[f]);
+                        }
+                        if (t0 + h * SCOLS + SCOLS - 1 > pos_min) {
+#pragma unroll
+                            for (int e = 0; e < SCOLS; ++e)
+                                if (t0 + h * SCOLS + e > pos) sv[h * SCOLS + e] = -INFINITY;
+                        }
+                        // raw scores; the scale (> 0) is applied inside the exponent's FFMA
+#pragma unroll
+                        for (int e = 0; e < SCOLS; e += 8)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) m4[f] = max3(m4[f], sv[h * SCOLS + e + f], sv[h * SCOLS + e + 4 + f]);
+                        mraw = max3(mraw, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        // (the vote depends on every value read from the slot)
+                        const int read = __any_sync(0xffffffffu, mraw > m_ref);
+                        if (lane == 0) arrive_peer(peer_addr(bar(B_RFREE + i), peer), read);
                     }
-                    // raw scores; the scale (> 0) is applied inside the exponent's FFMA
-                    float mk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mk[e] = fmaxf(sv[e], sv[4 + e]);
-#pragma unroll
-                    for (int e = 8; e < TK; e += 8)
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) mk[h] = max3(mk[h], sv[e + h], sv[e + 4 + h]);
-                    const float mx = max3(mk[0], mk[1], fmaxf(mk[2], mk[3])) * sl;
+                    if (!ok) break;
+                }
+                float alpha = 1.f, beta = 1.f;
+                if (active) {
+                    const float m_old = j > it.j0 ? m_sh[r] : -INFINITY;
+                    const float mx = mraw * sl;
                     // the reference moves only when the maximum has grown by 2^8 (P stays
                     // finite in fp32 and bf16, whose relative precision does not depend on
                     // its size): O is seldom rescaled
-                    float alpha = 1.f;
-                    if (mx > m_ref + RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
-                        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
-                        m_ref = mx;
+                    float m_new = m_old;
+                    if (mx > m_old + RESCALE_LOG2 || (m_old == -INFINITY && mx != -INFINITY)) {
+                        alpha = m_old == -INFINITY ? 0.f : ex2(m_old - mx);
+                        m_new = mx;
                     }
+                    if (m_new != m_ref) beta = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+                    m_ref = m_new;
+                    m_sh[r] = m_new;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(bar(B_MAX + w));
+                if (active) {
+                    const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
                     const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
                     const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
                     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -622,27 +705,53 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                     float s0, s1;
                     f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-                    l = l * alpha + (s0 + s1);
-                    // O is rescaled once PV(j-1) has accumulated into it; PV(j) waits for P
-                    if (j > it.j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (!wait_bar(bar(B_PVD), (x - 1) & 1, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
+                    l = l * beta + (s0 + s1);
+                    // PV(x - 1) has read P and accumulated into O
+                    if (x > 0 && !wait_bar(bar(B_PVD + (grp ^ 1)), ((x - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    if (j > it.j0 && rescale) {
 #pragma unroll 1
-                        for (int h = 0; h < HALF / 32; ++h) {
-                            float o[32];
-                            tmem_ld32(tO + lane_base + h * 32, o);
+                        for (int h = 0; h < HALF / 16; ++h) {
+                            float o[16];
+                            tmem_ld16(tO + lane_base + h * 16, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(tO + lane_base + h * 32, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                            tmem_st16(tO + lane_base + h * 16, o);
                         }
                     }
-                    tmem_st32u(tS(b) + lane_base, pw);
+                    tmem_st32u(tP + lane_base, pw);
                     tmem_wait_st();
                     tc_fence_before();
+                } else if (x > 0 && !wait_bar(bar(B_PVD + (grp ^ 1)), ((x - 1) >> 1) & 1, abort_flag)) {
+                    // (a warp without a real row arrives once a tile, too)
+                    ok = false;
+                    break;
                 }
-                mbar_arrive(bar(B_P + b));
+                mbar_arrive(bar(B_P));
             }
             if (!ok) break;
+            if (more && ((x - 1) & 1) != grp) {
+                // the next item's queries, once the last first product of this one (in
+                // the other group's buffer) has finished
+                if (!wait_bar(bar(B_S + (grp ^ 1)), ((x - 1) >> 1) & 1, abort_flag)) break;
+                load_queries(nx);
+            }
+            // both groups' sums, each relative to the maximum it last used (a group
+            // without a tile: 0 and -inf); the item's maximum is the larger
+            if (active) {
+                volatile float *mine = l_sh + ((sums & 1) * 4 + 2 * grp) * 128 + r;
+                const volatile float *other = l_sh + ((sums & 1) * 4 + 2 * (grp ^ 1)) * 128 + r;
+                mine[0] = l;
+                mine[128] = m_ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SUM + w));
+                if (!wait_bar(bar(B_SUM + w), sums & 1, abort_flag)) break;
+                ++sums;
+                const float lo = other[0], mo = other[128];
+                const float m = fmaxf(m_ref, mo);
+                l = (m_ref == -INFINITY ? 0.f : l * ex2(m_ref - m)) + (mo == -INFINITY ? 0.f : lo * ex2(mo - m));
+                m_ref = m;
+            }
             if (!wait_bar(bar(B_DRAIN), items & 1, abort_flag)) break;
             tc_fence_after();
             const bool whole = it.j0 == 0 && it.j1 == it.kt;
@@ -650,14 +759,15 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             if (active) {
                 const size_t row = (size_t)(it.q.a + it.t0) * p.heads + r;
                 const size_t pr = (size_t)slot * p.slot_rows + r;
+                const int d0 = c * HALF + grp * (HALF / 2);
                 const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-                for (int h = 0; h < HALF / 32; ++h) {
+                for (int h = 0; h < HALF / 64; ++h) {
                     float o[32];
-                    tmem_ld32(tO + lane_base + h * 32, o);
+                    tmem_ld32(tO + lane_base + grp * (HALF / 2) + h * 32, o);
                     if (r >= rows) continue;
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * LAT + c * HALF + h * 32);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * LAT + d0 + h * 32);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
@@ -665,13 +775,13 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                                                 pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                                                 pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * LAT + c * HALF + h * 32);
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * LAT + d0 + h * 32);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
-                if (!whole && r < rows && c == 0) {
+                if (!whole && r < rows && c == 0 && grp == 0) {
                     p.part_ml[2 * pr] = l > 0.f ? m_ref : -INFINITY;
                     p.part_ml[2 * pr + 1] = l;
                 }
@@ -679,13 +789,12 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             tc_fence_before();
             mbar_arrive(bar(B_OFREE));
             if (!whole && it.j0 == 0 && threadIdx.x == 0 && c == 0) {
-                // this cluster holds the unit's first tiles: what there is to merge
-                const long long last = it.g0 + it.kt - 1;       // the place of its last tile
-                long long kl = last * nc / W;                    // the cluster that holds it
-                while (W * (kl + 1) / nc <= last) ++kl;
-                while (W * kl / nc > last) --kl;
+                // this cluster holds the unit's first tiles: what there is to merge, up to
+                // the cluster that holds its last tile
+                const Cut all = {s_work[0], s_work[1]};
+                const int kl = all.owner(all.begin(k) + (range - it.left) + it.kt - 1);
                 p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
-                p.desc[k] = make_int4(1, (int)(kl - k + 1), rows, 0);
+                p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
                 merges = true;
             }
             ++items;
@@ -813,6 +922,8 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     if (num_heads > PAGEDKV_LATENT_MAX_HEADS || max_blocks_per_seq > INT32_MAX / BS || num_blocks > INT32_MAX / BS)
         return KV_ERR_UNSUPPORTED;
     if (!out || !q || !context_lens || !cache || !block_tables) return KV_ERR_INVALID;
+    // (a cluster counts its tiles in 32 bits)
+    if (((double)total_q_tokens + num_seqs) * (max_blocks_per_seq / (TK / BS) + 1) / NCL > 2e9) return KV_ERR_UNSUPPORTED;
     if (!cu_q_lens && total_q_tokens != num_seqs) return KV_ERR_INVALID;
     if (!(scale > 0.f) || !std::isfinite(scale)) return KV_ERR_INVALID;
     if (!pkv_host::aligned(out, 16) || !pkv_host::aligned(q, 16) || !pkv_host::aligned(cache, 16) ||
