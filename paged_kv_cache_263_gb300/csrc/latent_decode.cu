@@ -200,11 +200,24 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_byte
     return d;
 }
 
-// the peer's barrier expects `bytes` of what follows (relaxed: nothing before has to be seen)
-__device__ __forceinline__ void expect_peer(uint32_t bar, uint32_t bytes)
+// Lane i of four holds the 16-byte pieces v[0..3] of row i; afterwards v[j] is
+// piece i of row j.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4][4], int lane)
 {
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & d) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j][e] : v[j + d][e], d);
+                if (up) v[j][e] = got;
+                else v[j + d][e] = got;
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------------- the work
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     int *s_start = reinterpret_cast<int *>(tmem_slot + 2);        // the range's first sequence, unit and tile
     long long *s_work = reinterpret_cast<long long *>(bars + NBAR + 4);   // the cut: each, extra
     int *list = reinterpret_cast<int *>(smem + SBAR + LIST_OFF);
-    long long *scan = reinterpret_cast<long long *>(smem + SRECV);        // setup only
+    long long *scan = reinterpret_cast<long long *>(smem + SMAX);         // setup only
     auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t c = cluster_rank(), peer = c ^ 1u;
@@ -347,6 +360,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
     // ---- the cluster's range: prefix sums of the sequences' costs, a run of
     // consecutive sequences a thread
@@ -405,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     const int range = (int)(w1 - w0);
     Walk walk = {s_first, s_start[1], s_start[2], range};
     __syncthreads();
-    cluster_sync_all();   // the peer's barriers exist before anything is sent; its scan area is free
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist
     const uint32_t tmem = *tmem_slot;
     const uint32_t tQ = tmem, tP = tmem + QT / 2, tO = tmem + 256;
     auto tS = [&](int b) -> uint32_t { return tmem + 128 + b * TK; };
@@ -422,8 +437,9 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         while (ok && next_item(p, list, s_first, walk, it)) {
             const int32_t *bt = p.tables + (size_t)it.s * p.max_blocks;
             const int nblk = (it.q.L + BS - 1) / BS;
-            // the item's queries, into L2 (this warp runs up to four tiles ahead)
-            for (int r = lane; r < it.toks * p.heads; r += 32) {
+            // the item's queries, into L2 (this warp runs up to four tiles ahead; the
+            // first item's are being loaded already)
+            for (int r = lane; u > 0 && r < it.toks * p.heads; r += 32) {
                 const uint16_t *src = p.q + ((size_t)(it.q.a + it.t0) * p.heads + r) * LKD;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c * HALF + e * 64));
@@ -548,52 +564,69 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         int sums = 0;                         // items this warp had a real row in
         const float sl = p.scale_log2;
         bool merges = false;
-        // an item's queries, into tensor and shared memory
-        auto load_queries = [&](const Item &q) {
+        // an item's queries, into tensor and shared memory.  A row is a lane of
+        // tensor memory, but 16 bytes of 32 rows in one load would touch 32 lines
+        // (that took 6,400 cycles): 8 lanes read 128 bytes of a row, and the warp's
+        // part of the shared query tile turns them round, 64 dims at a time
+        auto load_queries = [&]() {                       // of the item that follows
+            Walk ahead = walk;
+            Item q;
+            if (!next_item(p, list, s_first, ahead, q)) return;
             const int rows = q.toks * p.heads;
-            const uint16_t *src = p.q + ((size_t)(q.q.a + q.t0) * p.heads + r) * LKD;
-            const uint4 *lat4 = reinterpret_cast<const uint4 *>(src + c * HALF), *rope4 = reinterpret_cast<const uint4 *>(src + LAT + c * RHALF);
+            const uint16_t *src = p.q + ((size_t)(q.q.a + q.t0) * p.heads + w * 32) * LKD;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            // (the loads of a half are in flight together)
-            uint4 y[20];
+            const int lr = lane >> 3, le = lane & 7;      // row within four, piece
+            const uint32_t qt = sbase + SQ + w * 4096;
+            uint4 y[2][8];
+            auto fetch = [&](int h, uint4 (&v)[8]) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = r < rows ? __ldg(lat4 + e) : zero;
+                for (int i = 0; i < 8; ++i)
+                    v[i] = w * 32 + 4 * i + lr < rows
+                               ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)(4 * i + lr) * LKD + c * HALF + h * 64) + le) : zero;
+            };
+            fetch(0, y[0]);
 #pragma unroll
-            for (int h = 0; h < 3; ++h) {
-                if (h == 2) {
+            for (int h = 0; h < 4; ++h) {
+                if (h < 3) {
+                    fetch(h + 1, y[(h + 1) & 1]);
+                } else {
+                    // the rotary part: 4 lanes read a row's 64 bytes
 #pragma unroll
-                    for (int e = 0; e < 20; ++e) y[e] = r < rows ? __ldg(e < 16 ? lat4 + 16 + e : rope4 + (e - 16)) : zero;
+                    for (int i = 0; i < 4; ++i)
+                        y[0][i] = w * 32 + 8 * i + (lane >> 2) < rows
+                                      ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)(8 * i + (lane >> 2)) * LKD + LAT + c * RHALF) + (lane & 3)) : zero;
                 }
-                uint32_t v[32];
+                // (128-byte swizzle: 16-byte pieces permuted by the row's bits 0-2)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint4 t = y[h == 1 ? 8 + e : e];
-                    v[4 * e] = t.x;
-                    v[4 * e + 1] = t.y;
-                    v[4 * e + 2] = t.z;
-                    v[4 * e + 3] = t.w;
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + lr;
+                    const uint4 t = y[h & 1][i];
+                    st_shared_v4(qt + row * 128 + ((le ^ (row & 7)) << 4), t.x, t.y, t.z, t.w);
                 }
-                tmem_st32u(tQ + lane_base + 32 * h, v);
+                __syncwarp();
+                if (h < 3) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        lds128(qt + lane * 128 + ((e ^ (lane & 7)) << 4), v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    tmem_st32u(tQ + lane_base + 32 * h, v);
+                    __syncwarp();
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                // (128-byte swizzle: 16-byte pieces permuted by the row's bits 0-2)
-                st_shared_v4(sbase + SQ + r * 128 + ((e ^ (r & 7)) << 4), y[8 + e].x, y[8 + e].y, y[8 + e].z, y[8 + e].w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int i = 0; i < 4; ++i) {
+                const int row = w * 32 + 8 * i + (lane >> 2);
                 // (64-byte swizzle: by the row's bits 1-2)
-                st_shared_v4(sbase + SQR + r * 64 + ((e ^ ((r >> 1) & 3)) << 4), y[16 + e].x, y[16 + e].y, y[16 + e].z, y[16 + e].w);
+                st_shared_v4(sbase + SQR + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), y[0][i].x, y[0][i].y, y[0][i].z, y[0][i].w);
+            }
             tmem_wait_st();
             tc_fence_before();
             fence_proxy_async_smem();
             mbar_arrive(bar(B_Q));
         };
-        Item nx;
-        bool ok = true, more = next_item(p, list, s_first, walk, nx);
-        if (more && grp == 1) load_queries(nx);
-        while (ok && more) {
-            it = nx;
-            more = next_item(p, list, s_first, walk, nx);
+        bool ok = true;
+        if (grp == 1) load_queries();
+        while (ok && next_item(p, list, s_first, walk, it)) {
             const int rows = it.toks * p.heads;
             const bool active = w * 32 < rows;
             const int tok = min(r, rows - 1) / p.heads;
@@ -626,7 +659,6 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                         const uint32_t dst = peer_addr(sbase + SRECV + slot * SLOT_BYTES + r * 16, peer);
                         const uint32_t rb = peer_addr(bar(B_RECV + i), peer);
                         if (ok) {
-                            if (lane == 0) expect_peer(rb, 32 * SCOLS * 4);
 #pragma unroll
                             for (int e = 0; e < SCOLS; e += 4)
                                 st_async_v4(dst + e * 512, sv[h * SCOLS + e], sv[h * SCOLS + e + 1], sv[h * SCOLS + e + 2],
@@ -644,6 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int h = 0; h < TK / SCOLS; ++h) {
                         const int slot = (hs + h) % SLOTS, i = 4 * slot + w;
+                        if (lane == 0) mbar_arrive_expect_tx(bar(B_RECV + i), 32 * SCOLS * 4);
                         if (!wait_bar(bar(B_RECV + i), ((hs + h) / SLOTS) & 1, abort_flag)) ok = false;
                         const uint32_t src = sbase + SRECV + slot * SLOT_BYTES + r * 16;
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -665,9 +698,6 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                             for (int f = 0; f < 4; ++f) m4[f] = max3(m4[f], sv[h * SCOLS + e + f], sv[h * SCOLS + e + 4 + f]);
                         mraw = max3(mraw, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                        // (the vote depends on every value read from the slot)
-                        const int read = __any_sync(0xffffffffu, mraw > m_ref);
-                        if (lane == 0) arrive_peer(peer_addr(bar(B_RFREE + i), peer), read);
                     }
                     if (!ok) break;
                 }
@@ -690,7 +720,13 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
                 if (lane == 0) mbar_arrive(bar(B_MAX + w));
                 if (active) {
+                    // (the vote depends on every value read from the slots)
                     const bool rescale = __any_sync(0xffffffffu, alpha != 1.f);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int h = 0; h < TK / SCOLS; ++h)
+                            arrive_peer(peer_addr(bar(B_RFREE + 4 * ((hs + h) % SLOTS) + w), peer), rescale);
+                    }
                     const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
                     const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
                     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -730,11 +766,11 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 mbar_arrive(bar(B_P));
             }
             if (!ok) break;
-            if (more && ((x - 1) & 1) != grp) {
+            if (((x - 1) & 1) != grp) {
                 // the next item's queries, once the last first product of this one (in
                 // the other group's buffer) has finished
                 if (!wait_bar(bar(B_S + (grp ^ 1)), ((x - 1) >> 1) & 1, abort_flag)) break;
-                load_queries(nx);
+                load_queries();
             }
             // both groups' sums, each relative to the maximum it last used (a group
             // without a tile: 0 and -inf); the item's maximum is the larger
@@ -757,28 +793,40 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             const bool whole = it.j0 == 0 && it.j1 == it.kt;
             const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
             if (active) {
-                const size_t row = (size_t)(it.q.a + it.t0) * p.heads + r;
-                const size_t pr = (size_t)slot * p.slot_rows + r;
+                const size_t row0 = (size_t)(it.q.a + it.t0) * p.heads;
+                const size_t pr0 = (size_t)slot * p.slot_rows, pr = pr0 + r;
                 const int d0 = c * HALF + grp * (HALF / 2);
                 const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                // 4 lanes exchange their rows' pieces so that they store 64 bytes of one
+                // row together (a store of 16 bytes to each of 32 rows touches 32 lines)
 #pragma unroll 1
                 for (int h = 0; h < HALF / 64; ++h) {
                     float o[32];
                     tmem_ld32(tO + lane_base + grp * (HALF / 2) + h * 32, o);
-                    if (r >= rows) continue;
+                    const int r4 = w * 32 + (lane & ~3), e4 = lane & 3;       // the quad's first row, this lane's piece
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * LAT + d0 + h * 32);
+                        uint32_t v[4][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                        for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                        quad_transpose(v, lane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (r4 + i < rows)
+                                reinterpret_cast<uint4 *>(p.out + (row0 + r4 + i) * LAT + d0 + h * 32)[e4] =
+                                    make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * LAT + d0 + h * 32);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t v[4][4];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = __float_as_uint(o[16 * g + e]);
+                            quad_transpose(v, lane);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (r4 + i < rows)
+                                    reinterpret_cast<uint4 *>(p.part_o + (pr0 + r4 + i) * LAT + d0 + h * 32 + g * 16)[e4] =
+                                        make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                        }
                     }
                 }
                 if (!whole && r < rows && c == 0 && grp == 0) {
@@ -807,47 +855,74 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     cluster_sync_all();   // nothing is sent to a CTA that has left
 }
 
-// Joins the partial sums of the units that a cut fell into: a warp for each
-// (row, 128 dims), cluster by cluster, with weights 2^(m_i - max m).  The partial
-// sums are read once, from L2 as a rule.
+// Joins the partial sums of the units that a cut fell into, cluster by cluster,
+// with weights 2^(m_i - max m): a warp for each (row, 128 dims), the units' rows
+// laid end to end over all CTAs.  The first partial rows are requested before the
+// maxima are known, so a unit cut once costs one round trip to L2.
+constexpr int MERGE_CTAS = 8 * 152, MERGE_PRE = 8;
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
 {
-    __shared__ int4 desc[NCL];
+    __shared__ int2 todo[NCL + 1];         // (partials, rows before) of cluster k's unit
+    const int lane = threadIdx.x & 31;
     griddep_wait();
-    for (int i = threadIdx.x; i < NCL; i += blockDim.x) desc[i] = p.desc[i];
+    if (threadIdx.x < 32) {
+        int run = 0;
+        for (int b = 0; b < NCL; b += 32) {
+            const int4 d = b + lane < NCL ? p.desc[b + lane] : make_int4(0, 0, 0, 0);
+            const int n = d.x ? d.z : 0;
+            int v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += t;
+            }
+            if (b + lane < NCL) todo[b + lane] = make_int2(d.y, run + v - n);
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) todo[NCL] = make_int2(0, run);
+    }
     __syncthreads();
-    const int lane = threadIdx.x & 31, nw = gridDim.x * (blockDim.x >> 5);
-    const int per = p.slot_rows * 4;
-    for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < NCL * per; t += nw) {
-        const int k = t / per, row = (t % per) >> 2, q4 = t & 3;
-        const int4 d = desc[k];
-        if (d.x == 0 || row >= d.z) continue;
+    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < todo[NCL].y * 4; t += MERGE_CTAS * 8) {
+        const int g = t >> 2, q4 = t & 3;
+        int k = 0, hi = NCL;                // the last k with rows before it <= g
+        while (hi - k > 1) {
+            const int mid = (k + hi) >> 1;
+            if (todo[mid].y <= g) k = mid;
+            else hi = mid;
+        }
+        const int row = g - todo[k].y, ns = todo[k].x;
+        const int64_t row0 = p.desc2[k];
         // partial i: the first is in its cluster's second slot, the others in their cluster's first
         auto slot = [&](int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows + row; };
-        float M = -INFINITY;
-        for (int i = lane; i < d.y; i += 32) M = fmaxf(M, p.part_ml[2 * slot(i)]);
+        auto part = [&](int i) -> float4 {
+            return i < ns ? reinterpret_cast<const float4 *>(p.part_o + slot(i) * LAT + q4 * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 pre[MERGE_PRE];
+#pragma unroll
+        for (int j = 0; j < MERGE_PRE; ++j) pre[j] = part(j);
+        float2 e0 = make_float2(-INFINITY, 0.f);
+        if (lane < ns) e0 = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(lane));
+        float M = e0.x;
+        for (int i = lane + 32; i < ns; i += 32) M = fmaxf(M, p.part_ml[2 * slot(i)]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
         if (M != -INFINITY) {
-            for (int i0 = 0; i0 < d.y; i0 += 32) {
-                float f = 0.f, fl = 0.f;
-                if (i0 + lane < d.y) {
-                    const float2 e = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(i0 + lane));
+            for (int i0 = 0; i0 < ns; i0 += 32) {
+                float f = 0.f;
+                if (i0 + lane < ns) {
+                    const float2 e = i0 == 0 ? e0 : *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(i0 + lane));
                     f = ex2(e.x - M);
-                    fl = f * e.y;
+                    l += f * e.y;
                 }
-                l += fl;
-                const int n = min(32, d.y - i0);
-                for (int j0 = 0; j0 < n; j0 += 8) {
-                    float4 v[8];
+                const int n = min(32, ns - i0);
+                for (int j0 = 0; j0 < n; j0 += MERGE_PRE) {
+                    float4 v[MERGE_PRE];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = j0 + j < n ? reinterpret_cast<const float4 *>(p.part_o + slot(i0 + j0 + j) * LAT + q4 * 128)[lane]
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < MERGE_PRE; ++j) v[j] = i0 + j0 == 0 ? pre[j] : part(i0 + j0 + j);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < MERGE_PRE; ++j) {
                         const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
                         if (j0 + j < n) {
                             acc.x += fj * v[j].x;
@@ -862,7 +937,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        reinterpret_cast<uint2 *>(p.out + (p.desc2[k] + row) * LAT + q4 * 128)[lane] =
+        reinterpret_cast<uint2 *>(p.out + (row0 + row) * LAT + q4 * 128)[lane] =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
 }
@@ -964,7 +1039,7 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     if (pkv_host::ensure_dynamic_smem<latent_kernel>(SMEM_BYTES) != cudaSuccess) return KV_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pkv_host::launch_ex(latent_kernel, dim3(2 * NCL), dim3(THREADS), SMEM_BYTES, st, true, lmap, rmap, p) != cudaSuccess ||
-        pkv_host::launch_ex(latent_merge_kernel, dim3(2 * NCL), dim3(256), 0, st, true, p) != cudaSuccess)
+        pkv_host::launch_ex(latent_merge_kernel, dim3(MERGE_CTAS), dim3(256), 0, st, true, p) != cudaSuccess)
         return KV_ERR_CUDA;
     return KV_OK;
 }
