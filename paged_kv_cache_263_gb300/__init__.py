@@ -437,57 +437,83 @@ def paged_attention_chunked_prefill(out, q, cu_q_lens, context_lens, max_q_len, 
 
 
 # ----------------------------------------------------------- latent attention
-def _on(name, t, device, dtype, shape):
-    """t is a contiguous CUDA tensor of this dtype and shape (None: any extent) on `device` (None: its own)."""
+# These calls are microseconds long on the GPU, so their checks are kept to a few
+# cheap attribute reads a tensor (device as a number, dtypes by identity); what is
+# wrong is worked out only after something is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_BF, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
+
+
+def _wrong(name, t, dev, dtype, shape):
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda or (device is not None and t.device != device):
+    if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    have = t.shape
-    if len(have) != len(shape) or any(b is not None and a != b for a, b in zip(have, shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(have)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device(name, t):
+    """Index of the CUDA device that t is on."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _at(name, t, dev, dtype, shape):
+    """Address of t, a contiguous CUDA tensor on device `dev` of this dtype and (whole) shape."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _wrong(name, t, dev, dtype, shape)
     return t.data_ptr()
 
 
-def _rows_on(name, t, device, width):
-    """Rows of `width` bf16 values whose first dimension may be strided; (pointer, row stride)."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} must be bf16 [tokens][{width}]")
-    row, one = t.stride()
+def _at_nd(name, t, dev, dtype, shape):
+    """As _at, with None for an extent that is free."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or \
+            len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        _wrong(name, t, dev, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows_at(name, t, dev, rows, width):
+    """Rows of `width` bf16 values whose first dimension may be strided: (address, row stride)."""
+    if t is None or t.get_device() != dev or t.dtype is not _BF or t.shape != (rows, width):
+        _wrong(name, t, dev, _BF, (rows, width))
     # (without rows no stride means anything, and with one row its distance to the next does not)
-    if one != 1 and t.shape[0] > 0:
+    row, one = t.stride()
+    if one != 1 and rows > 0:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), row if t.shape[0] > 1 else width
+    return t.data_ptr(), row if rows > 1 else width
 
 
-def _call_on(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current: its current stream unless one is given."""
+def _call_on(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current: its current stream unless one is given."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        raw = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device_index != dev:
         raise ValueError("stream must belong to the tensors' device")
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, stream.cuda_stream)
-    with torch.cuda.device(device):
-        return fn(*args, stream.cuda_stream)
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        return fn(*args, raw)
+    with torch.cuda.device(dev):
+        return fn(*args, raw)
 
 
-def _scratch(workspace, need, device, name):
-    """Pointer and size of the given workspace, or of a new one (returned too, to stay alive through the call)."""
+def _scratch(workspace, dev, size, *sizes):
+    """(address, bytes, tensor) of the given workspace, or of a new one of size(*sizes) bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{name}: workspace must be a contiguous CUDA tensor on the other tensors' device")
-    if workspace is None:
-        return None, 0, None
+        need = size(*sizes)
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the other tensors' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -501,32 +527,30 @@ def kv_build_step_tables(block_tables, context_lens, new_lens, free_blocks, num_
     total_lens [B], slot_mapping and positions [max_tokens], totals [2] (rows,
     free blocks taken).  Lengths that do not fit refuse the sequence and set the
     device status (see kv_last_device_status)."""
-    i32 = torch.int32
-    tables = _on("block_tables", block_tables, None, i32, (None, None))
-    dev = block_tables.device
+    dev = _device("block_tables", block_tables)
+    tables = _at_nd("block_tables", block_tables, dev, _I32, (None, None))
     B, mb = block_tables.shape
-    args = (tables, mb, _on("context_lens", context_lens, dev, i32, (B,)), _on("new_lens", new_lens, dev, i32, (B,)),
-            B, _on("free_blocks", free_blocks, dev, i32, (None,)), free_blocks.shape[0], int(num_blocks),
-            _on("cu_q_lens", cu_q_lens, dev, i32, (B + 1,)), _on("total_lens", total_lens, dev, i32, (B,)),
-            _on("slot_mapping", slot_mapping, dev, torch.int64, (None,)),
-            _on("positions", positions, dev, i32, (slot_mapping.shape[0],)), slot_mapping.shape[0],
-            _on("totals", totals, dev, i32, (2,)))
-    _check(_call_on(dev, stream, lib().kv_build_step_tables, *args), "kv_build_step_tables")
+    free = _at_nd("free_blocks", free_blocks, dev, _I32, (None,))
+    slots = _at_nd("slot_mapping", slot_mapping, dev, _I64, (None,))
+    n, each = slot_mapping.shape[0], (B,)
+    _check(_call_on(dev, stream, lib().kv_build_step_tables, tables, mb,
+                    _at("context_lens", context_lens, dev, _I32, each), _at("new_lens", new_lens, dev, _I32, each), B,
+                    free, free_blocks.shape[0], int(num_blocks), _at("cu_q_lens", cu_q_lens, dev, _I32, (B + 1,)),
+                    _at("total_lens", total_lens, dev, _I32, each), slots,
+                    _at("positions", positions, dev, _I32, (n,)), n, _at("totals", totals, dev, _I32, (2,))),
+           "kv_build_step_tables")
 
 
 def reshape_and_cache_latent(latent, rope, cache, slot_mapping, stream=None):
     """Write latent rows [T][512] and rotary keys [T][64] (bf16; rows may be views
     of a wider tensor) into the paged latent cache [num_blocks][16][576]."""
-    bf = torch.bfloat16
-    c = _on("cache", cache, None, bf, (None, BLOCK_SIZE, _LATENT_ROW))
-    dev = cache.device
-    slots = _on("slot_mapping", slot_mapping, dev, torch.int64, (None,))
-    T = slot_mapping.shape[0]
-    lat, ls = _rows_on("latent", latent, dev, LATENT_DIM)
-    rp, rs = _rows_on("rope", rope, dev, LATENT_ROPE_DIM)
-    if latent.shape[0] != T or rope.shape[0] != T:
-        raise ValueError("latent, rope and slot_mapping must have the same number of tokens")
-    _check(_call_on(dev, stream, lib().reshape_and_cache_latent, lat, ls, rp, rs, c, slots, T, cache.shape[0]),
+    dev = _device("cache", cache)
+    nb, T = cache.shape[0], 0 if slot_mapping is None else slot_mapping.shape[0]
+    c = _at("cache", cache, dev, _BF, (nb, BLOCK_SIZE, _LATENT_ROW))
+    slots = _at("slot_mapping", slot_mapping, dev, _I64, (T,))
+    lat, ls = _rows_at("latent", latent, dev, T, LATENT_DIM)
+    rp, rs = _rows_at("rope", rope, dev, T, LATENT_ROPE_DIM)
+    _check(_call_on(dev, stream, lib().reshape_and_cache_latent, lat, ls, rp, rs, c, slots, T, nb),
            "reshape_and_cache_latent")
 
 
@@ -539,23 +563,20 @@ def paged_latent_attention(out, q, cache, block_tables, context_lens, cu_q_lens=
     """Attention over the paged latent cache, absorbed form: out[R][H][512] from
     q[R][H][576] (bf16), one row a sequence, or cu_q_lens [B+1] rows.  scale
     defaults to (128 + 64) ** -0.5, the expanded form's."""
-    bf, i32 = torch.bfloat16, torch.int32
-    qp = _on("q", q, None, bf, (None, None, _LATENT_ROW))
-    dev = q.device
+    dev = _device("q", q)
+    qp = _at_nd("q", q, dev, _BF, (None, None, _LATENT_ROW))
     R, h, _ = q.shape
-    B, mb = block_tables.shape if block_tables is not None else (None, None)
-    args = (_on("out", out, dev, bf, (R, h, LATENT_DIM)), qp,
-            None if cu_q_lens is None else _on("cu_q_lens", cu_q_lens, dev, i32, (B + 1,)),
-            _on("context_lens", context_lens, dev, i32, (B,)), B, R,
-            _on("cache", cache, dev, bf, (None, BLOCK_SIZE, _LATENT_ROW)),
-            _on("block_tables", block_tables, dev, i32, (B, mb)), mb, h, cache.shape[0],
-            _EXPANDED_QK ** -0.5 if scale is None else float(scale))
+    tables = _at_nd("block_tables", block_tables, dev, _I32, (None, None))
+    B, mb = block_tables.shape
     if cu_q_lens is None and R != B:
         raise ValueError("without cu_q_lens, q must have one row a sequence")
+    c = _at_nd("cache", cache, dev, _BF, (None, BLOCK_SIZE, _LATENT_ROW))
     L = lib()
-    need = 0 if workspace is not None else L.paged_latent_attention_workspace_size(B, R, h, mb)
-    ws, nbytes, _keep = _scratch(workspace, need, dev, "paged_latent_attention")
-    _check(_call_on(dev, stream, L.paged_latent_attention, *args, ws, nbytes), "paged_latent_attention")
+    ws, nbytes, _keep = _scratch(workspace, dev, L.paged_latent_attention_workspace_size, B, R, h, mb)
+    _check(_call_on(dev, stream, L.paged_latent_attention, _at("out", out, dev, _BF, (R, h, LATENT_DIM)), qp,
+                    None if cu_q_lens is None else _at("cu_q_lens", cu_q_lens, dev, _I32, (B + 1,)),
+                    _at("context_lens", context_lens, dev, _I32, (B,)), B, R, c, tables, mb, h, cache.shape[0],
+                    _EXPANDED_QK ** -0.5 if scale is None else float(scale), ws, nbytes), "paged_latent_attention")
     return out
 
 
@@ -568,25 +589,21 @@ def latent_prefill_attention(out, q, kv, k_rope, cu_q_lens, cu_k_lens, scale=Non
     kv[Rk][H][256] (key part, value) and the shared rotary keys k_rope[Rk][64]
     (bf16; k_rope's rows may be views of a wider tensor), ragged by cu_q_lens and
     cu_k_lens [B+1], causal from the end.  scale defaults to 192 ** -0.5."""
-    bf, i32 = torch.bfloat16, torch.int32
-    qp = _on("q", q, None, bf, (None, None, _EXPANDED_QK))
-    dev = q.device
+    dev = _device("q", q)
+    qp = _at_nd("q", q, dev, _BF, (None, None, _EXPANDED_QK))
     R, h, _ = q.shape
-    kvp = _on("kv", kv, dev, bf, (None, h, 2 * HEAD_DIM))
-    rp, rs = _rows_on("k_rope", k_rope, dev, LATENT_ROPE_DIM)
-    if k_rope.shape[0] != kv.shape[0]:
-        raise ValueError("kv and k_rope must have the same number of tokens")
-    cu_q = _on("cu_q_lens", cu_q_lens, dev, i32, (None,))
+    kvp = _at_nd("kv", kv, dev, _BF, (None, h, 2 * HEAD_DIM))
+    K = kv.shape[0]
+    rp, rs = _rows_at("k_rope", k_rope, dev, K, LATENT_ROPE_DIM)
+    cu_q = _at_nd("cu_q_lens", cu_q_lens, dev, _I32, (None,))
     B = cu_q_lens.shape[0] - 1
     if B < 0:
         raise ValueError("cu_q_lens must have at least one entry")
-    args = (_on("out", out, dev, bf, (R, h, HEAD_DIM)), qp, kvp, rp, rs, cu_q,
-            _on("cu_k_lens", cu_k_lens, dev, i32, (B + 1,)), B, R, kv.shape[0], h,
-            _EXPANDED_QK ** -0.5 if scale is None else float(scale))
     L = lib()
-    need = 0 if workspace is not None else L.latent_prefill_attention_workspace_size(B, R, h)
-    ws, nbytes, _keep = _scratch(workspace, need, dev, "latent_prefill_attention")
-    _check(_call_on(dev, stream, L.latent_prefill_attention, *args, ws, nbytes), "latent_prefill_attention")
+    ws, nbytes, _keep = _scratch(workspace, dev, L.latent_prefill_attention_workspace_size, B, R, h)
+    _check(_call_on(dev, stream, L.latent_prefill_attention, _at("out", out, dev, _BF, (R, h, HEAD_DIM)), qp, kvp, rp,
+                    rs, cu_q, _at("cu_k_lens", cu_k_lens, dev, _I32, (B + 1,)), B, R, K, h,
+                    _EXPANDED_QK ** -0.5 if scale is None else float(scale), ws, nbytes), "latent_prefill_attention")
     return out
 
 

@@ -573,6 +573,26 @@ __device__ __forceinline__ float4 lse_merge_warp(const float *__restrict__ ml, c
     return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
+// Lane i of four holds the 16-byte pieces v[0..3] of row i; afterwards v[j] is
+// piece i of row j.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4][4], int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j & d) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j][e] : v[j + d][e], d);
+                if (up) v[j][e] = got;
+                else v[j + d][e] = got;
+            }
+        }
+    }
+}
+
 // max of three fp32 values
 __device__ __forceinline__ float max3(float a, float b, float c)
 {

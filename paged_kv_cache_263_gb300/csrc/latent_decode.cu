@@ -200,26 +200,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_byte
     return d;
 }
 
-// Lane i of four holds the 16-byte pieces v[0..3] of row i; afterwards v[j] is
-// piece i of row j.
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4][4], int lane)
-{
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-        const bool up = lane & d;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j & d) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j][e] : v[j + d][e], d);
-                if (up) v[j][e] = got;
-                else v[j + d][e] = got;
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------- the work
 // A sequence as the kernel sees it: n = 0 if it has no rows or was refused.
 struct Seq {
@@ -840,7 +820,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 // this cluster holds the unit's first tiles: what there is to merge, up to
                 // the cluster that holds its last tile
                 const Cut all = {s_work[0], s_work[1]};
-                const int kl = all.owner(all.begin(k) + (range - it.left) + it.kt - 1);
+                const int kl = max(k, min(nc - 1, all.owner(all.begin(k) + (range - it.left) + it.kt - 1)));
                 p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
                 p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
                 merges = true;

@@ -1,10 +1,31 @@
-// latent_prefill.cu -- attention over expanded latents, for prompts (sm_103a).
+// latent_prefill.cu -- attention over expanded latents, for prompts (sm_103a,
+// 5th-generation tensor cores).
 //
 // kv[t][h] holds head h's key part (128, expanded from the token's latent) and
 // value (128); the rotary key k_rope[t] (64) is shared by all heads:
 //   out[r][h] = sum_t p_t kv[t][h][128:],
 //   p = softmax_t(scale * (q[r][h][:128] . kv[t][h][:128] + q[r][h][128:] . k_rope[t]))
 // over the keys t <= nk - nq + i that row i of a sequence's nq rows sees.
+//
+// What bounds it: 2 x 320 operations a (row, head, key) on the tensor cores.  A
+// work item is one head's 256 query rows (a pair of 128-row tiles) of a sequence
+// with every key they see, so a key tile that was loaded serves 256 rows.
+//  * Key tiles of 128, in chunks of 128 keys x 64 dims (16 KiB, one TMA box each):
+//    the key part's two, the rotary one, the value's two -- read in place from kv
+//    and k_rope.  Eight chunks circulate in a ring beside the queries (96 KiB).
+//  * S[128 x 128] = Q K^T (A and B in shared memory) and O[128 x 128] += P V (A =
+//    P in bf16, written over S) run as tcgen05.mma.  128 keys a tile because a
+//    128 x 64 x 16 product with A in shared memory takes 48 cycles and a 128 x 128
+//    x 16 one 65 (measured): the query tile is read once per product.
+//  * Tensor memory holds one S and one O of each query tile: 512 columns.  The two
+//    tiles take turns: while one's softmax works, the other's products run.  P is
+//    handed over in halves of 64 keys, so that the second product starts before
+//    the softmax is done.
+//  * One CTA a SM takes items from a list, a device-built one: sequences with the
+//    most keys first, within a sequence eight heads at a time (their keys stay in
+//    L2 while all their query tiles pass), longest tiles first.
+// Warps 0-3 and 4-7: softmax and epilogue of the query tiles, one row a thread; 8:
+// items and TMA; 9 and 10: MMA issuers of the query tiles.
 #include "common.cuh"
 #include "trace.h"
 
@@ -18,58 +39,540 @@ __device__ uint32_t g_status;
 using namespace pkv;
 
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr int QKD = D + ROPE;                     // 192
+constexpr int BM = 128, BN = 128, PAIR = 2 * BM;
+constexpr int HGROUP = 8;                         // heads whose items are adjacent
+constexpr int CHUNKS = 8;
+constexpr uint32_t CHUNK_BYTES = BN * 128, Q_TILE = 3 * BM * 128;
+constexpr uint32_t SKV = 2 * Q_TILE, SBAR = SKV + CHUNKS * CHUNK_BYTES;
+constexpr int SMEM_BYTES = SBAR + 512 + 1024;     // + 1 KiB: aligned to 1 KiB at run time
+constexpr int W_PROD = 8, W_MMA = 9, THREADS = 32 * (W_MMA + 2);
+constexpr int NSLOT = 2;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
+
+enum {
+    B_FULL = 0,                     // + chunk: landed
+    B_EMPTY = B_FULL + CHUNKS,      // + chunk: every product that reads it has finished (one release an issuer)
+    B_Q = B_EMPTY + CHUNKS,         // the item's queries landed
+    B_QFREE = B_Q + 1,              // every first product of the item has finished (one an issuer)
+    B_S = B_QFREE + 1,              // + tile: S is in tensor memory
+    B_P = B_S + 2,                  // + 2 x tile + half: 64 keys of P are (128 arrivals)
+    B_DRAIN = B_P + 4,              // + tile: every product of the item has finished
+    B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (128 arrivals)
+    B_TAIL = B_OFREE + 2,           // + item parity: value rows past the sequence's end are zeroed
+    B_IFULL = B_TAIL + 2,           // + slot: an item is in the slot
+    B_IEMPTY = B_IFULL + NSLOT,     // + slot: every warp has read it
+    B_END = B_IEMPTY + NSLOT,       // + tile: everything its issuer issued has finished
+    NBAR = B_END + 2
+};
+// an item as the producer hands it on: valid, first query row, rows (up to 256),
+// the keys that row 0 sees, first key row, keys of the sequence, head, key tiles
+struct Slot {
+    int valid, row0, rows, see0, key0, nk, head, T;
+};
+static_assert(NBAR * 8 + 16 + NSLOT * sizeof(Slot) <= 512, "barrier area");
+
+// instruction descriptors, kind::f16: bf16 A and B, fp32 accumulate, M = 128
+constexpr uint32_t idesc(int n, bool b_mn_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? (1u << 16) : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(BM >> 4) << 24);
+}
+constexpr uint32_t IDESC_S = idesc(BN, false), IDESC_PV = idesc(64, true);
 
 struct ExpandedParams {
     uint16_t *out;
-    const uint16_t *q, *kv, *rope;
     const int32_t *cu_q, *cu_k;
-    int64_t rope_stride;
+    int4 *seqs;          // [num_seqs] sequences by falling key count: first row, rows, first key, keys
+    int32_t *before;     // [num_seqs + 1] items of the sequences before
+    int32_t *next;       // the next item that no CTA has taken
     int num_seqs, rows, keys, heads;
+    int grid, max_items; // CTAs of the attention kernel; items at most
     float scale_log2;
 };
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
 
-// One warp per (row, head): lane l holds dims l, l + 32, ... of q and of the sum.
-__global__ void __launch_bounds__(256) expanded_simple_kernel(const ExpandedParams p)
+// The item list: valid sequences with rows, by falling key count (in steps of a
+// quarter octave), and the prefix sums of their items.
+constexpr int BUCKETS = 128;
+__global__ void __launch_bounds__(1024) expanded_plan_kernel(const ExpandedParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w >= (long long)p.rows * p.heads) return;
-    const int row = (int)(w / p.heads), h = (int)(w % p.heads);
-    int s = -1, a = 0, n = 0;
-    for (int i = 0; i < p.num_seqs; ++i)
-        if (p.cu_q[i] <= row && row < p.cu_q[i + 1]) {
-            s = i;
-            a = p.cu_q[i];
-            n = p.cu_q[i + 1] - a;
-            break;
+    __shared__ int count[BUCKETS], start[BUCKETS], total;
+    __shared__ long long warp_sum[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    if (threadIdx.x < BUCKETS) count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) total = 0;
+    __syncthreads();
+    auto load = [&](int s, bool flagging) -> int4 {
+        const int a = p.cu_q[s], b = p.cu_q[s + 1], c = p.cu_k[s], d = p.cu_k[s + 1];
+        if (a == b) return make_int4(0, 0, 0, 0);
+        if (a < 0 || b < a || b > p.rows || c < 0 || d < c || d > p.keys) {
+            if (flagging) flag(ST_BAD_LEN);
+            return make_int4(0, 0, 0, 0);
         }
-    if (s < 0) return;
-    const int k0 = p.cu_k[s], nk = p.cu_k[s + 1] - k0;
-    if (a < 0 || a + n > p.rows || k0 < 0 || nk < 0 || k0 + nk > p.keys) {
-        if (lane == 0) flag(ST_BAD_LEN);
-        return;
+        return make_int4(a, b - a, c, d - c);
+    };
+    auto bucket = [](int nk) -> int {
+        const int t = (nk >> 5) + 1, e = 31 - __clz(t);                 // quarter octaves of 32 keys
+        return BUCKETS - 1 - min(BUCKETS - 1, 4 * e + (e >= 2 ? (t >> (e - 2)) & 3 : 0));
+    };
+    for (int s = threadIdx.x; s < p.num_seqs; s += 1024) {
+        const int4 q = load(s, true);
+        if (q.y > 0) atomicAdd(&count[bucket(q.w)], 1);
     }
-    const int last = nk - n + (row - a);
-    float q[6], o[4], m = -INFINITY, l = 0.f;
-    for (int k = 0; k < 6; ++k) q[k] = __uint_as_float((uint32_t)p.q[w * (D + ROPE) + lane + 32 * k] << 16);
-    for (int k = 0; k < 4; ++k) o[k] = 0.f;
-    for (int t = 0; t <= last; ++t) {
-        const uint16_t *x = p.kv + ((size_t)(k0 + t) * p.heads + h) * (2 * D);
-        const uint16_t *r = p.rope + (k0 + t) * p.rope_stride;
-        float d = 0.f;
-        for (int k = 0; k < 4; ++k) d += q[k] * __uint_as_float((uint32_t)x[lane + 32 * k] << 16);
-        for (int k = 0; k < 2; ++k) d += q[4 + k] * __uint_as_float((uint32_t)r[lane + 32 * k] << 16);
-        for (int b = 16; b > 0; b >>= 1) d += __shfl_xor_sync(0xffffffffu, d, b);
-        d *= p.scale_log2;
-        const float mn = fmaxf(m, d), c = ex2(m - mn), e = ex2(d - mn);
-        l = l * c + e;
-        for (int k = 0; k < 4; ++k) o[k] = o[k] * c + e * __uint_as_float((uint32_t)x[D + lane + 32 * k] << 16);
-        m = mn;
+    __syncthreads();
+    if (w == 0) {
+        int run = 0;
+        for (int b = lane; b < BUCKETS; b += 32) {
+            int v = count[b];
+            const int n = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += t;
+            }
+            start[b] = run + v - n;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) total = run;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int k = 0; k < 4; ++k) p.out[w * D + lane + 32 * k] = (uint16_t)(pack_bf16(o[k] * inv, 0.f) & 0xffffu);
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.num_seqs; s += 1024) {
+        const int4 q = load(s, false);
+        if (q.y > 0) p.seqs[atomicAdd(&start[bucket(q.w)], 1)] = q;     // (their order within a bucket changes no result)
+    }
+    __syncthreads();
+    const int n = total;
+    // (offsets that go backwards could list more items than the caller's sizes
+    // allow; what is past that bound is left out)
+    long long carry = 0;
+    for (int b = 0; b < n; b += 1024) {
+        const int i = b + threadIdx.x;
+        const long long mine = i < n ? (long long)((p.seqs[i].y + PAIR - 1) / PAIR) * p.heads : 0;
+        long long v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sum[w] = v;
+        __syncthreads();
+        long long before = carry;
+        for (int k = 0; k < 32; ++k) {
+            if (k < w) before += warp_sum[k];
+            carry += warp_sum[k];
+        }
+        if (i < n) p.before[i] = (int)min(before + v - mine, (long long)p.max_items);
+    }
+    if (carry > p.max_items && threadIdx.x == 0) flag(ST_BAD_LEN);
+    if (threadIdx.x == 0) {
+        p.next[0] = p.grid;           // (its CTAs start with item blockIdx.x)
+        p.next[1] = n;
+        p.before[n] = (int)min(carry, (long long)p.max_items);
+    }
+}
+
+// bounded wait that also gives up once another warp of the CTA has
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) {
+                ok = true;
+                break;
+            }
+            if ((it & 63u) == 0) {
+                if (*abort_flag) break;
+                if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+                    *abort_flag = 1;
+                    flag(ST_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);   // the roles run warp-collective instructions: a warp leaves as a whole
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    expanded_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
+                    const __grid_constant__ CUtensorMap rmap, const ExpandedParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SBAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile Slot *slots = reinterpret_cast<volatile Slot *>(bars + NBAR + 2);
+    auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < CHUNKS; ++i) {
+            mbar_init(bar(B_FULL + i), 1);
+            mbar_init(bar(B_EMPTY + i), 2);
+        }
+        mbar_init(bar(B_Q), 1);
+        mbar_init(bar(B_QFREE), 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + 2 * i), 128);
+            mbar_init(bar(B_P + 2 * i + 1), 128);
+            mbar_init(bar(B_DRAIN + i), 1);
+            mbar_init(bar(B_OFREE + i), 128);
+            mbar_init(bar(B_END + i), 1);
+        }
+        mbar_init(bar(B_TAIL), 1);
+        mbar_init(bar(B_TAIL + 1), 1);
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(bar(B_IFULL + i), 1);
+            mbar_init(bar(B_IEMPTY + i), W_PROD + 2);    // every warp but the producer
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&qmap);
+        prefetch_tmap(&kvmap);
+        prefetch_tmap(&rmap);
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // tensor memory: S of tile g at 128 g (P over its first 64 columns), O at 256 + 128 g
+    int k = 0;          // items
+    // the next item, as every warp but the producer reads it
+    auto read_item = [&](Slot &it) -> bool {
+        const int sl = k % NSLOT;
+        if (!wait_bar(bar(B_IFULL + sl), (k / NSLOT) & 1, abort_flag)) return false;
+        it.valid = slots[sl].valid;
+        it.row0 = slots[sl].row0;
+        it.rows = slots[sl].rows;
+        it.see0 = slots[sl].see0;
+        it.key0 = slots[sl].key0;
+        it.nk = slots[sl].nk;
+        it.head = slots[sl].head;
+        it.T = slots[sl].T;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IEMPTY + sl));
+        return it.valid != 0;
+    };
+    Slot it;
+
+    if (warp == W_PROD) {
+        // ======================= items and loads
+        griddep_wait();                  // the list, and everything before it on the stream
+        const int ns = p.next[1], items = p.before[ns];
+        int u = 0;                       // chunks issued
+        int idx = blockIdx.x;
+        bool ok = true;
+        for (;; ++k) {
+            const int sl = k % NSLOT;
+            if (k >= NSLOT && !wait_bar(bar(B_IEMPTY + sl), (k / NSLOT - 1) & 1, abort_flag)) break;
+            if (k > 0) {
+                if (lane == 0) idx = atomicAdd(p.next, 1);
+                idx = __shfl_sync(0xffffffffu, idx, 0);
+            }
+            it.valid = idx < items;
+            if (it.valid) {
+                // its sequence: the last one with before <= idx, 32 probes at a time
+                int lo = 0, len = ns;
+                while (len > 1) {
+                    const int step = (len + 31) / 32, x = lo + lane * step;
+                    const bool le = lane * step < len && p.before[x] <= idx;
+                    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));   // (lane 0 always is)
+                    lo += last * step;
+                    len = min(step, len - last * step);
+                }
+                const int4 q = p.seqs[lo];
+                const int units = (q.y + PAIR - 1) / PAIR, r = idx - p.before[lo];
+                const int g0 = r / (units * HGROUP) * HGROUP, gn = min(HGROUP, p.heads - g0);
+                const int r2 = r - g0 * units, unit = units - 1 - r2 / gn;
+                it.head = g0 + r2 % gn;
+                it.row0 = q.x + unit * PAIR;
+                it.rows = min(PAIR, q.y - unit * PAIR);
+                it.see0 = q.w - q.y + unit * PAIR + 1;
+                it.key0 = q.z;
+                it.nk = q.w;
+                // (rows that see nothing get one tile, all masked)
+                it.T = max(1, (it.see0 + it.rows - 1 + BN - 1) / BN);
+            }
+            if (lane == 0) {
+                slots[sl].valid = it.valid;
+                slots[sl].row0 = it.row0;
+                slots[sl].rows = it.rows;
+                slots[sl].see0 = it.see0;
+                slots[sl].key0 = it.key0;
+                slots[sl].nk = it.nk;
+                slots[sl].head = it.head;
+                slots[sl].T = it.T;
+                mbar_arrive(bar(B_IFULL + sl));
+            }
+            __syncwarp();
+            if (!it.valid) break;
+            // the queries, once every first product of the item before has finished
+            if (k > 0 && !wait_bar(bar(B_QFREE), (k - 1) & 1, abort_flag)) break;
+            const int tiles = it.rows > BM ? 2 : 1;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(B_Q), tiles * Q_TILE);
+                for (int g = 0; g < tiles; ++g)
+                    for (int i = 0; i < 3; ++i)
+                        tma_load_2d(sbase + g * Q_TILE + i * CHUNK_BYTES, &qmap, it.head * QKD + 64 * i, it.row0 + g * BM, bar(B_Q));
+            }
+            __syncwarp();
+            for (int j = 0; ok && j < it.T; ++j) {
+                const int y = it.key0 + j * BN;
+                for (int i = 0; ok && i < 5; ++i, ++u) {
+                    const int st = u % CHUNKS;
+                    if (u >= CHUNKS && !wait_bar(bar(B_EMPTY + st), (u / CHUNKS - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        fence_proxy_async_smem();
+                        mbar_arrive_expect_tx(bar(B_FULL + st), CHUNK_BYTES);
+                        const uint32_t dst = sbase + SKV + st * CHUNK_BYTES;
+                        if (i == 2) tma_load_2d(dst, &rmap, 0, y, bar(B_FULL + st));
+                        else tma_load_2d(dst, &kvmap, it.head * 2 * D + (i < 2 ? i : i - 1) * 64, y, bar(B_FULL + st));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            const int first = it.nk - (it.T - 1) * BN;
+            if (first < BN) {
+                // the last tile holds rows past the sequence's end, of another sequence
+                // or of none: P is 0 there, but 0 x NaN is NaN, so their values are zeroed
+                // once they have landed (the second product waits for it)
+                for (int i = 1; ok && i <= 2; ++i) {
+                    const int st = (u - i) % CHUNKS;
+                    ok = wait_bar(bar(B_FULL + st), ((u - i) / CHUNKS) & 1, abort_flag);
+                    for (int e = lane; ok && e < (BN - max(0, first)) * 8; e += 32)
+                        st_shared_v4(sbase + SKV + st * CHUNK_BYTES + (max(0, first) + (e >> 3)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_TAIL + (k & 1)));
+            }
+        }
+        if (*abort_flag) {               // loads in flight land before the CTA exits
+            for (int x = max(0, u - CHUNKS); x < u; ++x) (void)mbar_wait_bounded(bar(B_FULL + x % CHUNKS), (x / CHUNKS) & 1);
+            if (k > 0) (void)mbar_wait_bounded(bar(B_Q), k & 1);
+        }
+    } else if (warp >= W_MMA) {
+        // ======================= MMA issuers
+        const int g = warp - W_MMA;
+        const uint64_t qdesc = sdesc_sw128(sbase + g * Q_TILE, 16, 1024), kvdesc = sdesc_sw128(sbase + SKV, 16, 1024);
+        const uint32_t tS = tmem + g * 128, tO = tmem + 256 + g * 128;
+        int u = 0, n = 0, done = 0;      // chunks, S tiles and items of this query tile
+        unsigned tpar = 0;               // parity of the next tail, by item parity
+        bool ok = true;
+        for (; ok && read_item(it); ++k) {
+            const bool both = it.rows > BM, tail = it.nk < it.T * BN;
+            auto slot_of = [&](int x) -> uint32_t { return (uint32_t)(x % CHUNKS); };
+            // the tail of this item; both issuers wait for every phase of every barrier
+            // in turn (a parity cannot be waited for two phases ahead)
+            auto wait_tail = [&]() -> bool {
+                const bool zeroed = wait_bar(bar(B_TAIL + (k & 1)), (tpar >> (k & 1)) & 1, abort_flag);
+                tpar ^= 1u << (k & 1);
+                return zeroed;
+            };
+            if (g == 1 && !both) {
+                // no second query tile: every chunk is released as it lands
+                ok = wait_bar(bar(B_Q), k & 1, abort_flag);
+                if (lane == 0) mbar_arrive(bar(B_QFREE));
+                for (int j = 0; ok && j < it.T; ++j)
+                    for (int i = 0; ok && i < 5; ++i, ++u) {
+                        ok = wait_bar(bar(B_FULL + slot_of(u)), (u / CHUNKS) & 1, abort_flag);
+                        if (ok && tail && i == 3 && j == it.T - 1) ok = wait_tail();
+                        if (lane == 0) mbar_arrive(bar(B_EMPTY + slot_of(u)));
+                    }
+                continue;
+            }
+            // S = Q K^T of the tile whose chunks start at x
+            auto issue_s = [&](int x, bool last) -> bool {
+                for (int i = 0; i < 3; ++i)
+                    if (!wait_bar(bar(B_FULL + slot_of(x + i)), ((x + i) / CHUNKS) & 1, abort_flag)) return false;
+                if (elect_one()) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint64_t kd = kvdesc + (uint64_t)((slot_of(x + i) * CHUNK_BYTES) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(tS, qdesc + (uint64_t)((i * CHUNK_BYTES + kk * 32) >> 4), kd + (uint64_t)((kk * 32) >> 4),
+                                     IDESC_S, i + kk > 0);
+                    }
+                    umma_commit(bar(B_S + g));
+                    for (int i = 0; i < 3; ++i) umma_commit(bar(B_EMPTY + slot_of(x + i)));
+                    if (last) umma_commit(bar(B_QFREE));
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && issue_s(u, it.T == 1);
+            for (int j = 0; ok && j < it.T; ++j, u += 5, ++n) {
+                const int x = u + 3;                      // the values' two chunks
+                if (j == 0 && done > 0) ok = wait_bar(bar(B_OFREE + g), (done - 1) & 1, abort_flag);
+                for (int i = 0; ok && i < 2; ++i) ok = wait_bar(bar(B_FULL + slot_of(x + i)), ((x + i) / CHUNKS) & 1, abort_flag);
+                if (ok && tail && j == it.T - 1) ok = wait_tail();
+                // O += P V, 64 keys at a time
+                for (int h = 0; ok && h < 2; ++h) {
+                    ok = wait_bar(bar(B_P + 2 * g + h), n & 1, abort_flag);
+                    if (ok && elect_one()) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                umma_f16_ts(tO + 64 * i, tS + h * 32 + kk * 8,
+                                            kvdesc + (uint64_t)((slot_of(x + i) * CHUNK_BYTES + (h * 4 + kk) * 2048) >> 4), IDESC_PV,
+                                            (j > 0 || h + kk > 0) ? 1u : 0u);
+                        if (h == 1) {
+                            for (int i = 0; i < 2; ++i) umma_commit(bar(B_EMPTY + slot_of(x + i)));
+                            if (j == it.T - 1) umma_commit(bar(B_DRAIN + g));
+                        }
+                    }
+                    __syncwarp();
+                }
+                // (in issue order: the products above read P from the columns that S overwrites)
+                if (ok && j + 1 < it.T) ok = issue_s(u + 5, j + 2 == it.T);
+            }
+            ++done;
+        }
+        // everything issued has finished before tensor memory is released
+        if (elect_one()) umma_commit(bar(B_END + g));
+        __syncwarp();
+        (void)mbar_wait_bounded(bar(B_END + g), 0);
+    } else {
+        // ======================= softmax and epilogue: thread = query row = lane
+        const int g = warp >> 2, w = warp & 3, r = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+        const uint32_t tS = tmem + g * 128 + lane_base, tO = tmem + 256 + g * 128 + lane_base;
+        int n = 0, done = 0;             // S tiles and items of this query tile
+        const float sl = p.scale_log2;
+        bool ok = true;
+        for (; ok && read_item(it); ++k) {
+            if (g == 1 && it.rows <= BM) continue;
+            const int rows = min(BM, it.rows - g * BM);
+            // keys that this row sees (rows past the tile's last take the last one's)
+            const int see = it.see0 + g * BM + min(r, rows - 1), see_min = it.see0 + g * BM;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < it.T; ++j, ++n) {
+                if (!wait_bar(bar(B_S + g), n & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                const int t0 = j * BN;
+                float sv[BN];
+                tmem_ld64(tS, *reinterpret_cast<float(*)[64]>(sv));
+                tmem_ld64(tS + 64, *reinterpret_cast<float(*)[64]>(sv + 64));
+                if (t0 + BN > see_min) {
+#pragma unroll
+                    for (int e = 0; e < BN; ++e)
+                        if (t0 + e >= see) sv[e] = -INFINITY;
+                }
+                // raw scores; the scale (> 0) is applied inside the exponent's FFMA
+                float mk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mk[e] = fmaxf(sv[e], sv[4 + e]);
+#pragma unroll
+                for (int e = 8; e < BN; e += 8)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) mk[h] = max3(mk[h], sv[e + h], sv[e + 4 + h]);
+                const float mx = max3(mk[0], mk[1], fmaxf(mk[2], mk[3])) * sl;
+                // the reference moves only when the maximum has grown by 2^8 (P stays finite
+                // in fp32 and bf16, whose relative precision does not depend on its size)
+                float alpha = 1.f;
+                if (mx > m_ref + RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
+                    alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
+                    m_ref = mx;
+                }
+                // S(j) was issued after PV(j - 1) and has finished, so PV(j - 1) has: O may be
+                // rescaled, and P written over S
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int h = 0; h < D / 16; ++h) {
+                        float o[16];
+                        tmem_ld16(tO + h * 16, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                        tmem_st16(tO + h * 16, o);
+                    }
+                }
+                const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
+                const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float y0, y1;
+                        f2_unpack(f2_fma(f2_pack(sv[64 * h + 2 * e], sv[64 * h + 2 * e + 1]), sl2, mn2), y0, y1);
+                        const float p0 = ex2(y0), p1 = ex2(y1);
+                        acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+                        pw[e] = pack_bf16(p0, p1);   // the second product's operand type, beside bf16 values
+                    }
+                    tmem_st32u(tS + 32 * h, pw);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(B_P + 2 * g + h));
+                }
+                float s0, s1;
+                f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+                l = l * alpha + (s0 + s1);
+            }
+            if (!ok || !wait_bar(bar(B_DRAIN + g), done & 1, abort_flag)) break;
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int r4 = w * 32 + (lane & ~3), e4 = lane & 3;
+            uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D;
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+                float o[32];
+                tmem_ld32(tO + h * 32, o);
+                // 4 lanes exchange pieces, so that they store 64 bytes of one row together
+                uint32_t v[4][4];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                quad_transpose(v, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r4 + i < rows)
+                        reinterpret_cast<uint4 *>(dst + (size_t)(r4 + i) * p.heads * D + h * 32)[e4] =
+                            make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            }
+            tc_fence_before();
+            mbar_arrive(bar(B_OFREE + g));
+            ++done;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// workspace: the sequences, their prefix sums, two counters
+struct Layout {
+    size_t before, next, total;
+};
+Layout layout(int num_seqs)
+{
+    Layout y;
+    y.before = ((size_t)num_seqs * sizeof(int4) + 255) & ~(size_t)255;
+    y.next = y.before + (((size_t)num_seqs + 1) * 4 + 255 & ~(size_t)255);
+    y.total = y.next + 256;
+    return y;
 }
 
 }  // namespace
@@ -88,8 +591,8 @@ extern "C" {
 
 size_t latent_prefill_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int32_t num_heads)
 {
-    (void)num_seqs, (void)total_q_tokens, (void)num_heads;
-    return 0;
+    if (num_seqs < 1 || total_q_tokens < 1 || num_heads < 1 || num_heads > PAGEDKV_LATENT_MAX_HEADS) return 0;
+    return layout(num_seqs).total;
 }
 
 kv_status latent_prefill_attention(void *out, const void *q, const void *kv, const void *k_rope,
@@ -112,14 +615,45 @@ kv_status latent_prefill_attention(void *out, const void *q, const void *kv, con
         return KV_ERR_INVALID;
     const size_t need = latent_prefill_attention_workspace_size(num_seqs, total_q_tokens, num_heads);
     if (need && (!workspace || workspace_bytes < need || !pkv_host::aligned(workspace, 256))) return KV_ERR_INVALID;
-    const ExpandedParams p = {static_cast<uint16_t *>(out), static_cast<const uint16_t *>(q),
-                              static_cast<const uint16_t *>(kv), static_cast<const uint16_t *>(k_rope), cu_q_lens,
-                              cu_k_lens, k_rope_stride, num_seqs, total_q_tokens, total_k_tokens, num_heads,
-                              scale * LOG2E};
-    const long long warps = (long long)total_q_tokens * num_heads;
-    if ((warps + 7) / 8 > INT32_MAX) return KV_ERR_UNSUPPORTED;
-    expanded_simple_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    // (items are counted in 32 bits)
+    const int64_t items = ((int64_t)total_q_tokens / PAIR + num_seqs) * num_heads;
+    if (items > INT32_MAX) return KV_ERR_UNSUPPORTED;
+    const Layout y = layout(num_seqs);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ExpandedParams p;
+    p.out = static_cast<uint16_t *>(out);
+    p.cu_q = cu_q_lens;
+    p.cu_k = cu_k_lens;
+    p.seqs = reinterpret_cast<int4 *>(ws);
+    p.before = reinterpret_cast<int32_t *>(ws + y.before);
+    p.next = reinterpret_cast<int32_t *>(ws + y.next);
+    p.num_seqs = num_seqs;
+    p.rows = total_q_tokens;
+    p.keys = total_k_tokens;
+    p.heads = num_heads;
+    p.scale_log2 = scale * LOG2E;
+    CUtensorMap qmap, kvmap, rmap;
+    // (without any key nothing of kv is needed, but a map wants an extent: the
+    // query tensor stands in, its values masked)
+    const bool none = total_k_tokens == 0;
+    if (!pkv_host::encode_tmap_2d(&qmap, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)num_heads * QKD, total_q_tokens,
+                                  (uint64_t)num_heads * QKD * 2, 64, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !pkv_host::encode_tmap_2d(&kvmap, none ? q : kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                  none ? (uint64_t)num_heads * QKD : (uint64_t)num_heads * 2 * D, none ? 1 : total_k_tokens,
+                                  (uint64_t)num_heads * (none ? QKD : 2 * D) * 2, 64, BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !pkv_host::encode_tmap_2d(&rmap, none ? q : k_rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ROPE,
+                                  none ? 1 : total_k_tokens, (uint64_t)(none ? QKD : k_rope_stride) * 2, 64, BN,
+                                  CU_TENSOR_MAP_SWIZZLE_128B))
+        return KV_ERR_CUDA;
+    if (pkv_host::ensure_dynamic_smem<expanded_kernel>(SMEM_BYTES) != cudaSuccess) return KV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int grid = (int)std::min<int64_t>(items, 152);
+    p.grid = grid;
+    p.max_items = (int)items;
+    if (pkv_host::launch_ex(expanded_plan_kernel, dim3(1), dim3(1024), 0, st, true, p) != cudaSuccess ||
+        pkv_host::launch_ex(expanded_kernel, dim3(grid), dim3(THREADS), SMEM_BYTES, st, true, qmap, kvmap, rmap, p) != cudaSuccess)
+        return KV_ERR_CUDA;
+    return KV_OK;
 }
 
 }  // extern "C"
