@@ -18,14 +18,16 @@
 //    128 x 64 x 16 product with A in shared memory takes 48 cycles and a 128 x 128
 //    x 16 one 65 (measured): the query tile is read once per product.
 //  * Tensor memory holds one S and one O of each query tile: 512 columns.  The two
-//    tiles take turns: while one's softmax works, the other's products run.  P is
-//    handed over in halves of 64 keys, so that the second product starts before
-//    the softmax is done.
+//    tiles take turns: while one's softmax works, the other's products run, so the
+//    softmax has to be as quick as they are: two threads share a row (64 keys each)
+//    and exchange their maxima through shared memory.  With one thread a row, the
+//    4,096-token prompt over 128 heads took 590 us.
 //  * One CTA a SM takes items from a list, a device-built one: sequences with the
 //    most keys first, within a sequence eight heads at a time (their keys stay in
 //    L2 while all their query tiles pass), longest tiles first.
-// Warps 0-3 and 4-7: softmax and epilogue of the query tiles, one row a thread; 8:
-// items and TMA; 9 and 10: MMA issuers of the query tiles.
+// Warps 0-15: softmax and epilogue, four for each query tile and half of the keys
+// (0-3 tile 0 keys 0-63, 4-7 tile 0 keys 64-127, 8-15 tile 1); 16: items and TMA;
+// 17 and 18: MMA issuers of the query tiles, which take turns.
 #include "common.cuh"
 #include "trace.h"
 
@@ -46,24 +48,31 @@ constexpr int HGROUP = 8;                         // heads whose items are adjac
 constexpr int CHUNKS = 8;
 constexpr uint32_t CHUNK_BYTES = BN * 128, Q_TILE = 3 * BM * 128;
 constexpr uint32_t SKV = 2 * Q_TILE, SBAR = SKV + CHUNKS * CHUNK_BYTES;
-constexpr int SMEM_BYTES = SBAR + 512 + 1024;     // + 1 KiB: aligned to 1 KiB at run time
-constexpr int W_PROD = 8, W_MMA = 9, THREADS = 32 * (W_MMA + 2);
+constexpr uint32_t SMAX = SBAR + 512;             // row maxima (at an item's end: sums) [query tile][half][128]
+constexpr int SMEM_BYTES = SMAX + 2 * 2 * 128 * 4;
+constexpr int W_PROD = 16, W_MMA = 17, THREADS = 32 * (W_MMA + 2);
 constexpr int NSLOT = 2;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 
 enum {
-    B_FULL = 0,                     // + chunk: landed
-    B_EMPTY = B_FULL + CHUNKS,      // + chunk: every product that reads it has finished (one release an issuer)
-    B_Q = B_EMPTY + CHUNKS,         // the item's queries landed
+    B_KF = 0,                       // + key tile parity: its three key chunks landed
+    B_VF = B_KF + 2,                // + key tile parity: its two value chunks landed
+    B_KE = B_VF + 2,                // + key tile parity: both its first products have finished (one release an
+                                    // issuer; by parity, so that one issuer's releases of two tiles cannot add up)
+    B_VE = B_KE + 2,                // + key tile parity: both its second products have finished
+    B_TURN = B_VE + 2,              // + query tile: its issuer's turn
+    B_Q = B_TURN + 2,               // the item's queries landed
     B_QFREE = B_Q + 1,              // every first product of the item has finished (one an issuer)
     B_S = B_QFREE + 1,              // + tile: S is in tensor memory
     B_P = B_S + 2,                  // + 2 x tile + half: 64 keys of P are (128 arrivals)
     B_DRAIN = B_P + 4,              // + tile: every product of the item has finished
-    B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (128 arrivals)
-    B_TAIL = B_OFREE + 2,           // + item parity: value rows past the sequence's end are zeroed
-    B_IFULL = B_TAIL + 2,           // + slot: an item is in the slot
+    B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (256 arrivals)
+    B_TAIL = B_OFREE + 2,           // + item parity: value rows past the sequence's end are zeroed (the ring
+                                    // lets the producer finish one item ahead, not two)
+    B_MEET = B_TAIL + 2,            // + 4 x tile + row warp: both halves have written SMAX
+    B_IFULL = B_MEET + 8,           // + slot: an item is in the slot
     B_IEMPTY = B_IFULL + NSLOT,     // + slot: every warp has read it
-    B_END = B_IEMPTY + NSLOT,       // + tile: everything its issuer issued has finished
+    B_END = B_IEMPTY + NSLOT,       // + query tile: everything its issuer issued has finished
     NBAR = B_END + 2
 };
 // an item as the producer hands it on: valid, first query row, rows (up to 256),
@@ -206,19 +215,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const __grid_constant__ CUtensorMap rmap, const ExpandedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem = smem_raw;
     const uint32_t sbase = smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SBAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    if (sbase & 1023u) {
+        // the 128-byte swizzle needs 1 KiB-aligned tiles (there is no room to align
+        // them here; the array starts on such a boundary): refuse rather than
+        // compute with a wrong layout
+        if (threadIdx.x == 0) flag(ST_TIMEOUT);
+        return;
+    }
     volatile Slot *slots = reinterpret_cast<volatile Slot *>(bars + NBAR + 2);
     auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < CHUNKS; ++i) {
-            mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_KF + i), 1);
+            mbar_init(bar(B_VF + i), 1);
+            mbar_init(bar(B_TURN + i), 1);
+            mbar_init(bar(B_END + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_KE + i), 2);
+            mbar_init(bar(B_VE + i), 2);
         }
         mbar_init(bar(B_Q), 1);
         mbar_init(bar(B_QFREE), 2);
@@ -227,11 +249,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(bar(B_P + 2 * i), 128);
             mbar_init(bar(B_P + 2 * i + 1), 128);
             mbar_init(bar(B_DRAIN + i), 1);
-            mbar_init(bar(B_OFREE + i), 128);
-            mbar_init(bar(B_END + i), 1);
+            mbar_init(bar(B_OFREE + i), 256);
         }
         mbar_init(bar(B_TAIL), 1);
         mbar_init(bar(B_TAIL + 1), 1);
+        for (int i = 0; i < 8; ++i) mbar_init(bar(B_MEET + i), 2);
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(bar(B_IFULL + i), 1);
             mbar_init(bar(B_IEMPTY + i), W_PROD + 2);    // every warp but the producer
@@ -250,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // tensor memory: S of tile g at 128 g (P over its first 64 columns), O at 256 + 128 g
+    // tensor memory: S of tile g at 128 g (P of half h over its columns 64 h .. 64 h + 31), O at 256 + 128 g
     int k = 0;          // items
     // the next item, as every warp but the producer reads it
     auto read_item = [&](Slot &it) -> bool {
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ======================= items and loads
         griddep_wait();                  // the list, and everything before it on the stream
         const int ns = p.next[1], items = p.before[ns];
-        int u = 0;                       // chunks issued
+        int t = 0;                       // key tiles
         int idx = blockIdx.x;
         bool ok = true;
         for (;; ++k) {
@@ -331,23 +353,35 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tma_load_2d(sbase + g * Q_TILE + i * CHUNK_BYTES, &qmap, it.head * QKD + 64 * i, it.row0 + g * BM, bar(B_Q));
             }
             __syncwarp();
-            for (int j = 0; ok && j < it.T; ++j) {
+            // chunk i of tile t (0, 1 key part, 2 rotary key, 3, 4 value) takes ring slot
+            // (5 t + i) % 8, whose last holder was chunk i + 2 of tile t - 2 or i - 3 of t - 1
+            for (int j = 0; j < it.T; ++j, ++t) {
                 const int y = it.key0 + j * BN;
-                for (int i = 0; ok && i < 5; ++i, ++u) {
-                    const int st = u % CHUNKS;
-                    if (u >= CHUNKS && !wait_bar(bar(B_EMPTY + st), (u / CHUNKS - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        fence_proxy_async_smem();
-                        mbar_arrive_expect_tx(bar(B_FULL + st), CHUNK_BYTES);
-                        const uint32_t dst = sbase + SKV + st * CHUNK_BYTES;
-                        if (i == 2) tma_load_2d(dst, &rmap, 0, y, bar(B_FULL + st));
-                        else tma_load_2d(dst, &kvmap, it.head * 2 * D + (i < 2 ? i : i - 1) * 64, y, bar(B_FULL + st));
-                    }
-                    __syncwarp();
+                auto load = [&](int i, uint32_t b) {
+                    const uint32_t dst = sbase + SKV + (uint32_t)((5 * t + i) % CHUNKS) * CHUNK_BYTES;
+                    if (i == 2) tma_load_2d(dst, &rmap, 0, y, b);
+                    else tma_load_2d(dst, &kvmap, it.head * 2 * D + (i < 2 ? i : i - 1) * 64, y, b);
+                };
+                const uint32_t kb = bar(B_KF + (t & 1)), vb = bar(B_VF + (t & 1));
+                // (chunk 0: the keys of tile t - 2 were waited for with the values of t - 1)
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(kb, 3 * CHUNK_BYTES);
+                    load(0, kb);
                 }
+                if (t >= 2 && !wait_bar(bar(B_VE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag)) ok = false;
+                if (lane == 0 && ok) {
+                    load(1, kb);
+                    load(2, kb);
+                }
+                if (t >= 1 && ok && !wait_bar(bar(B_KE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag)) ok = false;
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(vb, 2 * CHUNK_BYTES);
+                    load(3, vb);
+                    load(4, vb);
+                }
+                __syncwarp();
             }
             if (!ok) break;
             const int first = it.nk - (it.T - 1) * BN;
@@ -355,11 +389,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // the last tile holds rows past the sequence's end, of another sequence
                 // or of none: P is 0 there, but 0 x NaN is NaN, so their values are zeroed
                 // once they have landed (the second product waits for it)
-                for (int i = 1; ok && i <= 2; ++i) {
-                    const int st = (u - i) % CHUNKS;
-                    ok = wait_bar(bar(B_FULL + st), ((u - i) / CHUNKS) & 1, abort_flag);
-                    for (int e = lane; ok && e < (BN - max(0, first)) * 8; e += 32)
-                        st_shared_v4(sbase + SKV + st * CHUNK_BYTES + (max(0, first) + (e >> 3)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                ok = wait_bar(bar(B_VF + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
+                for (int i = 3; ok && i < 5; ++i) {
+                    const uint32_t vt = sbase + SKV + (uint32_t)((5 * (t - 1) + i) % CHUNKS) * CHUNK_BYTES;
+                    for (int e = lane; e < (BN - max(0, first)) * 8; e += 32)
+                        st_shared_v4(vt + (max(0, first) + (e >> 3)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
@@ -368,87 +402,110 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         if (*abort_flag) {               // loads in flight land before the CTA exits
-            for (int x = max(0, u - CHUNKS); x < u; ++x) (void)mbar_wait_bounded(bar(B_FULL + x % CHUNKS), (x / CHUNKS) & 1);
+            // (bounded: a tile whose chunks were not all asked for never completes)
+            for (int x = max(0, t - 1); x <= t; ++x) {
+                (void)mbar_wait_bounded(bar(B_KF + (x & 1)), (x >> 1) & 1);
+                (void)mbar_wait_bounded(bar(B_VF + (x & 1)), (x >> 1) & 1);
+            }
             if (k > 0) (void)mbar_wait_bounded(bar(B_Q), k & 1);
         }
     } else if (warp >= W_MMA) {
-        // ======================= MMA issuers
+        // ======================= MMA issuers.  They take turns: one's second product
+        // of tile j and first of j + 1, then the other's, so that one query tile's
+        // softmax works while the other's products run.  Left alone the two fall into
+        // step -- both wait for the softmax, then both for the tensor cores -- and a
+        // key tile takes 5,100 cycles; and one warp for both spends its time on
+        // barriers (5,300).
         const int g = warp - W_MMA;
         const uint64_t qdesc = sdesc_sw128(sbase + g * Q_TILE, 16, 1024), kvdesc = sdesc_sw128(sbase + SKV, 16, 1024);
         const uint32_t tS = tmem + g * 128, tO = tmem + 256 + g * 128;
-        int u = 0, n = 0, done = 0;      // chunks, S tiles and items of this query tile
+        auto chunk = [&](int t, int i) -> uint32_t { return (uint32_t)((5 * t + i) % CHUNKS) * CHUNK_BYTES; };
+        int t = 0, n = 0, done = 0;      // key tiles; S tiles and items of this query tile
+        int turns = 0;                   // turns this issuer has taken
         unsigned tpar = 0;               // parity of the next tail, by item parity
         bool ok = true;
         for (; ok && read_item(it); ++k) {
             const bool both = it.rows > BM, tail = it.nk < it.T * BN;
-            auto slot_of = [&](int x) -> uint32_t { return (uint32_t)(x % CHUNKS); };
-            // the tail of this item; both issuers wait for every phase of every barrier
-            // in turn (a parity cannot be waited for two phases ahead)
+            // (both issuers wait for every phase of every barrier in turn: a parity
+            // cannot be waited for two phases ahead)
             auto wait_tail = [&]() -> bool {
                 const bool zeroed = wait_bar(bar(B_TAIL + (k & 1)), (tpar >> (k & 1)) & 1, abort_flag);
                 tpar ^= 1u << (k & 1);
                 return zeroed;
             };
             if (g == 1 && !both) {
-                // no second query tile: every chunk is released as it lands
+                // no second query tile: every tile is released as it lands
                 ok = wait_bar(bar(B_Q), k & 1, abort_flag);
                 if (lane == 0) mbar_arrive(bar(B_QFREE));
-                for (int j = 0; ok && j < it.T; ++j)
-                    for (int i = 0; ok && i < 5; ++i, ++u) {
-                        ok = wait_bar(bar(B_FULL + slot_of(u)), (u / CHUNKS) & 1, abort_flag);
-                        if (ok && tail && i == 3 && j == it.T - 1) ok = wait_tail();
-                        if (lane == 0) mbar_arrive(bar(B_EMPTY + slot_of(u)));
-                    }
+                for (int j = 0; ok && j < it.T; ++j, ++t) {
+                    ok = wait_bar(bar(B_KF + (t & 1)), (t >> 1) & 1, abort_flag);
+                    if (ok && lane == 0) mbar_arrive(bar(B_KE + (t & 1)));
+                    ok = ok && wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
+                    if (ok && tail && j == it.T - 1) ok = wait_tail();
+                    if (ok && lane == 0) mbar_arrive(bar(B_VE + (t & 1)));
+                }
                 continue;
             }
-            // S = Q K^T of the tile whose chunks start at x
-            auto issue_s = [&](int x, bool last) -> bool {
-                for (int i = 0; i < 3; ++i)
-                    if (!wait_bar(bar(B_FULL + slot_of(x + i)), ((x + i) / CHUNKS) & 1, abort_flag)) return false;
-                if (elect_one()) {
+            // the first turn of all is query tile 0's
+            auto take_turn = [&]() -> bool {
+                if (!both) return true;
+                const int x = turns++;
+                if (g == 0) return x == 0 || wait_bar(bar(B_TURN), (x - 1) & 1, abort_flag);
+                return wait_bar(bar(B_TURN + 1), x & 1, abort_flag);
+            };
+            auto pass_turn = [&]() {
+                if (both && lane == 0) mbar_arrive(bar(B_TURN + (g ^ 1)));
+            };
+            // S = Q K^T of key tile x (called by one lane)
+            auto issue_s = [&](int x, bool last) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const uint64_t kd = kvdesc + (uint64_t)(chunk(x, i) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16(tS, qdesc + (uint64_t)((i * CHUNK_BYTES + kk * 32) >> 4), kd + (uint64_t)((kk * 32) >> 4),
+                                 IDESC_S, i + kk > 0);
+                }
+                umma_commit(bar(B_S + g));
+                umma_commit(bar(B_KE + (x & 1)));
+                if (last) umma_commit(bar(B_QFREE));
+            };
+            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && wait_bar(bar(B_KF + (t & 1)), (t >> 1) & 1, abort_flag) && take_turn();
+            if (ok && elect_one()) {
+                tc_fence_after();
+                issue_s(t, it.T == 1);
+            }
+            __syncwarp();
+            pass_turn();
+            for (int j = 0; ok && j < it.T; ++j, ++t, ++n) {
+                const bool more = j + 1 < it.T;
+                ok = wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
+                if (ok && tail && !more) ok = wait_tail();
+                if (ok && j == 0 && done > 0) ok = wait_bar(bar(B_OFREE + g), (done - 1) & 1, abort_flag);
+                ok = ok && wait_bar(bar(B_P + 2 * g), n & 1, abort_flag) && wait_bar(bar(B_P + 2 * g + 1), n & 1, abort_flag) && take_turn();
+                if (ok && elect_one()) {
                     tc_fence_after();
+                    // O += P V
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint64_t kd = kvdesc + (uint64_t)((slot_of(x + i) * CHUNK_BYTES) >> 4);
+                    for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f16(tS, qdesc + (uint64_t)((i * CHUNK_BYTES + kk * 32) >> 4), kd + (uint64_t)((kk * 32) >> 4),
-                                     IDESC_S, i + kk > 0);
-                    }
-                    umma_commit(bar(B_S + g));
-                    for (int i = 0; i < 3; ++i) umma_commit(bar(B_EMPTY + slot_of(x + i)));
-                    if (last) umma_commit(bar(B_QFREE));
+                        for (int i = 0; i < 2; ++i)
+                            umma_f16_ts(tO + 64 * i, tS + (kk >> 2) * 64 + (kk & 3) * 8,
+                                        kvdesc + (uint64_t)((chunk(t, 3 + i) + kk * 2048) >> 4), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(bar(B_VE + (t & 1)));
+                    if (!more) umma_commit(bar(B_DRAIN + g));
                 }
                 __syncwarp();
-                return true;
-            };
-            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && issue_s(u, it.T == 1);
-            for (int j = 0; ok && j < it.T; ++j, u += 5, ++n) {
-                const int x = u + 3;                      // the values' two chunks
-                if (j == 0 && done > 0) ok = wait_bar(bar(B_OFREE + g), (done - 1) & 1, abort_flag);
-                for (int i = 0; ok && i < 2; ++i) ok = wait_bar(bar(B_FULL + slot_of(x + i)), ((x + i) / CHUNKS) & 1, abort_flag);
-                if (ok && tail && j == it.T - 1) ok = wait_tail();
-                // O += P V, 64 keys at a time
-                for (int h = 0; ok && h < 2; ++h) {
-                    ok = wait_bar(bar(B_P + 2 * g + h), n & 1, abort_flag);
-                    if (ok && elect_one()) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                umma_f16_ts(tO + 64 * i, tS + h * 32 + kk * 8,
-                                            kvdesc + (uint64_t)((slot_of(x + i) * CHUNK_BYTES + (h * 4 + kk) * 2048) >> 4), IDESC_PV,
-                                            (j > 0 || h + kk > 0) ? 1u : 0u);
-                        if (h == 1) {
-                            for (int i = 0; i < 2; ++i) umma_commit(bar(B_EMPTY + slot_of(x + i)));
-                            if (j == it.T - 1) umma_commit(bar(B_DRAIN + g));
-                        }
-                    }
-                    __syncwarp();
+                // (in issue order: the products above read P from the columns that S
+                // overwrites.  The keys are waited for only now: two of their chunks take
+                // the slots of the values before, so they arrive while PV runs)
+                if (ok && more) ok = wait_bar(bar(B_KF + ((t + 1) & 1)), ((t + 1) >> 1) & 1, abort_flag);
+                if (ok && more && elect_one()) {
+                    tc_fence_after();
+                    issue_s(t + 1, j + 2 == it.T);
                 }
-                // (in issue order: the products above read P from the columns that S overwrites)
-                if (ok && j + 1 < it.T) ok = issue_s(u + 5, j + 2 == it.T);
+                __syncwarp();
+                pass_turn();
             }
             ++done;
         }
@@ -457,13 +514,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         (void)mbar_wait_bounded(bar(B_END + g), 0);
     } else {
-        // ======================= softmax and epilogue: thread = query row = lane
-        const int g = warp >> 2, w = warp & 3, r = threadIdx.x & 127;
+        // ======================= softmax and epilogue: a row's threads are lanes of the
+        // tile's two halves
+        const int g = warp >> 3, half = (warp >> 2) & 1, w = warp & 3, r = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-        const uint32_t tS = tmem + g * 128 + lane_base, tO = tmem + 256 + g * 128 + lane_base;
-        int n = 0, done = 0;             // S tiles and items of this query tile
+        const uint32_t tS = tmem + g * 128 + half * 64 + lane_base, tO = tmem + 256 + g * 128 + half * 64 + lane_base;
+        volatile float *mine = reinterpret_cast<volatile float *>(smem + SMAX) + (g * 2 + half) * 128 + r;
+        volatile float *other = reinterpret_cast<volatile float *>(smem + SMAX) + (g * 2 + (half ^ 1)) * 128 + r;
+        int n = 0, done = 0, met = 0;    // S tiles and items of this query tile; exchanges with the other half
         const float sl = p.scale_log2;
         bool ok = true;
+        // the other half's value of this row (it is not overwritten before it is read:
+        // the next tile's S comes after both halves' P of this one)
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_MEET + 4 * g + w));
+            return wait_bar(bar(B_MEET + 4 * g + w), met++ & 1, abort_flag);
+        };
+        auto exchange = [&](float v, float &got) -> bool {
+            *mine = v;
+            const bool there = meet();
+            got = *other;
+            return there;
+        };
         for (; ok && read_item(it); ++k) {
             if (g == 1 && it.rows <= BM) continue;
             const int rows = min(BM, it.rows - g * BM);
@@ -473,24 +546,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < it.T; ++j, ++n) {
                 if (!wait_bar(bar(B_S + g), n & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                const int t0 = j * BN;
-                float sv[BN];
-                tmem_ld64(tS, *reinterpret_cast<float(*)[64]>(sv));
-                tmem_ld64(tS + 64, *reinterpret_cast<float(*)[64]>(sv + 64));
-                if (t0 + BN > see_min) {
+                const int t0 = j * BN + half * 64;
+                const bool masked = t0 + 64 > see_min;
+                // raw scores; the scale (> 0) is applied inside the exponent's FFMA.  They are
+                // read twice (the maximum first), 32 at a time: 19 warps leave 96 registers
+                // a thread
+                float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int e = 0; e < BN; ++e)
-                        if (t0 + e >= see) sv[e] = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    float sv[32];
+                    tmem_ld32(tS + 32 * h, sv);
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (t0 + 32 * h + e >= see) sv[e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) mk[f] = max3(mk[f], sv[e + f], sv[e + 4 + f]);
                 }
-                // raw scores; the scale (> 0) is applied inside the exponent's FFMA
-                float mk[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mk[e] = fmaxf(sv[e], sv[4 + e]);
-#pragma unroll
-                for (int e = 8; e < BN; e += 8)
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) mk[h] = max3(mk[h], sv[e + h], sv[e + 4 + h]);
-                const float mx = max3(mk[0], mk[1], fmaxf(mk[2], mk[3])) * sl;
+                float mx, mo;
+                mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
+                if (!exchange(mx, mo)) { ok = false; break; }
+                mx = fmaxf(mx, mo) * sl;
                 // the reference moves only when the maximum has grown by 2^8 (P stays finite
                 // in fp32 and bf16, whose relative precision does not depend on its size)
                 float alpha = 1.f;
@@ -499,10 +578,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     m_ref = mx;
                 }
                 // S(j) was issued after PV(j - 1) and has finished, so PV(j - 1) has: O may be
-                // rescaled, and P written over S
+                // rescaled (64 dims each half), and P written over S
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-                    for (int h = 0; h < D / 16; ++h) {
+                    for (int h = 0; h < 4; ++h) {
                         float o[16];
                         tmem_ld16(tO + h * 16, o);
 #pragma unroll
@@ -515,31 +594,40 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t pw[32];
+                    float sv[32];
+                    tmem_ld32(tS + 32 * h, sv);
+                    if (masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 32; ++e)
+                            if (t0 + 32 * h + e >= see) sv[e] = -INFINITY;
+                    }
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
                         float y0, y1;
-                        f2_unpack(f2_fma(f2_pack(sv[64 * h + 2 * e], sv[64 * h + 2 * e + 1]), sl2, mn2), y0, y1);
+                        f2_unpack(f2_fma(f2_pack(sv[2 * e], sv[2 * e + 1]), sl2, mn2), y0, y1);
                         const float p0 = ex2(y0), p1 = ex2(y1);
                         acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
                         pw[e] = pack_bf16(p0, p1);   // the second product's operand type, beside bf16 values
                     }
-                    tmem_st32u(tS + 32 * h, pw);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(bar(B_P + 2 * g + h));
+                    tmem_st16u(tS + 16 * h, pw);     // (over scores that have been read)
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(B_P + 2 * g + half));
                 float s0, s1;
                 f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
                 l = l * alpha + (s0 + s1);
             }
             if (!ok || !wait_bar(bar(B_DRAIN + g), done & 1, abort_flag)) break;
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            float lo;
+            if (!exchange(l, lo) || !meet()) break;      // (read by both before the next item's maxima)
+            const float inv = l + lo > 0.f ? 1.f / (l + lo) : 0.f;
             const int r4 = w * 32 + (lane & ~3), e4 = lane & 3;
-            uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D;
+            uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D + half * 64;
 #pragma unroll 1
-            for (int h = 0; h < D / 32; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 float o[32];
                 tmem_ld32(tO + h * 32, o);
                 // 4 lanes exchange pieces, so that they store 64 bytes of one row together
