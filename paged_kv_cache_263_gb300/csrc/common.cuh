@@ -298,6 +298,10 @@ __device__ __forceinline__ bool elect_one()
         : "=r"(ok));
     return ok != 0;
 }
+// a value that is the same in all lanes, made known as such to the compiler: what
+// an MMA's descriptors depend on then stays in uniform registers
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 consecutive fp32 columns of this thread's TMEM lane; the wait for the load

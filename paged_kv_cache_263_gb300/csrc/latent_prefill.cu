@@ -19,15 +19,15 @@
 //    x 16 one 65 (measured): the query tile is read once per product.
 //  * Tensor memory holds one S and one O of each query tile: 512 columns.  The two
 //    tiles take turns: while one's softmax works, the other's products run, so the
-//    softmax has to be as quick as they are: two threads share a row (64 keys each)
-//    and exchange their maxima through shared memory.  With one thread a row, the
-//    4,096-token prompt over 128 heads took 590 us.
+//    softmax has to be as quick as they are (1,300 cycles).  It takes its reference
+//    maximum from the first key tile and keeps it: a later tile's exponentials are
+//    computed at once, and only if their sum shows a score far above the reference
+//    is the maximum taken, the output rescaled and the tile done again.
 //  * One CTA a SM takes items from a list, a device-built one: sequences with the
 //    most keys first, within a sequence eight heads at a time (their keys stay in
 //    L2 while all their query tiles pass), longest tiles first.
-// Warps 0-15: softmax and epilogue, four for each query tile and half of the keys
-// (0-3 tile 0 keys 0-63, 4-7 tile 0 keys 64-127, 8-15 tile 1); 16: items and TMA;
-// 17 and 18: MMA issuers of the query tiles, which take turns.
+// Warps 0 and 1: MMA issuers of the query tiles, which take turns; 2: items and
+// TMA; 4-7 and 8-11: softmax and epilogue of the query tiles, one row a thread.
 #include "common.cuh"
 #include "trace.h"
 
@@ -41,16 +41,15 @@ __device__ uint32_t g_status;
 using namespace pkv;
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float FAR = 32768.0f;                  // a tile's sum above this: its maximum is taken anew
 constexpr int QKD = D + ROPE;                     // 192
 constexpr int BM = 128, BN = 128, PAIR = 2 * BM;
 constexpr int HGROUP = 8;                         // heads whose items are adjacent
 constexpr int CHUNKS = 8;
 constexpr uint32_t CHUNK_BYTES = BN * 128, Q_TILE = 3 * BM * 128;
 constexpr uint32_t SKV = 2 * Q_TILE, SBAR = SKV + CHUNKS * CHUNK_BYTES;
-constexpr uint32_t SMAX = SBAR + 512;             // row maxima (at an item's end: sums) [query tile][half][128]
-constexpr int SMEM_BYTES = SMAX + 2 * 2 * 128 * 4;
-constexpr int W_PROD = 16, W_MMA = 17, THREADS = 32 * (W_MMA + 2);
+constexpr int SMEM_BYTES = SBAR + 512 + 1024;     // + 1 KiB: aligned to 1 KiB at run time
+constexpr int W_MMA = 0, W_PROD = 2, W_SOFT = 4, THREADS = 32 * (W_SOFT + 8);
 constexpr int NSLOT = 2;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 
@@ -64,13 +63,12 @@ enum {
     B_Q = B_TURN + 2,               // the item's queries landed
     B_QFREE = B_Q + 1,              // every first product of the item has finished (one an issuer)
     B_S = B_QFREE + 1,              // + tile: S is in tensor memory
-    B_P = B_S + 2,                  // + 2 x tile + half: 64 keys of P are (128 arrivals)
-    B_DRAIN = B_P + 4,              // + tile: every product of the item has finished
-    B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (256 arrivals)
+    B_P = B_S + 2,                  // + tile: P is (128 arrivals)
+    B_DRAIN = B_P + 2,              // + tile: every product of the item has finished
+    B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (128 arrivals)
     B_TAIL = B_OFREE + 2,           // + item parity: value rows past the sequence's end are zeroed (the ring
                                     // lets the producer finish one item ahead, not two)
-    B_MEET = B_TAIL + 2,            // + 4 x tile + row warp: both halves have written SMAX
-    B_IFULL = B_MEET + 8,           // + slot: an item is in the slot
+    B_IFULL = B_TAIL + 2,           // + slot: an item is in the slot
     B_IEMPTY = B_IFULL + NSLOT,     // + slot: every warp has read it
     B_END = B_IEMPTY + NSLOT,       // + query tile: everything its issuer issued has finished
     NBAR = B_END + 2
@@ -215,21 +213,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const __grid_constant__ CUtensorMap rmap, const ExpandedParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = smem_raw;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SBAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    if (sbase & 1023u) {
-        // the 128-byte swizzle needs 1 KiB-aligned tiles (there is no room to align
-        // them here; the array starts on such a boundary): refuse rather than
-        // compute with a wrong layout
-        if (threadIdx.x == 0) flag(ST_TIMEOUT);
-        return;
-    }
     volatile Slot *slots = reinterpret_cast<volatile Slot *>(bars + NBAR + 2);
     auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -246,17 +237,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(bar(B_QFREE), 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_S + i), 1);
-            mbar_init(bar(B_P + 2 * i), 128);
-            mbar_init(bar(B_P + 2 * i + 1), 128);
+            mbar_init(bar(B_P + i), 128);
             mbar_init(bar(B_DRAIN + i), 1);
-            mbar_init(bar(B_OFREE + i), 256);
+            mbar_init(bar(B_OFREE + i), 128);
         }
         mbar_init(bar(B_TAIL), 1);
         mbar_init(bar(B_TAIL + 1), 1);
-        for (int i = 0; i < 8; ++i) mbar_init(bar(B_MEET + i), 2);
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(bar(B_IFULL + i), 1);
-            mbar_init(bar(B_IEMPTY + i), W_PROD + 2);    // every warp but the producer
+            mbar_init(bar(B_IEMPTY + i), 10);            // the issuers and the softmax warps
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -264,28 +253,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         prefetch_tmap(&kvmap);
         prefetch_tmap(&rmap);
     }
-    if (warp == 0) {
+    if (warp == W_PROD) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    // tensor memory: S of tile g at 128 g (P of half h over its columns 64 h .. 64 h + 31), O at 256 + 128 g
+    const uint32_t tmem = uniform(*tmem_slot);
+    // tensor memory: S of tile g at 128 g (P over its first 64 columns), O at 256 + 128 g
     int k = 0;          // items
     // the next item, as every warp but the producer reads it
     auto read_item = [&](Slot &it) -> bool {
         const int sl = k % NSLOT;
         if (!wait_bar(bar(B_IFULL + sl), (k / NSLOT) & 1, abort_flag)) return false;
-        it.valid = slots[sl].valid;
-        it.row0 = slots[sl].row0;
-        it.rows = slots[sl].rows;
-        it.see0 = slots[sl].see0;
-        it.key0 = slots[sl].key0;
-        it.nk = slots[sl].nk;
-        it.head = slots[sl].head;
-        it.T = slots[sl].T;
+        it.valid = uniform(slots[sl].valid);
+        it.row0 = uniform(slots[sl].row0);
+        it.rows = uniform(slots[sl].rows);
+        it.see0 = uniform(slots[sl].see0);
+        it.key0 = uniform(slots[sl].key0);
+        it.nk = uniform(slots[sl].nk);
+        it.head = uniform(slots[sl].head);
+        it.T = uniform(slots[sl].T);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + sl));
         return it.valid != 0;
@@ -409,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (k > 0) (void)mbar_wait_bounded(bar(B_Q), k & 1);
         }
-    } else if (warp >= W_MMA) {
+    } else if (warp < W_MMA + 2) {
         // ======================= MMA issuers.  They take turns: one's second product
         // of tile j and first of j + 1, then the other's, so that one query tile's
         // softmax works while the other's products run.  Left alone the two fall into
@@ -453,9 +442,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (g == 0) return x == 0 || wait_bar(bar(B_TURN), (x - 1) & 1, abort_flag);
                 return wait_bar(bar(B_TURN + 1), x & 1, abort_flag);
             };
-            auto pass_turn = [&]() {
-                if (both && lane == 0) mbar_arrive(bar(B_TURN + (g ^ 1)));
-            };
             // S = Q K^T of key tile x (called by one lane)
             auto issue_s = [&](int x, bool last) {
 #pragma unroll
@@ -465,6 +451,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int kk = 0; kk < 4; ++kk)
                         umma_f16(tS, qdesc + (uint64_t)((i * CHUNK_BYTES + kk * 32) >> 4), kd + (uint64_t)((kk * 32) >> 4),
                                  IDESC_S, i + kk > 0);
+                    // (the turn takes about as long to pass as the last four products)
+                    if (i == 1 && both) mbar_arrive(bar(B_TURN + (g ^ 1)));
                 }
                 umma_commit(bar(B_S + g));
                 umma_commit(bar(B_KE + (x & 1)));
@@ -476,13 +464,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 issue_s(t, it.T == 1);
             }
             __syncwarp();
-            pass_turn();
             for (int j = 0; ok && j < it.T; ++j, ++t, ++n) {
                 const bool more = j + 1 < it.T;
                 ok = wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
                 if (ok && tail && !more) ok = wait_tail();
                 if (ok && j == 0 && done > 0) ok = wait_bar(bar(B_OFREE + g), (done - 1) & 1, abort_flag);
-                ok = ok && wait_bar(bar(B_P + 2 * g), n & 1, abort_flag) && wait_bar(bar(B_P + 2 * g + 1), n & 1, abort_flag) && take_turn();
+                ok = ok && wait_bar(bar(B_P + g), n & 1, abort_flag) && take_turn();
                 if (ok && elect_one()) {
                     tc_fence_after();
                     // O += P V
@@ -490,10 +477,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            umma_f16_ts(tO + 64 * i, tS + (kk >> 2) * 64 + (kk & 3) * 8,
+                            umma_f16_ts(tO + 64 * i, tS + kk * 8,
                                         kvdesc + (uint64_t)((chunk(t, 3 + i) + kk * 2048) >> 4), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
                     umma_commit(bar(B_VE + (t & 1)));
-                    if (!more) umma_commit(bar(B_DRAIN + g));
+                    if (!more) {
+                        umma_commit(bar(B_DRAIN + g));
+                        if (both) mbar_arrive(bar(B_TURN + (g ^ 1)));
+                    }
                 }
                 __syncwarp();
                 // (in issue order: the products above read P from the columns that S
@@ -505,7 +495,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     issue_s(t + 1, j + 2 == it.T);
                 }
                 __syncwarp();
-                pass_turn();
             }
             ++done;
         }
@@ -513,30 +502,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) umma_commit(bar(B_END + g));
         __syncwarp();
         (void)mbar_wait_bounded(bar(B_END + g), 0);
-    } else {
-        // ======================= softmax and epilogue: a row's threads are lanes of the
-        // tile's two halves
-        const int g = warp >> 3, half = (warp >> 2) & 1, w = warp & 3, r = threadIdx.x & 127;
+    } else if (warp >= W_SOFT) {
+        // ======================= softmax and epilogue: thread = query row = lane
+        const int g = (warp - W_SOFT) >> 2, w = warp & 3, r = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-        const uint32_t tS = tmem + g * 128 + half * 64 + lane_base, tO = tmem + 256 + g * 128 + half * 64 + lane_base;
-        volatile float *mine = reinterpret_cast<volatile float *>(smem + SMAX) + (g * 2 + half) * 128 + r;
-        volatile float *other = reinterpret_cast<volatile float *>(smem + SMAX) + (g * 2 + (half ^ 1)) * 128 + r;
-        int n = 0, done = 0, met = 0;    // S tiles and items of this query tile; exchanges with the other half
+        const uint32_t tS = tmem + g * 128 + lane_base, tO = tmem + 256 + g * 128 + lane_base;
+        int n = 0, done = 0;             // S tiles and items of this query tile
         const float sl = p.scale_log2;
         bool ok = true;
-        // the other half's value of this row (it is not overwritten before it is read:
-        // the next tile's S comes after both halves' P of this one)
-        auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_MEET + 4 * g + w));
-            return wait_bar(bar(B_MEET + 4 * g + w), met++ & 1, abort_flag);
-        };
-        auto exchange = [&](float v, float &got) -> bool {
-            *mine = v;
-            const bool there = meet();
-            got = *other;
-            return there;
-        };
         for (; ok && read_item(it); ++k) {
             if (g == 1 && it.rows <= BM) continue;
             const int rows = min(BM, it.rows - g * BM);
@@ -546,88 +519,89 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < it.T; ++j, ++n) {
                 if (!wait_bar(bar(B_S + g), n & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                const int t0 = j * BN + half * 64;
-                const bool masked = t0 + 64 > see_min;
-                // raw scores; the scale (> 0) is applied inside the exponent's FFMA.  They are
-                // read twice (the maximum first), 32 at a time: 19 warps leave 96 registers
-                // a thread
-                float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float sv[32];
-                    tmem_ld32(tS + 32 * h, sv);
+                const int t0 = j * BN;
+                const bool masked = t0 + BN > see_min;
+                // 32 raw scores (the scale, > 0, is applied inside the exponent's FFMA)
+                auto scores = [&](int c, float (&sv)[32]) {
+                    tmem_ld32(tS + 32 * c, sv);
                     if (masked) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (t0 + 32 * h + e >= see) sv[e] = -INFINITY;
+                            if (t0 + 32 * c + e >= see) sv[e] = -INFINITY;
                     }
+                };
+                uint32_t pw[BN / 2];
+                float sum;
+                auto exponentials = [&]() {
+                    const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
+                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                    for (int c = 0; c < 4; ++c) {
+                        float sv[32];
+                        scores(c, sv);
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) mk[f] = max3(mk[f], sv[e + f], sv[e + 4 + f]);
+                        for (int e = 0; e < 16; ++e) {
+                            float y0, y1;
+                            f2_unpack(f2_fma(f2_pack(sv[2 * e], sv[2 * e + 1]), sl2, mn2), y0, y1);
+                            const float p0 = ex2(y0), p1 = ex2(y1);
+                            acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
+                            pw[16 * c + e] = pack_bf16(p0, p1);   // the second product's operand type, beside bf16 values
+                        }
+                    }
+                    float s0, s1;
+                    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+                    sum = s0 + s1;
+                };
+                // P relative to a maximum that is not the largest any more is as exact (fp32
+                // and bf16 keep their relative precision) while nothing comes near overflow
+                bool fresh = __any_sync(0xffffffffu, m_ref == -INFINITY);
+                if (!fresh) {
+                    exponentials();
+                    fresh = __any_sync(0xffffffffu, sum > FAR);
                 }
-                float mx, mo;
-                mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
-                if (!exchange(mx, mo)) { ok = false; break; }
-                mx = fmaxf(mx, mo) * sl;
-                // the reference moves only when the maximum has grown by 2^8 (P stays finite
-                // in fp32 and bf16, whose relative precision does not depend on its size)
-                float alpha = 1.f;
-                if (mx > m_ref + RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
-                    alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mx);
-                    m_ref = mx;
-                }
-                // S(j) was issued after PV(j - 1) and has finished, so PV(j - 1) has: O may be
-                // rescaled (64 dims each half), and P written over S
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (fresh) {
+                    float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
-                        float o[16];
-                        tmem_ld16(tO + h * 16, o);
+                    for (int c = 0; c < 4; ++c) {
+                        float sv[32];
+                        scores(c, sv);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                        tmem_st16(tO + h * 16, o);
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) mk[f] = max3(mk[f], sv[e + f], sv[e + 4 + f]);
                     }
+                    const float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * sl;
+                    const float m_new = fmaxf(m_ref, mx), alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+                    // S(j) was issued after PV(j - 1) and has finished, so PV(j - 1) has
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int h = 0; h < D / 16; ++h) {
+                            float o[16];
+                            tmem_ld16(tO + h * 16, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                            tmem_st16(tO + h * 16, o);
+                        }
+                    }
+                    l *= alpha;
+                    m_ref = m_new;
+                    exponentials();
                 }
-                const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
-                const uint64_t sl2 = f2_pack(sl, sl), mn2 = f2_pack(mneg, mneg);
-                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float sv[32];
-                    tmem_ld32(tS + 32 * h, sv);
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (t0 + 32 * h + e >= see) sv[e] = -INFINITY;
-                    }
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float y0, y1;
-                        f2_unpack(f2_fma(f2_pack(sv[2 * e], sv[2 * e + 1]), sl2, mn2), y0, y1);
-                        const float p0 = ex2(y0), p1 = ex2(y1);
-                        acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
-                        pw[e] = pack_bf16(p0, p1);   // the second product's operand type, beside bf16 values
-                    }
-                    tmem_st16u(tS + 16 * h, pw);     // (over scores that have been read)
-                }
+                l += sum;
+                tmem_st32u(tS, *reinterpret_cast<const uint32_t(*)[32]>(pw));
+                tmem_st32u(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_P + 2 * g + half));
-                float s0, s1;
-                f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-                l = l * alpha + (s0 + s1);
+                mbar_arrive(bar(B_P + g));
             }
             if (!ok || !wait_bar(bar(B_DRAIN + g), done & 1, abort_flag)) break;
             tc_fence_after();
-            float lo;
-            if (!exchange(l, lo) || !meet()) break;      // (read by both before the next item's maxima)
-            const float inv = l + lo > 0.f ? 1.f / (l + lo) : 0.f;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             const int r4 = w * 32 + (lane & ~3), e4 = lane & 3;
-            uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D + half * 64;
+            uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < D / 32; ++h) {
                 float o[32];
                 tmem_ld32(tO + h * 32, o);
                 // 4 lanes exchange pieces, so that they store 64 bytes of one row together
@@ -647,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == W_PROD) tmem_dealloc(tmem, 512);
 }
 
 // workspace: the sequences, their prefix sums, two counters
