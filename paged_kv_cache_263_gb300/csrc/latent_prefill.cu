@@ -54,7 +54,8 @@ constexpr int NSLOT = 2;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 
 enum {
-    B_KF = 0,                       // + key tile parity: its three key chunks landed
+    B_K0 = 0,                       // + key tile parity: its first key chunk landed
+    B_KF = B_K0 + 2,                // + key tile parity: its second key chunk and the rotary one landed
     B_VF = B_KF + 2,                // + key tile parity: its two value chunks landed
     B_KE = B_VF + 2,                // + key tile parity: both its first products have finished (one release an
                                     // issuer; by parity, so that one issuer's releases of two tiles cannot add up)
@@ -77,6 +78,12 @@ enum {
 // the keys that row 0 sees, first key row, keys of the sequence, head, key tiles
 struct Slot {
     int valid, row0, rows, see0, key0, nk, head, T;
+    // key tiles of query tile g: the first one's rows may see fewer (rows that see
+    // nothing get one tile, all masked)
+    __device__ __forceinline__ int tiles(int g) const
+    {
+        return g == 0 ? max(1, (see0 + min(rows, BM) - 1 + BN - 1) / BN) : T;
+    }
 };
 static_assert(NBAR * 8 + 16 + NSLOT * sizeof(Slot) <= 512, "barrier area");
 
@@ -96,6 +103,7 @@ struct ExpandedParams {
     int32_t *next;       // the next item that no CTA has taken
     int num_seqs, rows, keys, heads;
     int grid, max_items; // CTAs of the attention kernel; items at most
+    int small;           // no list: up to 32 sequences, few items (see expanded_kernel)
     float scale_log2;
 };
 
@@ -224,6 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_K0 + i), 1);
             mbar_init(bar(B_KF + i), 1);
             mbar_init(bar(B_VF + i), 1);
             mbar_init(bar(B_TURN + i), 1);
@@ -284,7 +293,50 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == W_PROD) {
         // ======================= items and loads
         griddep_wait();                  // the list, and everything before it on the stream
-        const int ns = p.next[1], items = p.before[ns];
+        // small batches (up to 32 sequences, 4 items a CTA) need no list: a lane holds a
+        // sequence, and the CTAs take every grid-th item.  That saves the list's
+        // kernel, 4 us of the 26 that eight short prompts over 32 heads took
+        int ns = 0, items = 0, my_before = INT_MAX;
+        int4 mine = make_int4(0, 0, 0, 0);
+        if (p.small) {
+            if (lane < p.num_seqs) {
+                const int a = p.cu_q[lane], b = p.cu_q[lane + 1], c = p.cu_k[lane], d = p.cu_k[lane + 1];
+                if (a != b) {
+                    if (a < 0 || b < a || b > p.rows || c < 0 || d < c || d > p.keys) {
+                        if (blockIdx.x == 0) flag(ST_BAD_LEN);
+                    } else {
+                        mine = make_int4(a, b - a, c, d - c);
+                    }
+                }
+            }
+            // longest first: lane r takes the sequence of rank r (those without rows last)
+            const int key = mine.y > 0 ? mine.w : -1;
+            int rank = 0, from = 0;
+            for (int i = 0; i < 32; ++i) {
+                const int other = __shfl_sync(0xffffffffu, key, i);
+                rank += other > key || (other == key && i < lane);
+            }
+            for (int i = 0; i < 32; ++i) {
+                const unsigned who = __ballot_sync(0xffffffffu, rank == i);
+                if (lane == i) from = __ffs(who) - 1;
+            }
+            mine = make_int4(__shfl_sync(0xffffffffu, mine.x, from), __shfl_sync(0xffffffffu, mine.y, from),
+                             __shfl_sync(0xffffffffu, mine.z, from), __shfl_sync(0xffffffffu, mine.w, from));
+            const int n = (mine.y + PAIR - 1) / PAIR * p.heads;      // (offsets are within max_items: checked below)
+            long long v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            const long long all = __shfl_sync(0xffffffffu, v, 31);
+            if (all > p.max_items && lane == 0 && blockIdx.x == 0) flag(ST_BAD_LEN);
+            items = (int)min(all, (long long)p.max_items);
+            my_before = (int)min(v - n, (long long)p.max_items);
+        } else {
+            ns = p.next[1];
+            items = p.before[ns];
+        }
         int t = 0;                       // key tiles
         int idx = blockIdx.x;
         bool ok = true;
@@ -292,22 +344,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int sl = k % NSLOT;
             if (k >= NSLOT && !wait_bar(bar(B_IEMPTY + sl), (k / NSLOT - 1) & 1, abort_flag)) break;
             if (k > 0) {
-                if (lane == 0) idx = atomicAdd(p.next, 1);
-                idx = __shfl_sync(0xffffffffu, idx, 0);
+                if (p.small) {
+                    idx += gridDim.x;
+                } else {
+                    if (lane == 0) idx = atomicAdd(p.next, 1);
+                    idx = __shfl_sync(0xffffffffu, idx, 0);
+                }
             }
             it.valid = idx < items;
             if (it.valid) {
                 // its sequence: the last one with before <= idx, 32 probes at a time
                 int lo = 0, len = ns;
-                while (len > 1) {
+                while (!p.small && len > 1) {
                     const int step = (len + 31) / 32, x = lo + lane * step;
                     const bool le = lane * step < len && p.before[x] <= idx;
                     const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));   // (lane 0 always is)
                     lo += last * step;
                     len = min(step, len - last * step);
                 }
-                const int4 q = p.seqs[lo];
-                const int units = (q.y + PAIR - 1) / PAIR, r = idx - p.before[lo];
+                int4 q;
+                int r;
+                if (p.small) {
+                    lo = 31 - __clz(__ballot_sync(0xffffffffu, my_before <= idx && mine.y > 0));   // (lane 0 always is)
+                    q = make_int4(__shfl_sync(0xffffffffu, mine.x, lo), __shfl_sync(0xffffffffu, mine.y, lo),
+                                  __shfl_sync(0xffffffffu, mine.z, lo), __shfl_sync(0xffffffffu, mine.w, lo));
+                    r = idx - __shfl_sync(0xffffffffu, my_before, lo);
+                } else {
+                    q = p.seqs[lo];
+                    r = idx - p.before[lo];
+                }
+                const int units = (q.y + PAIR - 1) / PAIR;
                 const int g0 = r / (units * HGROUP) * HGROUP, gn = min(HGROUP, p.heads - g0);
                 const int r2 = r - g0 * units, unit = units - 1 - r2 / gn;
                 it.head = g0 + r2 % gn;
@@ -351,15 +417,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (i == 2) tma_load_2d(dst, &rmap, 0, y, b);
                     else tma_load_2d(dst, &kvmap, it.head * 2 * D + (i < 2 ? i : i - 1) * 64, y, b);
                 };
-                const uint32_t kb = bar(B_KF + (t & 1)), vb = bar(B_VF + (t & 1));
+                const uint32_t k0 = bar(B_K0 + (t & 1)), kb = bar(B_KF + (t & 1)), vb = bar(B_VF + (t & 1));
                 // (chunk 0: the keys of tile t - 2 were waited for with the values of t - 1)
                 if (lane == 0) {
                     fence_proxy_async_smem();
-                    mbar_arrive_expect_tx(kb, 3 * CHUNK_BYTES);
-                    load(0, kb);
+                    mbar_arrive_expect_tx(k0, CHUNK_BYTES);
+                    load(0, k0);
                 }
                 if (t >= 2 && !wait_bar(bar(B_VE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag)) ok = false;
                 if (lane == 0 && ok) {
+                    mbar_arrive_expect_tx(kb, 2 * CHUNK_BYTES);
                     load(1, kb);
                     load(2, kb);
                 }
@@ -393,6 +460,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (*abort_flag) {               // loads in flight land before the CTA exits
             // (bounded: a tile whose chunks were not all asked for never completes)
             for (int x = max(0, t - 1); x <= t; ++x) {
+                (void)mbar_wait_bounded(bar(B_K0 + (x & 1)), (x >> 1) & 1);
                 (void)mbar_wait_bounded(bar(B_KF + (x & 1)), (x >> 1) & 1);
                 (void)mbar_wait_bounded(bar(B_VF + (x & 1)), (x >> 1) & 1);
             }
@@ -422,19 +490,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tpar ^= 1u << (k & 1);
                 return zeroed;
             };
+            // a tile that this query tile has no use for is released as it lands
+            auto pass_by = [&](bool last) -> bool {
+                if (!wait_bar(bar(B_K0 + (t & 1)), (t >> 1) & 1, abort_flag) || !wait_bar(bar(B_KF + (t & 1)), (t >> 1) & 1, abort_flag))
+                    return false;
+                if (lane == 0) mbar_arrive(bar(B_KE + (t & 1)));
+                if (!wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag) || (tail && last && !wait_tail())) return false;
+                if (lane == 0) mbar_arrive(bar(B_VE + (t & 1)));
+                return true;
+            };
             if (g == 1 && !both) {
-                // no second query tile: every tile is released as it lands
                 ok = wait_bar(bar(B_Q), k & 1, abort_flag);
                 if (lane == 0) mbar_arrive(bar(B_QFREE));
-                for (int j = 0; ok && j < it.T; ++j, ++t) {
-                    ok = wait_bar(bar(B_KF + (t & 1)), (t >> 1) & 1, abort_flag);
-                    if (ok && lane == 0) mbar_arrive(bar(B_KE + (t & 1)));
-                    ok = ok && wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
-                    if (ok && tail && j == it.T - 1) ok = wait_tail();
-                    if (ok && lane == 0) mbar_arrive(bar(B_VE + (t & 1)));
-                }
+                for (int j = 0; ok && j < it.T; ++j, ++t) ok = pass_by(j + 1 == it.T);
                 continue;
             }
+            const int T = it.tiles(g);
             // the first turn of all is query tile 0's
             auto take_turn = [&]() -> bool {
                 if (!both) return true;
@@ -442,32 +513,42 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (g == 0) return x == 0 || wait_bar(bar(B_TURN), (x - 1) & 1, abort_flag);
                 return wait_bar(bar(B_TURN + 1), x & 1, abort_flag);
             };
-            // S = Q K^T of key tile x (called by one lane)
-            auto issue_s = [&](int x, bool last) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
+            // S = Q K^T of key tile x.  Its first chunk is waited for, and multiplied,
+            // before the others: those two take the slots of the values before, which
+            // the other issuer's products have only just released
+            auto issue_s = [&](int x, bool last) -> bool {
+                auto products = [&](int i) {
                     const uint64_t kd = kvdesc + (uint64_t)(chunk(x, i) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_f16(tS, qdesc + (uint64_t)((i * CHUNK_BYTES + kk * 32) >> 4), kd + (uint64_t)((kk * 32) >> 4),
                                  IDESC_S, i + kk > 0);
-                    // (the turn takes about as long to pass as the last four products)
-                    if (i == 1 && both) mbar_arrive(bar(B_TURN + (g ^ 1)));
+                };
+                if (!wait_bar(bar(B_K0 + (x & 1)), (x >> 1) & 1, abort_flag)) return false;
+                if (elect_one()) {
+                    tc_fence_after();
+                    products(0);
                 }
-                umma_commit(bar(B_S + g));
-                umma_commit(bar(B_KE + (x & 1)));
-                if (last) umma_commit(bar(B_QFREE));
+                __syncwarp();
+                if (!wait_bar(bar(B_KF + (x & 1)), (x >> 1) & 1, abort_flag)) return false;
+                if (elect_one()) {
+                    tc_fence_after();
+                    products(1);
+                    // (the turn takes about as long to pass as the last four products)
+                    if (both) mbar_arrive(bar(B_TURN + (g ^ 1)));
+                    products(2);
+                    umma_commit(bar(B_S + g));
+                    umma_commit(bar(B_KE + (x & 1)));
+                    if (last) umma_commit(bar(B_QFREE));
+                }
+                __syncwarp();
+                return true;
             };
-            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && wait_bar(bar(B_KF + (t & 1)), (t >> 1) & 1, abort_flag) && take_turn();
-            if (ok && elect_one()) {
-                tc_fence_after();
-                issue_s(t, it.T == 1);
-            }
-            __syncwarp();
-            for (int j = 0; ok && j < it.T; ++j, ++t, ++n) {
-                const bool more = j + 1 < it.T;
+            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && take_turn() && issue_s(t, T == 1);
+            for (int j = 0; ok && j < T; ++j, ++t, ++n) {
+                const bool more = j + 1 < T;
                 ok = wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
-                if (ok && tail && !more) ok = wait_tail();
+                if (ok && tail && j + 1 == it.T) ok = wait_tail();
                 if (ok && j == 0 && done > 0) ok = wait_bar(bar(B_OFREE + g), (done - 1) & 1, abort_flag);
                 ok = ok && wait_bar(bar(B_P + g), n & 1, abort_flag) && take_turn();
                 if (ok && elect_one()) {
@@ -486,15 +567,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 __syncwarp();
-                // (in issue order: the products above read P from the columns that S
-                // overwrites.  The keys are waited for only now: two of their chunks take
-                // the slots of the values before, so they arrive while PV runs)
-                if (ok && more) ok = wait_bar(bar(B_KF + ((t + 1) & 1)), ((t + 1) >> 1) & 1, abort_flag);
-                if (ok && more && elect_one()) {
-                    tc_fence_after();
-                    issue_s(t + 1, j + 2 == it.T);
-                }
-                __syncwarp();
+                // (in issue order: the products above read P from the columns that S overwrites)
+                if (ok && more) ok = issue_s(t + 1, j + 2 == T);
+            }
+            for (int j = T; ok && j < it.T; ++j, ++t) {
+                ok = take_turn();
+                if (ok && lane == 0) mbar_arrive(bar(B_TURN + (g ^ 1)));
+                ok = ok && pass_by(j + 1 == it.T);
             }
             ++done;
         }
@@ -516,7 +595,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             // keys that this row sees (rows past the tile's last take the last one's)
             const int see = it.see0 + g * BM + min(r, rows - 1), see_min = it.see0 + g * BM;
             float m_ref = -INFINITY, l = 0.f;
-            for (int j = 0; j < it.T; ++j, ++n) {
+            const int T = it.tiles(g);
+            for (int j = 0; j < T; ++j, ++n) {
                 if (!wait_bar(bar(B_S + g), n & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const int t0 = j * BN;
@@ -712,7 +792,8 @@ kv_status latent_prefill_attention(void *out, const void *q, const void *kv, con
     const int grid = (int)std::min<int64_t>(items, 152);
     p.grid = grid;
     p.max_items = (int)items;
-    if (pkv_host::launch_ex(expanded_plan_kernel, dim3(1), dim3(1024), 0, st, true, p) != cudaSuccess ||
+    p.small = num_seqs <= 32 && items <= 4 * 152;
+    if ((!p.small && pkv_host::launch_ex(expanded_plan_kernel, dim3(1), dim3(1024), 0, st, true, p) != cudaSuccess) ||
         pkv_host::launch_ex(expanded_kernel, dim3(grid), dim3(THREADS), SMEM_BYTES, st, true, qmap, kvmap, rmap, p) != cudaSuccess)
         return KV_ERR_CUDA;
     return KV_OK;
