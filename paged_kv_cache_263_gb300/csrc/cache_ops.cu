@@ -142,6 +142,7 @@ namespace pkv_prefill { uint32_t take_status(); }
 namespace pkv_swap { uint32_t take_status(); }
 namespace pkv_step { uint32_t take_status(); }
 namespace pkv_latent { uint32_t take_status(); }
+namespace pkv_latent_small { uint32_t take_status(); }
 namespace pkv_latent_prefill { uint32_t take_status(); }
 
 static uint32_t take_status_cache()
@@ -230,7 +231,7 @@ kv_status kv_last_device_status(void *stream)
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KV_ERR_CUDA;
     uint32_t f = take_status_cache() | pkv_decode::take_status() | pkv_prefill::take_status() |
                  pkv_swap::take_status() | pkv_step::take_status() | pkv_latent::take_status() |
-                 pkv_latent_prefill::take_status();
+                 pkv_latent_small::take_status() | pkv_latent_prefill::take_status();
     g_last_flags.store(f, std::memory_order_relaxed);
     return f ? KV_ERR_DEVICE_BOUNDS : KV_OK;
 }

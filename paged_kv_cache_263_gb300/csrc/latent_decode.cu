@@ -48,21 +48,20 @@
 // balance without a plan on the host, and one long context is split over all
 // SMs.  A unit that a cut falls into leaves fp32 partial sums in the workspace
 // (at most two a cluster), which latent_merge_kernel joins in cluster order.
-#include "common.cuh"
+#include "latent_work.cuh"
 #include "trace.h"
 
 #include <algorithm>
 #include <cmath>
 
+namespace pkv_latent_small {
+kv_status launch(const void *params, const void *q, const void *cache, cudaStream_t st);
+}
+
 namespace {
-
-__device__ uint32_t g_status;
-
-using namespace pkv;
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
-constexpr int TK = 64;                            // keys per tile
 constexpr int HALF = LAT / 2, RHALF = ROPE / 2;   // a CTA's latent and rotary dims
 constexpr int NCL = 76;                           // clusters: a pair of CTAs on each pair of the 152 SMs
 constexpr int MIN_TILES = 2;                      // tiles a cluster takes at least, if there are as many
@@ -115,45 +114,6 @@ constexpr uint32_t idesc(int n, bool b_mn_major)
 constexpr uint32_t IDESC_S = idesc(TK, false);
 constexpr uint32_t IDESC_PV = idesc(HALF, true);
 
-struct LatentParams {
-    uint16_t *out;
-    const uint16_t *q;
-    const int32_t *cu, *lens, *tables;
-    int4 *desc;       // [NCL] the unit to merge whose first tiles cluster k holds: 1 (0: none), partials, rows, -
-    int64_t *desc2;   // [NCL] the unit's first (row, head)
-    float *part_o;    // [2 NCL][slot_rows][512]
-    float *part_ml;   // [2 NCL][slot_rows][2]
-    int slot_rows;    // rows of a unit, at most
-    int num_seqs, rows, heads, tpt, max_blocks, num_blocks;
-    float scale_log2;
-};
-
-__device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
-
-// bounded wait that also gives up once another warp of the CTA has
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
-{
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const unsigned long long t0 = globaltimer();
-        for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(bar, parity)) {
-                ok = true;
-                break;
-            }
-            if ((it & 63u) == 0) {
-                if (*abort_flag) break;
-                if (globaltimer() - t0 > WAIT_LIMIT_NS) {
-                    *abort_flag = 1;
-                    flag(ST_TIMEOUT);
-                    break;
-                }
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);   // the roles run warp-collective instructions: a warp leaves as a whole
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -199,90 +159,6 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_byte
     d |= (uint64_t)4 << 61;
     return d;
 }
-
-// ------------------------------------------------------------------- the work
-// A sequence as the kernel sees it: n = 0 if it has no rows or was refused.
-struct Seq {
-    int a, n, L;
-};
-__device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagging)
-{
-    Seq q;
-    q.a = p.cu ? __ldg(p.cu + s) : s;
-    const int b = p.cu ? __ldg(p.cu + s + 1) : s + 1;
-    q.n = b - q.a;
-    q.L = __ldg(p.lens + s);
-    if (q.n == 0) return q;
-    if (q.a < 0 || b < q.a || b > p.rows || q.L < 0 || q.L > p.max_blocks * BS || (q.L != 0 && q.L < q.n)) {
-        if (flagging) flag(ST_BAD_LEN);
-        q.n = 0;
-    }
-    return q;
-}
-__device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK - 1) / TK); }
-// a / b for a >= 0, b > 0 (a 64-bit division costs several hundred cycles)
-__device__ __forceinline__ long long quotient(long long a, long long b)
-{
-    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-// tiles of all its units: every unit is charged the whole context (the causal
-// end of a prompt chunk's earlier units leaves the rest of their charge empty)
-__device__ __forceinline__ long long seq_cost(const LatentParams &p, const Seq &q)
-{
-    if (q.n <= 0) return 0;
-    return (long long)(q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
-}
-
-struct Item {
-    Seq q;
-    int s, t0, toks;     // the unit's first token within the sequence, and its tokens
-    int j0, j1, kt;      // its tiles in this cluster's range, and all its tiles
-    int left;            // tiles of the range from its first one on
-};
-// Walks a cluster's range; every role keeps one and sees the same items.  (No
-// division and no memory but shared: it runs between two items of every role.)
-struct Walk {
-    int s, u, j, left;   // next: sequence, unit, tile; tiles left
-};
-__device__ __forceinline__ bool next_item(const LatentParams &p, const int *list, int s_first, Walk &w, Item &it)
-{
-    while (w.left > 0 && w.s < p.num_seqs) {
-        const int i = w.s - s_first;
-        Seq q;
-        if (i < LIST) q = {list[3 * i], list[3 * i + 1], list[3 * i + 2]};
-        else q = read_seq(p, w.s, false);
-        const int t0 = w.u * p.tpt;
-        if (t0 >= q.n) {             // (a sequence without rows, too)
-            ++w.s;
-            w.u = w.j = 0;
-            continue;
-        }
-        it.q = q;
-        it.s = w.s;
-        it.t0 = t0;
-        it.toks = min(p.tpt, q.n - t0);
-        it.j0 = w.j;
-        it.left = w.left;
-        const int jend = min(seq_tiles(q), w.j + w.left);
-        w.left -= jend - w.j;
-        ++w.u;
-        w.j = 0;
-        it.kt = max(1, (q.L - q.n + t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
-        it.j1 = min(jend, it.kt);
-        if (it.j0 < it.kt) return true;
-    }
-    return false;
-}
-
-// The range of cluster k of nc: W tiles in nc runs, the first W % nc one longer.
-struct Cut {
-    long long each, extra;
-    __device__ __forceinline__ long long begin(int k) const { return k * each + min((long long)k, extra); }
-    __device__ __forceinline__ int owner(long long pos) const
-    {
-        return (int)(pos < extra * (each + 1) ? quotient(pos, each + 1) : extra + quotient(pos - extra * (each + 1), each));
-    }
-};
 
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     latent_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
@@ -340,66 +216,13 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    tc_fence_before();
     __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
-    // ---- the cluster's range: prefix sums of the sequences' costs, a run of
-    // consecutive sequences a thread
-    const int per = (p.num_seqs + THREADS - 1) / THREADS;
-    const int sa = min(p.num_seqs, (int)threadIdx.x * per), sb = min(p.num_seqs, sa + per);
-    long long mine = 0;
-    for (int s = sa; s < sb; ++s) mine += seq_cost(p, read_seq(p, s, blockIdx.x == 0));
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 31) scan[warp] = incl;
-    tc_fence_before();
-    __syncthreads();
+    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
+    Walk walk = range.walk;
     tc_fence_after();
-    long long before = 0, W = 0;
-    for (int i = 0; i < THREADS / 32; ++i) {
-        const long long t = scan[i];
-        if (i < warp) before += t;
-        W += t;
-    }
-    // clusters with work, and this one's range
-    const int nc = (int)max(1ll, min((long long)NCL, W / MIN_TILES));
-    Cut cut;
-    cut.each = quotient(W, nc);
-    cut.extra = W - cut.each * nc;
-    const long long w0 = k < nc ? cut.begin(k) : W, w1 = k < nc ? cut.begin(k + 1) : W;
-    {
-        long long b = before + incl - mine;
-        if (w0 < w1 && b <= w0 && w0 < b + mine) {
-            int s = sa;
-            for (; s < sb; ++s) {
-                const long long cost = seq_cost(p, read_seq(p, s, false));
-                if (w0 < b + cost) break;
-                b += cost;
-            }
-            const int KT = seq_tiles(read_seq(p, s, false));
-            const long long u = quotient(w0 - b, KT);
-            s_start[0] = s;
-            s_start[1] = (int)u;
-            s_start[2] = (int)(w0 - b - u * KT);
-            s_work[0] = cut.each;
-            s_work[1] = cut.extra;
-        }
-    }
-    __syncthreads();
-    const int s_first = s_start[0];
-    for (int i = threadIdx.x; i < LIST; i += THREADS) {
-        const Seq q = s_first + i < p.num_seqs ? read_seq(p, s_first + i, false) : Seq{0, 0, 0};
-        list[3 * i] = q.a;
-        list[3 * i + 1] = q.n;
-        list[3 * i + 2] = q.L;
-    }
-    const int range = (int)(w1 - w0);
-    Walk walk = {s_first, s_start[1], s_start[2], range};
-    __syncthreads();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist
     const uint32_t tmem = *tmem_slot;
     const uint32_t tQ = tmem, tP = tmem + QT / 2, tO = tmem + 256;
@@ -414,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         const int blk = is_r ? lane - 16 : lane >> 2, chunk = lane & 3;
         int u = 0;
         bool ok = true;
-        while (ok && next_item(p, list, s_first, walk, it)) {
+        while (ok && next_item(p, range, walk, it)) {
             const int32_t *bt = p.tables + (size_t)it.s * p.max_blocks;
             const int nblk = (it.q.L + BS - 1) / BS;
             // the item's queries, into L2 (this warp runs up to four tiles ahead; the
@@ -471,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             const uint64_t kdesc0 = sdesc_sw128(sbase, 16, 1024);
             const uint64_t rdesc0 = sdesc_sw64(sbase + ROPE_OFF, 512);
             const uint64_t qdesc = sdesc_sw128(sbase + SQ, 16, 1024), qrdesc = sdesc_sw64(sbase + SQR, 512);
-            for (; ok && next_item(p, list, s_first, walk, it); ++items) {
+            for (; ok && next_item(p, range, walk, it); ++items) {
                 ok = wait_bar(bar(B_Q), items & 1, abort_flag);
                 for (int j = it.j0; ok && j < it.j1; ++j, ++x) {
                     const int st = x % STAGES, b = x & 1;
@@ -510,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             }
         } else {
             const uint64_t vdesc0 = sdesc_sw128(sbase, CHUNK_BYTES, 1024);
-            for (; ok && next_item(p, list, s_first, walk, it); ++items) {
+            for (; ok && next_item(p, range, walk, it); ++items) {
                 for (int j = it.j0; j < it.j1; ++j, ++x) {
                     const int st = x % STAGES;
                     // the item before: its O has been read
@@ -551,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         auto load_queries = [&]() {                       // of the item that follows
             Walk ahead = walk;
             Item q;
-            if (!next_item(p, list, s_first, ahead, q)) return;
+            if (!next_item(p, range, ahead, q)) return;
             const int rows = q.toks * p.heads;
             const uint16_t *src = p.q + ((size_t)(q.q.a + q.t0) * p.heads + w * 32) * LKD;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -606,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         };
         bool ok = true;
         if (grp == 1) load_queries();
-        while (ok && next_item(p, list, s_first, walk, it)) {
+        while (ok && next_item(p, range, walk, it)) {
             const int rows = it.toks * p.heads;
             const bool active = w * 32 < rows;
             const int tok = min(r, rows - 1) / p.heads;
@@ -817,12 +640,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             tc_fence_before();
             mbar_arrive(bar(B_OFREE));
             if (!whole && it.j0 == 0 && threadIdx.x == 0 && c == 0) {
-                // this cluster holds the unit's first tiles: what there is to merge, up to
-                // the cluster that holds its last tile
-                const Cut all = {s_work[0], s_work[1]};
-                const int kl = max(k, min(nc - 1, all.owner(all.begin(k) + (range - it.left) + it.kt - 1)));
-                p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
-                p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
+                list_merge(p, range, it, k, rows);
                 merges = true;
             }
             ++items;
@@ -842,13 +660,13 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 constexpr int MERGE_CTAS = 8 * 152, MERGE_PRE = 8;
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
 {
-    __shared__ int2 todo[NCL + 1];         // (partials, rows before) of cluster k's unit
+    __shared__ int2 todo[MAX_WORKERS + 1]; // (partials, rows before) of worker k's unit
     const int lane = threadIdx.x & 31;
     griddep_wait();
     if (threadIdx.x < 32) {
         int run = 0;
-        for (int b = 0; b < NCL; b += 32) {
-            const int4 d = b + lane < NCL ? p.desc[b + lane] : make_int4(0, 0, 0, 0);
+        for (int b = 0; b < p.workers; b += 32) {
+            const int4 d = b + lane < p.workers ? p.desc[b + lane] : make_int4(0, 0, 0, 0);
             const int n = d.x ? d.z : 0;
             int v = n;
 #pragma unroll
@@ -856,15 +674,15 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
                 const int t = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += t;
             }
-            if (b + lane < NCL) todo[b + lane] = make_int2(d.y, run + v - n);
+            if (b + lane < p.workers) todo[b + lane] = make_int2(d.y, run + v - n);
             run += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) todo[NCL] = make_int2(0, run);
+        if (lane == 0) todo[p.workers] = make_int2(0, run);
     }
     __syncthreads();
-    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < todo[NCL].y * 4; t += MERGE_CTAS * 8) {
+    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < todo[p.workers].y * 4; t += MERGE_CTAS * 8) {
         const int g = t >> 2, q4 = t & 3;
-        int k = 0, hi = NCL;                // the last k with rows before it <= g
+        int k = 0, hi = p.workers;          // the last k with rows before it <= g
         while (hi - k > 1) {
             const int mid = (k + hi) >> 1;
             if (todo[mid].y <= g) k = mid;
@@ -872,7 +690,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
         }
         const int row = g - todo[k].y, ns = todo[k].x;
         const int64_t row0 = p.desc2[k];
-        // partial i: the first is in its cluster's second slot, the others in their cluster's first
+        // partial i: the first is in its worker's second slot, the others in their worker's first
         auto slot = [&](int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows + row; };
         auto part = [&](int i) -> float4 {
             return i < ns ? reinterpret_cast<const float4 *>(p.part_o + slot(i) * LAT + q4 * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -922,24 +740,29 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
     }
 }
 
-int unit_tokens(int heads) { return 128 / heads; }
-
-// workspace: the merge list, then the partial maxima and sums, then the partial outputs
-struct Layout {
-    size_t desc2, ml, o, total;
-    int slot_rows;
+// How a call's work is laid out.  Units of up to 64 rows take a CTA each
+// (latent_small.cu), if that is all that an average sequence has; else a pair of
+// CTAs takes 128 (a longer chunk's keys are then read half as often).
+struct Plan {
+    bool small;
+    int tpt, slot_rows, workers;
+    size_t desc2, ml, o, total;    // workspace: merge list, partial sums, partial outputs
 };
-Layout layout(int heads)
+Plan plan(bool small, int heads)
 {
-    Layout y;
-    y.slot_rows = unit_tokens(heads) * heads;
-    y.desc2 = NCL * sizeof(int4);
-    y.ml = 2048;
-    y.o = y.ml + (((size_t)2 * NCL * y.slot_rows * 8 + 255) & ~(size_t)255);
-    y.total = y.o + (size_t)2 * NCL * y.slot_rows * LAT * 4;
+    Plan y;
+    y.small = small;
+    y.workers = small ? MAX_WORKERS : NCL;
+    y.tpt = (small ? 64 : 128) / heads;
+    y.slot_rows = y.tpt * heads;
+    y.desc2 = y.workers * sizeof(int4);
+    y.ml = 4096;
+    y.o = y.ml + (((size_t)2 * y.workers * y.slot_rows * 8 + 255) & ~(size_t)255);
+    y.total = y.o + (size_t)2 * y.workers * y.slot_rows * LAT * 4;
     return y;
 }
-static_assert(NCL * (sizeof(int4) + 8) <= 2048, "merge list");
+static_assert(MAX_WORKERS * (sizeof(int4) + 8) <= 4096, "merge list");
+static_assert(MAX_WORKERS == 2 * NCL, "64 / heads x 2 <= 128 / heads: the pairs' workspace is never the smaller");
 
 }  // namespace
 
@@ -961,7 +784,7 @@ size_t paged_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q_t
     if (num_seqs < 1 || total_q_tokens < 1 || num_heads < 1 || num_heads > PAGEDKV_LATENT_MAX_HEADS ||
         max_blocks_per_seq < 1)
         return 0;
-    return layout(num_heads).total;
+    return plan(false, num_heads).total;
 }
 
 kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
@@ -988,7 +811,7 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     const size_t need =
         paged_latent_attention_workspace_size(num_seqs, total_q_tokens, num_heads, max_blocks_per_seq);
     if (need && (!workspace || workspace_bytes < need || !pkv_host::aligned(workspace, 256))) return KV_ERR_INVALID;
-    const Layout y = layout(num_heads);
+    const Plan y = plan((int64_t)total_q_tokens * num_heads <= 64ll * num_seqs && num_heads <= 64, num_heads);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     LatentParams p;
     p.out = static_cast<uint16_t *>(out);
@@ -1001,26 +824,32 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     p.part_ml = reinterpret_cast<float *>(ws + y.ml);
     p.part_o = reinterpret_cast<float *>(ws + y.o);
     p.slot_rows = y.slot_rows;
+    p.workers = y.workers;
     p.num_seqs = num_seqs;
     p.rows = total_q_tokens;
     p.heads = num_heads;
-    p.tpt = unit_tokens(num_heads);
+    p.tpt = y.tpt;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * LOG2E;
-    // the cache as rows of 576: boxes of 16 rows (a block) x 64 latent or 32 rotary dims
-    CUtensorMap lmap, rmap;
-    const uint64_t rows = (uint64_t)num_blocks * BS;
-    if (!pkv_host::encode_tmap_2d(&lmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, 64, BS,
-                                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !pkv_host::encode_tmap_2d(&rmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, RHALF, BS,
-                                  CU_TENSOR_MAP_SWIZZLE_64B))
-        return KV_ERR_CUDA;
-    if (pkv_host::ensure_dynamic_smem<latent_kernel>(SMEM_BYTES) != cudaSuccess) return KV_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (pkv_host::launch_ex(latent_kernel, dim3(2 * NCL), dim3(THREADS), SMEM_BYTES, st, true, lmap, rmap, p) != cudaSuccess ||
-        pkv_host::launch_ex(latent_merge_kernel, dim3(MERGE_CTAS), dim3(256), 0, st, true, p) != cudaSuccess)
-        return KV_ERR_CUDA;
+    if (y.small) {
+        const kv_status launched = pkv_latent_small::launch(&p, q, cache, st);
+        if (launched != KV_OK) return launched;
+    } else {
+        // the cache as rows of 576: boxes of 16 rows (a block) x 64 latent or 32 rotary dims
+        CUtensorMap lmap, rmap;
+        const uint64_t rows = (uint64_t)num_blocks * BS;
+        if (!pkv_host::encode_tmap_2d(&lmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, 64, BS,
+                                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !pkv_host::encode_tmap_2d(&rmap, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, LKD, rows, LKD * 2, RHALF, BS,
+                                      CU_TENSOR_MAP_SWIZZLE_64B))
+            return KV_ERR_CUDA;
+        if (pkv_host::ensure_dynamic_smem<latent_kernel>(SMEM_BYTES) != cudaSuccess) return KV_ERR_CUDA;
+        if (pkv_host::launch_ex(latent_kernel, dim3(2 * NCL), dim3(THREADS), SMEM_BYTES, st, true, lmap, rmap, p) != cudaSuccess)
+            return KV_ERR_CUDA;
+    }
+    if (pkv_host::launch_ex(latent_merge_kernel, dim3(MERGE_CTAS), dim3(256), 0, st, true, p) != cudaSuccess) return KV_ERR_CUDA;
     return KV_OK;
 }
 

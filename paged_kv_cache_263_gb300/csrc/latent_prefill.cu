@@ -192,28 +192,27 @@ __global__ void __launch_bounds__(1024) expanded_plan_kernel(const ExpandedParam
     }
 }
 
-// bounded wait that also gives up once another warp of the CTA has
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+// bounded wait that also gives up once another warp of the CTA has.  The loop is a
+// call: a dozen copies of it in a role's loop would crowd the instruction cache
+__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const unsigned long long t0 = globaltimer();
-        for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(bar, parity)) {
-                ok = true;
-                break;
-            }
-            if ((it & 63u) == 0) {
-                if (*abort_flag) break;
-                if (globaltimer() - t0 > WAIT_LIMIT_NS) {
-                    *abort_flag = 1;
-                    flag(ST_TIMEOUT);
-                    break;
-                }
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+                *abort_flag = 1;
+                flag(ST_TIMEOUT);
+                return false;
             }
         }
     }
-    return __all_sync(0xffffffffu, ok);   // the roles run warp-collective instructions: a warp leaves as a whole
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    // (the roles run warp-collective instructions: a warp leaves as a whole)
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort_flag));
 }
 
 __global__ void __launch_bounds__(THREADS, 1)

@@ -1,0 +1,230 @@
+// latent_work.cuh -- what the two kernels of absorbed latent attention share: the
+// division of a batch's work, and their bounded waits.
+//
+// The key tiles of all (sequence, unit of query rows) pairs are laid end to end and
+// cut into equal ranges, one a worker (a CTA, or a pair of CTAs).  A unit that a cut
+// falls into leaves fp32 partial sums, at most two a worker: in slot 2k if worker k
+// does not hold its first tile, else in slot 2k + 1.
+#pragma once
+
+#include "common.cuh"
+
+namespace {
+
+__device__ uint32_t g_status;
+
+using namespace pkv;
+
+constexpr int TK = 64;                 // keys per tile
+constexpr int MAX_WORKERS = 152;
+
+struct LatentParams {
+    uint16_t *out;
+    const uint16_t *q;
+    const int32_t *cu, *lens, *tables;
+    int4 *desc;       // [workers] the unit to merge whose first tiles worker k holds: 1 (0: none), partials, rows, -
+    int64_t *desc2;   // [workers] the unit's first (row, head)
+    float *part_o;    // [2 workers][slot_rows][512]
+    float *part_ml;   // [2 workers][slot_rows][2]
+    int slot_rows;    // rows of a unit, at most
+    int workers;
+    int num_seqs, rows, heads, tpt, max_blocks, num_blocks;
+    float scale_log2;
+};
+
+__device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
+
+// bounded wait that also gives up once another warp of the CTA has
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) {
+                ok = true;
+                break;
+            }
+            if ((it & 63u) == 0) {
+                if (*abort_flag) break;
+                if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+                    *abort_flag = 1;
+                    flag(ST_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);   // the roles run warp-collective instructions: a warp leaves as a whole
+}
+
+// A sequence as the kernel sees it: n = 0 if it has no rows or was refused.
+struct Seq {
+    int a, n, L;
+};
+__device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagging)
+{
+    Seq q;
+    q.a = p.cu ? __ldg(p.cu + s) : s;
+    const int b = p.cu ? __ldg(p.cu + s + 1) : s + 1;
+    q.n = b - q.a;
+    q.L = __ldg(p.lens + s);
+    if (q.n == 0) return q;
+    if (q.a < 0 || b < q.a || b > p.rows || q.L < 0 || q.L > p.max_blocks * BS || (q.L != 0 && q.L < q.n)) {
+        if (flagging) flag(ST_BAD_LEN);
+        q.n = 0;
+    }
+    return q;
+}
+__device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK - 1) / TK); }
+// a / b for a >= 0, b > 0 (a 64-bit division costs several hundred cycles)
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// tiles of all its units: every unit is charged the whole context (the causal
+// end of a prompt chunk's earlier units leaves the rest of their charge empty)
+__device__ __forceinline__ long long seq_cost(const LatentParams &p, const Seq &q)
+{
+    if (q.n <= 0) return 0;
+    return (long long)(q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
+}
+
+struct Item {
+    Seq q;
+    int s, t0, toks;     // the unit's first token within the sequence, and its tokens
+    int j0, j1, kt;      // its tiles in this worker's range, and all its tiles
+    int left;            // tiles of the range from its first one on
+};
+// Walks a worker's range; every role keeps one and sees the same items.  (No
+// division and no memory but shared: it runs between two items of every role.)
+struct Walk {
+    int s, u, j, left;   // next: sequence, unit, tile; tiles left
+};
+// The range of worker k of nc: W tiles in nc runs, the first W % nc one longer.
+struct Cut {
+    long long each, extra;
+    __device__ __forceinline__ long long begin(int k) const { return k * each + min((long long)k, extra); }
+    __device__ __forceinline__ int owner(long long pos) const
+    {
+        return (int)(pos < extra * (each + 1) ? quotient(pos, each + 1) : extra + quotient(pos - extra * (each + 1), each));
+    }
+};
+
+// A worker's range: where it starts, and how it was cut.
+struct Range {
+    Walk walk;
+    int tiles, nc;           // its tiles; workers with work
+    int s_first, listed;     // its first sequence; sequences tabled in shared memory from there on
+    const int *list;
+    const long long *cut;    // shared memory: Cut's two numbers
+};
+__device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g, Walk &w, Item &it)
+{
+    while (w.left > 0 && w.s < p.num_seqs) {
+        const int i = w.s - g.s_first;
+        Seq q;
+        if (i < g.listed) q = {g.list[3 * i], g.list[3 * i + 1], g.list[3 * i + 2]};
+        else q = read_seq(p, w.s, false);
+        const int t0 = w.u * p.tpt;
+        if (t0 >= q.n) {             // (a sequence without rows, too)
+            ++w.s;
+            w.u = w.j = 0;
+            continue;
+        }
+        it.q = q;
+        it.s = w.s;
+        it.t0 = t0;
+        it.toks = min(p.tpt, q.n - t0);
+        it.j0 = w.j;
+        it.left = w.left;
+        const int jend = min(seq_tiles(q), w.j + w.left);
+        w.left -= jend - w.j;
+        ++w.u;
+        w.j = 0;
+        it.kt = max(1, (q.L - q.n + t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
+        it.j1 = min(jend, it.kt);
+        if (it.j0 < it.kt) return true;
+    }
+    return false;
+}
+
+// Finds worker k's range (all threads of the CTA; two barriers and one more at the
+// end): prefix sums of the sequences' costs, a run of consecutive sequences a
+// thread.  scan: THREADS / 32 numbers, start: 3, cut: 2, list: 3 x listed, all in
+// shared memory; start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
+template <int THREADS>
+__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int min_tiles, bool flagging,
+                                            long long *scan, int *start, long long *cut_sh, int *list, int listed)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.num_seqs + THREADS - 1) / THREADS;
+    const int sa = min(p.num_seqs, (int)threadIdx.x * per), sb = min(p.num_seqs, sa + per);
+    long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += seq_cost(p, read_seq(p, s, flagging));
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, W = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+        const long long t = scan[i];
+        if (i < warp) before += t;
+        W += t;
+    }
+    Range g;
+    g.nc = (int)max(1ll, min((long long)workers, W / min_tiles));
+    Cut cut;
+    cut.each = quotient(W, g.nc);
+    cut.extra = W - cut.each * g.nc;
+    const long long w0 = k < g.nc ? cut.begin(k) : W, w1 = k < g.nc ? cut.begin(k + 1) : W;
+    {
+        long long b = before + incl - mine;
+        if (w0 < w1 && b <= w0 && w0 < b + mine) {
+            int s = sa;
+            for (; s < sb; ++s) {
+                const long long cost = seq_cost(p, read_seq(p, s, false));
+                if (w0 < b + cost) break;
+                b += cost;
+            }
+            const int KT = seq_tiles(read_seq(p, s, false));
+            const long long u = quotient(w0 - b, KT);
+            start[0] = s;
+            start[1] = (int)u;
+            start[2] = (int)(w0 - b - u * KT);
+            cut_sh[0] = cut.each;
+            cut_sh[1] = cut.extra;
+        }
+    }
+    __syncthreads();
+    g.s_first = start[0];
+    for (int i = threadIdx.x; i < listed; i += THREADS) {
+        const Seq q = g.s_first + i < p.num_seqs ? read_seq(p, g.s_first + i, false) : Seq{0, 0, 0};
+        list[3 * i] = q.a;
+        list[3 * i + 1] = q.n;
+        list[3 * i + 2] = q.L;
+    }
+    g.tiles = (int)(w1 - w0);
+    g.walk = {g.s_first, start[1], start[2], g.tiles};
+    g.listed = listed;
+    g.list = list;
+    g.cut = cut_sh;
+    __syncthreads();
+    return g;
+}
+
+// What a worker that holds a unit's first tiles, but not all, writes into the merge
+// list: the partials go up to the worker that holds its last tile.
+__device__ __forceinline__ void list_merge(const LatentParams &p, const Range &g, const Item &it, int k, int rows)
+{
+    const Cut cut = {g.cut[0], g.cut[1]};
+    const int kl = max(k, min(g.nc - 1, cut.owner(cut.begin(k) + (g.tiles - it.left) + it.kt - 1)));
+    p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
+    p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
+}
+
+}  // namespace
