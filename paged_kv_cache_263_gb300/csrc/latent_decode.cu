@@ -657,86 +657,143 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 // with weights 2^(m_i - max m): a warp for each (row, 128 dims), the units' rows
 // laid end to end over all CTAs.  The first partial rows are requested before the
 // maxima are known, so a unit cut once costs one round trip to L2.
-constexpr int MERGE_CTAS = 8 * 152, MERGE_PRE = 8;
-__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p)
+constexpr int MERGE_CTAS = 4 * 152, MERGE_WARPS = 8, MERGE_WIDE = 16, MERGE_PRE = 4;
+
+__device__ __forceinline__ void merge_add(float4 &acc, float f, const float4 &v)
 {
-    __shared__ int2 todo[MAX_WORKERS + 1]; // (partials, rows before) of worker k's unit
-    const int lane = threadIdx.x & 31;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+}
+
+__global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const LatentParams p)
+{
+    __shared__ int before[MAX_WORKERS + 1];      // rows of the units before worker k's: narrow ones + (wide ones << 16)
+    __shared__ int parts[MAX_WORKERS];           // partials of worker k's unit
+    __shared__ float4 sums[MERGE_WARPS][32];
+    __shared__ float factor[MAX_WORKERS], red[2][MERGE_WARPS];
+    static_assert(MAX_WORKERS * 128 < 32768 && MAX_WORKERS <= 32 * MERGE_WARPS, "packed sums; a thread a partial");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_launch_dependents();
     griddep_wait();
-    if (threadIdx.x < 32) {
+    if (warp == 0) {
         int run = 0;
         for (int b = 0; b < p.workers; b += 32) {
             const int4 d = b + lane < p.workers ? p.desc[b + lane] : make_int4(0, 0, 0, 0);
-            const int n = d.x ? d.z : 0;
+            const int n = !d.x ? 0 : d.y > MERGE_WIDE ? d.z << 16 : d.z;
             int v = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += t;
             }
-            if (b + lane < p.workers) todo[b + lane] = make_int2(d.y, run + v - n);
+            if (b + lane < p.workers) {
+                parts[b + lane] = d.y;
+                before[b + lane] = run + v - n;
+            }
             run += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) todo[p.workers] = make_int2(0, run);
+        if (lane == 0) before[p.workers] = run;
     }
     __syncthreads();
-    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < todo[p.workers].y * 4; t += MERGE_CTAS * 8) {
-        const int g = t >> 2, q4 = t & 3;
-        int k = 0, hi = p.workers;          // the last k with rows before it <= g
+    // the worker with the g-th row of a kind: the last one with no more rows before its own
+    auto worker = [&](int g, int shift) -> int {
+        int k = 0, hi = p.workers;
         while (hi - k > 1) {
             const int mid = (k + hi) >> 1;
-            if (todo[mid].y <= g) k = mid;
+            if (((before[mid] >> shift) & 0xffff) <= g) k = mid;
             else hi = mid;
         }
-        const int row = g - todo[k].y, ns = todo[k].x;
-        const int64_t row0 = p.desc2[k];
-        // partial i: the first is in its worker's second slot, the others in their worker's first
-        auto slot = [&](int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows + row; };
+        return k;
+    };
+    // partial i of worker k's unit: the first is in its worker's second slot, the others in their worker's first
+    auto slot = [&](int k, int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows; };
+    auto store = [&](int64_t row, int q4, const float4 &a, float l) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<uint2 *>(p.out + row * LAT + q4 * 128)[lane] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    };
+    // up to 16 partials: a warp a quarter of a row
+    const int narrow = (before[p.workers] & 0xffff) * 4;
+    for (int t = blockIdx.x * MERGE_WARPS + warp; t < narrow; t += MERGE_CTAS * MERGE_WARPS) {
+        const int g = t >> 2, q4 = t & 3, k = worker(g, 0), row = g - (before[k] & 0xffff), ns = parts[k];
         auto part = [&](int i) -> float4 {
-            return i < ns ? reinterpret_cast<const float4 *>(p.part_o + slot(i) * LAT + q4 * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            return i < ns ? reinterpret_cast<const float4 *>(p.part_o + (slot(k, i) + row) * LAT + q4 * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        float4 pre[MERGE_PRE];
+        float4 v[MERGE_PRE];
 #pragma unroll
-        for (int j = 0; j < MERGE_PRE; ++j) pre[j] = part(j);
-        float2 e0 = make_float2(-INFINITY, 0.f);
-        if (lane < ns) e0 = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(lane));
-        float M = e0.x;
-        for (int i = lane + 32; i < ns; i += 32) M = fmaxf(M, p.part_ml[2 * slot(i)]);
+        for (int j = 0; j < MERGE_PRE; ++j) v[j] = part(j);
+        const float2 e = lane < ns ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * (slot(k, lane) + row)) : make_float2(-INFINITY, 0.f);
+        const int64_t row0 = p.desc2[k];
+        float M = e.x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        M = __shfl_sync(0xffffffffu, M, 0);
+        const float f = M == -INFINITY ? 0.f : ex2(e.x - M);
+        float l = f * e.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        l = __shfl_sync(0xffffffffu, l, 0);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        if (M != -INFINITY) {
-            for (int i0 = 0; i0 < ns; i0 += 32) {
-                float f = 0.f;
-                if (i0 + lane < ns) {
-                    const float2 e = i0 == 0 ? e0 : *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(i0 + lane));
-                    f = ex2(e.x - M);
-                    l += f * e.y;
-                }
-                const int n = min(32, ns - i0);
-                for (int j0 = 0; j0 < n; j0 += MERGE_PRE) {
-                    float4 v[MERGE_PRE];
+        for (int j0 = 0; j0 < ns; j0 += MERGE_PRE) {
+            if (j0 > 0) {
 #pragma unroll
-                    for (int j = 0; j < MERGE_PRE; ++j) v[j] = i0 + j0 == 0 ? pre[j] : part(i0 + j0 + j);
+                for (int j = 0; j < MERGE_PRE; ++j) v[j] = part(j0 + j);
+            }
 #pragma unroll
-                    for (int j = 0; j < MERGE_PRE; ++j) {
-                        const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
-                        if (j0 + j < n) {
-                            acc.x += fj * v[j].x;
-                            acc.y += fj * v[j].y;
-                            acc.z += fj * v[j].z;
-                            acc.w += fj * v[j].w;
-                        }
-                    }
-                }
+            for (int j = 0; j < MERGE_PRE; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
+                if (j0 + j < ns && M != -INFINITY) merge_add(acc, fj, v[j]);
             }
         }
+        store(row0 + row, q4, acc, l);
+    }
+    // more: the CTA takes a quarter of a row, its warps every eighth partial
+    const int wide = (before[p.workers] >> 16) * 4;
+    for (int t = blockIdx.x; t < wide; t += MERGE_CTAS) {
+        const int g = t >> 2, q4 = t & 3, k = worker(g, 16), row = g - (before[k] >> 16), ns = parts[k];
+        auto part = [&](int i) -> float4 {
+            return i < ns ? reinterpret_cast<const float4 *>(p.part_o + (slot(k, i) + row) * LAT + q4 * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 v[2 * MERGE_PRE];
+#pragma unroll
+        for (int j = 0; j < 2 * MERGE_PRE; ++j) v[j] = part(warp + j * MERGE_WARPS);
+        float2 e = make_float2(-INFINITY, 0.f);
+        if (threadIdx.x < ns) e = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (slot(k, threadIdx.x) + row));
+        float M = e.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (lane == 0) red[0][warp] = M;
+        __syncthreads();
+        for (int i = 0; i < MERGE_WARPS; ++i) M = fmaxf(M, red[0][i]);
+        const float f = M == -INFINITY ? 0.f : ex2(e.x - M);
+        if (threadIdx.x < ns) factor[threadIdx.x] = f;
+        float l = f * e.y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        reinterpret_cast<uint2 *>(p.out + (row0 + row) * LAT + q4 * 128)[lane] =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (lane == 0) red[1][warp] = l;
+        __syncthreads();
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; warp + j0 * MERGE_WARPS < ns; j0 += 2 * MERGE_PRE) {
+            if (j0 > 0) {
+#pragma unroll
+                for (int j = 0; j < 2 * MERGE_PRE; ++j) v[j] = part(warp + (j0 + j) * MERGE_WARPS);
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * MERGE_PRE; ++j) {
+                const int i = warp + (j0 + j) * MERGE_WARPS;
+                if (i < ns && M != -INFINITY) merge_add(acc, factor[i], v[j]);
+            }
+        }
+        sums[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0) {
+            l = 0.f;
+            for (int i = 0; i < MERGE_WARPS; ++i) l += red[1][i];
+            for (int i = 1; i < MERGE_WARPS; ++i) merge_add(acc, 1.f, sums[i][lane]);
+            store(p.desc2[k] + row, q4, acc, l);
+        }
+        __syncthreads();      // the shared sums may be the next row's
     }
 }
 
