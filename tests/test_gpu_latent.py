@@ -247,6 +247,37 @@ def test_absorbed_growing_scores():
     check(w.run(), *w.expected())
 
 
+# rows x heads at most 64 an average sequence: another kernel than for more
+@pytest.mark.parametrize("heads,lens,rows", [
+    (1, [300, 70, 129], [64, 60, 65]), (5, [100, 90, 13, 64], [12, 13, 12, 13]), (33, [100, 64, 40, 7], [1, 1, 1, 4]),
+    (17, [500, 65, 2], [3, 5, 2]), (64, [700, 64, 1], [1, 1, 1]), (8, [900, 10, 9, 8, 7, 6], [40, 1, 1, 1, 1, 1]),
+    (8, [30000, 5], [9, 1]), (2, [64, 65, 0, 1], [33, 31, 1, 1]), (49, [3000], [1])])
+def test_absorbed_units_of_64_rows(heads, lens, rows):
+    assert sum(rows) * heads <= 64 * len(rows)
+    w = Paged(heads, lens, rows, seed=heads, extra_rows=2)
+    got = w.run()
+    assert pkv.kv_last_device_status() == 0
+    check(got, *w.expected())
+    assert np.isnan(got[int(w.cu[-1]):]).all()
+    assert np.array_equal(w.run(), got, equal_nan=True)
+
+
+@pytest.mark.parametrize("heads,rows", [(8, 1), (64, 1), (4, 3), (128, 1), (16, 20)])
+@pytest.mark.parametrize("top", [200, 3000])
+def test_absorbed_scores_that_keep_growing(heads, rows, top):
+    """One head's scores grow past any reference tile after tile; the others' do not."""
+    w = Paged(heads, [1000], [rows], seed=heads)
+    x = w.small[w.tables[0, :63]].reshape(-1, 576)[:1000]
+    q = f64(w.q)[-1, heads // 2]
+    x += np.linspace(0, top, 1000)[:, None] * q[None, :] / (q ** 2).sum() / SCALE
+    t = np.arange(1000)
+    w.small[w.tables[0, t // 16], t % 16] = x
+    w.cache.copy_(bf(w.small))
+    w.small = f64(w.cache)
+    check(w.run(), *w.expected())
+    assert pkv.kv_last_device_status() == 0
+
+
 def test_absorbed_padded_batch():
     """Entries without keys give zeros, entries without rows nothing, and rows of no sequence stay as they were."""
     w = Paged(12, [0, 30, 0, 17, 5], [1, 2, 0, 0, 1], seed=6, extra_rows=3)
@@ -376,7 +407,8 @@ class Prompt:
 @pytest.mark.parametrize("heads,nq,nk", [
     (4, [1, 2, 15, 16, 17, 63, 64, 65], None), (3, [127, 128, 129], None), (2, [255, 256, 257, 300], None),
     (1, [700], None), (5, [1, 40, 130], [1, 90, 500]), (8, [3, 1, 200], [70, 64, 201]), (128, [9], None),
-    (16, [128, 1, 1], [128, 700, 1]), (2, [513], [1030])])
+    (16, [128, 1, 1], [128, 700, 1]), (2, [513], [1030]),
+    (100, [513, 40, 700, 129], [513, 41, 700, 300])])
 def test_expanded(heads, nq, nk):
     w = Prompt(heads, nq, nk or nq, seed=heads)
     got = w.run()
