@@ -49,7 +49,7 @@ constexpr int CHUNKS = 8;
 constexpr uint32_t CHUNK_BYTES = BN * 128, Q_TILE = 3 * BM * 128;
 constexpr uint32_t SKV = 2 * Q_TILE, SBAR = SKV + CHUNKS * CHUNK_BYTES;
 constexpr int SMEM_BYTES = SBAR + 512 + 1024;     // + 1 KiB: aligned to 1 KiB at run time
-constexpr int W_MMA = 0, W_PROD = 2, W_SOFT = 4, THREADS = 32 * (W_SOFT + 8);
+constexpr int W_MMA = 0, W_PROD = 2, W_ITEM = 3, W_SOFT = 4, THREADS = 32 * (W_SOFT + 8);
 constexpr int NSLOT = 2;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 
@@ -61,9 +61,9 @@ enum {
                                     // issuer; by parity, so that one issuer's releases of two tiles cannot add up)
     B_VE = B_KE + 2,                // + key tile parity: both its second products have finished
     B_TURN = B_VE + 2,              // + query tile: its issuer's turn
-    B_Q = B_TURN + 2,               // the item's queries landed
-    B_QFREE = B_Q + 1,              // every first product of the item has finished (one an issuer)
-    B_S = B_QFREE + 1,              // + tile: S is in tensor memory
+    B_Q = B_TURN + 2,               // + query tile: the item's queries landed
+    B_QFREE = B_Q + 2,              // + query tile: every first product of the item has finished
+    B_S = B_QFREE + 2,              // + tile: S is in tensor memory
     B_P = B_S + 2,                  // + tile: P is (128 arrivals)
     B_DRAIN = B_P + 2,              // + tile: every product of the item has finished
     B_OFREE = B_DRAIN + 2,          // + tile: the item's O was read (128 arrivals)
@@ -71,7 +71,8 @@ enum {
                                     // lets the producer finish one item ahead, not two)
     B_IFULL = B_TAIL + 2,           // + slot: an item is in the slot
     B_IEMPTY = B_IFULL + NSLOT,     // + slot: every warp has read it
-    B_END = B_IEMPTY + NSLOT,       // + query tile: everything its issuer issued has finished
+    B_NEXT = B_IEMPTY + NSLOT,      // the item's loads are nearly through: time to take the next
+    B_END = B_NEXT + 1,             // + query tile: everything its issuer issued has finished
     NBAR = B_END + 2
 };
 // an item as the producer hands it on: valid, first query row, rows (up to 256),
@@ -215,6 +216,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort_flag));
 }
 
+// a box of a tensor into L2
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap *map, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y)
+                 : "memory");
+}
+
 __global__ void __launch_bounds__(THREADS, 1)
     expanded_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kvmap,
                     const __grid_constant__ CUtensorMap rmap, const ExpandedParams p)
@@ -241,9 +249,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(bar(B_KE + i), 2);
             mbar_init(bar(B_VE + i), 2);
         }
-        mbar_init(bar(B_Q), 1);
-        mbar_init(bar(B_QFREE), 2);
+        mbar_init(bar(B_NEXT), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_Q + i), 1);
+            mbar_init(bar(B_QFREE + i), 1);
             mbar_init(bar(B_S + i), 1);
             mbar_init(bar(B_P + i), 128);
             mbar_init(bar(B_DRAIN + i), 1);
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(bar(B_TAIL + 1), 1);
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(bar(B_IFULL + i), 1);
-            mbar_init(bar(B_IEMPTY + i), 10);            // the issuers and the softmax warps
+            mbar_init(bar(B_IEMPTY + i), 11);            // every warp but W_ITEM
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = uniform(*tmem_slot);
     // tensor memory: S of tile g at 128 g (P over its first 64 columns), O at 256 + 128 g
     int k = 0;          // items
-    // the next item, as every warp but the producer reads it
+    // the next item, as every warp but W_ITEM reads it
     auto read_item = [&](Slot &it) -> bool {
         const int sl = k % NSLOT;
         if (!wait_bar(bar(B_IFULL + sl), (k / NSLOT) & 1, abort_flag)) return false;
@@ -289,8 +298,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     Slot it;
 
-    if (warp == W_PROD) {
-        // ======================= items and loads
+    if (warp == W_ITEM) {
+        // ======================= items
         griddep_wait();                  // the list, and everything before it on the stream
         // small batches (up to 32 sequences, 4 items a CTA) need no list: a lane holds a
         // sequence, and the CTAs take every grid-th item.  That saves the list's
@@ -336,13 +345,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             ns = p.next[1];
             items = p.before[ns];
         }
-        int t = 0;                       // key tiles
         int idx = blockIdx.x;
-        bool ok = true;
         for (;; ++k) {
             const int sl = k % NSLOT;
             if (k >= NSLOT && !wait_bar(bar(B_IEMPTY + sl), (k / NSLOT - 1) & 1, abort_flag)) break;
             if (k > 0) {
+                // (not earlier, or an item would wait here that an idle CTA could take)
+                if (!wait_bar(bar(B_NEXT), (k - 1) & 1, abort_flag)) break;
                 if (p.small) {
                     idx += gridDim.x;
                 } else {
@@ -397,16 +406,51 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
             if (!it.valid) break;
-            // the queries, once every first product of the item before has finished
-            if (k > 0 && !wait_bar(bar(B_QFREE), (k - 1) & 1, abort_flag)) break;
-            const int tiles = it.rows > BM ? 2 : 1;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(B_Q), tiles * Q_TILE);
-                for (int g = 0; g < tiles; ++g)
-                    for (int i = 0; i < 3; ++i)
-                        tma_load_2d(sbase + g * Q_TILE + i * CHUNK_BYTES, &qmap, it.head * QKD + 64 * i, it.row0 + g * BM, bar(B_Q));
+            // its queries' and first keys' way from memory is long: into L2 with them
+            if (lane < 9) {
+                if (lane >= 6 || it.rows > BM * (lane / 3))
+                    prefetch_tile(lane < 6 ? &qmap : lane < 8 ? &kvmap : &rmap,
+                                  lane < 6 ? it.head * QKD + 64 * (lane % 3) : lane < 8 ? it.head * 2 * D + 64 * (lane - 6) : 0,
+                                  lane < 6 ? it.row0 + BM * (lane / 3) : it.key0);
             }
             __syncwarp();
+        }
+    } else if (warp == W_PROD) {
+        // ======================= loads
+        griddep_wait();                  // everything before the kernel on the stream
+        int t = 0;                       // key tiles
+        bool ok = true;
+        int tail_first = BN;             // rows of the last tile loaded that are its sequence's
+        auto zero_tail = [&]() -> bool {
+            const int x = t - 1, first = max(0, tail_first);
+            if (!wait_bar(bar(B_VF + (x & 1)), (x >> 1) & 1, abort_flag)) return false;
+            for (int i = 3; i < 5; ++i) {
+                const uint32_t vt = sbase + SKV + (uint32_t)((5 * x + i) % CHUNKS) * CHUNK_BYTES;
+                for (int e = lane; e < (BN - first) * 8; e += 32) st_shared_v4(vt + (first + (e >> 3)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_TAIL + ((k - 1) & 1)));
+            return true;
+        };
+        auto queries = [&](int g) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(B_Q + g), Q_TILE);
+                for (int i = 0; i < 3; ++i)
+                    tma_load_2d(sbase + g * Q_TILE + i * CHUNK_BYTES, &qmap, it.head * QKD + 64 * i, it.row0 + g * BM, bar(B_Q + g));
+            }
+            __syncwarp();
+        };
+        for (; ok && read_item(it); ++k) {
+            // query tile 0, once every first product of the item before's has finished
+            if (k > 0 && !wait_bar(bar(B_QFREE), (k - 1) & 1, abort_flag)) break;
+            queries(0);
+            if (tail_first < BN) {
+                // the last tile of the item before holds rows past the sequence's end, of
+                // another sequence or of none: P is 0 there, but 0 x NaN is NaN, so their
+                // values are zeroed once they have landed (the second product waits for it)
+                if (!zero_tail()) break;
+            }
             // chunk i of tile t (0, 1 key part, 2 rotary key, 3, 4 value) takes ring slot
             // (5 t + i) % 8, whose last holder was chunk i + 2 of tile t - 2 or i - 3 of t - 1
             for (int j = 0; j < it.T; ++j, ++t) {
@@ -430,7 +474,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     load(2, kb);
                 }
                 if (t >= 1 && ok && !wait_bar(bar(B_KE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag)) ok = false;
+                if (ok && j == 0) {
+                    // query tile 1: its first products of the item before are among those just waited for
+                    if (k > 0) ok = wait_bar(bar(B_QFREE + 1), (k - 1) & 1, abort_flag);
+                    if (ok && it.rows > BM) queries(1);
+                    else if (lane == 0) mbar_arrive(bar(B_Q + 1));
+                }
                 if (!ok) break;
+                if (lane == 0 && j == max(0, it.T - 3)) mbar_arrive(bar(B_NEXT));
                 if (lane == 0) {
                     mbar_arrive_expect_tx(vb, 2 * CHUNK_BYTES);
                     load(3, vb);
@@ -438,24 +489,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
-            if (!ok) break;
-            const int first = it.nk - (it.T - 1) * BN;
-            if (first < BN) {
-                // the last tile holds rows past the sequence's end, of another sequence
-                // or of none: P is 0 there, but 0 x NaN is NaN, so their values are zeroed
-                // once they have landed (the second product waits for it)
-                ok = wait_bar(bar(B_VF + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag);
-                for (int i = 3; ok && i < 5; ++i) {
-                    const uint32_t vt = sbase + SKV + (uint32_t)((5 * (t - 1) + i) % CHUNKS) * CHUNK_BYTES;
-                    for (int e = lane; e < (BN - max(0, first)) * 8; e += 32)
-                        st_shared_v4(vt + (max(0, first) + (e >> 3)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
-                }
-                if (!ok) break;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_TAIL + (k & 1)));
-            }
+            tail_first = it.nk - (it.T - 1) * BN;
         }
+        if (ok && tail_first < BN) (void)zero_tail();
         if (*abort_flag) {               // loads in flight land before the CTA exits
             // (bounded: a tile whose chunks were not all asked for never completes)
             for (int x = max(0, t - 1); x <= t; ++x) {
@@ -463,7 +499,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 (void)mbar_wait_bounded(bar(B_KF + (x & 1)), (x >> 1) & 1);
                 (void)mbar_wait_bounded(bar(B_VF + (x & 1)), (x >> 1) & 1);
             }
-            if (k > 0) (void)mbar_wait_bounded(bar(B_Q), k & 1);
+            for (int g = 0; g < 2; ++g)
+                for (int x = max(0, k - 1); x <= k; ++x) (void)mbar_wait_bounded(bar(B_Q + g), x & 1);
         }
     } else if (warp < W_MMA + 2) {
         // ======================= MMA issuers.  They take turns: one's second product
@@ -499,8 +536,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return true;
             };
             if (g == 1 && !both) {
-                ok = wait_bar(bar(B_Q), k & 1, abort_flag);
-                if (lane == 0) mbar_arrive(bar(B_QFREE));
+                ok = wait_bar(bar(B_Q + 1), k & 1, abort_flag);
+                if (lane == 0) mbar_arrive(bar(B_QFREE + 1));
                 for (int j = 0; ok && j < it.T; ++j, ++t) ok = pass_by(j + 1 == it.T);
                 continue;
             }
@@ -515,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // S = Q K^T of key tile x.  Its first chunk is waited for, and multiplied,
             // before the others: those two take the slots of the values before, which
             // the other issuer's products have only just released
-            auto issue_s = [&](int x, bool last) -> bool {
+            auto issue_s = [&](int x, bool pass, bool last) -> bool {
                 auto products = [&](int i) {
                     const uint64_t kd = kvdesc + (uint64_t)(chunk(x, i) >> 4);
 #pragma unroll
@@ -534,16 +571,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     products(1);
                     // (the turn takes about as long to pass as the last four products)
-                    if (both) mbar_arrive(bar(B_TURN + (g ^ 1)));
+                    if (pass) mbar_arrive(bar(B_TURN + (g ^ 1)));
                     products(2);
                     umma_commit(bar(B_S + g));
                     umma_commit(bar(B_KE + (x & 1)));
-                    if (last) umma_commit(bar(B_QFREE));
+                    if (last) umma_commit(bar(B_QFREE + g));
                 }
                 __syncwarp();
                 return true;
             };
-            ok = wait_bar(bar(B_Q), k & 1, abort_flag) && take_turn() && issue_s(t, T == 1);
+            // (the item's first product takes no turn: it runs beside the other's last ones)
+            ok = wait_bar(bar(B_Q + g), k & 1, abort_flag) && issue_s(t, false, T == 1);
             for (int j = 0; ok && j < T; ++j, ++t, ++n) {
                 const bool more = j + 1 < T;
                 ok = wait_bar(bar(B_VF + (t & 1)), (t >> 1) & 1, abort_flag);
@@ -567,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
                 // (in issue order: the products above read P from the columns that S overwrites)
-                if (ok && more) ok = issue_s(t + 1, j + 2 == T);
+                if (ok && more) ok = issue_s(t + 1, both, j + 2 == T);
             }
             for (int j = T; ok && j < it.T; ++j, ++t) {
                 ok = take_turn();
