@@ -33,15 +33,21 @@
 //    products run ahead of the softmax.  With P written over S (and all of Q in
 //    tensor memory) a tile took 2,000-2,800 cycles, all of it the latency of the
 //    loop S -> exchange -> softmax -> PV -> next S over two buffers.
-//  * The exchange goes in slots of 32 columns (three of 16 KiB), each released
-//    as soon as it is added, so that three slots keep both directions busy.
+//  * The exchange goes in slots of 32 columns (two of 16 KiB), each released
+//    as soon as it is added: a tile is in the slots while the next is multiplied.
 //  * Warps 0-7: exchange, softmax and epilogue, one query row a thread; warps 0-3
 //    take the even tiles (S buffer 0), warps 4-7 the odd ones, and hand the
 //    running maximum on through shared memory.  A tile costs its warps about
-//    2,000 cycles, nearly all latency, so one group alone set the pace.  The
+//    4,000 cycles, nearly all latency, so one group alone would set the pace.  The
 //    group that does not have an item's last tile loads the next item's queries.
 //    Warp 8: TMA producer, four stages of 64 keys (36 KiB).  Warps 9 and 10: MMA
 //    issuers.
+//  * A stage is held for 10,500 cycles -- 4,000 until it has landed, 1,100 for S,
+//    4,000 for exchange and softmax, 1,100 for PV -- so four of them give a tile
+//    every 2,650, where its bytes need 1,570 and its products 1,090.  (Three stages:
+//    143 us for 64 sequences of 1,500 to 8,200 tokens x 128 heads; four: 123, 3.1
+//    TB/s; a ring of four and a half in halves of 32 keys: 129, for its second set of
+//    waits and products; blocks brought into L2 two tiles ahead: 126.)
 //
 // Work split.  The tiles of all (sequence, 128-row unit) pairs are laid end to
 // end and cut into equal ranges, one a cluster: the batch's ragged lengths
@@ -72,7 +78,7 @@ constexpr uint32_t STAGE_BYTES = ROPE_OFF + TK * 64;
 constexpr int QT = 192;                           // a CTA's query dims in tensor memory; the other 64 are in shared
 constexpr uint32_t SQ = STAGES * STAGE_BYTES;     // query dims 192..255 of the CTA's 256, 128 rows x 128 bytes
 constexpr uint32_t SQR = SQ + 128 * 128;          // the queries' rotary part, 128 rows x 64 bytes
-constexpr int SLOTS = 3, SCOLS = 32;              // the peer's partial scores: slots of 32 columns,
+constexpr int SLOTS = 2, SCOLS = 32;              // the peer's partial scores: slots of 32 columns,
 constexpr uint32_t SRECV = SQR + 128 * 64;        // [8 groups of 4 columns][128 rows] float4
 constexpr uint32_t SLOT_BYTES = 128 * SCOLS * 4;
 constexpr uint32_t SMAX = SRECV + SLOTS * SLOT_BYTES;   // running maxima [128]; at an item's end [item parity][group](sum, maximum)[128]
@@ -653,10 +659,12 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     cluster_sync_all();   // nothing is sent to a CTA that has left
 }
 
-// Joins the partial sums of the units that a cut fell into, cluster by cluster,
-// with weights 2^(m_i - max m): a warp for each (row, 128 dims), the units' rows
-// laid end to end over all CTAs.  The first partial rows are requested before the
-// maxima are known, so a unit cut once costs one round trip to L2.
+// Joins the partial sums of the units that a cut fell into, worker by worker, with
+// weights 2^(m_i - max m).  Bound by latency: the first partial rows are requested
+// before the maxima are known, one wave of CTAs does it all (four a SM; with 98
+// registers a thread and 1,216 CTAs it took four waves, 19 us behind 113 for 64
+// sequences x 128 heads, now 10), and a unit cut more than 16 times -- one long
+// context -- gets a whole CTA a (row, 128 dims) instead of a warp (24 us -> 10).
 constexpr int MERGE_CTAS = 4 * 152, MERGE_WARPS = 8, MERGE_WIDE = 16, MERGE_PRE = 4;
 
 __device__ __forceinline__ void merge_add(float4 &acc, float f, const float4 &v)
@@ -799,7 +807,11 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
 
 // How a call's work is laid out.  Units of up to 64 rows take a CTA each
 // (latent_small.cu), if that is all that an average sequence has; else a pair of
-// CTAs takes 128 (a longer chunk's keys are then read half as often).
+// CTAs takes 128 (a longer chunk's keys are then read half as often).  Pair and one
+// CTA, us: 64 sequences of 1,500 to 8,200 tokens x 64 rows 103 and 91, x 16 rows 95
+// and 76; 256 of up to 4,096 x 8 rows 168 and 121; 48 of 300 to 6,000 x 64 rows 68
+// and 60, x 96 rows 74 and 86, x 128 rows 81 and 93.  (A single sequence of 1,000:
+// 16 and 18.5, which the host cannot tell: the lengths are on the device.)
 struct Plan {
     bool small;
     int tpt, slot_rows, workers;

@@ -6,18 +6,28 @@
 // turned round, with keys and dims along M and the query columns along N:
 //   S^T[64 keys x N] = K Q^T,   O^T[512 x N] += V^T P^T (four products of 128 dims)
 // Nothing is exchanged with another CTA, and what a product costs falls with N.
-//  * Bound by memory: a tile of 64 keys is 72 KiB, 3,100 cycles of a SM's share of
-//    the bandwidth; the products take 960 (N = 16) to 2,100 (N = 64) of them.
+//  * Bound by memory at few columns: a tile of 64 keys is 72 KiB, 3,100 cycles of a
+//    SM's share of the bandwidth, and the products take 1,540 (N = 16).  256 sequences
+//    of 17 to 4,096 tokens, 8 heads: 121 us, 5.0 TB/s; a tile takes 3,350 cycles, the
+//    first 12,000 of 210,000 go by until the first tile has landed.
+//  * At 64 columns the products take 2,050 cycles, all of them at the full rate of
+//    shared memory (128 bytes a cycle: both operands come from there), and the loads'
+//    576 come on top: a tile takes 3,700.  One context of 131,072, 64 heads: 49 us.
+//    (Two such CTAs a 128-row unit, each tile loaded once for both: 144 us for the
+//    64 sequences x 128 heads that latent_decode.cu does in 123.)
 //  * Shared memory: queries 72 KiB, two key stages of 72 KiB, P^T 8 KiB.  A stage is
 //    the K-major A operand of the first product and the MN-major A operand of the
 //    second.
 //  * Tensor memory: S^T 2 x 64 columns, O^T 4 x 64, and 64 for the row sums: a
 //    product of a block of ones with P^T adds up exactly the bf16 values that the
 //    second product uses, and no thread has to.
-//  * Softmax: warp w holds keys 16 w .. 16 w + 15 of the tile, a thread two keys and
-//    column pairs.  A column's reference is a power of two near its first scores and
+//  * Softmax: warps w and w + 4 hold keys 16 w .. 16 w + 15 of the tile and half of
+//    its columns each, a thread two keys and column pairs.  A column's reference is a power of two near its first scores and
 //    moves only when an exponential exceeds 2^15 (by a power of two, so without
-//    error); until then nothing is exchanged between keys but that vote.
+//    error).  The warps do not wait for each other to learn of that: the issuer of the
+//    second products refuses the tile, and it is done again.
+//  * A tile is loaded, multiplied and released in two halves of its dims, so that a
+//    stage is filled again while its other half is still in use (133 -> 126 us).
 // Warps 0-3: softmax and epilogue; 4: TMA producer; 5: first products; 6: second.
 #include "latent_work.cuh"
 
