@@ -22,13 +22,14 @@
 //    product of a block of ones with P^T adds up exactly the bf16 values that the
 //    second product uses, and no thread has to.
 //  * Softmax: warps w and w + 4 hold keys 16 w .. 16 w + 15 of the tile and half of
-//    its columns each, a thread two keys and column pairs.  A column's reference is a power of two near its first scores and
-//    moves only when an exponential exceeds 2^15 (by a power of two, so without
-//    error).  The warps do not wait for each other to learn of that: the issuer of the
-//    second products refuses the tile, and it is done again.
+//    its columns each, a thread two keys and column pairs.  A column's reference is a
+//    power of two near its first scores and moves only when an exponential exceeds
+//    2^15 (by a power of two, so without error).  The warps do not wait for each other
+//    to learn of that: the issuer of the second products refuses the tile, and it is
+//    done again.
 //  * A tile is loaded, multiplied and released in two halves of its dims, so that a
 //    stage is filled again while its other half is still in use (133 -> 126 us).
-// Warps 0-3: softmax and epilogue; 4: TMA producer; 5: first products; 6: second.
+// Warps 0-7: softmax and epilogue; 8: TMA producer; 9: first products; 10: second.
 #include "latent_work.cuh"
 
 #include <cmath>
@@ -36,7 +37,7 @@
 namespace {
 
 constexpr float FAR = 32768.0f;
-constexpr float NO_REF = -1048576.0f;            // any finite score is far from it
+constexpr float NO_REF = -3.0e38f;                // no score yet: any finite one is far above
 constexpr int MIN_TILES = 2;                      // tiles a CTA takes at least, if there are as many
 constexpr int STAGES = 2;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys (or query columns) x 64 dims
