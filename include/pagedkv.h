@@ -443,7 +443,9 @@ PAGEDKV_API kv_status kv_build_step_tables(int32_t *block_tables, int32_t max_bl
  * Latent attention: keys and values of all heads come from one vector a token,
  * a latent of 512 values and a rotary key of 64.
  *  Latent cache: [num_blocks][16][576] bf16, one row a token (latent, then
- *  rotary key), in the same blocks and tables as the K/V cache.
+ *  rotary key), in the same blocks and tables as the K/V cache.  (A kv_pool
+ *  serves it as well; kv_copy_on_write takes NULL caches then, and the caller
+ *  copies the block's 18,432 bytes.)
  *
  * reshape_and_cache_latent writes new tokens' rows:
  *  latent         device bf16, row t at latent + t x latent_stride, 512 values
@@ -479,7 +481,10 @@ PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t laten
  *                 so are rows that belong to no sequence (not flagged).
  *  cache, block_tables, num_blocks   as above; the keys of a block outside the
  *                 pool are not read, the sequence's output is then unspecified
- *                 (flag 1)
+ *                 (flag 1).  Keys 0 .. L-1 have to be finite: one that is not
+ *                 may reach rows of its sequence that do not see it (the
+ *                 product of a probability of 0 and NaN).  What lies past key
+ *                 L-1 does not matter.
  *  num_heads      1 .. 128 (KV_ERR_UNSUPPORTED above)
  *  scale          > 0 and finite
  *  workspace      device scratch of paged_latent_attention_workspace_size()
@@ -512,7 +517,8 @@ PAGEDKV_API kv_status paged_latent_attention(void *out, const void *q, const int
  *
  *  out            device bf16 [total_q_tokens][num_heads][128]
  *  q              device bf16 [total_q_tokens][num_heads][192]
- *  kv             device bf16 [total_k_tokens][num_heads][256]
+ *  kv             device bf16 [total_k_tokens][num_heads][256]; a sequence's own
+ *                 keys have to be finite, as above
  *  k_rope         device bf16, row t at k_rope + t x k_rope_stride, 64 values
  *                 (stride in elements, >= 64, a multiple of 8)
  *  cu_q_lens, cu_k_lens   device int32 [num_seqs + 1], non-decreasing; a

@@ -472,11 +472,11 @@ def _at(name, t, dev, dtype, shape):
     return t.data_ptr()
 
 
-def _at_nd(name, t, dev, dtype, shape):
-    """As _at, with None for an extent that is free."""
-    if t is None or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or \
-            len(t.shape) != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
-        _wrong(name, t, dev, dtype, shape)
+def _at_nd(name, t, dev, dtype, free, ends=()):
+    """As _at, for a tensor whose first `free` extents may be anything, the others `ends`."""
+    if t is None or t.get_device() != dev or t.dtype is not dtype or t.dim() != free + len(ends) or \
+            (ends and t.shape[free:] != ends) or not t.is_contiguous():
+        _wrong(name, t, dev, dtype, (None,) * free + ends)
     return t.data_ptr()
 
 
@@ -528,10 +528,10 @@ def kv_build_step_tables(block_tables, context_lens, new_lens, free_blocks, num_
     free blocks taken).  Lengths that do not fit refuse the sequence and set the
     device status (see kv_last_device_status)."""
     dev = _device("block_tables", block_tables)
-    tables = _at_nd("block_tables", block_tables, dev, _I32, (None, None))
+    tables = _at_nd("block_tables", block_tables, dev, _I32, 2)
     B, mb = block_tables.shape
-    free = _at_nd("free_blocks", free_blocks, dev, _I32, (None,))
-    slots = _at_nd("slot_mapping", slot_mapping, dev, _I64, (None,))
+    free = _at_nd("free_blocks", free_blocks, dev, _I32, 1)
+    slots = _at_nd("slot_mapping", slot_mapping, dev, _I64, 1)
     n, each = slot_mapping.shape[0], (B,)
     _check(_call_on(dev, stream, lib().kv_build_step_tables, tables, mb,
                     _at("context_lens", context_lens, dev, _I32, each), _at("new_lens", new_lens, dev, _I32, each), B,
@@ -564,13 +564,13 @@ def paged_latent_attention(out, q, cache, block_tables, context_lens, cu_q_lens=
     q[R][H][576] (bf16), one row a sequence, or cu_q_lens [B+1] rows.  scale
     defaults to (128 + 64) ** -0.5, the expanded form's."""
     dev = _device("q", q)
-    qp = _at_nd("q", q, dev, _BF, (None, None, _LATENT_ROW))
+    qp = _at_nd("q", q, dev, _BF, 2, (_LATENT_ROW,))
     R, h, _ = q.shape
-    tables = _at_nd("block_tables", block_tables, dev, _I32, (None, None))
+    tables = _at_nd("block_tables", block_tables, dev, _I32, 2)
     B, mb = block_tables.shape
     if cu_q_lens is None and R != B:
         raise ValueError("without cu_q_lens, q must have one row a sequence")
-    c = _at_nd("cache", cache, dev, _BF, (None, BLOCK_SIZE, _LATENT_ROW))
+    c = _at_nd("cache", cache, dev, _BF, 1, (BLOCK_SIZE, _LATENT_ROW))
     L = lib()
     ws, nbytes, _keep = _scratch(workspace, dev, L.paged_latent_attention_workspace_size, B, R, h, mb)
     _check(_call_on(dev, stream, L.paged_latent_attention, _at("out", out, dev, _BF, (R, h, LATENT_DIM)), qp,
@@ -590,12 +590,12 @@ def latent_prefill_attention(out, q, kv, k_rope, cu_q_lens, cu_k_lens, scale=Non
     (bf16; k_rope's rows may be views of a wider tensor), ragged by cu_q_lens and
     cu_k_lens [B+1], causal from the end.  scale defaults to 192 ** -0.5."""
     dev = _device("q", q)
-    qp = _at_nd("q", q, dev, _BF, (None, None, _EXPANDED_QK))
+    qp = _at_nd("q", q, dev, _BF, 2, (_EXPANDED_QK,))
     R, h, _ = q.shape
-    kvp = _at_nd("kv", kv, dev, _BF, (None, h, 2 * HEAD_DIM))
+    kvp = _at_nd("kv", kv, dev, _BF, 1, (h, 2 * HEAD_DIM))
     K = kv.shape[0]
     rp, rs = _rows_at("k_rope", k_rope, dev, K, LATENT_ROPE_DIM)
-    cu_q = _at_nd("cu_q_lens", cu_q_lens, dev, _I32, (None,))
+    cu_q = _at_nd("cu_q_lens", cu_q_lens, dev, _I32, 1)
     B = cu_q_lens.shape[0] - 1
     if B < 0:
         raise ValueError("cu_q_lens must have at least one entry")
