@@ -236,11 +236,10 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 
     Item it;
     if (warp == W_PROD) {
-        // ======================= producer: lanes 0-15 one 2 KiB box each (block
-        // lane / 4, 64 dims lane % 4), lanes 16-19 a block's rotary box; each lane
-        // reads its block id of the next tile while it waits for the stage
-        const bool is_r = lane >= 16;
-        const int blk = is_r ? lane - 16 : lane >> 2, chunk = lane & 3;
+        // ======================= producer: a box of a block's 16 keys x 64 (or 32 rotary)
+        // dims at a time, issued by one elected lane; each lane reads the id of block
+        // lane % 4 of the next tile while it waits for the stage
+        const int blk = lane & 3;
         int u = 0;
         bool ok = true;
         while (ok && next_item(p, range, walk, it)) {
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             auto block_id = [&](int j) -> int32_t {
                 const int b = j * (TK / BS) + blk;
-                return (lane < 20 && j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
+                return (j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
             };
             int32_t next_id = block_id(it.j0);
             for (int j = it.j0; j < it.j1; ++j, ++u) {
@@ -268,20 +267,27 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                     ok = false;
                     break;
                 }
-                const bool in = lane < 20 && j * (TK / BS) + blk < nblk;
+                const bool in = j * (TK / BS) + blk < nblk;
                 const bool valid = in && id >= 0 && id < p.num_blocks;
-                if (in && !valid) flag(ST_BAD_BLOCK);
-                const unsigned vm = __ballot_sync(0xffffffffu, valid);
-                if (lane == 0) {
+                if (in && !valid && lane < 4) flag(ST_BAD_BLOCK);
+                const unsigned vm = __ballot_sync(0xffffffffu, valid) & 15u;
+                int32_t rows[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) rows[b] = __shfl_sync(0xffffffffu, id, b) * BS;
+                if (elect_one()) {
                     fence_proxy_async_smem();
-                    mbar_arrive_expect_tx(bar(B_KVF + st), __popc(vm & 0xffffu) * 2048 + __popc(vm >> 16) * 1024);
+                    mbar_arrive_expect_tx(bar(B_KVF + st), __popc(vm) * (4 * 2048 + 1024));
+                    const uint32_t stg = sbase + st * STAGE_BYTES;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (!(vm >> b & 1)) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            tma_load_2d(stg + e * CHUNK_BYTES + b * 2048, &lmap, c * HALF + e * 64, rows[b], bar(B_KVF + st));
+                        tma_load_2d(stg + ROPE_OFF + b * 1024, &rmap, LAT + c * RHALF, rows[b], bar(B_KVF + st));
+                    }
                 }
                 __syncwarp();
-                if (valid) {
-                    const uint32_t stg = sbase + st * STAGE_BYTES;
-                    if (is_r) tma_load_2d(stg + ROPE_OFF + blk * 1024, &rmap, LAT + c * RHALF, id * BS, bar(B_KVF + st));
-                    else tma_load_2d(stg + chunk * CHUNK_BYTES + blk * 2048, &lmap, c * HALF + chunk * 64, id * BS, bar(B_KVF + st));
-                }
             }
         }
         if (*abort_flag)      // loads in flight land before the CTA exits

@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto columns = [&]() -> int { return (it.toks * p.heads + 15) & ~15; };
 
     if (warp == W_PROD) {
-        // ======================= producer: lanes 0-15 a 2 KiB box of each half (block
-        // lane / 4), lanes 16-19 a block's rotary box; each lane reads its block id of
-        // the next tile while it waits
-        const bool is_r = lane >= 16;
-        const int blk = is_r ? lane & 3 : lane >> 2, chunk = lane & 3;
+        // ======================= producer: a box of 2 KiB (a block's 16 keys x 64 dims)
+        // at a time, issued by one elected lane (every 27 cycles; with a lane for each box
+        // they left every 70, 2,500 cycles a tile); each lane reads the id of block
+        // lane % 4 of the next tile while it waits
+        const int blk = lane & 3;
         int u = 0, items = 0;       // halves, items
         bool ok = true;
         for (; ok && next_item(p, range, walk, it); ++items) {
@@ -175,43 +175,53 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int nblk = (it.q.L + BS - 1) / BS;
             auto block_id = [&](int j) -> int32_t {
                 const int b = j * (TK / BS) + blk;
-                return (lane < 20 && j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
+                return (j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
             };
             int32_t next_id = block_id(it.j0);
+            auto queries = [&]() {
+                const int boxes = columns() / 16 * 9;                 // 16 rows x 64 dims each
+                if (lane == 0) mbar_arrive_expect_tx(bar(B_Q), boxes * 2048);
+                __syncwarp();
+                for (int e = lane; e < boxes; e += 32)
+                    tma_load_2d(sbase + (e % 9) * CHUNK_BYTES + (e / 9) * 2048, &qmap, (e % 9) * 64,
+                                (it.q.a + it.t0) * p.heads + (e / 9) * 16, bar(B_Q));
+            };
+            if (items == 0) queries();
             for (int j = it.j0; ok && j < it.j1; ++j) {
                 const int32_t id = next_id;
                 next_id = block_id(j + 1);
-                const bool in = lane < 20 && j * (TK / BS) + blk < nblk, valid = in && id >= 0 && id < p.num_blocks;
-                if (in && !valid && is_r) flag(ST_BAD_BLOCK);
-                const unsigned vm = __ballot_sync(0xffffffffu, valid);
+                const bool in = j * (TK / BS) + blk < nblk, valid = in && id >= 0 && id < p.num_blocks;
+                if (in && !valid && lane < 4) flag(ST_BAD_BLOCK);
+                const unsigned vm = __ballot_sync(0xffffffffu, valid) & 15u;
+                int32_t rows[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) rows[b] = __shfl_sync(0xffffffffu, id, b) * BS;
                 for (int h = 0; h < 2; ++h, ++u) {
                     const int st = (u >> 1) % STAGES, sh = 2 * st + h, turn = (u >> 1) / STAGES;
                     if (turn > 0 && !wait_bar(bar(B_KVE + sh), (turn - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
+                    if (elect_one()) {
                         fence_proxy_async_smem();
-                        mbar_arrive_expect_tx(bar(B_KVF + sh), __popc(vm & (h == 0 ? 0xffffu : 0xfffffu)) * 2048);
+                        mbar_arrive_expect_tx(bar(B_KVF + sh), __popc(vm) * (4 + h) * 2048);
+                        const uint32_t at = sbase + SSTAGE + st * TILE_BYTES + h * 4 * CHUNK_BYTES;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            if (!(vm >> b & 1)) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                tma_load_2d(at + e * CHUNK_BYTES + b * 2048, &kmap, (4 * h + e) * 64, rows[b], bar(B_KVF + sh));
+                            if (h == 1) tma_load_2d(at + 4 * CHUNK_BYTES + b * 2048, &kmap, LAT, rows[b], bar(B_KVF + sh));
+                        }
                     }
                     __syncwarp();
-                    const uint32_t at = sbase + SSTAGE + st * TILE_BYTES + blk * 2048;
-                    if (valid && !is_r) tma_load_2d(at + (4 * h + chunk) * CHUNK_BYTES, &kmap, (4 * h + chunk) * 64, id * BS, bar(B_KVF + sh));
-                    if (valid && is_r && h == 1) tma_load_2d(at + 8 * CHUNK_BYTES, &kmap, LAT, id * BS, bar(B_KVF + sh));
                 }
-                if (ok && j == it.j0) {
-                    // the item's queries, once every first product of the item before has finished
-                    // (rows past the unit's are multiplied along, never stored)
-                    if (items > 0 && !wait_bar(bar(B_QFREE), (items - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const int groups = columns() / 16;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(B_Q), groups * 9 * 2048);
-                    __syncwarp();
-                    for (int e = lane; e < groups * 9; e += 32)
-                        tma_load_2d(sbase + (e % 9) * CHUNK_BYTES + (e / 9) * 2048, &qmap, (e % 9) * 64,
-                                    (it.q.a + it.t0) * p.heads + (e / 9) * 16, bar(B_Q));
+                // the item's queries, once every first product of the item before has finished
+                // (rows past the unit's are multiplied along, never stored)
+                if (ok && j == it.j0 && items > 0) {
+                    ok = wait_bar(bar(B_QFREE), (items - 1) & 1, abort_flag);
+                    if (ok) queries();
                 }
             }
         }

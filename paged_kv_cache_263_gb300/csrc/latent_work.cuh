@@ -196,6 +196,8 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
             start[0] = s;
             start[1] = (int)u;
             start[2] = (int)(w0 - b - u * KT);
+            // the first block ids, which the loads wait for
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.tables + (size_t)s * p.max_blocks + min(start[2] * (TK / BS), p.max_blocks - 1)));
             cut_sh[0] = cut.each;
             cut_sh[1] = cut.extra;
         }
