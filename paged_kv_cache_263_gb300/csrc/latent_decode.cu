@@ -70,7 +70,11 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int HALF = LAT / 2, RHALF = ROPE / 2;   // a CTA's latent and rotary dims
 constexpr int NCL = 76;                           // clusters: a pair of CTAs on each pair of the 152 SMs
-constexpr int MIN_TILES = 2;                      // tiles a cluster takes at least, if there are as many
+// Tiles a cluster takes at least, if there are as many, but up to FEW clusters with one:
+// a tile costs a cluster 1.4 us, a cluster more the sequence 128 rows more to merge.
+// (1,000 keys, 128 heads, one tile or two a cluster: 15.8 and 17.2 us; eight sequences of
+// 500 to 2,000, two or three: 29.4 and 26.0.)
+constexpr int MIN_TILES = 3, FEW = 32;
 constexpr int STAGES = 4;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys x 64 dims
 constexpr uint32_t ROPE_OFF = 4 * CHUNK_BYTES;    // within a stage
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
+    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, FEW, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
     Walk walk = range.walk;
     tc_fence_after();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist
@@ -669,9 +673,10 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 // weights 2^(m_i - max m).  Bound by latency: the first partial rows are requested
 // before the maxima are known, one wave of CTAs does it all (four a SM; with 98
 // registers a thread and 1,216 CTAs it took four waves, 19 us behind 113 for 64
-// sequences x 128 heads, now 10), and a unit cut more than 16 times -- one long
-// context -- gets a whole CTA a (row, 128 dims) instead of a warp (24 us -> 10).
-constexpr int MERGE_CTAS = 4 * 152, MERGE_WARPS = 8, MERGE_WIDE = 16, MERGE_PRE = 4;
+// sequences x 128 heads, now 10), and a unit of more than 16 partials -- one long
+// context: 24 us -> 10 -- gets a whole CTA a (row, 128 dims) instead of a warp; one of
+// more than 4 if there are CTAs for all (1,000 keys, 128 heads: 17.8 us -> 17.2).
+constexpr int MERGE_CTAS = 4 * 152, MERGE_WARPS = 8, MERGE_FEW = 4, MERGE_MANY = 16, MERGE_PRE = 4;
 
 __device__ __forceinline__ void merge_add(float4 &acc, float f, const float4 &v)
 {
@@ -692,10 +697,22 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
     griddep_launch_dependents();
     griddep_wait();
     if (warp == 0) {
-        int run = 0;
-        for (int b = 0; b < p.workers; b += 32) {
-            const int4 d = b + lane < p.workers ? p.desc[b + lane] : make_int4(0, 0, 0, 0);
-            const int n = !d.x ? 0 : d.y > MERGE_WIDE ? d.z << 16 : d.z;
+        int4 units[(MAX_WORKERS + 31) / 32];
+        int rows = 0, run = 0;
+#pragma unroll
+        for (int i = 0; i < (MAX_WORKERS + 31) / 32; ++i) {
+            units[i] = 32 * i + lane < p.workers ? p.desc[32 * i + lane] : make_int4(0, 0, 0, 0);
+            if (!units[i].x) units[i].z = 0;
+            rows += units[i].z;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+        const int wide = rows * 4 <= MERGE_CTAS ? MERGE_FEW : MERGE_MANY;
+#pragma unroll
+        for (int i = 0; i < (MAX_WORKERS + 31) / 32; ++i) {
+            const int b = 32 * i;
+            const int4 d = units[i];
+            const int n = d.y > wide ? d.z << 16 : d.z;
             int v = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -727,7 +744,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
         const float inv = l > 0.f ? 1.f / l : 0.f;
         reinterpret_cast<uint2 *>(p.out + row * LAT + q4 * 128)[lane] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     };
-    // up to 16 partials: a warp a quarter of a row
+    // few partials: a warp a quarter of a row
     const int narrow = (before[p.workers] & 0xffff) * 4;
     for (int t = blockIdx.x * MERGE_WARPS + warp; t < narrow; t += MERGE_CTAS * MERGE_WARPS) {
         const int g = t >> 2, q4 = t & 3, k = worker(g, 0), row = g - (before[k] & 0xffff), ns = parts[k];

@@ -151,10 +151,11 @@ __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g,
 
 // Finds worker k's range (all threads of the CTA; two barriers and one more at the
 // end): prefix sums of the sequences' costs, a run of consecutive sequences a
-// thread.  scan: THREADS / 32 numbers, start: 3, cut: 2, list: 3 x listed, all in
+// thread.  `each` tiles a worker at least, if there are as many; but up to `few`
+// workers with one.  scan: THREADS / 32 numbers, start: 3, cut: 2, list: 3 x listed, all in
 // shared memory; start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
 template <int THREADS>
-__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int min_tiles, bool flagging,
+__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int each, int few, bool flagging,
                                             long long *scan, int *start, long long *cut_sh, int *list, int listed)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -177,7 +178,7 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
         W += t;
     }
     Range g;
-    g.nc = (int)max(1ll, min((long long)workers, W / min_tiles));
+    g.nc = (int)max(1ll, min((long long)workers, max(W / each, min(W, (long long)few))));
     Cut cut;
     cut.each = quotient(W, g.nc);
     cut.extra = W - cut.each * g.nc;
