@@ -505,13 +505,19 @@ def _call_on(dev, stream, fn, *args):
         return fn(*args, raw)
 
 
-def _scratch(workspace, dev, size, *sizes):
-    """(address, bytes, tensor) of the given workspace, or of a new one of size(*sizes) bytes."""
+def _scratch(workspace, dev, stream, size, *sizes):
+    """(address, bytes, tensor) of the given workspace, or of a new one of size(*sizes) bytes.
+    The new one belongs to the stream that the call runs on: it is given back as the call
+    returns, and what that stream does next with the memory comes after the call's kernels."""
     if workspace is None:
         need = size(*sizes)
         if not need:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the other tensors' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -572,7 +578,7 @@ def paged_latent_attention(out, q, cache, block_tables, context_lens, cu_q_lens=
         raise ValueError("without cu_q_lens, q must have one row a sequence")
     c = _at_nd("cache", cache, dev, _BF, 1, (BLOCK_SIZE, _LATENT_ROW))
     L = lib()
-    ws, nbytes, _keep = _scratch(workspace, dev, L.paged_latent_attention_workspace_size, B, R, h, mb)
+    ws, nbytes, _keep = _scratch(workspace, dev, stream, L.paged_latent_attention_workspace_size, B, R, h, mb)
     _check(_call_on(dev, stream, L.paged_latent_attention, _at("out", out, dev, _BF, (R, h, LATENT_DIM)), qp,
                     None if cu_q_lens is None else _at("cu_q_lens", cu_q_lens, dev, _I32, (B + 1,)),
                     _at("context_lens", context_lens, dev, _I32, (B,)), B, R, c, tables, mb, h, cache.shape[0],
@@ -600,7 +606,7 @@ def latent_prefill_attention(out, q, kv, k_rope, cu_q_lens, cu_k_lens, scale=Non
     if B < 0:
         raise ValueError("cu_q_lens must have at least one entry")
     L = lib()
-    ws, nbytes, _keep = _scratch(workspace, dev, L.latent_prefill_attention_workspace_size, B, R, h)
+    ws, nbytes, _keep = _scratch(workspace, dev, stream, L.latent_prefill_attention_workspace_size, B, R, h)
     _check(_call_on(dev, stream, L.latent_prefill_attention, _at("out", out, dev, _BF, (R, h, HEAD_DIM)), qp, kvp, rp,
                     rs, cu_q, _at("cu_k_lens", cu_k_lens, dev, _I32, (B + 1,)), B, R, K, h,
                     _EXPANDED_QK ** -0.5 if scale is None else float(scale), ws, nbytes), "latent_prefill_attention")

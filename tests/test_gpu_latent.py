@@ -378,6 +378,29 @@ def test_absorbed_on_other_streams_and_in_graphs():
     assert pkv.kv_last_device_status() == 0
 
 
+def test_scratch_of_a_call_on_another_stream():
+    """A call without a workspace on a given stream: its scratch is not handed to the
+    current stream's next allocation while the call still runs."""
+    a, b = Paged(16, [9000, 50], [1, 1], seed=3), Prompt(8, [300] * 40, [300] * 40, seed=4)
+    ra, rb = a.run(), b.run()
+    side = torch.cuda.Stream()
+    args, held = a.args(), (i32(b.cu_q), i32(b.cu_k))
+    sizes = [pkv.paged_latent_attention_workspace_size(2, 2, 16, a.width),
+             pkv.latent_prefill_attention_workspace_size(40, b.q.shape[0], 8)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a.out.fill_(float("nan"))
+        b.out.fill_(float("nan"))
+        side.wait_stream(torch.cuda.current_stream())
+        pkv.paged_latent_attention(**args, stream=side)
+        pkv.latent_prefill_attention(b.out, b.q, b.kv, b.rope, *held, scale=SCALE, stream=side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(a.out), ra) and np.array_equal(f64(b.out), rb)
+        del junk
+    assert pkv.kv_last_device_status() == 0
+
+
 # ----------------------------------------------------------------- expanded form
 class Prompt:
     def __init__(self, heads, nq, nk, seed=0, extra_q=0, extra_k=0, std=1.0):
