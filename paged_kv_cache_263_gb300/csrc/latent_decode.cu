@@ -75,6 +75,7 @@ constexpr int NCL = 76;                           // clusters: a pair of CTAs on
 // (1,000 keys, 128 heads, one tile or two a cluster: 15.8 and 17.2 us; eight sequences of
 // 500 to 2,000, two or three: 29.4 and 26.0.)
 constexpr int MIN_TILES = 3, FEW = 32;
+constexpr int SNAP = 3;                           // (eight sequences of 500 to 2,000, 128 heads: 26.4 us without, 22.5 with)
 constexpr int STAGES = 4;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys x 64 dims
 constexpr uint32_t ROPE_OFF = 4 * CHUNK_BYTES;    // within a stage
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, FEW, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
+    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, FEW, SNAP, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
     Walk walk = range.walk;
     tc_fence_after();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist

@@ -41,12 +41,13 @@ constexpr float NO_REF = -3.0e38f;                // no score yet: any finite on
 // tiles a CTA takes at least (16 sequences of 100 to 1,000 x 64 rows: 19.2 us, with two
 // 22.1; four of 2,000 to 5,000: 26.8 and 24.7)
 constexpr int MIN_TILES = 1;
+constexpr int SNAP = 2;                           // (256 sequences of 50 to 300 x 16 rows: 32.1 us without, 30.2 with)
 constexpr int STAGES = 2;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys (or query columns) x 64 dims
 constexpr uint32_t TILE_BYTES = 9 * CHUNK_BYTES;  // eight latent chunks and the rotary one
 constexpr uint32_t SSTAGE = TILE_BYTES;           // the queries come first
 constexpr uint32_t SP = SSTAGE + STAGES * TILE_BYTES, SONES = SP + TK * 128, SBAR = SONES + 1024;
-constexpr uint32_t LIST_OFF = 728;                // within the barrier area
+constexpr uint32_t LIST_OFF = 736;                // within the barrier area
 constexpr int LIST = 24;
 constexpr int SMEM_BYTES = SBAR + 1024;
 constexpr int SOFT = 8;                           // softmax warps
@@ -67,10 +68,10 @@ enum {
     B_END = B_MEET + 1,         // + issuer: everything it issued has finished
     NBAR = B_END + 2
 };
-// after the barriers: tensor memory address, abort flag, start[3], votes[2], -, cut[2]; then 64 each of
+// after the barriers: tensor memory address, abort flag, start[3], votes[2], -, cut[4]; then 64 each of
 // the columns' references, key limits and (in turn) sums
-constexpr uint32_t REF_OFF = 216;
-static_assert(NBAR * 8 + 8 + 24 + 16 <= REF_OFF && REF_OFF + 2 * 256 == LIST_OFF && LIST_OFF + LIST * 12 <= 1024, "barrier area");
+constexpr uint32_t REF_OFF = 224;
+static_assert(NBAR * 8 + 8 + 24 + 32 <= REF_OFF && REF_OFF + 2 * 256 == LIST_OFF && LIST_OFF + LIST * 12 <= 1024, "barrier area");
 
 constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn)
 {
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
     tc_fence_before();
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS>(p, k, p.workers, MIN_TILES, 0, k == 0, reinterpret_cast<long long *>(smem + SP), s_start, s_cut, list, LIST);
+    const Range range = find_range<THREADS>(p, k, p.workers, MIN_TILES, 0, SNAP, k == 0, reinterpret_cast<long long *>(smem + SP), s_start, s_cut, list, LIST);
     Walk walk = {uniform(range.walk.s), uniform(range.walk.u), uniform(range.walk.j), uniform(range.walk.left)};
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);

@@ -114,7 +114,8 @@ struct Cut {
 // A worker's range: where it starts, and how it was cut.
 struct Range {
     Walk walk;
-    int tiles, nc;           // its tiles; workers with work
+    long long begin;         // its place among all tiles
+    int tiles, nc, snap;     // its tiles; workers with work; tiles that a cut moves to a unit's end
     int s_first, listed;     // its first sequence; sequences tabled in shared memory from there on
     const int *list;
     const long long *cut;    // shared memory: Cut's two numbers
@@ -152,10 +153,12 @@ __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g,
 // Finds worker k's range (all threads of the CTA; two barriers and one more at the
 // end): prefix sums of the sequences' costs, a run of consecutive sequences a
 // thread.  `each` tiles a worker at least, if there are as many; but up to `few`
-// workers with one.  scan: THREADS / 32 numbers, start: 3, cut: 2, list: 3 x listed, all in
-// shared memory; start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
+// workers with one.  A cut that falls within `snap` tiles of a unit's end moves there:
+// the worker would spend more on the few tiles' queries and partial sums.  scan:
+// THREADS / 32 numbers, start: 3, cut: 4, list: 3 x listed, all in shared memory;
+// start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
 template <int THREADS>
-__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int each, int few, bool flagging,
+__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int each, int few, int snap, bool flagging,
                                             long long *scan, int *start, long long *cut_sh, int *list, int listed)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -182,25 +185,41 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
     Cut cut;
     cut.each = quotient(W, g.nc);
     cut.extra = W - cut.each * g.nc;
+    g.snap = snap = (int)min((long long)snap, cut.each / 2);
     const long long w0 = k < g.nc ? cut.begin(k) : W, w1 = k < g.nc ? cut.begin(k + 1) : W;
-    {
-        long long b = before + incl - mine;
-        if (w0 < w1 && b <= w0 && w0 < b + mine) {
-            int s = sa;
-            for (; s < sb; ++s) {
-                const long long cost = seq_cost(p, read_seq(p, s, false));
-                if (w0 < b + cost) break;
-                b += cost;
-            }
-            const int KT = seq_tiles(read_seq(p, s, false));
-            const long long u = quotient(w0 - b, KT);
+    if (threadIdx.x == 0) {
+        cut_sh[0] = cut.each;
+        cut_sh[1] = cut.extra;
+        if (w1 >= W) cut_sh[3] = W;
+    }
+    // where it begins and ends, by the thread whose sequences hold the place
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        long long pos = e == 0 ? w0 : w1, b = before + incl - mine;
+        if (w0 >= w1 || pos < b || pos >= b + mine) continue;
+        int s = sa;
+        for (; s < sb; ++s) {
+            const long long cost = seq_cost(p, read_seq(p, s, false));
+            if (pos < b + cost) break;
+            b += cost;
+        }
+        const int KT = seq_tiles(read_seq(p, s, false));
+        int u = (int)quotient(pos - b, KT), t = (int)(pos - b - (long long)u * KT);
+        if (t <= snap) {
+            pos -= t;
+            t = 0;
+        } else if (KT - t <= snap) {
+            pos += KT - t;
+            ++u;
+            t = 0;
+        }
+        cut_sh[2 + e] = pos;
+        if (e == 0) {
             start[0] = s;
-            start[1] = (int)u;
-            start[2] = (int)(w0 - b - u * KT);
+            start[1] = u;
+            start[2] = t;
             // the first block ids, which the loads wait for
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.tables + (size_t)s * p.max_blocks + min(start[2] * (TK / BS), p.max_blocks - 1)));
-            cut_sh[0] = cut.each;
-            cut_sh[1] = cut.extra;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.tables + (size_t)s * p.max_blocks + min(t * (TK / BS), p.max_blocks - 1)));
         }
     }
     __syncthreads();
@@ -211,7 +230,8 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
         list[3 * i + 1] = q.n;
         list[3 * i + 2] = q.L;
     }
-    g.tiles = (int)(w1 - w0);
+    g.begin = w0 < w1 ? cut_sh[2] : W;
+    g.tiles = w0 < w1 ? (int)max(0ll, cut_sh[3] - cut_sh[2]) : 0;
     g.walk = {g.s_first, start[1], start[2], g.tiles};
     g.listed = listed;
     g.list = list;
@@ -225,7 +245,9 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
 __device__ __forceinline__ void list_merge(const LatentParams &p, const Range &g, const Item &it, int k, int rows)
 {
     const Cut cut = {g.cut[0], g.cut[1]};
-    const int kl = max(k, min(g.nc - 1, cut.owner(cut.begin(k) + (g.tiles - it.left) + it.kt - 1)));
+    const long long first = g.begin + (g.tiles - it.left);
+    // (a cut in the unit's last `snap` tiles has moved to its end)
+    const int kl = max(k, min(g.nc - 1, cut.owner(first + min(it.kt, seq_tiles(it.q) - g.snap) - 1)));
     p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
     p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
 }
