@@ -44,10 +44,11 @@
 //    issuers.
 //  * A stage is held for 10,500 cycles -- 4,000 until it has landed, 1,100 for S,
 //    4,000 for exchange and softmax, 1,100 for PV -- so four of them give a tile
-//    every 2,650, where its bytes need 1,570 and its products 1,090.  (Three stages:
-//    143 us for 64 sequences of 1,500 to 8,200 tokens x 128 heads; four: 123, 3.1
-//    TB/s; a ring of four and a half in halves of 32 keys: 129, for its second set of
-//    waits and products; blocks brought into L2 two tiles ahead: 126.)
+//    every 2,650, where its bytes need 1,570 and its products 1,090.  (64
+//    sequences of 1,500 to 8,200 tokens x 128 heads: 118 us, 3.2 TB/s.  Measured when
+//    it took 123: three stages 143; a ring of four and a half in halves of 32 keys 129,
+//    for its second set of waits and products; blocks brought into L2 two tiles ahead
+//    126.)
 //
 // Work split.  The tiles of all (sequence, 128-row unit) pairs are laid end to
 // end and cut into equal ranges, one a cluster: the batch's ragged lengths
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 // before the maxima are known, one wave of CTAs does it all (four a SM; with 98
 // registers a thread and 1,216 CTAs it took four waves, 19 us behind 113 for 64
 // sequences x 128 heads, now 10), and a unit of more than 16 partials -- one long
-// context: 24 us -> 10 -- gets a whole CTA a (row, 128 dims) instead of a warp; one of
+// context: 24 us, then 10 -- gets a whole CTA a (row, 128 dims) instead of a warp; one of
 // more than 4 if there are CTAs for all (1,000 keys, 128 heads: 17.8 us -> 17.2).
 constexpr int MERGE_CTAS = 4 * 152, MERGE_WARPS = 8, MERGE_FEW = 4, MERGE_MANY = 16, MERGE_PRE = 4;
 
@@ -832,10 +833,10 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
 // How a call's work is laid out.  Units of up to 64 rows take a CTA each
 // (latent_small.cu), if that is all that an average sequence has; else a pair of
 // CTAs takes 128 (a longer chunk's keys are then read half as often).  Pair and one
-// CTA, us: 64 sequences of 1,500 to 8,200 tokens x 64 rows 103 and 91, x 16 rows 95
-// and 76; 256 of up to 4,096 x 8 rows 168 and 121; 48 of 300 to 6,000 x 64 rows 68
-// and 60, x 96 rows 74 and 86, x 128 rows 81 and 93.  (A single sequence of 1,000:
-// 16 and 18.5, which the host cannot tell: the lengths are on the device.)
+// CTA, us: 64 sequences of 1,500 to 8,200 tokens x 64 rows 100 and 87, x 16 rows 92
+// and 72; 256 of up to 4,096 x 8 rows 161 and 116; 48 of 300 to 6,000 x 64 rows 63
+// and 56, x 96 rows 68 and 89, x 128 rows 75 and 96.  (A single sequence of 1,000:
+// 14.4 and 15.1, which the host cannot tell: the lengths are on the device.)
 struct Plan {
     bool small;
     int tpt, slot_rows, workers;

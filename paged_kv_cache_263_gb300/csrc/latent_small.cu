@@ -8,13 +8,13 @@
 // Nothing is exchanged with another CTA, and what a product costs falls with N.
 //  * Bound by memory at few columns: a tile of 64 keys is 72 KiB, 3,100 cycles of a
 //    SM's share of the bandwidth, and the products take 1,540 (N = 16).  256 sequences
-//    of 17 to 4,096 tokens, 8 heads: 121 us, 5.0 TB/s; a tile takes 3,350 cycles, the
-//    first 12,000 of 210,000 go by until the first tile has landed.
+//    of 17 to 4,096 tokens, 8 heads: 116 us, 5.3 TB/s; a tile takes 3,300 cycles, and
+//    12,000 of 200,000 go by until the first has landed.
 //  * At 64 columns the products take 2,050 cycles, all of them at the full rate of
 //    shared memory (128 bytes a cycle: both operands come from there), and the loads'
-//    576 come on top: a tile takes 3,700.  One context of 131,072, 64 heads: 49 us.
-//    (Two such CTAs a 128-row unit, each tile loaded once for both: 144 us for the
-//    64 sequences x 128 heads that latent_decode.cu does in 123.)
+//    576 come on top: a tile takes 3,700.  One context of 131,072, 64 heads: 47 us.
+//    (Two such CTAs a 128-row unit, each tile loaded once for both: 144 us for 64
+//    sequences x 128 heads that latent_decode.cu did in 123 at that time.)
 //  * Shared memory: queries 72 KiB, two key stages of 72 KiB, P^T 8 KiB.  A stage is
 //    the K-major A operand of the first product and the MN-major A operand of the
 //    second.
