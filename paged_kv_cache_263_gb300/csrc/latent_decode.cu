@@ -183,9 +183,9 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_start = reinterpret_cast<int *>(tmem_slot + 2);        // the range's first sequence, unit and tile
-    long long *s_work = reinterpret_cast<long long *>(bars + NBAR + 4);   // the cut: each, extra
+    int *s_work = reinterpret_cast<int *>(bars + NBAR + 4);   // the cut: each, extra
     int *list = reinterpret_cast<int *>(smem + SBAR + LIST_OFF);
-    long long *scan = reinterpret_cast<long long *>(smem + SMAX);         // setup only
+    int *scan = reinterpret_cast<int *>(smem + SMAX);         // setup only
     auto bar = [&](int i) -> uint32_t { return sbase + SBAR + i * 8; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t c = cluster_rank(), peer = c ^ 1u;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS>(p, k, NCL, MIN_TILES, FEW, SNAP, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
+    const Range range = find_range<THREADS, MIN_TILES, FEW, SNAP>(p, k, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
     Walk walk = range.walk;
     tc_fence_after();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist
@@ -894,8 +894,8 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     if (num_heads > PAGEDKV_LATENT_MAX_HEADS || max_blocks_per_seq > INT32_MAX / BS || num_blocks > INT32_MAX / BS)
         return KV_ERR_UNSUPPORTED;
     if (!out || !q || !context_lens || !cache || !block_tables) return KV_ERR_INVALID;
-    // (a cluster counts its tiles in 32 bits)
-    if (((double)total_q_tokens + num_seqs) * (max_blocks_per_seq / (TK / BS) + 1) / NCL > 2e9) return KV_ERR_UNSUPPORTED;
+    // (tiles are counted in 32 bits)
+    if (((double)total_q_tokens + num_seqs) * (max_blocks_per_seq / (TK / BS) + 1) > 2147483647.0) return KV_ERR_UNSUPPORTED;
     if (!cu_q_lens && total_q_tokens != num_seqs) return KV_ERR_INVALID;
     if (!(scale > 0.f) || !std::isfinite(scale)) return KV_ERR_INVALID;
     if (!pkv_host::aligned(out, 16) || !pkv_host::aligned(q, 16) || !pkv_host::aligned(cache, 16) ||

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_start = reinterpret_cast<int *>(tmem_slot + 2);
     volatile int *votes = reinterpret_cast<volatile int *>(tmem_slot + 5);
-    long long *s_cut = reinterpret_cast<long long *>(tmem_slot + 8);
+    int *s_cut = reinterpret_cast<int *>(tmem_slot + 8);
     volatile float *ref_sh = reinterpret_cast<volatile float *>(smem + SBAR + REF_OFF);
     volatile int *lim_sh = reinterpret_cast<volatile int *>(smem + SBAR + REF_OFF + 256);
     int *list = reinterpret_cast<int *>(smem + SBAR + LIST_OFF);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
     tc_fence_before();
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS>(p, k, p.workers, MIN_TILES, 0, SNAP, k == 0, reinterpret_cast<long long *>(smem + SP), s_start, s_cut, list, LIST);
+    const Range range = find_range<THREADS, MIN_TILES, 0, SNAP>(p, k, k == 0, reinterpret_cast<int *>(smem + SP), s_start, s_cut, list, LIST);
     Walk walk = {uniform(range.walk.s), uniform(range.walk.u), uniform(range.walk.j), uniform(range.walk.left)};
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);

@@ -77,17 +77,12 @@ __device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagg
     return q;
 }
 __device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK - 1) / TK); }
-// a / b for a >= 0, b > 0 (a 64-bit division costs several hundred cycles)
-__device__ __forceinline__ long long quotient(long long a, long long b)
-{
-    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
 // tiles of all its units: every unit is charged the whole context (the causal
 // end of a prompt chunk's earlier units leaves the rest of their charge empty)
-__device__ __forceinline__ long long seq_cost(const LatentParams &p, const Seq &q)
+__device__ __forceinline__ int seq_cost(const LatentParams &p, const Seq &q)
 {
     if (q.n <= 0) return 0;
-    return (long long)(q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
+    return (q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
 }
 
 struct Item {
@@ -103,22 +98,23 @@ struct Walk {
 };
 // The range of worker k of nc: W tiles in nc runs, the first W % nc one longer.
 struct Cut {
-    long long each, extra;
-    __device__ __forceinline__ long long begin(int k) const { return k * each + min((long long)k, extra); }
-    __device__ __forceinline__ int owner(long long pos) const
+    int each, extra;
+    __device__ __forceinline__ int begin(int k) const { return k * each + min(k, extra); }
+    __device__ __forceinline__ int owner(int pos) const
     {
-        return (int)(pos < extra * (each + 1) ? quotient(pos, each + 1) : extra + quotient(pos - extra * (each + 1), each));
+        const bool longer = pos < extra * (each + 1);
+        return (longer ? 0 : extra) + (pos - (longer ? 0 : extra * (each + 1))) / (longer ? each + 1 : each);
     }
 };
 
 // A worker's range: where it starts, and how it was cut.
 struct Range {
     Walk walk;
-    long long begin;         // its place among all tiles
+    int begin;               // its place among all tiles (which the host has made sure are fewer than 2^31)
     int tiles, nc, snap;     // its tiles; workers with work; tiles that a cut moves to a unit's end
     int s_first, listed;     // its first sequence; sequences tabled in shared memory from there on
     const int *list;
-    const long long *cut;    // shared memory: Cut's two numbers
+    const int *cut;          // shared memory: Cut's two numbers
 };
 __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g, Walk &w, Item &it)
 {
@@ -152,41 +148,42 @@ __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g,
 
 // Finds worker k's range (all threads of the CTA; two barriers and one more at the
 // end): prefix sums of the sequences' costs, a run of consecutive sequences a
-// thread.  `each` tiles a worker at least, if there are as many; but up to `few`
-// workers with one.  A cut that falls within `snap` tiles of a unit's end moves there:
+// thread.  EACH tiles a worker at least, if there are as many; but up to FEW workers
+// with one.  A cut that falls within SNAP tiles of a unit's end moves there:
 // the worker would spend more on the few tiles' queries and partial sums.  scan:
 // THREADS / 32 numbers, start: 3, cut: 4, list: 3 x listed, all in shared memory;
 // start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
-template <int THREADS>
-__device__ __forceinline__ Range find_range(const LatentParams &p, int k, int workers, int each, int few, int snap, bool flagging,
-                                            long long *scan, int *start, long long *cut_sh, int *list, int listed)
+template <int THREADS, int EACH, int FEW, int SNAP>
+__device__ __forceinline__ Range find_range(const LatentParams &p, int k, bool flagging, int *scan, int *start, int *cut_sh, int *list,
+                                            int listed)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.num_seqs + THREADS - 1) / THREADS;
     const int sa = min(p.num_seqs, (int)threadIdx.x * per), sb = min(p.num_seqs, sa + per);
-    long long mine = 0;
+    int mine = 0;
     for (int s = sa; s < sb; ++s) mine += seq_cost(p, read_seq(p, s, flagging));
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    long long before = 0, W = 0;
+    int before = 0, W = 0;
+#pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
-        const long long t = scan[i];
+        const int t = scan[i];
         if (i < warp) before += t;
         W += t;
     }
     Range g;
-    g.nc = (int)max(1ll, min((long long)workers, max(W / each, min(W, (long long)few))));
+    g.nc = max(1, min(p.workers, max(W / EACH, min(W, FEW))));
     Cut cut;
-    cut.each = quotient(W, g.nc);
+    cut.each = W / g.nc;
     cut.extra = W - cut.each * g.nc;
-    g.snap = snap = (int)min((long long)snap, cut.each / 2);
-    const long long w0 = k < g.nc ? cut.begin(k) : W, w1 = k < g.nc ? cut.begin(k + 1) : W;
+    g.snap = min(SNAP, cut.each * 2 / 3);
+    const int w0 = k < g.nc ? cut.begin(k) : W, w1 = k < g.nc ? cut.begin(k + 1) : W;
     if (threadIdx.x == 0) {
         cut_sh[0] = cut.each;
         cut_sh[1] = cut.extra;
@@ -195,20 +192,20 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
     // where it begins and ends, by the thread whose sequences hold the place
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-        long long pos = e == 0 ? w0 : w1, b = before + incl - mine;
+        int pos = e == 0 ? w0 : w1, b = before + incl - mine;
         if (w0 >= w1 || pos < b || pos >= b + mine) continue;
         int s = sa;
-        for (; s < sb; ++s) {
-            const long long cost = seq_cost(p, read_seq(p, s, false));
+        for (; s < sb - 1; ++s) {
+            const int cost = seq_cost(p, read_seq(p, s, false));
             if (pos < b + cost) break;
             b += cost;
         }
         const int KT = seq_tiles(read_seq(p, s, false));
-        int u = (int)quotient(pos - b, KT), t = (int)(pos - b - (long long)u * KT);
-        if (t <= snap) {
+        int u = (pos - b) / KT, t = pos - b - u * KT;
+        if (t <= g.snap) {
             pos -= t;
             t = 0;
-        } else if (KT - t <= snap) {
+        } else if (KT - t <= g.snap) {
             pos += KT - t;
             ++u;
             t = 0;
@@ -231,7 +228,7 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
         list[3 * i + 2] = q.L;
     }
     g.begin = w0 < w1 ? cut_sh[2] : W;
-    g.tiles = w0 < w1 ? (int)max(0ll, cut_sh[3] - cut_sh[2]) : 0;
+    g.tiles = w0 < w1 ? max(0, cut_sh[3] - cut_sh[2]) : 0;
     g.walk = {g.s_first, start[1], start[2], g.tiles};
     g.listed = listed;
     g.list = list;
@@ -245,7 +242,7 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, int wo
 __device__ __forceinline__ void list_merge(const LatentParams &p, const Range &g, const Item &it, int k, int rows)
 {
     const Cut cut = {g.cut[0], g.cut[1]};
-    const long long first = g.begin + (g.tiles - it.left);
+    const int first = g.begin + (g.tiles - it.left);
     // (a cut in the unit's last `snap` tiles has moved to its end)
     const int kl = max(k, min(g.nc - 1, cut.owner(first + min(it.kt, seq_tiles(it.q) - g.snap) - 1)));
     p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
