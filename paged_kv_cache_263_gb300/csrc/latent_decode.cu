@@ -10,8 +10,9 @@
 // costs 2 x (576 + 512) operations a key.  One token of 128 heads makes 242
 // operations a byte, just under the GPU's ratio (1,916 TFLOP/s : 6,789 GB/s =
 // 282), so decode is bound by memory as long as the products run on the tensor
-// cores with full tiles: 128 query rows = (tokens x heads) packed, padded with
-// zero rows when a sequence has fewer.
+// cores with full tiles: a sequence's (row, head) pairs in units of 128, padded with
+// zero rows when there are fewer.  (A unit may begin and end within a row: 12 chunks
+// of 70 rows x 96 heads take 117 us; in units of whole rows they took 140.)
 //
 // Why a pair of CTAs.  The output of 128 rows is 128 x 512 fp32, all of one SM's
 // tensor memory, and the queries (144 KiB) and a key tile do not fit its shared
@@ -253,8 +254,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             const int nblk = (it.q.L + BS - 1) / BS;
             // the item's queries, into L2 (this warp runs up to four tiles ahead; the
             // first item's are being loaded already)
-            for (int r = lane; u > 0 && r < it.toks * p.heads; r += 32) {
-                const uint16_t *src = p.q + ((size_t)(it.q.a + it.t0) * p.heads + r) * LKD;
+            for (int r = lane; u > 0 && r < it.rows; r += 32) {
+                const uint16_t *src = p.q + ((size_t)it.q.a * p.heads + it.r0 + r) * LKD;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c * HALF + e * 64));
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(src + LAT + c * RHALF));
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             Walk ahead = walk;
             Item q;
             if (!next_item(p, range, ahead, q)) return;
-            const int rows = q.toks * p.heads;
-            const uint16_t *src = p.q + ((size_t)(q.q.a + q.t0) * p.heads + w * 32) * LKD;
+            const int rows = q.rows;
+            const uint16_t *src = p.q + ((size_t)q.q.a * p.heads + q.r0 + w * 32) * LKD;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             const int lr = lane >> 3, le = lane & 7;      // row within four, piece
             const uint32_t qt = sbase + SQ + w * 4096;
@@ -448,10 +449,10 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
         bool ok = true;
         if (grp == 1) load_queries();
         while (ok && next_item(p, range, walk, it)) {
-            const int rows = it.toks * p.heads;
+            const int rows = it.rows;
             const bool active = w * 32 < rows;
-            const int tok = min(r, rows - 1) / p.heads;
-            const int first_pos = it.q.L - it.q.n + it.t0;
+            const int first_pos = it.q.L - it.q.n + (int)((uint32_t)it.r0 / (uint32_t)p.heads);
+            const int tok = (int)((uint32_t)(it.r0 + min(r, rows - 1)) / (uint32_t)p.heads - (uint32_t)it.r0 / (uint32_t)p.heads);
             const int pos = it.q.L > 0 ? first_pos + tok : -1;    // the last key this row sees
             const int pos_min = it.q.L > 0 ? first_pos : -1;
             float m_ref = -INFINITY, l = 0.f;                     // (l relative to m_ref)
@@ -614,8 +615,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             const bool whole = it.j0 == 0 && it.j1 == it.kt;
             const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
             if (active) {
-                const size_t row0 = (size_t)(it.q.a + it.t0) * p.heads;
-                const size_t pr0 = (size_t)slot * p.slot_rows, pr = pr0 + r;
+                const size_t row0 = (size_t)it.q.a * p.heads + it.r0;
+                const size_t pr0 = (size_t)slot * p.unit, pr = pr0 + r;
                 const int d0 = c * HALF + grp * (HALF / 2);
                 const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
                 // 4 lanes exchange their rows' pieces so that they store 64 bytes of one
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
         return k;
     };
     // partial i of worker k's unit: the first is in its worker's second slot, the others in their worker's first
-    auto slot = [&](int k, int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.slot_rows; };
+    auto slot = [&](int k, int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.unit; };
     auto store = [&](int64_t row, int q4, const float4 &a, float l) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         reinterpret_cast<uint2 *>(p.out + row * LAT + q4 * 128)[lane] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
@@ -839,24 +840,23 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
 // 14.4 and 15.1, which the host cannot tell: the lengths are on the device.)
 struct Plan {
     bool small;
-    int tpt, slot_rows, workers;
+    int unit, workers;
     size_t desc2, ml, o, total;    // workspace: merge list, partial sums, partial outputs
 };
-Plan plan(bool small, int heads)
+Plan plan(bool small)
 {
     Plan y;
     y.small = small;
     y.workers = small ? MAX_WORKERS : NCL;
-    y.tpt = (small ? 64 : 128) / heads;
-    y.slot_rows = y.tpt * heads;
+    y.unit = small ? 64 : 128;
     y.desc2 = y.workers * sizeof(int4);
     y.ml = 4096;
-    y.o = y.ml + (((size_t)2 * y.workers * y.slot_rows * 8 + 255) & ~(size_t)255);
-    y.total = y.o + (size_t)2 * y.workers * y.slot_rows * LAT * 4;
+    y.o = y.ml + (((size_t)2 * y.workers * y.unit * 8 + 255) & ~(size_t)255);
+    y.total = y.o + (size_t)2 * y.workers * y.unit * LAT * 4;
     return y;
 }
 static_assert(MAX_WORKERS * (sizeof(int4) + 8) <= 4096, "merge list");
-static_assert(MAX_WORKERS == 2 * NCL, "64 / heads x 2 <= 128 / heads: the pairs' workspace is never the smaller");
+static_assert(MAX_WORKERS == 2 * NCL, "both layouts take the same workspace");
 
 }  // namespace
 
@@ -878,7 +878,7 @@ size_t paged_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q_t
     if (num_seqs < 1 || total_q_tokens < 1 || num_heads < 1 || num_heads > PAGEDKV_LATENT_MAX_HEADS ||
         max_blocks_per_seq < 1)
         return 0;
-    return plan(false, num_heads).total;
+    return plan(false).total;
 }
 
 kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_lens, const int32_t *context_lens,
@@ -905,7 +905,7 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     const size_t need =
         paged_latent_attention_workspace_size(num_seqs, total_q_tokens, num_heads, max_blocks_per_seq);
     if (need && (!workspace || workspace_bytes < need || !pkv_host::aligned(workspace, 256))) return KV_ERR_INVALID;
-    const Plan y = plan((int64_t)total_q_tokens * num_heads <= 64ll * num_seqs && num_heads <= 64, num_heads);
+    const Plan y = plan((int64_t)total_q_tokens * num_heads <= 64ll * num_seqs && num_heads <= 64);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     LatentParams p;
     p.out = static_cast<uint16_t *>(out);
@@ -917,12 +917,11 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     p.desc2 = reinterpret_cast<int64_t *>(ws + y.desc2);
     p.part_ml = reinterpret_cast<float *>(ws + y.ml);
     p.part_o = reinterpret_cast<float *>(ws + y.o);
-    p.slot_rows = y.slot_rows;
+    p.unit = y.unit;
     p.workers = y.workers;
     p.num_seqs = num_seqs;
     p.rows = total_q_tokens;
     p.heads = num_heads;
-    p.tpt = y.tpt;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * LOG2E;

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tO = tmem + 128, tL = tmem + 384;              // S^T at 64 b
     Item it = {};
     // columns that the products take: the unit's rows, in steps of 16
-    auto columns = [&]() -> int { return (it.toks * p.heads + 15) & ~15; };
+    auto columns = [&]() -> int { return (it.rows + 15) & ~15; };
 
     if (warp == W_PROD) {
         // ======================= producer: a box of 2 KiB (a block's 16 keys x 64 dims)
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 for (int e = lane; e < boxes; e += 32)
                     tma_load_2d(sbase + (e % 9) * CHUNK_BYTES + (e / 9) * 2048, &qmap, (e % 9) * 64,
-                                (it.q.a + it.t0) * p.heads + (e / 9) * 16, bar(B_Q));
+                                it.q.a * p.heads + it.r0 + (e / 9) * 16, bar(B_Q));
             };
             if (items == 0) queries();
             for (int j = it.j0; ok && j < it.j1; ++j) {
@@ -333,11 +333,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             return wait_bar(bar(B_MEET), met++ & 1, abort_flag);
         };
         while (ok && next_item(p, range, walk, it)) {
-            const int rows = it.toks * p.heads, N = columns();
+            const int rows = it.rows, N = columns();
             const int c0 = grp * (N >> 1), steps = N >> 4;                      // this warp's columns: 8 steps from c0
-            const int see0 = it.q.L > 0 ? it.q.L - it.q.n + it.t0 + 1 : 0;      // keys that the first token sees
+            // keys that the first row sees
+            const int see0 = it.q.L > 0 ? it.q.L - it.q.n + 1 + (int)((uint32_t)it.r0 / (uint32_t)p.heads) : 0;
             if (tid < 64) {
-                lim_sh[tid] = it.q.L > 0 ? see0 + min(tid, rows - 1) / p.heads : 0;
+                lim_sh[tid] = it.q.L > 0 ? it.q.L - it.q.n + 1 + (int)((uint32_t)(it.r0 + min(tid, rows - 1)) / (uint32_t)p.heads) : 0;
                 ref_sh[tid] = 0.f;
             }
             if (!meet()) break;
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_after();
             const bool whole = it.j0 == 0 && it.j1 == it.kt;
             const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
-            const size_t row0 = (size_t)(it.q.a + it.t0) * p.heads, pr0 = (size_t)slot * p.slot_rows;
+            const size_t row0 = (size_t)it.q.a * p.heads + it.r0, pr0 = (size_t)slot * p.unit;
             // the sums: every lane of their accumulator holds the column's
             volatile float *sum_sh = reinterpret_cast<volatile float *>(const_cast<int *>(lim_sh));
             if (w == 0) {
@@ -524,7 +525,7 @@ uint32_t take_status()
     return v;
 }
 
-// params: a LatentParams with tpt x heads <= 64
+// params: a LatentParams with units of 64
 kv_status launch(const void *params, const void *q, const void *cache, cudaStream_t st)
 {
     const LatentParams &p = *static_cast<const LatentParams *>(params);

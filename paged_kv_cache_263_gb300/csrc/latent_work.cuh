@@ -24,11 +24,11 @@ struct LatentParams {
     const int32_t *cu, *lens, *tables;
     int4 *desc;       // [workers] the unit to merge whose first tiles worker k holds: 1 (0: none), partials, rows, -
     int64_t *desc2;   // [workers] the unit's first (row, head)
-    float *part_o;    // [2 workers][slot_rows][512]
-    float *part_ml;   // [2 workers][slot_rows][2]
-    int slot_rows;    // rows of a unit, at most
+    float *part_o;    // [2 workers][unit][512]
+    float *part_ml;   // [2 workers][unit][2]
+    int unit;         // (row, head) pairs of a unit, at most: 128 or 64
     int workers;
-    int num_seqs, rows, heads, tpt, max_blocks, num_blocks;
+    int num_seqs, rows, heads, max_blocks, num_blocks;
     float scale_log2;
 };
 
@@ -82,12 +82,12 @@ __device__ __forceinline__ int seq_tiles(const Seq &q) { return max(1, (q.L + TK
 __device__ __forceinline__ int seq_cost(const LatentParams &p, const Seq &q)
 {
     if (q.n <= 0) return 0;
-    return (q.n <= p.tpt ? 1 : (q.n + p.tpt - 1) / p.tpt) * seq_tiles(q);
+    return (int)((uint32_t)(q.n * p.heads + p.unit - 1) / (uint32_t)p.unit) * seq_tiles(q);
 }
 
 struct Item {
     Seq q;
-    int s, t0, toks;     // the unit's first token within the sequence, and its tokens
+    int s, r0, rows;     // the unit's first (row, head) pair within the sequence, and its pairs
     int j0, j1, kt;      // its tiles in this worker's range, and all its tiles
     int left;            // tiles of the range from its first one on
 };
@@ -123,23 +123,24 @@ __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g,
         Seq q;
         if (i < g.listed) q = {g.list[3 * i], g.list[3 * i + 1], g.list[3 * i + 2]};
         else q = read_seq(p, w.s, false);
-        const int t0 = w.u * p.tpt;
-        if (t0 >= q.n) {             // (a sequence without rows, too)
+        const int r0 = w.u * p.unit, all = q.n * p.heads;
+        if (r0 >= all) {             // (a sequence without rows, too)
             ++w.s;
             w.u = w.j = 0;
             continue;
         }
         it.q = q;
         it.s = w.s;
-        it.t0 = t0;
-        it.toks = min(p.tpt, q.n - t0);
+        it.r0 = r0;
+        it.rows = min(p.unit, all - r0);
         it.j0 = w.j;
         it.left = w.left;
         const int jend = min(seq_tiles(q), w.j + w.left);
         w.left -= jend - w.j;
         ++w.u;
         w.j = 0;
-        it.kt = max(1, (q.L - q.n + t0 + it.toks + TK - 1) / TK);   // tiles that its last row sees
+        const int last = q.n == 1 ? 0 : (int)((uint32_t)(r0 + it.rows - 1) / (uint32_t)p.heads);
+        it.kt = max(1, (q.L - q.n + last + 1 + TK - 1) / TK);       // tiles that its last row sees
         it.j1 = min(jend, it.kt);
         if (it.j0 < it.kt) return true;
     }
@@ -245,7 +246,7 @@ __device__ __forceinline__ void list_merge(const LatentParams &p, const Range &g
     const int first = g.begin + (g.tiles - it.left);
     // (a cut in the unit's last `snap` tiles has moved to its end)
     const int kl = max(k, min(g.nc - 1, cut.owner(first + min(it.kt, seq_tiles(it.q) - g.snap) - 1)));
-    p.desc2[k] = (int64_t)(it.q.a + it.t0) * p.heads;
+    p.desc2[k] = (int64_t)it.q.a * p.heads + it.r0;
     p.desc[k] = make_int4(1, kl - k + 1, rows, 0);
 }
 
