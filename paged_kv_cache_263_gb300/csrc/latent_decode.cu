@@ -72,7 +72,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int HALF = LAT / 2, RHALF = ROPE / 2;   // a CTA's latent and rotary dims
 constexpr int NCL = 76;                           // clusters: a pair of CTAs on each pair of the 152 SMs
-// Tiles a cluster takes at least, if there are as many, but up to FEW clusters with one:
+// Tiles a cluster takes at least, if there are as many, but up to FEW clusters with two,
+// or one if that is all (one and a half would cut many units, each with its queries):
 // a tile costs a cluster 1.4 us, a cluster more the sequence 128 rows more to merge.
 // (1,000 keys, 128 heads, one tile or two a cluster: 15.8 and 17.2 us; eight sequences of
 // 500 to 2,000, two or three: 29.4 and 26.0.)

@@ -150,7 +150,7 @@ __device__ __forceinline__ bool next_item(const LatentParams &p, const Range &g,
 // Finds worker k's range (all threads of the CTA; two barriers and one more at the
 // end): prefix sums of the sequences' costs, a run of consecutive sequences a
 // thread.  EACH tiles a worker at least, if there are as many; but up to FEW workers
-// with one.  A cut that falls within SNAP tiles of a unit's end moves there:
+// with one, if that is all, or two.  A cut that falls within SNAP tiles of a unit's end moves there:
 // the worker would spend more on the few tiles' queries and partial sums.  scan:
 // THREADS / 32 numbers, start: 3, cut: 4, list: 3 x listed, all in shared memory;
 // start[0] = num_seqs, start[1] = start[2] = 0 beforehand.
@@ -179,7 +179,7 @@ __device__ __forceinline__ Range find_range(const LatentParams &p, int k, bool f
         W += t;
     }
     Range g;
-    g.nc = max(1, min(p.workers, max(W / EACH, min(W, FEW))));
+    g.nc = max(1, min(p.workers, W <= FEW ? W : max(W / EACH, min(W / 2, FEW))));
     Cut cut;
     cut.each = W / g.nc;
     cut.extra = W - cut.each * g.nc;
