@@ -471,7 +471,8 @@ PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t laten
  * n rows), and row i sees keys 0 .. L-n+i.
  *
  *  out            device bf16 [total_q_tokens][num_heads][512]
- *  q              device bf16 [total_q_tokens][num_heads][576]
+ *  q              device bf16 [total_q_tokens][num_heads][576]; a query that is not
+ *                 finite gives NaN in its own output row alone
  *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
  *                 sequence (total_q_tokens = num_seqs)
  *  context_lens   device int32 [num_seqs]; L = 0 (a padded entry): the
@@ -518,7 +519,7 @@ PAGEDKV_API kv_status paged_latent_attention(void *out, const void *q, const int
  * nq rows sees the first nk-nq+i+1 of its nk keys (a row that sees none: zeros).
  *
  *  out            device bf16 [total_q_tokens][num_heads][128]
- *  q              device bf16 [total_q_tokens][num_heads][192]
+ *  q              device bf16 [total_q_tokens][num_heads][192], as above
  *  kv             device bf16 [total_k_tokens][num_heads][256]; a sequence's own
  *                 keys have to be finite, as above
  *  k_rope         device bf16, row t at k_rope + t x k_rope_stride, 64 values

@@ -608,7 +608,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 ++sums;
                 const float lo = other[0], mo = other[128];
                 const float m = fmaxf(m_ref, mo);
-                l = (m_ref == -INFINITY ? 0.f : l * ex2(m_ref - m)) + (mo == -INFINITY ? 0.f : lo * ex2(mo - m));
+                // (without a score above -inf a sum is 0, or NaN if the query was not finite)
+                l = (m_ref == -INFINITY ? l : l * ex2(m_ref - m)) + (mo == -INFINITY ? lo : lo * ex2(mo - m));
                 m_ref = m;
             }
             if (!wait_bar(bar(B_DRAIN), items & 1, abort_flag)) break;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                 const size_t row0 = (size_t)it.q.a * p.heads + it.r0;
                 const size_t pr0 = (size_t)slot * p.unit, pr = pr0 + r;
                 const int d0 = c * HALF + grp * (HALF / 2);
-                const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 // 4 lanes exchange their rows' pieces so that they store 64 bytes of one
                 // row together (a store of 16 bytes to each of 32 rows touches 32 lines)
 #pragma unroll 1
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
                 if (!whole && r < rows && c == 0 && grp == 0) {
-                    p.part_ml[2 * pr] = l > 0.f ? m_ref : -INFINITY;
+                    p.part_ml[2 * pr] = l == 0.f ? -INFINITY : m_ref;
                     p.part_ml[2 * pr + 1] = l;
                 }
             }
@@ -745,7 +746,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
     // partial i of worker k's unit: the first is in its worker's second slot, the others in their worker's first
     auto slot = [&](int k, int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.unit; };
     auto store = [&](int64_t row, int q4, const float4 &a, float l) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;       // (NaN stays NaN, also with partial sums left out)
         reinterpret_cast<uint2 *>(p.out + row * LAT + q4 * 128)[lane] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     };
     // few partials: a warp a quarter of a row

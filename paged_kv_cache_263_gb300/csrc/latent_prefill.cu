@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok || !wait_bar(bar(B_DRAIN + g), done & 1, abort_flag)) break;
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             const int r4 = w * 32 + (lane & ~3), e4 = lane & 3;
             uint16_t *dst = p.out + ((size_t)(it.row0 + g * BM) * p.heads + it.head) * D;
 #pragma unroll 1

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     p.part_ml[2 * (pr0 + tid)] = l == 0.f ? -INFINITY : ref_sh[tid];
                     p.part_ml[2 * (pr0 + tid) + 1] = l;
                 }
-                sum_sh[tid] = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                sum_sh[tid] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
             }
             if (!meet()) break;
             // a lane holds one dim of 16 columns (rows of the output) at a time
