@@ -34,14 +34,31 @@ struct LatentParams {
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
 
+// PEER: what completes the phase comes from the other CTA of the cluster
+template <bool PEER>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
+{
+    if (!PEER) return mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // bounded wait that also gives up once another warp of the CTA has
+template <bool PEER = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = try_wait<PEER>(bar, parity);
     if (!ok) {
         const unsigned long long t0 = globaltimer();
         for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(bar, parity)) {
+            if (try_wait<PEER>(bar, parity)) {
                 ok = true;
                 break;
             }
