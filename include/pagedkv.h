@@ -488,7 +488,8 @@ PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t laten
  *                 L-1 does not matter.
  *  num_heads      1 .. 128 (KV_ERR_UNSUPPORTED above)
  *  sizes          (total_q_tokens + num_seqs) x (max_blocks_per_seq / 4 + 1) is
- *                 at most 2^31 - 1 (KV_ERR_UNSUPPORTED above)
+ *                 at most 2^31 - 1, max_blocks_per_seq at most 2^27 - 4
+ *                 (KV_ERR_UNSUPPORTED above)
  *  scale          > 0 and finite
  *  workspace      device scratch of paged_latent_attention_workspace_size()
  *                 bytes, 256-byte aligned.  Calls that may overlap on the GPU

@@ -892,7 +892,8 @@ kv_status paged_latent_attention(void *out, const void *q, const int32_t *cu_q_l
     if (num_seqs < 0 || total_q_tokens < 0) return KV_ERR_INVALID;
     if (num_seqs == 0 || total_q_tokens == 0) return KV_OK;
     if (num_heads < 1 || max_blocks_per_seq < 1 || num_blocks < 1) return KV_ERR_INVALID;
-    if (num_heads > PAGEDKV_LATENT_MAX_HEADS || max_blocks_per_seq > INT32_MAX / BS || num_blocks > INT32_MAX / BS)
+    // (key positions are counted in 32 bits, up to the end of a context's last tile)
+    if (num_heads > PAGEDKV_LATENT_MAX_HEADS || max_blocks_per_seq > (INT32_MAX - TK + 1) / BS || num_blocks > INT32_MAX / BS)
         return KV_ERR_UNSUPPORTED;
     if (!out || !q || !context_lens || !cache || !block_tables) return KV_ERR_INVALID;
     // (tiles are counted in 32 bits)
