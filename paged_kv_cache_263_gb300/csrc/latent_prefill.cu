@@ -40,6 +40,7 @@
 // Warps 0 and 1: MMA issuers of the query tiles, which take turns; 2: TMA; 3: items;
 // 4-7 and 8-11: softmax and epilogue of the query tiles, one row a thread.
 #include "common.cuh"
+#include "latent_loads.h"
 #include "trace.h"
 
 #include <algorithm>
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         griddep_wait();                  // everything before the kernel on the stream
         int t = 0;                       // key tiles
         bool ok = true;
+        pkv_loads::Asked asked;
         int tail_first = BN;             // rows of the last tile loaded that are its sequence's
         auto zero_tail = [&]() -> bool {
             const int x = t - 1, first = max(0, tail_first);
@@ -450,6 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 3; ++i)
                     tma_load_2d(sbase + g * Q_TILE + i * CHUNK_BYTES, &qmap, it.head * QKD + 64 * i, it.row0 + g * BM, bar(B_Q + g));
             }
+            ++asked.queries[g];
             __syncwarp();
         };
         for (; ok && read_item(it); ++k) {
@@ -478,18 +481,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive_expect_tx(k0, CHUNK_BYTES);
                     load(0, k0);
                 }
+                asked.tiles[pkv_loads::KEY0] = t + 1;
                 if (t >= 2 && !wait_bar(bar(B_VE + (t & 1)), ((t - 2) >> 1) & 1, abort_flag)) ok = false;
                 if (lane == 0 && ok) {
                     mbar_arrive_expect_tx(kb, 2 * CHUNK_BYTES);
                     load(1, kb);
                     load(2, kb);
                 }
+                if (ok) asked.tiles[pkv_loads::KEYS] = t + 1;
                 if (t >= 1 && ok && !wait_bar(bar(B_KE + ((t - 1) & 1)), ((t - 1) >> 1) & 1, abort_flag)) ok = false;
                 if (ok && j == 0) {
                     // query tile 1: its first products of the item before are among those just waited for
                     if (k > 0) ok = wait_bar(bar(B_QFREE + 1), (k - 1) & 1, abort_flag);
-                    if (ok && it.rows > BM) queries(1);
-                    else if (lane == 0) mbar_arrive(bar(B_Q + 1));
+                    if (ok && it.rows > BM) {
+                        queries(1);
+                    } else if (ok) {
+                        if (lane == 0) mbar_arrive(bar(B_Q + 1));
+                        ++asked.queries[1];
+                    }
                 }
                 if (!ok) break;
                 if (lane == 0 && j == max(0, it.T - 3)) mbar_arrive(bar(B_NEXT));
@@ -498,21 +507,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     load(3, vb);
                     load(4, vb);
                 }
+                asked.tiles[pkv_loads::VALUES] = t + 1;
                 __syncwarp();
             }
             tail_first = it.nk - (it.T - 1) * BN;
         }
         if (ok && tail_first < BN) (void)zero_tail();
-        if (*abort_flag) {               // loads in flight land before the CTA exits
-            // (bounded: a tile whose chunks were not all asked for never completes)
-            for (int x = max(0, t - 1); x <= t; ++x) {
-                (void)mbar_wait_bounded(bar(B_K0 + (x & 1)), (x >> 1) & 1);
-                (void)mbar_wait_bounded(bar(B_KF + (x & 1)), (x >> 1) & 1);
-                (void)mbar_wait_bounded(bar(B_VF + (x & 1)), (x >> 1) & 1);
-            }
-            for (int g = 0; g < 2; ++g)
-                for (int x = max(0, k - 1); x <= k; ++x) (void)mbar_wait_bounded(bar(B_Q + g), x & 1);
-        }
+        if (*abort_flag)                 // loads in flight land before the CTA exits
+            asked.drain(
+                [&](int part, int x) {
+                    const int b = part == pkv_loads::KEY0 ? B_K0 : part == pkv_loads::KEYS ? B_KF : B_VF;
+                    (void)mbar_wait_bounded(bar(b + (x & 1)), (x >> 1) & 1);
+                },
+                [&](int g, int x) { (void)mbar_wait_bounded(bar(B_Q + g), x & 1); });
     } else if (warp < W_MMA + 2) {
         // ======================= MMA issuers.  They take turns: one's second product
         // of tile j and first of j + 1, then the other's, so that one query tile's

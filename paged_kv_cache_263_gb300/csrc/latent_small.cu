@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // they left every 70, 2,500 cycles a tile); each lane reads the id of block
         // lane % 4 of the next tile while it waits
         const int blk = lane & 3;
-        int u = 0, items = 0;       // halves, items
+        int u = 0, items = 0, asked = 0;   // halves, items, items whose queries have been asked for
         bool ok = true;
         for (; ok && next_item(p, range, walk, it); ++items) {
             const int32_t *bt = p.tables + (size_t)it.s * p.max_blocks;
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = lane; e < boxes; e += 32)
                     tma_load_2d(sbase + (e % 9) * CHUNK_BYTES + (e / 9) * 2048, &qmap, (e % 9) * 64,
                                 it.q.a * p.heads + it.r0 + (e / 9) * 16, bar(B_Q));
+                ++asked;
             };
             if (items == 0) queries();
             for (int j = it.j0; ok && j < it.j1; ++j) {
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (*abort_flag) {    // loads in flight land before the CTA exits
             for (int x = max(0, u - 2 * STAGES); x < u; ++x)
                 (void)mbar_wait_bounded(bar(B_KVF + 2 * ((x >> 1) % STAGES) + (x & 1)), ((x >> 1) / STAGES) & 1);
-            if (items > 0) (void)mbar_wait_bounded(bar(B_Q), (items - 1) & 1);
+            if (asked > 0) (void)mbar_wait_bounded(bar(B_Q), (asked - 1) & 1);
         }
     } else if (warp == W_S) {
         // ======================= S^T = K Q^T
