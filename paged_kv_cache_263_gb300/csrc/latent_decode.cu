@@ -862,13 +862,7 @@ static_assert(MAX_WORKERS == 2 * NCL, "both layouts take the same workspace");
 }  // namespace
 
 namespace pkv_latent {
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 }  // namespace pkv_latent
 
 extern "C" {

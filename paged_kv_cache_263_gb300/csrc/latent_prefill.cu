@@ -775,13 +775,7 @@ Layout layout(int num_seqs)
 }  // namespace
 
 namespace pkv_latent_prefill {
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 }  // namespace pkv_latent_prefill
 
 extern "C" {

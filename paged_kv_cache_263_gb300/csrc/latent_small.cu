@@ -518,13 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 namespace pkv_latent_small {
 
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 
 // params: a LatentParams with units of 64
 kv_status launch(const void *params, const void *q, const void *cache, cudaStream_t st)

@@ -1529,13 +1529,7 @@ Trace *trace_for_call()
 }  // namespace
 
 namespace pkv_prefill {
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 }  // namespace pkv_prefill
 
 extern "C" {

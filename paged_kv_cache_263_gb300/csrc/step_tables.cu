@@ -227,13 +227,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
 }  // namespace
 
 namespace pkv_step {
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 }  // namespace pkv_step
 
 extern "C" kv_status kv_build_step_tables(int32_t *block_tables, int32_t max_blocks_per_seq,

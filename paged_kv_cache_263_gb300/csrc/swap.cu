@@ -126,13 +126,7 @@ kv_status launch(bool to_host, void *k_cache, void *v_cache, int32_t num_blocks,
 }  // namespace
 
 namespace pkv_swap {
-uint32_t take_status()
-{
-    uint32_t v = 0, z = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof v) != cudaSuccess) return 0;
-    if (v) cudaMemcpyToSymbol(g_status, &z, sizeof z);
-    return v;
-}
+cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 }  // namespace pkv_swap
 
 extern "C" {
