@@ -71,14 +71,7 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int HALF = LAT / 2, RHALF = ROPE / 2;   // a CTA's latent and rotary dims
-constexpr int NCL = 76;                           // clusters: a pair of CTAs on each pair of the 152 SMs
-// Tiles a cluster takes at least, if there are as many, but up to FEW clusters with two,
-// or one if that is all (one and a half would cut many units, each with its queries):
-// a tile costs a cluster 1.4 us, a cluster more the sequence 128 rows more to merge.
-// (1,000 keys, 128 heads, one tile or two a cluster: 15.8 and 17.2 us; eight sequences of
-// 500 to 2,000, two or three: 29.4 and 26.0.)
-constexpr int MIN_TILES = 3, FEW = 32;
-constexpr int SNAP = 3;                           // (eight sequences of 500 to 2,000, 128 heads: 26.4 us without, 22.5 with)
+constexpr int NCL = pkv_split::PAIR.workers;      // clusters: a pair of CTAs on each pair of the 152 SMs
 constexpr int STAGES = 4;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys x 64 dims
 constexpr uint32_t ROPE_OFF = 4 * CHUNK_BYTES;    // within a stage
@@ -234,7 +227,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
     __syncthreads();      // the barriers exist: the peer may use them once it has waited for this CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS, MIN_TILES, FEW, SNAP>(p, k, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
+    constexpr pkv_split::Rule rule = pkv_split::PAIR;
+    const Range range = find_range<THREADS>(p, rule, k, blockIdx.x == 0, scan, s_start, s_work, list, LIST);
     Walk walk = range.walk;
     tc_fence_after();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // the peer's barriers exist
@@ -613,8 +607,8 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             }
             if (!wait_bar(bar(B_DRAIN), items & 1, abort_flag)) break;
             tc_fence_after();
-            const bool whole = it.j0 == 0 && it.j1 == it.kt;
-            const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
+            const bool whole = it.whole();
+            const int slot = pkv_split::own_slot(k, it);
             if (active) {
                 const size_t row0 = (size_t)it.q.a * p.heads + it.r0;
                 const size_t pr0 = (size_t)slot * p.unit, pr = pr0 + r;
@@ -742,8 +736,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS, 4) latent_merge_kernel(const
         }
         return k;
     };
-    // partial i of worker k's unit: the first is in its worker's second slot, the others in their worker's first
-    auto slot = [&](int k, int i) -> size_t { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)) * p.unit; };
+    // partial i of worker k's unit
+    auto slot = [&](int k, int i) -> size_t { return (size_t)pkv_split::partial_slot(k, i) * p.unit; };
     auto store = [&](int64_t row, int q4, const float4 &a, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l;       // (NaN stays NaN, also with partial sums left out)
         reinterpret_cast<uint2 *>(p.out + row * LAT + q4 * 128)[lane] = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
@@ -848,8 +842,8 @@ Plan plan(bool small)
 {
     Plan y;
     y.small = small;
-    y.workers = small ? MAX_WORKERS : NCL;
-    y.unit = small ? 64 : 128;
+    y.workers = (small ? pkv_split::ONE : pkv_split::PAIR).workers;
+    y.unit = (small ? pkv_split::ONE : pkv_split::PAIR).unit;
     y.desc2 = y.workers * sizeof(int4);
     y.ml = 4096;
     y.o = y.ml + (((size_t)2 * y.workers * y.unit * 8 + 255) & ~(size_t)255);

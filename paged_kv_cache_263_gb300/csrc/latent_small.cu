@@ -38,10 +38,6 @@ namespace {
 
 constexpr float FAR = 32768.0f;
 constexpr float NO_REF = -3.0e38f;                // no score yet: any finite one is far above
-// tiles a CTA takes at least (16 sequences of 100 to 1,000 x 64 rows: 19.2 us, with two
-// 22.1; four of 2,000 to 5,000: 26.8 and 24.7)
-constexpr int MIN_TILES = 1;
-constexpr int SNAP = 2;                           // (256 sequences of 50 to 300 x 16 rows: 32.1 us without, 30.2 with)
 constexpr int STAGES = 2;
 constexpr uint32_t CHUNK_BYTES = TK * 128;        // 64 keys (or query columns) x 64 dims
 constexpr uint32_t TILE_BYTES = 9 * CHUNK_BYTES;  // eight latent chunks and the rotary one
@@ -156,7 +152,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_proxy_async_smem();
     tc_fence_before();
     griddep_wait();       // everything below reads what earlier kernels wrote
-    const Range range = find_range<THREADS, MIN_TILES, 0, SNAP>(p, k, k == 0, reinterpret_cast<int *>(smem + SP), s_start, s_cut, list, LIST);
+    constexpr pkv_split::Rule rule = pkv_split::ONE;
+    const Range range = find_range<THREADS>(p, rule, k, k == 0, reinterpret_cast<int *>(smem + SP), s_start, s_cut, list, LIST);
     Walk walk = {uniform(range.walk.s), uniform(range.walk.u), uniform(range.walk.j), uniform(range.walk.left)};
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
@@ -448,8 +445,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok) break;
             tc_fence_after();
-            const bool whole = it.j0 == 0 && it.j1 == it.kt;
-            const int slot = 2 * k + (it.j0 == 0 ? 1 : 0);
+            const bool whole = it.whole();
+            const int slot = pkv_split::own_slot(k, it);
             const size_t row0 = (size_t)it.q.a * p.heads + it.r0, pr0 = (size_t)slot * p.unit;
             // the sums: every lane of their accumulator holds the column's
             volatile float *sum_sh = reinterpret_cast<volatile float *>(const_cast<int *>(lim_sh));
