@@ -471,8 +471,9 @@ PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t laten
  * n rows), and row i sees keys 0 .. L-n+i.
  *
  *  out            device bf16 [total_q_tokens][num_heads][512]
- *  q              device bf16 [total_q_tokens][num_heads][576]; a query that is not
- *                 finite gives NaN in its own output row alone
+ *  q              device bf16 [total_q_tokens][num_heads][576]; scores that are NaN
+ *                 or +inf (a query that is not finite) make their own row NaN,
+ *                 and no other
  *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
  *                 sequence (total_q_tokens = num_seqs)
  *  context_lens   device int32 [num_seqs]; L = 0 (a padded entry): the
@@ -496,7 +497,9 @@ PAGEDKV_API kv_status reshape_and_cache_latent(const void *latent, int64_t laten
  *                 (captured graphs replayed side by side among them) need one
  *                 each.
  * Scores, softmax statistics and sums are fp32; probabilities are rounded to
- * bf16 for the second product, and the output once at the end.  Split points
+ * bf16 for the second product (their sum adds them before that where rows x heads
+ * are many a sequence, and after it where they are few), and the output once at
+ * the end.  Split points
  * depend on the batch's lengths and sizes only, and no atomics touch the
  * arithmetic: the same call gives the same bits. */
 PAGEDKV_API size_t paged_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
@@ -529,7 +532,8 @@ PAGEDKV_API kv_status paged_latent_attention(void *out, const void *q, const int
  *                 sequence whose rows or keys lie outside the tensors is left
  *                 out, its rows as they were (flag 4); so are rows that belong
  *                 to no sequence (not flagged)
- *  num_heads, scale, workspace, rounding   as for paged_latent_attention */
+ *  num_heads, scale, workspace, rounding   as for paged_latent_attention (the
+ *                 sum adds the probabilities before they are rounded) */
 PAGEDKV_API size_t latent_prefill_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
                                                            int32_t num_heads);
 PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const void *kv, const void *k_rope,

@@ -46,10 +46,15 @@
 //  * A stage is held for 10,500 cycles -- 4,000 until it has landed, 1,100 for S,
 //    4,000 for exchange and softmax, 1,100 for PV -- so four of them give a tile
 //    every 2,650, where its bytes need 1,570 and its products 1,090.  (64
-//    sequences of 1,500 to 8,200 tokens x 128 heads: 118 us, 3.2 TB/s.  Measured when
-//    it took 123: three stages 143; a ring of four and a half in halves of 32 keys 129,
-//    for its second set of waits and products; blocks brought into L2 two tiles ahead
-//    126.)
+//    sequences of 1,500 to 8,200 tokens x 128 heads: 118 us, 3.2 TB/s.  Three stages
+//    made it 16 % slower; a ring of four and a half in halves of 32 keys 5 %, for its
+//    second set of waits and products; blocks brought into L2 two tiles ahead 2 %.)
+//  * The sum that a row is divided by adds its probabilities as fp32, before their
+//    rounding to bf16 for the second product.  Both errors are roundings of a
+//    probability; adding the rounded ones instead would cancel part of them and costs
+//    1 % here.  (Relative RMS error of the output, emulated: 1,000 keys, scores spread
+//    by 1.7: 2.28e-3 and 2.21e-3, of which the output's own rounding is 1.64e-3; spread
+//    by 5: 2.30e-3 and 1.84e-3.)
 //
 // Work split.  The tiles of all (sequence, 128-row unit) pairs are laid end to
 // end and cut into equal ranges, one a cluster: the batch's ragged lengths

@@ -29,14 +29,20 @@
 //  * Each query tile goes on to its next item by itself: its queries are loaded as
 //    soon as its own first products are through, and its first product runs beside
 //    the other tile's last ones.  (Waiting for each other cost 4,000 cycles an item:
-//    442 us for 4,096 tokens x 128 heads, 435 without.)
+//    442 us for 4,096 tokens x 128 heads in a short run, 435 without.)
 //  * What is left: both operands of S come from shared memory at its full rate, 128
 //    bytes a cycle, and the loads' writes and P V's reads share it -- 168 KiB, 1,310
 //    cycles of a 1,770-cycle turn.  Handing P on in halves, so that P V starts before
-//    the softmax ends, changes nothing in that (455 us).
-//    4,096 tokens x 128 heads: 435 us, 1.58 PFLOP/s (480 us at the clock that the
-//    power limit leaves in a long run); six chunks of 333 to 2,048 tokens over 799 to
-//    2,398 keys, 64 heads: 257 us; eight of 40 to 300 tokens, 32 heads: 22 us.
+//    the softmax ends, changes nothing in that.
+//    4,096 tokens x 128 heads: 477 us in a long run, at the clock that the power limit
+//    leaves (1.44 PFLOP/s), 438 in a short one; six chunks of 333 to 2,048 tokens over
+//    799 to 2,398 keys, 64 heads: 278 and 260 us; eight of 40 to 300 tokens, 32 heads:
+//    21 us.
+//  * The sum that a row is divided by adds its probabilities as fp32, before their
+//    rounding to bf16 for the second product.  Adding the rounded ones would cancel
+//    part of the rounding (see latent_decode.cu) and costs 2.5 % (a mixed addition for
+//    each instead of one a pair, 437 to 448 us; 459 with integer operations to unpack
+//    them, 464 once P has been handed on, for the registers that it then holds).
 // Warps 0 and 1: MMA issuers of the query tiles, which take turns; 2: TMA; 3: items;
 // 4-7 and 8-11: softmax and epilogue of the query tiles, one row a thread.
 #include "common.cuh"

@@ -8,13 +8,15 @@
 // Nothing is exchanged with another CTA, and what a product costs falls with N.
 //  * Bound by memory at few columns: a tile of 64 keys is 72 KiB, 3,100 cycles of a
 //    SM's share of the bandwidth, and the products take 1,540 (N = 16).  256 sequences
-//    of 17 to 4,096 tokens, 8 heads: 116 us, 5.3 TB/s; a tile takes 3,300 cycles, and
+//    of 17 to 4,096 tokens, 8 heads: 117 us, 5.2 TB/s; a tile takes 3,300 cycles, and
 //    12,000 of 200,000 go by until the first has landed.
 //  * At 64 columns the products take 2,050 cycles, all of them at the full rate of
 //    shared memory (128 bytes a cycle: both operands come from there), and the loads'
-//    576 come on top: a tile takes 3,700.  One context of 131,072, 64 heads: 47 us.
-//    (Two such CTAs a 128-row unit, each tile loaded once for both: 144 us for 64
-//    sequences x 128 heads that latent_decode.cu did in 123 at that time.)
+//    576 come on top: a tile takes 3,700.  One context of 131,072, 64 heads: 47 us, of
+//    which the tiles are 25, the way to the first tile 6; the partial sums of 152 CTAs
+//    (20 MB out and in again) and the merge take the rest.  (Two such CTAs a 128-row
+//    unit, each tile loaded once for both, were 17 % slower than latent_decode.cu for 64
+//    sequences x 128 heads.)
 //  * Shared memory: queries 72 KiB, two key stages of 72 KiB, P^T 8 KiB.  A stage is
 //    the K-major A operand of the first product and the MN-major A operand of the
 //    second.
@@ -28,7 +30,7 @@
 //    to learn of that: the issuer of the second products refuses the tile, and it is
 //    done again.
 //  * A tile is loaded, multiplied and released in two halves of its dims, so that a
-//    stage is filled again while its other half is still in use (133 -> 126 us).
+//    stage is filled again while its other half is still in use (5 % of the time).
 // Warps 0-7: softmax and epilogue; 8: TMA producer; 9: first products; 10: second.
 #include "latent_work.cuh"
 
