@@ -144,6 +144,21 @@ PAGEDKV_API kv_status kv_block_refcount(const kv_pool *pool, int32_t id, int32_t
 
 PAGEDKV_API kv_status kv_pool_stats(const kv_pool *pool, kv_pool_stats_t *out);
 
+/* Compaction: moves live blocks from the pool's upper end into free blocks at its
+ * lower end, so that the live blocks come to lie in 0 .. live_blocks-1 and the rest
+ * of the pool is one free range.  With live blocks numbering `live`, every live id
+ * >= live moves to a free id < live; of these the max_moves highest, if there are
+ * more.  Each moved block keeps its references under its new id, and its old id is
+ * free, in the new id's place in the order of allocation.
+ *  out_src, out_dst   host int32 [max_moves]: the moves, both lists ascending, no id
+ *                     in both
+ *  out_n              how many
+ * Only the bookkeeping changes: the caller copies the blocks (kv_copy_blocks) and
+ * rewrites what holds ids -- block tables (kv_remap_tables), a prefix cache
+ * (kv_prefix_remap) -- before it allocates from the pool again. */
+PAGEDKV_API kv_status kv_pool_compact(kv_pool *pool, int32_t max_moves, int32_t *out_src, int32_t *out_dst,
+                                      int32_t *out_n);
+
 /* Memory waste of a set of requests, contiguous against paged ([P2]
  * "PagedAttention": each request reserving a maximum-length buffer leaves most
  * of it untouched; "Small block size": paged waste is at most 15 tokens per
@@ -243,6 +258,12 @@ PAGEDKV_API kv_status kv_prefix_evict(kv_prefix_cache *cache, int32_t n, int32_t
 PAGEDKV_API kv_status kv_prefix_alloc(kv_prefix_cache *cache, int32_t n, int32_t *out_ids);
 
 PAGEDKV_API kv_status kv_prefix_stats(const kv_prefix_cache *cache, kv_prefix_stats_t *out);
+
+/* After kv_pool_compact on the cache's pool: every cached block src[i] is block
+ * dst[i] from now on (src strictly ascending, host int32 [n]; KV_ERR_INVALID and
+ * nothing changes otherwise).  What the cache holds, its order of eviction and its
+ * statistics stay as they are. */
+PAGEDKV_API kv_status kv_prefix_remap(kv_prefix_cache *cache, const int32_t *src, const int32_t *dst, int32_t n);
 
 /* ------------------------------------------------------------------------
  * Cache write ("blocks allocated on demand as a sequence grows" [P1]
@@ -542,6 +563,128 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
                                                int32_t total_q_tokens, int32_t total_k_tokens,
                                                int32_t num_heads, float scale, void *workspace,
                                                size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Shared prefixes: decode attention that attends a common prefix once.
+ *
+ * Sequences that begin with the same tokens hold those tokens' blocks in common
+ * ([P2] "Sharing, and what makes a prefix reusable"; [P3] block management (e)).
+ * paged_attention_decode reads them once a sequence; this call reads them once a
+ * group, as the keys of one product with the queries of all the group's rows, and
+ * joins the result with each sequence's own tail by the log-sum-exp rule:
+ *   out[r][h] = sum_t p_t v_t,  p = softmax_t(scale x q[r][h] . k_t)
+ * over the row's whole context, prefix and tail, as the calls above give it.
+ *
+ * Group g is the sequences cu_groups[g] .. cu_groups[g+1]-1 of the batch, whose
+ * first prefix_lens[g] tokens are the same.  Only whole blocks are shared: P =
+ * prefix_lens[g] rounded down to a multiple of 16.  The prefix's P / 16 block ids
+ * are read from the table row of the group's first sequence; the other rows'
+ * first P / 16 entries are not read.  Sequences before the first group and behind
+ * the last share nothing.
+ * Sequence s owns rows cu_q_lens[s] .. cu_q_lens[s+1]-1 at positions L-n .. L-1 (L =
+ * context_lens[s], n rows), and row i sees keys 0 .. L-n+i.  The rows' own tokens
+ * lie behind the prefix: L - n >= P.
+ *
+ *  out            device bf16 [total_q_tokens][num_q_heads][128]
+ *  q              device bf16 [total_q_tokens][num_q_heads][128]; scores that are
+ *                 NaN or +inf (a query that is not finite) make their own row of
+ *                 that head NaN.  KV_FP8_E4M3: the query range of
+ *                 paged_attention_decode
+ *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
+ *                 sequence (total_q_tokens = num_seqs, max_q_len = 1)
+ *  context_lens   device int32 [num_seqs]; L = 0 (a padded entry): the sequence's
+ *                 rows are zeros.
+ *  max_q_len      host int: an upper bound on every n
+ *  cu_groups      device int32 [num_groups + 1], non-decreasing; prefix_lens device
+ *                 int32 [num_groups].  Groups may be empty.
+ *  max_prefix_len, max_tail_len   host ints: upper bounds on every P and on every
+ *                 L - P.  They size the grids and the workspace, so bounds far above
+ *                 the lengths cost time.
+ *  A sequence is left out, its rows as they were (flag 4), if its rows are outside
+ *  the tensors or more than max_q_len, if its group's sequences or rows are, if a
+ *  length is negative, above max_blocks_per_seq x 16 or above its bound, or if
+ *  L - n < P.  Rows that belong to no sequence stay as they were (not flagged).
+ *  k_cache, v_cache, block_tables, dtype, scales   as above; the keys of a block
+ *                 outside the pool are not read, and the rows that see it are then
+ *                 unspecified (flag 1).  Keys 0 .. L-1 have to be finite; what lies
+ *                 past key L-1 does not matter.
+ *  workspace      device scratch of paged_attention_shared_prefix_workspace_size()
+ *                 bytes, 256-byte aligned.  Calls that may overlap on the GPU need
+ *                 one each.
+ * Scores, softmax statistics, sums and partial outputs are fp32; probabilities are
+ * rounded to bf16 (f16 over an fp8 cache) for the second product, and the output
+ * once at the end.  Split points depend on the call's sizes and bounds and on each
+ * prefix's and tail's length, and no atomics touch the arithmetic: the same call
+ * gives the same bits under any placement of the blocks.
+ * ---------------------------------------------------------------------- */
+PAGEDKV_API size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
+                                                                int32_t max_q_len, int32_t num_groups,
+                                                                int32_t num_q_heads, int32_t num_kv_heads,
+                                                                int32_t max_prefix_len, int32_t max_tail_len);
+PAGEDKV_API kv_status paged_attention_shared_prefix(
+    void *out, const void *q, const int32_t *cu_q_lens, const int32_t *context_lens, int32_t num_seqs,
+    int32_t total_q_tokens, int32_t max_q_len, const int32_t *cu_groups, const int32_t *prefix_lens,
+    int32_t num_groups, int32_t max_prefix_len, int32_t max_tail_len, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t num_blocks, float scale, kv_dtype dtype, const float *k_scale, const float *v_scale, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Copies whole blocks, in several caches at once: for every cache c and every i <
+ * n, block src[i] of the cache goes to block dst[i].
+ *  caches       host array of num_caches device addresses, 16-byte aligned: the K
+ *               and V caches of all layers, latent caches, anything laid out as
+ *               num_blocks blocks of block_bytes (a multiple of 16) each.  Read
+ *               before the call returns.
+ *  src, dst     device int32 [n].  A pair of two negative ids is skipped; any other
+ *               with an id outside the pool is skipped and flagged (flag 1).  A
+ *               source may be listed any number of times.  A block listed as a
+ *               destination twice, or as a source and a destination of different
+ *               pairs, gets (or gives) one or the other value in each 16 bytes.
+ * One launch for up to 128 caches. */
+PAGEDKV_API kv_status kv_copy_blocks(void *const *caches, int32_t num_caches, int64_t block_bytes,
+                                     int32_t num_blocks, const int32_t *src, const int32_t *dst, int32_t n,
+                                     void *stream);
+
+/* Forks sequences on the device ([P3] block management (e), (g): samples of one
+ * prompt, beams of a search): child c becomes a copy of sequence parents[c].  It
+ * shares the parent's full blocks.  A partly filled last block is not shared: the
+ * first child of a parent keeps it if first_keeps is not 0 (the parent itself does
+ * not go on), and every other child gets a block from free_blocks, in child order,
+ * for the caller to copy.
+ *  block_tables   device int32 [num_parents][max_blocks_per_seq]
+ *  context_lens   device int32 [num_parents]
+ *  parents        device int32 [num_children]
+ *  free_blocks    device int32 [num_free]: ids in the order they are handed out
+ *                 (reserved beforehand; num_children are always enough)
+ *  child_tables   out, device int32 [num_children][max_blocks_per_seq]; entries past
+ *                 a child's last block stay as they were
+ *  child_lens     out, device int32 [num_children]
+ *  copy_src, copy_dst   out, device int32 [num_children]: the block to copy for each
+ *                 child, -1 and -1 for none -- as kv_copy_blocks takes them
+ *  taken          out, device int32 [1]: how many ids of free_blocks were used
+ *  A child is refused -- child_lens[c] = 0, no blocks, no copy -- if its parent is
+ *  outside 0 .. num_parents-1 or the parent's length outside 0 ..
+ *  max_blocks_per_seq x 16 (flag 4), or if the free list has run out (flag 16).
+ *  At most 16,384 parents and children (KV_ERR_UNSUPPORTED above).  No output may
+ *  overlap an input or another output (KV_ERR_INVALID).  References are the host's:
+ *  kv_block_share for each child's shared blocks. */
+PAGEDKV_API kv_status kv_fork_tables(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t *context_lens, int32_t num_parents, const int32_t *parents,
+                                     int32_t num_children, int32_t first_keeps, const int32_t *free_blocks,
+                                     int32_t num_free, int32_t *child_tables, int32_t *child_lens,
+                                     int32_t *copy_src, int32_t *copy_dst, int32_t *taken, void *stream);
+
+/* Rewrites block tables after blocks have moved: of the first ceil(L/16) entries of
+ * each row, those equal to src[i] become dst[i], each once.
+ *  block_tables   device int32 [num_seqs][max_blocks_per_seq], in and out
+ *  context_lens   device int32 [num_seqs]; a length outside 0 ..
+ *                 max_blocks_per_seq x 16: the row stays as it was (flag 4)
+ *  src, dst       device int32 [n], src strictly ascending (as kv_pool_compact
+ *                 gives it); with a list that is not, ids may be missed
+ *  The lists and lengths may not overlap the tables (KV_ERR_INVALID). */
+PAGEDKV_API kv_status kv_remap_tables(int32_t *block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, int32_t num_seqs, const int32_t *src,
+                                      const int32_t *dst, int32_t n, void *stream);
 
 /* ------------------------------------------------------------------------
  * Swap of KV blocks to host memory and back ([P2] "When it runs out anyway":

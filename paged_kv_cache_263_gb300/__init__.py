@@ -24,6 +24,8 @@ __all__ = [
     "kv_build_step_tables", "reshape_and_cache_latent", "paged_latent_attention",
     "paged_latent_attention_workspace_size", "latent_prefill_attention",
     "latent_prefill_attention_workspace_size", "LATENT_DIM", "LATENT_ROPE_DIM", "LATENT_MAX_HEADS",
+    "paged_attention_shared_prefix", "paged_attention_shared_prefix_workspace_size", "kv_copy_blocks",
+    "kv_fork_tables", "kv_remap_tables",
 ]
 
 HEAD_DIM = 128
@@ -110,6 +112,14 @@ def lib():
             "paged_latent_attention": (c.c_int, [P, P, P, P, I, I, P, P, I, I, I, F, P, SZ, P]),
             "latent_prefill_attention_workspace_size": (SZ, [I, I, I]),
             "latent_prefill_attention": (c.c_int, [P, P, P, P, I64, P, P, I, I, I, I, F, P, SZ, P]),
+            "kv_pool_compact": (c.c_int, [P, I, P, P, c.POINTER(I)]),
+            "kv_prefix_remap": (c.c_int, [P, P, P, I]),
+            "paged_attention_shared_prefix_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
+            "paged_attention_shared_prefix": (c.c_int, [P, P, P, P, I, I, I, P, P, I, I, I, P, P, P, I, I, I, I, F,
+                                                        c.c_int, P, P, P, SZ, P]),
+            "kv_copy_blocks": (c.c_int, [P, I, I64, I, P, P, I, P]),
+            "kv_fork_tables": (c.c_int, [P, I, P, I, P, I, I, P, I, P, P, P, P, P, P]),
+            "kv_remap_tables": (c.c_int, [P, I, P, I, P, P, I, P]),
             "kv_swap_out": (c.c_int, [P, P, I, I, c.c_int, P, I, P, P, P]),
             "kv_swap_in": (c.c_int, [P, P, I, I, c.c_int, P, I, P, P, P]),
             "kv_trace_prefill": (c.c_int, [I]),
@@ -237,6 +247,19 @@ class KVPool:
         return {"num_blocks": s.num_blocks, "free": s.free_blocks, "live": s.live_blocks,
                 "shared": s.shared_blocks, "cow_copies": s.cow_copies, "alloc_failures": s.alloc_failures}
 
+    def compact(self, max_moves=None):
+        """Moves live blocks from the pool's upper end into free ones at its lower end:
+        (src, dst), both ascending.  The caller copies the blocks (kv_copy_blocks) and
+        rewrites what holds ids (kv_remap_tables, PrefixCache.remap) before it allocates
+        again."""
+        import numpy as np
+        n = self.num_blocks if max_moves is None else int(max_moves)
+        src, dst = np.empty(max(n, 0), dtype=np.int32), np.empty(max(n, 0), dtype=np.int32)
+        k = ctypes.c_int32()
+        _check(lib().kv_pool_compact(self._p, n, src.ctypes.data_as(ctypes.c_void_p),
+                                     dst.ctypes.data_as(ctypes.c_void_p), ctypes.byref(k)), "kv_pool_compact")
+        return src[:k.value].copy(), dst[:k.value].copy()
+
     def fail_alloc_after(self, k: int):
         _check(lib().kv_pool_fail_alloc_after(self._p, int(k)), "kv_pool_fail_alloc_after")
 
@@ -311,6 +334,15 @@ class PrefixCache:
         out = np.empty(max(int(n), 0), dtype=np.int32)
         _check(lib().kv_prefix_alloc(self._c, int(n), out.ctypes.data_as(ctypes.c_void_p)), "kv_prefix_alloc")
         return out
+
+    def remap(self, src, dst):
+        """The cached blocks src[i] (strictly ascending) are blocks dst[i] from now on (see KVPool.compact)."""
+        import numpy as np
+        a, b = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
+        if a.shape != b.shape:
+            raise ValueError("src and dst must have the same length")
+        _check(lib().kv_prefix_remap(self._c, a.ctypes.data_as(ctypes.c_void_p), b.ctypes.data_as(ctypes.c_void_p),
+                                     a.size), "kv_prefix_remap")
 
     def stats(self) -> dict:
         s = _PrefixStats()
@@ -611,6 +643,127 @@ def latent_prefill_attention(out, q, kv, k_rope, cu_q_lens, cu_k_lens, scale=Non
                     rs, cu_q, _at("cu_k_lens", cu_k_lens, dev, _I32, (B + 1,)), B, R, K, h,
                     _EXPANDED_QK ** -0.5 if scale is None else float(scale), ws, nbytes), "latent_prefill_attention")
     return out
+
+
+# ------------------------------------------------- shared prefixes, forks, moves
+_CACHE_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+
+
+def _cache_at(name, t, dev, shape=None):
+    """Address of a K or V cache [num_blocks][Hkv][16][128], bf16 or e4m3."""
+    if t is None or t.get_device() != dev or t.dtype not in _CACHE_TYPES or t.dim() != 4 or \
+            t.shape[2:] != (BLOCK_SIZE, HEAD_DIM) or (shape is not None and t.shape != shape) or not t.is_contiguous():
+        if t is not None and t.is_cuda and t.dtype not in _CACHE_TYPES:
+            raise ValueError(f"{name} must be bf16 or e4m3 (uint8 or float8_e4m3fn), got {t.dtype}")
+        _wrong(name, t, dev, None if t is None else t.dtype, (None, None, BLOCK_SIZE, HEAD_DIM) if shape is None else shape)
+    return t.data_ptr()
+
+
+def paged_attention_shared_prefix_workspace_size(num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads,
+                                                 num_kv_heads, max_prefix_len, max_tail_len) -> int:
+    return int(lib().paged_attention_shared_prefix_workspace_size(
+        num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len, max_tail_len))
+
+
+def paged_attention_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens, cu_groups, prefix_lens,
+                                  cu_q_lens=None, max_q_len=None, max_prefix_len=None, max_tail_len=None, scale=None,
+                                  k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Decode attention that attends a prefix once for all sequences that share it:
+    out[R][Hq][128] from q[R][Hq][128] (bf16), one row a sequence, or cu_q_lens [B+1]
+    rows (at most max_q_len each).
+
+    Sequences cu_groups[g] .. cu_groups[g+1]-1 (int32 [G+1]) have their first
+    prefix_lens[g] tokens in common (int32 [G]; rounded down to whole blocks, and read
+    through the first of these sequences' row of block_tables).  max_prefix_len and
+    max_tail_len bound the prefixes and what follows them; without them the width of
+    block_tables does, which sizes grids and workspace for far more than most batches
+    hold."""
+    dev = _device("q", q)
+    qp = _at_nd("q", q, dev, _BF, 2, (HEAD_DIM,))
+    R, hq, _ = q.shape
+    tables = _at_nd("block_tables", block_tables, dev, _I32, 2)
+    B, mb = block_tables.shape
+    if cu_q_lens is None:
+        if R != B:
+            raise ValueError("without cu_q_lens, q must have one row a sequence")
+        n = 1
+    else:
+        n = max(R, 1) if max_q_len is None else int(max_q_len)
+    kc = _cache_at("k_cache", k_cache, dev)
+    vc = _cache_at("v_cache", v_cache, dev, k_cache.shape)
+    nb, hkv = k_cache.shape[0], k_cache.shape[1]
+    if v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one dtype")
+    groups = _at_nd("cu_groups", cu_groups, dev, _I32, 1)
+    G = cu_groups.shape[0] - 1
+    if G < 0:
+        raise ValueError("cu_groups must have at least one entry")
+    longest = mb * BLOCK_SIZE
+    mp = longest if max_prefix_len is None else int(max_prefix_len)
+    mt = longest if max_tail_len is None else int(max_tail_len)
+    L = lib()
+    ws, nbytes, _keep = _scratch(workspace, dev, stream, L.paged_attention_shared_prefix_workspace_size, B, R, n, G, hq,
+                                 hkv, mp, mt)
+    each = (hkv,)
+    _check(_call_on(dev, stream, L.paged_attention_shared_prefix, _at("out", out, dev, _BF, (R, hq, HEAD_DIM)), qp,
+                    None if cu_q_lens is None else _at("cu_q_lens", cu_q_lens, dev, _I32, (B + 1,)),
+                    _at("context_lens", context_lens, dev, _I32, (B,)), B, R, n, groups,
+                    _at("prefix_lens", prefix_lens, dev, _I32, (G,)), G, mp, mt, kc, vc, tables, mb, hq, hkv, nb,
+                    HEAD_DIM ** -0.5 if scale is None else float(scale), _cache_dtype(k_cache),
+                    None if k_scale is None else _at("k_scale", k_scale, dev, torch.float32, each),
+                    None if v_scale is None else _at("v_scale", v_scale, dev, torch.float32, each), ws, nbytes),
+           "paged_attention_shared_prefix")
+    return out
+
+
+def kv_copy_blocks(caches, src, dst, stream=None):
+    """Copy block src[i] to block dst[i] (int32) in every cache of the list: tensors of
+    one shape and dtype whose first dimension counts blocks (the K and V caches of all
+    layers, or latent caches).  A pair of negative ids is skipped."""
+    dev = _device("src", src)
+    s = _at_nd("src", src, dev, _I32, 1)
+    n = src.shape[0]
+    d = _at("dst", dst, dev, _I32, (n,))
+    if not caches:
+        return
+    shape, dtype = caches[0].shape, caches[0].dtype
+    if len(shape) < 2 or shape[0] < 1:
+        raise ValueError("caches must be [num_blocks][...]")
+    at = (ctypes.c_void_p * len(caches))(*[_at("caches", t, dev, dtype, shape) for t in caches])
+    _check(_call_on(dev, stream, lib().kv_copy_blocks, at, len(caches), caches[0].stride(0) * caches[0].element_size(),
+                    shape[0], s, d, n), "kv_copy_blocks")
+
+
+def kv_fork_tables(block_tables, context_lens, parents, free_blocks, child_tables, child_lens, copy_src, copy_dst, taken,
+                   first_keeps=False, stream=None):
+    """Fork sequences on the device: child c shares the full blocks of sequence
+    parents[c]; a partly filled last block stays with the parent's first child if
+    first_keeps, and every other child gets a block of free_blocks, to be filled by
+    kv_copy_blocks(caches, copy_src, copy_dst).  Outputs (int32): child_tables [C][mb],
+    child_lens, copy_src, copy_dst [C], taken [1] (free blocks used)."""
+    dev = _device("block_tables", block_tables)
+    tables = _at_nd("block_tables", block_tables, dev, _I32, 2)
+    P, mb = block_tables.shape
+    par = _at_nd("parents", parents, dev, _I32, 1)
+    C = parents.shape[0]
+    free, each = _at_nd("free_blocks", free_blocks, dev, _I32, 1), (C,)
+    _check(_call_on(dev, stream, lib().kv_fork_tables, tables, mb, _at("context_lens", context_lens, dev, _I32, (P,)), P,
+                    par, C, 1 if first_keeps else 0, free, free_blocks.shape[0],
+                    _at("child_tables", child_tables, dev, _I32, (C, mb)), _at("child_lens", child_lens, dev, _I32, each),
+                    _at("copy_src", copy_src, dev, _I32, each), _at("copy_dst", copy_dst, dev, _I32, each),
+                    _at("taken", taken, dev, _I32, (1,))), "kv_fork_tables")
+
+
+def kv_remap_tables(block_tables, context_lens, src, dst, stream=None):
+    """Rewrite block tables after blocks have moved: of each row's used entries, those
+    equal to src[i] become dst[i] (int32, src strictly ascending)."""
+    dev = _device("block_tables", block_tables)
+    tables = _at_nd("block_tables", block_tables, dev, _I32, 2)
+    B, mb = block_tables.shape
+    s = _at_nd("src", src, dev, _I32, 1)
+    n = src.shape[0]
+    _check(_call_on(dev, stream, lib().kv_remap_tables, tables, mb, _at("context_lens", context_lens, dev, _I32, (B,)), B,
+                    s, _at("dst", dst, dev, _I32, (n,)), n), "kv_remap_tables")
 
 
 def _swap_args(k_cache, v_cache, block_ids, host_k, host_v):

@@ -13,6 +13,7 @@
 #include "trace.h"
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 #include <new>
 #include <unordered_map>
@@ -209,6 +210,33 @@ kv_status kv_pool_stats(const kv_pool *pool, kv_pool_stats_t *out)
     out->shared_blocks = shared;
     out->cow_copies = pool->cow_copies;
     out->alloc_failures = pool->alloc_failures;
+    return KV_OK;
+}
+
+kv_status kv_pool_compact(kv_pool *pool, int32_t max_moves, int32_t *out_src, int32_t *out_dst, int32_t *out_n)
+{
+    if (!pool || !out_n || max_moves < 0 || (max_moves > 0 && (!out_src || !out_dst))) return KV_ERR_INVALID;
+    std::lock_guard<std::mutex> g(pool->mu);
+    int32_t live = 0;
+    for (int32_t r : pool->ref) live += r > 0;
+    // as many live ids lie at or past `live` as there are holes before it
+    int32_t n = 0;
+    for (int32_t b = live; b < pool->num_blocks; ++b) n += pool->ref[b] > 0;
+    const int32_t m = n < max_moves ? n : max_moves;
+    for (int32_t b = pool->num_blocks - 1, i = m; i > 0; --b)
+        if (pool->ref[b] > 0) out_src[--i] = b;          // the m highest, ascending
+    for (int32_t b = 0, i = 0; i < m; ++b)
+        if (pool->ref[b] == 0) out_dst[i++] = b;         // the m lowest holes
+    // (a block listed in neither keeps its place in the free list)
+    for (int32_t &f : pool->stack) {
+        const int32_t *at = std::lower_bound(out_dst, out_dst + m, f);
+        if (at != out_dst + m && *at == f) f = out_src[at - out_dst];
+    }
+    for (int32_t i = 0; i < m; ++i) {
+        pool->ref[out_dst[i]] = pool->ref[out_src[i]];
+        pool->ref[out_src[i]] = 0;
+    }
+    *out_n = m;
     return KV_OK;
 }
 

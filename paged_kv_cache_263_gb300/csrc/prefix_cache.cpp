@@ -287,6 +287,20 @@ kv_status kv_prefix_alloc(kv_prefix_cache *c, int32_t n, int32_t *out_ids)
     return kv_block_alloc(c->pool, n, out_ids);
 }
 
+kv_status kv_prefix_remap(kv_prefix_cache *cache, const int32_t *src, const int32_t *dst, int32_t n)
+{
+    if (!cache || n < 0 || (n > 0 && (!src || !dst))) return KV_ERR_INVALID;
+    for (int32_t i = 1; i < n; ++i)
+        if (src[i] <= src[i - 1]) return KV_ERR_INVALID;
+    std::lock_guard<std::mutex> g(cache->mu);
+    for (Node &x : cache->nodes) {
+        if (!x.live) continue;
+        const int32_t *at = std::lower_bound(src, src + n, x.block);
+        if (at != src + n && *at == x.block) x.block = dst[at - src];
+    }
+    return KV_OK;
+}
+
 kv_status kv_prefix_stats(const kv_prefix_cache *c, kv_prefix_stats_t *out)
 {
     if (!c || !out) return KV_ERR_INVALID;

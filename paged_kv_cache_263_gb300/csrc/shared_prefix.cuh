@@ -1,0 +1,100 @@
+// shared_prefix.cuh -- how a batch of sequences in groups with a common prefix is
+// described on the device, read alike by the kernel that attends the prefixes, the
+// one that attends the tails and the one that joins the two.
+//
+// Group g holds sequences cu_groups[g] .. cu_groups[g+1]-1 of the batch, and their
+// first prefix_lens[g] tokens are the same.  Only whole blocks can be shared, so P =
+// prefix_lens[g] rounded down to blocks is attended once, through the table row of
+// the group's first sequence; every sequence attends its keys from P on through
+// its own row.  Sequences of no group have P = 0.
+#pragma once
+
+#include "common.cuh"
+
+namespace pkv {
+
+struct SharedBatch {
+    const int32_t *cu_groups, *prefix_lens;   // [num_groups + 1], [num_groups]
+    const int32_t *cu_q_lens;                 // [num_seqs + 1], or null: one row a sequence
+    const int32_t *context_lens;              // [num_seqs]
+    int num_groups, num_seqs, total_rows, max_q_len;
+    int max_prefix, max_tail;                 // keys, bounds given by the caller (max_prefix in whole blocks)
+    int max_blocks;
+};
+
+#if defined(__CUDACC__)
+// the last i in [0, n) with v[i] <= x, or 0 (bounded whatever v holds)
+__device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(v + mid) <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct SharedGroup {
+    int s0, s1, row0, rows, P;
+    bool ok;          // within the batch, the tensors and the caller's bounds
+};
+__device__ __forceinline__ SharedGroup shared_group(const SharedBatch &b, int g)
+{
+    SharedGroup r;
+    r.s0 = __ldg(b.cu_groups + g);
+    r.s1 = __ldg(b.cu_groups + g + 1);
+    const int p = __ldg(b.prefix_lens + g);
+    r.P = p & ~(BS - 1);
+    r.ok = r.s0 >= 0 && r.s0 <= r.s1 && r.s1 <= b.num_seqs && p >= 0 && r.P <= b.max_prefix;
+    r.row0 = r.rows = 0;
+    if (r.ok && r.s0 < r.s1) {
+        const int a = b.cu_q_lens ? __ldg(b.cu_q_lens + r.s0) : r.s0;
+        const int e = b.cu_q_lens ? __ldg(b.cu_q_lens + r.s1) : r.s1;
+        r.ok = a >= 0 && a <= e && e <= b.total_rows;
+        r.row0 = a;
+        r.rows = r.ok ? e - a : 0;
+    }
+    return r;
+}
+
+enum { SEQ_BAD = 0, SEQ_EMPTY = 1, SEQ_OK = 2 };
+struct SharedSeq {
+    int state;        // SEQ_BAD: left out; SEQ_EMPTY: no context, its rows are zeros
+    int row0, n;      // its query rows
+    int L, P;         // context, and how much of it is its group's prefix
+    int first;        // the sequence whose table row the prefix is read through
+};
+__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s)
+{
+    SharedSeq r;
+    r.state = SEQ_BAD;
+    r.row0 = b.cu_q_lens ? __ldg(b.cu_q_lens + s) : s;
+    r.n = b.cu_q_lens ? __ldg(b.cu_q_lens + s + 1) - r.row0 : 1;
+    r.L = __ldg(b.context_lens + s);
+    r.P = 0;
+    r.first = s;
+    if (r.row0 < 0 || r.n < 0 || r.row0 > b.total_rows - r.n || r.n > b.max_q_len) return r;
+    bool ok = true;
+    if (b.num_groups > 0) {
+        const int g = last_at_most(b.cu_groups, b.num_groups, s);
+        const int s0 = __ldg(b.cu_groups + g), s1 = __ldg(b.cu_groups + g + 1);
+        if (s >= s0 && s < s1) {
+            const SharedGroup gr = shared_group(b, g);
+            ok = gr.ok && r.row0 >= gr.row0 && r.row0 + r.n <= gr.row0 + gr.rows;
+            r.P = gr.P;
+            r.first = s0;
+        }
+    }
+    if (r.L == 0) {
+        r.state = SEQ_EMPTY;
+        return r;
+    }
+    // the rows' own tokens lie behind the prefix
+    if (!ok || r.L < 0 || r.L > b.max_blocks * BS || r.L - r.n < r.P || r.L - r.P > b.max_tail) return r;
+    r.state = SEQ_OK;
+    return r;
+}
+#endif  // __CUDACC__
+
+}  // namespace pkv

@@ -1,0 +1,335 @@
+"""Parity of attention over shared prefixes with its fp64 reference.  The tolerances
+are the reference's own bounds, per output element (see oracle/shared_prefix.py)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_263_gb300 as pkv
+from oracle import shared_prefix as osp
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+D, BS = 128, 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    require_gpu()
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+class Batch:
+    """A batch with its caches: sizes [sequences per group], prefix lengths, tails
+    (tokens behind the whole blocks of the prefix), rows a sequence."""
+
+    def __init__(self, sizes, prefix, tails, rows=1, hq=8, hkv=2, fp8=False, seed=0, loose=0, before=0, width=None, spread=1.0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.B = B = before + sum(sizes) + loose
+        n = np.broadcast_to(rows, (B,)) if np.ndim(rows) else np.full(B, rows)
+        self.cu = np.concatenate([[0], np.cumsum(n)])
+        self.groups = before + np.concatenate([[0], np.cumsum(sizes)])
+        self.prefix = np.asarray(prefix)
+        held = np.zeros(B, int)
+        for i, s in enumerate(sizes):
+            held[self.groups[i]:self.groups[i] + s] = prefix[i] // BS
+        self.lens = held * BS + np.asarray(tails)
+        self.width = width or max(1, int((-(-self.lens // BS)).max()))
+        need = [max(0, -(-int(x) // BS) - int(h)) for x, h in zip(self.lens, held)]
+        shared = [int(p) // BS for p in prefix]
+        self.nb = nb = sum(need) + sum(shared) + 3
+        ids = rng.permutation(nb - 1)
+        # what a row must not read holds a block of NaN or an id outside the pool
+        self.poison = nb - 1
+        self.tables = np.where(rng.random((B, self.width)) < 0.5, -7, self.poison)
+        at = sum(shared)
+        for i, s in enumerate(sizes):
+            p0 = sum(shared[:i])
+            if s:
+                self.tables[self.groups[i], :shared[i]] = ids[p0:p0 + shared[i]]
+        for s in range(B):
+            self.tables[s, held[s]:held[s] + need[s]] = ids[at:at + need[s]]
+            at += need[s]
+        self.k, self.v = (torch.randn(nb, hkv, BS, D, generator=g, device="cuda") for _ in range(2))
+        self.q = (spread * torch.randn(int(self.cu[-1]), hq, D, generator=g, device="cuda")).to(torch.bfloat16)
+        self.fp8, self.hq, self.hkv, self.rows = fp8, hq, hkv, n
+        self.ks = self.vs = None
+        if fp8:
+            self.ks, self.vs = (torch.rand(hkv, generator=g, device="cuda") * 0.02 + 0.01 for _ in range(2))
+            self.k, self.v = ((x / s[:, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn) for x, s in
+                              ((self.k, self.ks), (self.v, self.vs)))
+            self.k64, self.v64 = f64(self.k) * f64(self.ks)[:, None, None], f64(self.v) * f64(self.vs)[:, None, None]
+            self.k, self.v = self.k.view(torch.uint8), self.v.view(torch.uint8)
+            nan = 0x7F
+        else:
+            self.k, self.v = self.k.to(torch.bfloat16), self.v.to(torch.bfloat16)
+            self.k64, self.v64 = f64(self.k), f64(self.v)
+            nan = float("nan")
+        # keys past every context, and the block that nobody owns, are not numbers
+        for x in (self.k, self.v):
+            x[self.poison] = nan
+            for s in range(B):
+                if self.lens[s] % BS and need[s] and self.lens[s] > held[s] * BS:
+                    x[self.tables[s, (self.lens[s] - 1) // BS], :, self.lens[s] % BS:] = nan
+        self.scale = D ** -0.5
+
+    def call(self, out=None, **kw):
+        if out is None:
+            out = torch.full(self.q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
+        args = dict(cu_q_lens=None if (self.rows == 1).all() else i32(self.cu), max_q_len=int(max(self.rows.max(), 1)),
+                    scale=self.scale, k_scale=self.ks, v_scale=self.vs, max_prefix_len=int(max([0, *self.prefix])),
+                    max_tail_len=self.width * BS)
+        args.update(kw)
+        pkv.paged_attention_shared_prefix(out, self.q, self.k, self.v, i32(self.tables).reshape(self.B, self.width),
+                                          i32(self.lens), i32(self.groups), i32(self.prefix), **args)
+        return out
+
+    def reference(self, **kw):
+        return osp.shared(f64(self.q), self.k64, self.v64, self.tables, self.lens, self.groups, self.prefix, self.scale,
+                          cu=self.cu, fp8=self.fp8, **kw)
+
+    def check(self, flags=0, got=None, ref=None, **kw):
+        got = self.call(**kw) if got is None else got
+        assert pkv.kv_last_device_status() == (5 if flags else 0)
+        assert pkv.kv_last_device_status_flags() == flags
+        exp, tol, f = ref or self.reference()
+        assert f == flags
+        compare(f64(got), exp, tol)
+        return got
+
+
+def compare(got, exp, tol):
+    kept = np.isnan(exp)
+    assert (got[kept] == 77.0).all()
+    assert np.isfinite(got[~kept]).all()
+    off = np.abs(got - exp)[~kept] - tol[~kept]
+    assert off.size == 0 or off.max() <= 0, (off.max(), np.abs(got - exp)[~kept].max())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 8), (4, 2), (8, 2), (16, 2), (16, 1), (64, 8)])
+def test_head_layouts(hq, hkv, fp8):
+    Batch([3, 5], [100, 33], [7, 1, 16, 17, 40, 2, 31, 90], hq=hq, hkv=hkv, fp8=fp8, seed=hq + hkv).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("p", [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 144, 255, 640, 1000, 2048, 5000])
+def test_prefix_lengths(p, fp8):
+    Batch([4], [p], [1, 16, 33, 250], hq=16, hkv=2, fp8=fp8, seed=p).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("tail", [1, 2, 15, 16, 17, 64, 65, 333, 1024, 1025, 4100])
+def test_tail_lengths(tail, fp8):
+    Batch([2, 1], [48, 200], [tail, 5, tail], hq=8, hkv=1, fp8=fp8, seed=tail).check()
+
+
+@pytest.mark.parametrize("size", [1, 2, 7, 8, 15, 16, 17, 31, 33, 64, 130, 300])
+def test_group_sizes(size):
+    """Up to several query tiles a group, whole and partly filled."""
+    rng = np.random.default_rng(size)
+    Batch([size], [300], rng.integers(1, 60, size), hq=16, hkv=2, seed=size).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_groups_of_all_sizes(fp8):
+    rng = np.random.default_rng(5)
+    sizes = [0, 1, 9, 0, 0, 40, 2, 17, 1, 1, 3, 0] + [2] * 40
+    n = sum(sizes) + 4
+    Batch(sizes, rng.integers(0, 700, len(sizes)), rng.integers(1, 90, n), hq=8, hkv=2, fp8=fp8, loose=3, before=1).check()
+
+
+@pytest.mark.parametrize("ng", [31, 32, 33, 100, 1025])
+def test_numbers_of_groups(ng):
+    rng = np.random.default_rng(ng)
+    sizes = rng.integers(0, 3, ng)
+    Batch(list(sizes), rng.integers(0, 100, ng), rng.integers(1, 20, int(sizes.sum()) + 1), hq=2, hkv=1, loose=1).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [2, 3, 4, 8, 20])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 1)])
+def test_drafts(rows, hq, hkv, fp8):
+    """Several rows a sequence, causal among themselves, all of them behind the prefix."""
+    Batch([3, 4], [130, 500], [rows, rows + 1, 40, 17 + rows, 64, 33, 200], rows=rows, hq=hq, hkv=hkv, fp8=fp8, loose=0,
+          seed=rows).check()
+
+
+def test_rows_of_all_lengths():
+    """Ragged rows, sequences without any among them."""
+    rows = [0, 1, 5, 2, 0, 7, 1, 3]
+    Batch([4, 3], [95, 260], [9, 1, 5, 20, 30, 77, 1, 4], rows=rows, hq=8, hkv=2, loose=1).check()
+    Batch([4, 3], [95, 260], [9, 1, 5, 20, 30, 77, 1, 4], rows=rows, hq=8, hkv=2, loose=1, fp8=True).check(max_q_len=9)
+
+
+def test_long_prefix_of_many_parts():
+    b = Batch([20], [40000], np.arange(1, 21), hq=8, hkv=1, seed=3)
+    b.check()
+    b.check(max_prefix_len=65536)
+
+
+def test_sharp_scores():
+    """Scores spread so far that the running maximum moves often and most weights vanish."""
+    Batch([6, 6], [700, 320], [3, 90, 200, 16, 1, 33] * 2, hq=16, hkv=2, spread=30.0).check()
+
+
+def test_default_bounds():
+    b = Batch([3], [77], [20, 9, 1])
+    b.check(max_prefix_len=None, max_tail_len=None)
+    b.check(got=b.call(cu_q_lens=i32(b.cu), max_q_len=None))
+
+
+def test_without_groups():
+    b = Batch([], [], [20, 9, 1, 400], loose=0, before=4)
+    b.check()
+
+
+def test_padded_and_bad_sequences():
+    """L = 0 gives zeros; sequences that break a rule are left as they were."""
+    b = Batch([4, 4, 3], [100, 64, 33], [5, 6, 7, 8, 20, 21, 22, 23, 40, 41, 42], hq=8, hkv=2)
+    b.lens[1] = 0
+    b.check()
+    for what, value in (("short", 97), ("equal", 96), ("negative", -3), ("wide", 16 * b.width + 1)):
+        lens, old = b.lens.copy(), b.lens
+        lens[2] = value
+        b.lens = lens
+        ok = what == "short"           # one key behind the prefix's 96
+        b.check(flags=0 if ok else 4)
+        b.lens = old
+    prefix = b.prefix
+    b.prefix = np.array([100, -1, 33])
+    b.check(flags=4, max_prefix_len=100)
+    b.prefix = prefix
+    # bounds that the batch breaks
+    b.check(flags=4, max_prefix_len=95, ref=b.reference(max_prefix=95))
+    b.check(flags=4, max_tail_len=30, ref=b.reference(max_tail=30))
+    groups = b.groups
+    for bad in ([0, 4, 8, 12], [-1, 4, 8, 11], [0, 4, 99, 11]):
+        b.groups = np.array(bad)
+        got = b.call()
+        assert pkv.kv_last_device_status_flags() in (0, 4) and pkv.kv_last_device_status() == 5
+        rows = f64(got)
+        assert (np.isfinite(rows)).all()
+    b.groups = groups
+    b.check()
+
+
+def test_more_rows_than_announced():
+    b = Batch([2, 2], [40, 50], [9, 9, 9, 9], rows=[3, 1, 2, 3], hq=4, hkv=1)
+    b.check(flags=4, max_q_len=2, ref=b.reference(max_q=2))
+
+
+def test_blocks_outside_the_pool():
+    """Flagged and not read; the other groups' rows are as ever."""
+    for where in ("prefix", "tail"):
+        b = Batch([3, 3], [200, 150], [20, 30, 40, 50, 60, 70], hq=8, hkv=2)
+        exp, tol, _ = b.reference()
+        b.tables[0, 3 if where == "prefix" else 13] = b.nb + 5
+        got = b.call()
+        assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 1
+        first = 3 if where == "prefix" else 1
+        compare(f64(got)[first:], exp[first:], tol[first:])
+
+
+@pytest.mark.parametrize("where", [0, 5])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite(bad, where):
+    """They make their own row of that head NaN, and no other."""
+    b = Batch([4, 3], [200, 90], [20, 30, 40, 5, 7, 9, 11], hq=8, hkv=2)
+    exp, tol, _ = b.reference()
+    b.q[where, 3, 17] = bad
+    got = f64(b.call())
+    assert pkv.kv_last_device_status() == 0
+    assert np.isnan(got[where, 3]).all()
+    got[where, 3] = exp[where, 3]
+    compare(got, exp, tol)
+
+
+def test_any_placement_and_workspace_gives_the_same_bits():
+    args = dict(sizes=[20, 7], prefix=[3000, 800], tails=np.arange(1, 28) * 11, hq=16, hkv=2)
+    b = Batch(**args)
+    need = pkv.paged_attention_shared_prefix_workspace_size(b.B, b.B, 1, 2, 16, 2, 3000, b.width * BS)
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = ws[-ws.data_ptr() % 256:][:need]
+    first = b.check(workspace=ws if need else None).view(torch.int16).clone()
+    ws.fill_(0x7F)
+    assert torch.equal(b.call(workspace=ws if need else None).view(torch.int16), first)
+    # another order of the blocks
+    perm = np.random.default_rng(8).permutation(b.nb)
+    inv = torch.tensor(np.argsort(perm), device="cuda")
+    b.k, b.v = b.k[inv].contiguous(), b.v[inv].contiguous()
+    b.tables = np.where(b.tables >= 0, perm[b.tables.clip(0)], b.tables)
+    assert torch.equal(b.call().view(torch.int16), first)
+    assert pkv.kv_last_device_status() == 0
+
+
+def test_agrees_with_decode_over_the_whole_context():
+    """The same rows through paged_attention_decode with the prefix in every table row."""
+    b = Batch([16, 9], [2000, 512], np.arange(1, 26) * 13, hq=16, hkv=2)
+    exp, tol, _ = b.reference()
+    tables = b.tables.copy()
+    for i in range(2):
+        a, e, n = b.groups[i], b.groups[i + 1], b.prefix[i] // BS
+        tables[a:e, :n] = tables[a, :n]
+    out = torch.empty(b.B, 16, D, device="cuda")
+    pkv.paged_attention_decode(out, b.q, b.k, b.v, i32(tables), i32(b.lens), b.scale)
+    got = b.check()
+    assert (np.abs(f64(got) - f64(out)) <= 2 * tol).all()
+
+
+def test_on_another_stream_and_twice_at_once():
+    b, c = Batch([9], [900], np.arange(1, 10) * 30, seed=1), Batch([5, 5], [300, 2000], np.arange(1, 11), seed=2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            x = b.call()
+        with torch.cuda.stream(s2):
+            y = c.call()
+        z = b.call(stream=s2, out=torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device="cuda"))
+        torch.cuda.synchronize()
+        b.check(got=x)
+        c.check(got=y)
+        b.check(got=z)
+
+
+def test_captured_and_replayed_with_other_lengths():
+    """One graph, padded to its size, replayed over batches with other groups, prefixes and tails."""
+    big = Batch([8, 8, 4], [900, 400, 200], np.arange(1, 21) * 9, hq=8, hkv=2, loose=0)
+    tables, lens = i32(big.tables), i32(big.lens)
+    groups, prefix, q = i32(big.groups), i32(big.prefix), big.q.clone()
+    out = torch.full(q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(pkv.paged_attention_shared_prefix_workspace_size(20, 20, 1, 3, 8, 2, 1024, 256), dtype=torch.uint8,
+                     device="cuda")
+
+    def call():
+        pkv.paged_attention_shared_prefix(out, q, big.k, big.v, tables, lens, groups, prefix, max_prefix_len=1024,
+                                          max_tail_len=256, scale=big.scale, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    full = big.lens
+    for cut, sizes in ((0, [8, 8, 4]), (3, [8, 8, 4]), (0, [8, 8, 0])):
+        # (at least one key behind the whole blocks of each prefix)
+        big.lens = np.maximum(full - cut, np.repeat([897, 401, 193], [8, 8, 4]))
+        big.groups = np.concatenate([[0], np.cumsum(sizes)])
+        if sizes[2] == 0:
+            big.lens[16:] = 0              # padding
+        lens.copy_(i32(big.lens))
+        groups.copy_(i32(big.groups))
+        out.fill_(77.0)
+        graph.replay()
+        big.check(got=out)
