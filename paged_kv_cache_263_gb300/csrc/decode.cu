@@ -33,11 +33,13 @@
 //    writes its partial (max, sum, O) and a second kernel merges the
 //    partitions with the log-sum-exp rule in fixed order -- no atomics, so the
 //    result is bitwise independent of physical placement.
-#include "common.cuh"
+#include "shared_prefix.cuh"
+#include "shared_prefix.h"
 #include "trace.h"
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 // ---- device code begin (hashed with the ncu counters of profiles/)
 namespace {
@@ -76,6 +78,14 @@ struct DecodeParams {
     // kernel, so only the first CTA waits for the chunk kernel (the grid then
     // completes after it, and the kernels behind it see both grids' results)
     int corun;
+};
+
+// TAIL: the sequences' own keys behind a prefix that another kernel attends for
+// whole groups; every result is a partial one, of row r and head h at
+// ((r x hq + h) x part_stride + part_off + split)
+struct TailParams : DecodeParams {
+    SharedBatch b;
+    int part_stride, part_off;
 };
 
 // Ring depth per warp and CTAs per SM (compile-time).  Measured on GB300:
@@ -152,10 +162,10 @@ __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CU
 // speculative draft being verified) reads each K/V tile once for all its
 // rows.  Row i of the chunk sees keys 0 .. L-n+i; longer chunks take several
 // column groups (CTAs next to each other in the grid, sharing tiles in L2).
-template <bool FP8, int NT, bool MR>
+template <bool FP8, int NT, bool MR, bool TAIL>
 __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const DecodeParams p)
+                  const std::conditional_t<TAIL, TailParams, DecodeParams> p)
 {
     using GE = Geo<FP8>;
     extern __shared__ uint8_t smem_raw[];
@@ -174,8 +184,21 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
 
     // s: sequence (block table); row: (first) row of q/out; wi: index of the
     // partials; nq: query rows of the sequence this CTA covers
-    int s = blockIdx.z, row = s, wi = s, L, nq = 1;
-    if constexpr (MR) {
+    int s = blockIdx.z, row = s, wi = s, L, nq = 1, skip = 0;
+    if constexpr (TAIL) {
+        // from here on key 0 is the first one behind the prefix
+        const SharedSeq w = shared_seq(p.b, s);
+        if constexpr (MR) {
+            cg = split % p.col_groups;
+            split /= p.col_groups;
+        }
+        if (w.state == SEQ_BAD && split == 0 && cg == 0 && g == 0 && threadIdx.x == 0) flag(ST_BAD_LEN);
+        if (w.state != SEQ_OK || cg * CW >= w.n * p.group) return;
+        nq = w.n;
+        row = w.row0;
+        L = w.L - w.P;
+        skip = w.P / BS;
+    } else if constexpr (MR) {
         cg = split % p.col_groups;
         split /= p.col_groups;
         const int a = p.cu_q_lens[s], b = p.cu_q_lens[s + 1];
@@ -222,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     if (b0 >= nblk) return;
     const int b1 = min(nblk, b0 + p.part_blocks);
     const int nsplit_s = (nblk + p.part_blocks - 1) / p.part_blocks;
-    const int32_t *bt = p.block_tables + (size_t)s * p.max_blocks;
+    const int32_t *bt = p.block_tables + (size_t)s * p.max_blocks + skip;
     // blocks of this warp: b0 + warp + k * WARPS, k < count
     // (b1 - b0 >= 1 and warp <= 3, so the numerator is never negative)
     const int count = (b1 - b0 - warp + WARPS - 1) / WARPS;
@@ -235,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // the 128-sequence shared-prefix batch: 3.5% less time, the prefix's
     // re-reads no longer reaching DRAM).
     uint64_t l2pol;
-    if (split > 0) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
+    if (TAIL || split > 0) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
     else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(l2pol));
     const uint32_t ring = smem_u32(smem + warp * GE::RING);
     const uint32_t bar0 = smem_u32(bars + warp * GE::STAGES);
@@ -558,11 +581,19 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
                 O += f * sm_o[(w * HL + hl) * D + d];
             }
         }
+        // (a query that is not finite may leave no score to be the largest: its sums
+        // are NaN then, and stay so)
+        if (TAIL && M == -INFINITY && !any_to)
+            Ls = sm_l[hl] + sm_l[HL + hl] + sm_l[2 * HL + hl] + sm_l[3 * HL + hl];
         // MR: column -> (row of the chunk, head); partials are per row
         const int gc = cg * CW + hl;
         const int orow = MR ? row + gc / G : row, owi = MR ? orow : wi;
         const int h = g * G + (MR ? gc % G : hl);
-        if (nsplit_s == 1) {
+        if constexpr (TAIL) {
+            const size_t pi = ((size_t)orow * p.hq + h) * p.part_stride + p.part_off + split;
+            p.part_o[pi * D + d] = O * vsc;
+            if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(Ls > 0.f ? M : -INFINITY, Ls);
+        } else if (nsplit_s == 1) {
             p.out[((size_t)orow * p.hq + h) * D + d] = Ls > 0.f ? O * vsc / Ls : 0.f;
         } else {
             const size_t pi = ((size_t)owi * p.hq + h) * p.num_splits + split;
@@ -613,10 +644,11 @@ template <bool FP8, int NT, bool MR>
 cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const DecodeParams &p,
                        cudaStream_t st, bool pdl)
 {
-    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR>>(Geo<FP8>::SMEM);
+    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR, false>>(Geo<FP8>::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(p.num_splits * (MR ? p.col_groups : 1), p.hkv, p.num_seqs);
-    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, pdl, km, vm, p);
+    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR, false>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, pdl, km, vm,
+                               p);
 }
 
 template <bool FP8>
@@ -626,6 +658,16 @@ cudaError_t launch_for(const CUtensorMap &km, const CUtensorMap &vm, const Decod
     if (p.col_groups > 0)
         return nt == 2 ? launch_one<FP8, 2, true>(km, vm, p, st, pdl) : launch_one<FP8, 1, true>(km, vm, p, st, pdl);
     return nt == 2 ? launch_one<FP8, 2, false>(km, vm, p, st, pdl) : launch_one<FP8, 1, false>(km, vm, p, st, pdl);
+}
+
+template <bool FP8, int NT, bool MR>
+cudaError_t launch_tails_as(const CUtensorMap &km, const CUtensorMap &vm, const TailParams &p, cudaStream_t st)
+{
+    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR, true>>(Geo<FP8>::SMEM);
+    if (e != cudaSuccess) return e;
+    dim3 grid(p.num_splits * (MR ? p.col_groups : 1), p.hkv, p.num_seqs);
+    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR, true>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, true, km, vm,
+                               p);
 }
 
 }  // namespace
@@ -784,6 +826,45 @@ kv_status run(float *out, const void *q, const void *k_cache, const void *v_cach
 }
 
 cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
+
+// The tails of a batch in groups (see TailParams), launched programmatically; beside:
+// behind the kernel of the prefixes, to run beside it (see DecodeParams::corun).
+cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
+{
+    TailParams p{};
+    p.q = c.q;
+    p.block_tables = c.block_tables;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.part_o = c.part_o;
+    p.part_ml = c.part_ml;
+    p.max_blocks = c.b.max_blocks;
+    p.num_seqs = c.b.num_seqs;
+    p.total_rows = c.b.total_rows;
+    p.hq = c.hq;
+    p.hkv = c.hkv;
+    p.group = c.hq / c.hkv;
+    p.num_blocks = c.num_blocks;
+    p.part_blocks = c.tail_part_blocks;
+    p.num_splits = c.tail_splits;
+    p.scale_log2 = c.scale_log2;
+    p.corun = beside ? 1 : 0;
+    p.b = c.b;
+    p.part_stride = c.prefix_splits + c.tail_splits;
+    p.part_off = c.prefix_splits;
+    CUtensorMap km, vm;
+    if (!make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, c.fp8 ? KV_FP8_E4M3 : KV_BF16, &km, &vm))
+        return cudaErrorInvalidValue;
+    const int64_t cols = (int64_t)c.b.max_q_len * p.group;
+    const bool two = cols > 8;
+    if (c.b.max_q_len > 1) {
+        p.col_groups = (int)((cols + (two ? 15 : 7)) / (two ? 16 : 8));
+        if (c.fp8) return two ? launch_tails_as<true, 2, true>(km, vm, p, st) : launch_tails_as<true, 1, true>(km, vm, p, st);
+        return two ? launch_tails_as<false, 2, true>(km, vm, p, st) : launch_tails_as<false, 1, true>(km, vm, p, st);
+    }
+    if (c.fp8) return two ? launch_tails_as<true, 2, false>(km, vm, p, st) : launch_tails_as<true, 1, false>(km, vm, p, st);
+    return two ? launch_tails_as<false, 2, false>(km, vm, p, st) : launch_tails_as<false, 1, false>(km, vm, p, st);
+}
 
 }  // namespace pkv_decode
 

@@ -60,11 +60,13 @@
 // f16 operands (one type per product); k_scale folds into the softmax scale and
 // v_scale into O.  Quantising Q to e4m3 for a kind::f8f6f4 product would cost
 // precision the bf16 queries carry.
-#include "common.cuh"
+#include "shared_prefix.cuh"
+#include "shared_prefix.h"
 #include "trace.h"
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace {
 
@@ -201,6 +203,15 @@ struct PrefillParams {
     float scale_log2;
     const float *k_scale;  // fp8 cache: [Hkv] (folded into the softmax scale)
     const float *v_scale;  // fp8 cache: [Hkv] (applied to O)
+};
+
+// SHARED: the prefixes that groups of sequences share.  A work item is (group, KV
+// head, part of the prefix, query tiles of the group's rows x G heads); every row
+// sees every key, and every result is a partial one, at ((row x hq + head) x
+// max_splits + part).  The parts are tiles_per_split KV tiles, so the items are
+// nearly equal and each CTA finds its own, without a list (see SharedItems).
+struct PrefixParams : PrefillParams {
+    SharedBatch b;
 };
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
@@ -626,6 +637,77 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(PrefillParams p)
     }
 }
 
+// Which work items the CTAs of the shared mode take.  The groups' items lie end to
+// end in the order (group, part, KV head, query item), the last fastest, so that
+// CTAs next to each other read the same keys; CTA c of the C that take items takes
+// items c, c + C, ...  One warp walks over the groups, 32 at a time.
+struct SharedItems {
+    int w0, x, total;                          // the window's first group; the next item's place in it; its items
+    int incl, nq, ns, KT, row0, rows, P, s0;   // this lane's group: items up to it, query items, parts, ...
+};
+__device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &w, int tpt, int lane)
+{
+    const int gi = w.w0 + lane;
+    w.nq = w.ns = w.KT = w.row0 = w.rows = w.P = w.s0 = 0;
+    if (gi < p.b.num_groups) {
+        const SharedGroup gr = shared_group(p.b, gi);
+        if (gr.ok && gr.rows > 0 && gr.P > 0) {
+            w.nq = ((gr.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
+            w.KT = (gr.P + p.tile_keys - 1) / p.tile_keys;
+            w.ns = (w.KT + p.tiles_per_split - 1) / p.tiles_per_split;
+            w.row0 = gr.row0;
+            w.rows = gr.rows;
+            w.P = gr.P;
+            w.s0 = gr.s0;
+        }
+    }
+    w.incl = w.nq * w.ns * p.hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, w.incl, o);
+        if (lane >= o) w.incl += t;
+    }
+    w.total = __shfl_sync(0xffffffffu, w.incl, 31);
+}
+
+// How many CTAs take items (C above; the same in every CTA).  The others leave their
+// SMs to the tails, which the decode kernel reads meanwhile: an SM without a CTA of
+// this kernel reads decode_sm_bytes of K/V in one KV tile's time, all together at
+// most bytes_per_tile, and what is left afterwards is read at that rate.  Items are
+// nearly equal, so only the least C for each number of waves is a candidate: a lane
+// each.
+__device__ __forceinline__ int shared_ctas(const PrefixParams &p, int tpt, int lane)
+{
+    float items = 0.f, tiles = 0.f, tail = 0.f;
+    for (int g = lane; g < p.b.num_groups; g += 32) {
+        const SharedGroup gr = shared_group(p.b, g);
+        if (!gr.ok || gr.rows == 0 || gr.P == 0) continue;
+        const int nq = ((gr.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
+        const int KT = (gr.P + p.tile_keys - 1) / p.tile_keys, ns = (KT + p.tiles_per_split - 1) / p.tiles_per_split;
+        items += (float)nq * ns * p.hkv;
+        tiles += (float)nq * KT * p.hkv;
+        tail -= (float)gr.P * (gr.s1 - gr.s0);
+    }
+    for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, __ldg(p.b.context_lens + s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        tail += __shfl_xor_sync(0xffffffffu, tail, o);
+    }
+    if (items < 1.f) return 0;
+    const float bytes = fmaxf(tail, 0.f) * p.decode_key_bytes, each = tiles / items + 2.f * ITEM_TILES;
+    const float waves = ceilf(items / (float)p.grid_ctas) + (float)lane;
+    const float c = ceilf(items / waves), chunk = waves * each;
+    const float beside = fminf((float)(p.num_sms - c) * p.decode_sm_bytes, p.bytes_per_tile);
+    float t = chunk + fmaxf(0.f, bytes - chunk * beside) / p.bytes_per_tile;
+    float best = t;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    const int at = __ffs(__ballot_sync(0xffffffffu, t <= best)) - 1;
+    return max(1, min(p.grid_ctas, (int)__shfl_sync(0xffffffffu, c, at)));
+}
+
 // (the fp8 variant declares 512 threads so that registers stay <= 128, which 15
 // warps need on an SM partition holding four of them)
 //
@@ -637,10 +719,11 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(PrefillParams p)
 // the S buffers and every barrier phase run on across items, so the next item's
 // Q and first K/V tiles load, and its first QK^T products run, while the
 // softmax warps still finish the item before.
-template <bool FP8, bool BIG>
+template <bool FP8, bool BIG, bool SHARED = false>
 __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
+                   const __grid_constant__ CUtensorMap vmap,
+                   const std::conditional_t<SHARED, PrefixParams, PrefillParams> p)
 {
     using LY = Lay<FP8, BIG>;
     constexpr int KV_STAGES = LY::KV_STAGES, F8_STAGES = LY::F8_STAGES;
@@ -663,7 +746,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
     };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, tpt = BM / G;
-    griddep_launch_dependents();   // the merge kernel may be scheduled; it waits for this grid
+    // the merge kernel may be scheduled; it waits for this grid.  (SHARED: the kernel
+    // behind this one reads its inputs without waiting, so it may start only when
+    // everything before this grid is complete: below)
+    if constexpr (!SHARED) griddep_launch_dependents();
     if (sbase & 1023u) {
         // the 128-byte swizzle needs 1024-byte aligned tiles; never observed, but
         // refuse rather than compute with a wrong layout
@@ -707,6 +793,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if constexpr (SHARED) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
     const uint32_t tmem = *tmem_slot;
     // TMEM columns per query tile gi: two S buffers of BN fp32 columns at
     // S_COLS gi + BN b (P overwrites the first BN/2 of a buffer with 16-bit pairs
@@ -776,6 +866,15 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
         // the work list (and everything before it on the stream) is complete;
         // the other warps learn of each item through the slots, after this wait
         griddep_wait();
+        SharedItems win = {};
+        int ctas = 0;
+        if constexpr (SHARED) {
+            if (role == 0) {
+                ctas = shared_ctas(p, tpt, lane);
+                load_window(p, win, tpt, lane);
+                win.x = (int)blockIdx.x;
+            }
+        }
         for (int k = 0; !failed; ++k) {
             ItemSlot it;
             if (role == 0) {
@@ -786,7 +885,36 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 // to keep its pipelines in step
                 it.valid = 0;
                 // CTAs past the work list's count leave their SMs to the decode rows
-                const bool idle = k == 0 && (int)blockIdx.x >= p.order_count[3];
+                if constexpr (SHARED) {
+                    if ((int)blockIdx.x < ctas) {
+                        while (win.x >= win.total && win.w0 + 32 < p.b.num_groups) {
+                            win.x -= win.total;
+                            win.w0 += 32;
+                            load_window(p, win, tpt, lane);
+                        }
+                        const int x = win.x;
+                        win.x += ctas;
+                        if (x < win.total) {
+                            const int at = __ffs(__ballot_sync(0xffffffffu, win.incl > x)) - 1;
+                            const int nq = __shfl_sync(0xffffffffu, win.nq, at), ns = __shfl_sync(0xffffffffu, win.ns, at);
+                            const int r = x - (__shfl_sync(0xffffffffu, win.incl, at) - nq * ns * p.hkv);
+                            const int KT = __shfl_sync(0xffffffffu, win.KT, at), part_tiles = (KT + ns - 1) / ns;
+                            it.s = __shfl_sync(0xffffffffu, win.s0, at);
+                            it.row0 = __shfl_sync(0xffffffffu, win.row0, at);
+                            it.n = __shfl_sync(0xffffffffu, win.rows, at);
+                            it.L = __shfl_sync(0xffffffffu, win.P, at);
+                            it.t0q = p.item_tiles * (r % nq);
+                            it.has1 = p.item_tiles == 2 && (it.t0q + 1) * tpt < it.n;
+                            it.g = (r / nq) % p.hkv;
+                            it.split = r / nq / p.hkv;
+                            it.nsplit = ns;
+                            it.j0 = it.split * part_tiles;
+                            it.T = min(KT, it.j0 + part_tiles) - it.j0;
+                            it.valid = it.T > 0;    // (always: (ns - 1) x part_tiles < KT)
+                        }
+                    }
+                }
+                const bool idle = SHARED || (k == 0 && (int)blockIdx.x >= p.order_count[3]);
                 for (int tries = 0; !idle; ++tries) {
                     int idx = (int)blockIdx.x;           // the first item: no round trip
                     if (k > 0 || tries > 0) {
@@ -1185,8 +1313,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             // last key this row may attend; rows past the chunk (computed only to fill
             // the tile, never stored) take the tile's last valid row, so no row ever
             // sees a key at or beyond L
-            const int pos = row_valid ? L - n + i : L - n + i1 - 1;
-            const int pos_min = L - n + i0;
+            // (SHARED: every row attends every key of the prefix)
+            const int pos = SHARED ? L - 1 : row_valid ? L - n + i : L - n + i1 - 1;
+            const int pos_min = SHARED ? L - 1 : L - n + i0;
             float m_ref = -INFINITY, l = 0.f;
             // fp8 cache: the k scale folds into the softmax scale, the v scale into O
             const float sl = FP8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
@@ -1297,8 +1426,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 tc_fence_after();
                 const size_t rh = (size_t)(row0 + (row_valid ? i : i0)) * p.hq + head;
                 const size_t pi = rh * p.max_splits + split;
-                const float inv = ((nsplit == 1 && l > 0.f) ? 1.f / l : (nsplit == 1 ? 0.f : 1.f)) * vsc;
-                float4 *dst = reinterpret_cast<float4 *>(nsplit == 1 ? p.out + rh * D : p.part_o + pi * D);
+                const bool whole = !SHARED && nsplit == 1;
+                const float inv = ((whole && l > 0.f) ? 1.f / l : (whole ? 0.f : 1.f)) * vsc;
+                float4 *dst = reinterpret_cast<float4 *>(whole ? p.out + rh * D : p.part_o + pi * D);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {       // 32 columns at a time (the load is warp-wide)
                     float o[32];
@@ -1310,7 +1440,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                                                          o[4 * e + 2] * inv, o[4 * e + 3] * inv);
                     }
                 }
-                if (row_valid && nsplit > 1) {
+                if (row_valid && !whole) {
                     p.part_ml[pi * 2] = l > 0.f ? m_ref : -INFINITY;
                     p.part_ml[pi * 2 + 1] = l;
                 }
@@ -1530,6 +1660,98 @@ Trace *trace_for_call()
 
 namespace pkv_prefill {
 cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
+
+// The layout and the parts of shared prefixes.  One query tile a CTA (128-key tiles)
+// when the groups' rows x heads fill one tile on average, over a bf16 cache.  The
+// number of parts minimises a makespan: waves of equal items over the SMs, each with
+// a fixed cost, and the partial results' write and read.
+void plan_prefixes(SharedCall &c)
+{
+    const int G = c.hq / c.hkv, ng = std::max(1, c.b.num_groups);
+    c.big = !c.fp8 && (int64_t)c.b.total_rows * G <= (int64_t)BM * ng;
+    const int tile_keys = c.big ? 128 : 64, item_rows = (BM / G) * (c.big ? 1 : 2);
+    const int W = (c.b.max_prefix + tile_keys - 1) / tile_keys;
+    if (W == 0 || c.b.num_groups == 0) {
+        c.prefix_splits = c.prefix_tiles = 0;
+        c.prefix_items = 0;
+        return;
+    }
+    const int64_t rows = ((int64_t)c.b.total_rows + ng - 1) / ng;
+    const int64_t problems = ng * ((rows + item_rows - 1) / item_rows) * c.hkv;
+    const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / (BYTES_PER_TILE_TIME * tile_keys / 64.0);
+    const double fixed = CTA_FIXED_TILES * 64.0 / tile_keys;
+    double best = 0;
+    int pick = 0;
+    for (int s = 1; s <= std::min(W, 256); ++s) {
+        const int len = (W + s - 1) / s, parts = (W + len - 1) / len;
+        const int64_t waves = (problems * parts + NUM_SMS - 1) / NUM_SMS;
+        const double cost = (double)waves * (len + fixed) + parts * merge;
+        if (pick == 0 || cost < best) {
+            best = cost;
+            pick = s;
+        }
+    }
+    c.prefix_tiles = (W + pick - 1) / pick;
+    c.prefix_splits = (W + c.prefix_tiles - 1) / c.prefix_tiles;
+    // at most: every group's rows in tiles of their own
+    c.prefix_items = ((int64_t)c.b.total_rows / item_rows + c.b.num_groups) * c.hkv * c.prefix_splits;
+}
+
+cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
+{
+    const int G = c.hq / c.hkv, tpt = BM / G;
+    PrefixParams p{};
+    p.b = c.b;
+    p.q = c.q;
+    p.block_tables = c.block_tables;
+    p.part_o = c.part_o;
+    p.part_ml = c.part_ml;
+    p.max_blocks = c.b.max_blocks;
+    p.num_seqs = c.b.num_seqs;
+    p.hq = c.hq;
+    p.hkv = c.hkv;
+    p.group = G;
+    p.num_blocks = c.num_blocks;
+    p.total_rows = c.b.total_rows;
+    p.tiles_per_split = c.prefix_tiles;
+    p.max_splits = c.prefix_splits + c.tail_splits;
+    p.scale_log2 = c.scale_log2;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.item_tiles = c.big ? 1 : 2;
+    p.tile_keys = c.big ? 128 : 64;
+    p.num_sms = num_sms();
+    p.bytes_per_tile = (float)(BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
+    p.decode_key_bytes = (float)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+    p.decode_sm_bytes = (float)(DECODE_SM_BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
+    p.q_box_bytes = tpt * G * 128;
+    p.grid_ctas = (int)std::min<int64_t>(c.prefix_items, p.num_sms);
+    CUtensorMap qm, km, vm;
+    if (!pkv_host::encode_tmap_3d(&qm, c.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, c.hq, c.b.total_rows, (uint64_t)D * 2,
+                                  (uint64_t)c.hq * D * 2, 64, G, tpt, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !pkv_decode::make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, c.fp8 ? KV_FP8_E4M3 : KV_BF16, &km, &vm))
+        return cudaErrorInvalidValue;
+    // (V as in the chunk call: one 3-D box of both 64-dim halves)
+    if (!c.fp8 && !pkv_host::encode_tmap_3d(&vm, c.v_cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64,
+                                            (uint64_t)c.num_blocks * c.hkv * BS, 2, (uint64_t)D * 2, 128, 64, BS, 2,
+                                            CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto launch = [&](auto kernel, cudaError_t smem_ok, int threads, int smem) {
+        if (smem_ok != cudaSuccess) return smem_ok;
+        return pkv_host::launch_ex(kernel, dim3((unsigned)p.grid_ctas), dim3(threads), smem, st, true, qm, km, vm, p);
+    };
+    if (c.fp8)
+        return launch(prefill_kernel<true, false, true>,
+                      pkv_host::ensure_dynamic_smem<prefill_kernel<true, false, true>>(Lay<true>::SMEM_BYTES),
+                      Lay<true>::THREADS, Lay<true>::SMEM_BYTES);
+    if (c.big)
+        return launch(prefill_kernel<false, true, true>,
+                      pkv_host::ensure_dynamic_smem<prefill_kernel<false, true, true>>(Lay<false, true>::SMEM_BYTES),
+                      Lay<false, true>::THREADS, Lay<false, true>::SMEM_BYTES);
+    return launch(prefill_kernel<false, false, true>,
+                  pkv_host::ensure_dynamic_smem<prefill_kernel<false, false, true>>(Lay<false>::SMEM_BYTES),
+                  Lay<false>::THREADS, Lay<false>::SMEM_BYTES);
+}
 }  // namespace pkv_prefill
 
 extern "C" {

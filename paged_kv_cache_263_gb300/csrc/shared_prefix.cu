@@ -3,11 +3,10 @@
 //
 //   out[r][h] = sum_t p_t v_t,  p = softmax_t(scale x q[r][h] . k_t)
 // over the keys of a row's whole context: its group's prefix, then its own tail.
-#include "shared_prefix.cuh"
+#include "shared_prefix.h"
 #include "trace.h"
 
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
@@ -19,95 +18,74 @@ using namespace pkv;
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-__device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
-
-struct SharedParams {
+struct MergeParams {
     SharedBatch b;
     __nv_bfloat16 *out;
-    const uint16_t *q;
-    const void *k_cache, *v_cache;
-    const int32_t *block_tables;
-    const float *k_scale, *v_scale;
-    int hq, hkv, num_blocks;
-    float scale_log2;
+    const float *part_o, *part_ml;
+    int hq, prefix_splits, splits;         // splits: of prefix and tail together
+    int tile_keys, prefix_tiles, tail_part_blocks;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float4 load4(const void *cache, size_t at)
+// Joins a row's parts, those of its group's prefix and those of its own tail, by the
+// log-sum-exp rule in a fixed order: one warp a (row, head), four dims a lane.
+constexpr int MERGE_WARPS = 8;
+__global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const MergeParams p)
 {
-    if constexpr (FP8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(cache) + at);
-        const uint32_t a = e4m3x2_to_f16x2(w & 0xffffu), b = e4m3x2_to_f16x2(w >> 16);
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-        return make_float4(x.x, x.y, y.x, y.y);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(cache) + at);
-        return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-    }
-}
-
-// One CTA of 4 warps a (sequence, head): every row of the sequence in turn, keys
-// t = warp, warp + 4, ..., four dims a lane.
-template <bool FP8>
-__global__ void __launch_bounds__(128) shared_prefix_kernel(const SharedParams p)
-{
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-    const int s = blockIdx.x, h = blockIdx.y, g = h / (p.hq / p.hkv);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x, h = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    // (what describes the batch was written before the kernels of the parts began)
+    const int s = p.b.cu_q_lens ? last_at_most(p.b.cu_q_lens, p.b.num_seqs, row) : row;
     const SharedSeq w = shared_seq(p.b, s);
-    if (w.state == SEQ_BAD) {
-        if (h == 0 && threadIdx.x == 0) flag(ST_BAD_LEN);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (h >= p.hq || w.state == SEQ_BAD || row < w.row0 || row >= w.row0 + w.n) return;
+    uint2 *out = reinterpret_cast<uint2 *>(p.out + ((size_t)row * p.hq + h) * D) + lane;
+    if (w.state == SEQ_EMPTY) {
+        *out = make_uint2(0u, 0u);
         return;
     }
-    const float ks = FP8 ? p.k_scale[g] : 1.f, vs = FP8 ? p.v_scale[g] : 1.f;
-    for (int i = 0; i < w.n; ++i) {
-        __nv_bfloat16 *out = p.out + ((size_t)(w.row0 + i) * p.hq + h) * D;
-        if (w.state == SEQ_EMPTY) {
-            out[threadIdx.x] = __float2bfloat16(0.f);
-            continue;
-        }
-        const uint2 qw = *reinterpret_cast<const uint2 *>(p.q + ((size_t)(w.row0 + i) * p.hq + h) * D + 4 * lane);
-        const float4 q = make_float4(bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y));
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int keys = w.L - w.n + i + 1;
-        for (int t = warp; t < keys; t += 4) {
-            const int row = t < w.P ? w.first : s;
-            const int id = __ldg(p.block_tables + (size_t)row * p.b.max_blocks + t / BS);
-            if (id < 0 || id >= p.num_blocks) {
-                if (lane == 0) flag(ST_BAD_BLOCK);
-                continue;
-            }
-            const size_t at = (((size_t)id * p.hkv + g) * BS + t % BS) * D + 4 * lane;
-            const float4 k = load4<FP8>(p.k_cache, at), v = load4<FP8>(p.v_cache, at);
-            float x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+    const int KT = (w.P + p.tile_keys - 1) / p.tile_keys, np = KT ? (KT + p.prefix_tiles - 1) / p.prefix_tiles : 0;
+    const int blocks = (w.L - w.P + BS - 1) / BS, nt = (blocks + p.tail_part_blocks - 1) / p.tail_part_blocks;
+    const size_t base = ((size_t)row * p.hq + h) * p.splits;
+    auto at = [&](int i) { return base + (i < np ? i : p.prefix_splits + i - np); };
+    const int n = np + nt;
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[2 * at(i)]);
 #pragma unroll
-            for (int o2 = 16; o2 > 0; o2 >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o2);
-            x *= p.scale_log2 * ks;
-            const float mn = fmaxf(m, x), r = mn == -INFINITY ? 0.f : mn;
-            const float a = ex2(m - r), e = ex2(x - r);
-            m = mn;
-            l = l * a + e;
-            o = make_float4(o.x * a + e * v.x, o.y * a + e * v.y, o.z * a + e * v.z, o.w * a + e * v.w);
-        }
-        if (lane == 0) {
-            sm_m[warp] = m;
-            sm_l[warp] = l;
-        }
-        *reinterpret_cast<float4 *>(&sm_o[warp][4 * lane]) = o;
-        __syncthreads();
-        const float M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3])), R = M == -INFINITY ? 0.f : M;
-        float ls = 0.f, os = 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float f = ex2(sm_m[u] - R);
-            ls += f * sm_l[u];
-            os += f * sm_o[u][threadIdx.x];
-        }
-        out[threadIdx.x] = __float2bfloat16(ls == 0.f ? 0.f : os * vs / ls);
-        __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    // (no finite maximum: a row whose sums are not numbers stays one)
+    const float R = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int i = 0; i < n; ++i) {
+        const float2 e = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at(i));
+        const float f = ex2(e.x - R);
+        sum += f * e.y;
+        const float4 o = reinterpret_cast<const float4 *>(p.part_o + at(i) * D)[lane];
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+// The parts of prefixes and tails, from the call's sizes and bounds.
+void plan(SharedCall &c, int32_t max_tail_len)
+{
+    pkv_prefill::plan_prefixes(c);
+    pkv_decode::plan_splits(std::max(1, (max_tail_len + BS - 1) / BS), 0, c.b.num_seqs, c.hq, &c.tail_part_blocks,
+                            &c.tail_splits);
+}
+
+size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+size_t part_o_bytes(const SharedCall &c)
+{
+    return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * D * sizeof(float));
+}
+size_t part_ml_bytes(const SharedCall &c)
+{
+    return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * 2 * sizeof(float));
 }
 
 }  // namespace
@@ -122,9 +100,24 @@ size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t to
                                                     int32_t num_groups, int32_t num_q_heads, int32_t num_kv_heads,
                                                     int32_t max_prefix_len, int32_t max_tail_len)
 {
-    (void)num_seqs, (void)total_q_tokens, (void)max_q_len, (void)num_groups, (void)num_q_heads, (void)num_kv_heads;
-    (void)max_prefix_len, (void)max_tail_len;
-    return 0;
+    // (the caches' type is not given: room for the plan of either)
+    if (num_seqs < 1 || total_q_tokens < 1 || max_q_len < 1 || num_groups < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+        max_prefix_len < 0 || max_tail_len < 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16)
+        return 0;
+    size_t most = 0;
+    for (const bool fp8 : {false, true}) {
+        SharedCall c{};
+        c.b.num_seqs = num_seqs;
+        c.b.total_rows = total_q_tokens;
+        c.b.num_groups = num_groups;
+        c.b.max_prefix = max_prefix_len / BS * BS;
+        c.hq = num_q_heads;
+        c.hkv = num_kv_heads;
+        c.fp8 = fp8;
+        plan(c, max_tail_len);
+        most = std::max(most, part_o_bytes(c) + part_ml_bytes(c));
+    }
+    return most;
 }
 
 kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t *cu_q_lens,
@@ -157,26 +150,43 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
         if (!pkv_host::aligned(x, 16)) return KV_ERR_INVALID;
     for (const int32_t *x : {cu_q_lens, context_lens, cu_groups, prefix_lens, block_tables})
         if (!pkv_host::aligned(x, 4)) return KV_ERR_INVALID;
-    SharedParams p{};
-    p.b = {cu_groups, prefix_lens, cu_q_lens, context_lens, num_groups, num_seqs, total_q_tokens, max_q_len,
+    SharedCall c{};
+    c.b = {cu_groups, prefix_lens, cu_q_lens, context_lens, num_groups, num_seqs, total_q_tokens, max_q_len,
            max_prefix_len / BS * BS, max_tail_len, max_blocks_per_seq};
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.q = static_cast<const uint16_t *>(q);
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.block_tables = block_tables;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.hq = num_q_heads;
-    p.hkv = num_kv_heads;
-    p.num_blocks = num_blocks;
-    p.scale_log2 = scale * LOG2E;
-    (void)workspace, (void)workspace_bytes;
-    const dim3 grid(num_seqs, num_q_heads);
+    c.q = static_cast<const uint16_t *>(q);
+    c.k_cache = k_cache;
+    c.v_cache = v_cache;
+    c.block_tables = block_tables;
+    c.k_scale = k_scale;
+    c.v_scale = v_scale;
+    c.hq = num_q_heads;
+    c.hkv = num_kv_heads;
+    c.num_blocks = num_blocks;
+    c.fp8 = dtype == KV_FP8_E4M3;
+    c.scale_log2 = scale * LOG2E;
+    plan(c, max_tail_len);
+    // (32 groups that claim all rows, as malformed data may, still count their items in 32 bits)
+    if (c.prefix_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
+    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)c.tail_splits * ((int64_t)max_q_len * G / 8 + 1) > INT32_MAX)
+        return KV_ERR_UNSUPPORTED;
+    // (the plan goes by the bounds as given, which the workspace's size goes by; no
+    // length passes what a table row holds)
+    c.b.max_prefix = std::min(c.b.max_prefix, max_blocks_per_seq * BS);
+    c.b.max_tail = std::min(c.b.max_tail, max_blocks_per_seq * BS);
+    const size_t o_bytes = part_o_bytes(c);
+    if (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < o_bytes + part_ml_bytes(c))
+        return KV_ERR_INVALID;
+    c.part_o = static_cast<float *>(workspace);
+    c.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == KV_BF16) shared_prefix_kernel<false><<<grid, 128, 0, st>>>(p);
-    else shared_prefix_kernel<true><<<grid, 128, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    const bool prefixes = c.prefix_splits > 0;
+    if (prefixes && pkv_prefill::launch_prefixes(c, st) != cudaSuccess) return KV_ERR_CUDA;
+    if (pkv_decode::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
+    const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
+                           c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks};
+    const dim3 grid(total_q_tokens, (num_q_heads + MERGE_WARPS - 1) / MERGE_WARPS);
+    return pkv_host::launch_ex(shared_merge_kernel, grid, dim3(32 * MERGE_WARPS), 0, st, true, m) == cudaSuccess
+               ? KV_OK : KV_ERR_CUDA;
 }
 
 }  // extern "C"

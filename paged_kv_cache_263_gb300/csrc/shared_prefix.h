@@ -1,0 +1,33 @@
+// shared_prefix.h -- what the host side of attention over shared prefixes
+// (shared_prefix.cu) hands to the two kernels that do its products: the chunk
+// kernel's shared mode (prefill.cu) for the prefixes, the decode kernel's tail mode
+// (decode.cu) for each sequence's own keys.
+#pragma once
+
+#include "shared_prefix.cuh"
+
+struct SharedCall {
+    pkv::SharedBatch b;
+    const uint16_t *q;
+    const void *k_cache, *v_cache;
+    const int32_t *block_tables;
+    const float *k_scale, *v_scale;   // fp8 cache
+    float *part_o, *part_ml;          // [rows][hq][prefix_splits + tail_splits][128], [..][2] (max, sum)
+    int hq, hkv, num_blocks;
+    bool fp8, big;                    // big: one query tile a CTA, 128-key tiles
+    int prefix_splits, prefix_tiles;  // parts of a prefix at most, and KV tiles a part
+    int64_t prefix_items;             // work items of the prefixes at most
+    int tail_splits, tail_part_blocks;
+    float scale_log2;
+};
+
+namespace pkv_decode {
+cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st);
+void plan_splits(int32_t max_blocks, int32_t num_splits, int32_t num_seqs, int32_t hq, int32_t *part_blocks,
+                 int32_t *splits);
+}  // namespace pkv_decode
+namespace pkv_prefill {
+// the parts that prefixes are cut into (fields big and prefix_*)
+void plan_prefixes(SharedCall &c);
+cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st);
+}  // namespace pkv_prefill

@@ -48,6 +48,14 @@ def test_attention_refuses(change, status):
     assert _call("paged_attention_shared_prefix", ATT, **change) == status
 
 
+@pytest.mark.parametrize("change", [dict(ws=None), dict(ws=10 * A + 128), dict(nbytes=-1), dict(nbytes=0)])
+def test_attention_refuses_a_workspace(change):
+    need = pkv.paged_attention_shared_prefix_workspace_size(4, 8, 2, 2, 32, 8, 640, 4096)
+    assert need > 0
+    change = dict(change, nbytes=need - 1) if change.get("nbytes") == -1 else change
+    assert _call("paged_attention_shared_prefix", ATT, **change) == INVALID
+
+
 @pytest.mark.parametrize("change", [dict(B=0), dict(R=0)])
 def test_attention_of_nothing(change):
     assert _call("paged_attention_shared_prefix", ATT, **change) == OK
