@@ -37,6 +37,8 @@
 #include "shared_prefix.h"
 #include "trace.h"
 
+#include <cuda_bf16.h>
+
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -81,11 +83,15 @@ struct DecodeParams {
 };
 
 // TAIL: the sequences' own keys behind a prefix that another kernel attends for
-// whole groups; every result is a partial one, of row r and head h at
-// ((r x hq + h) x part_stride + part_off + split)
+// whole groups.  Every result is a partial one, of row r and head h at
+// ((r x hq + h) x part_stride + part_off + split), or with a single partition and
+// nothing to join it to (out16) the output.  whole: there is no other kernel, and a
+// sequence's keys begin with its prefix, read through the group's first row.
 struct TailParams : DecodeParams {
     SharedBatch b;
+    __nv_bfloat16 *out16;
     int part_stride, part_off;
+    int whole;
 };
 
 // Ring depth per warp and CTAs per SM (compile-time).  Measured on GB300:
@@ -184,20 +190,32 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
 
     // s: sequence (block table); row: (first) row of q/out; wi: index of the
     // partials; nq: query rows of the sequence this CTA covers
-    int s = blockIdx.z, row = s, wi = s, L, nq = 1, skip = 0;
+    int s = blockIdx.z, row = s, wi = s, L, nq = 1;
+    [[maybe_unused]] int skip = 0, shared_blocks = 0, first = 0;
     if constexpr (TAIL) {
         // from here on key 0 is the first one behind the prefix
-        const SharedSeq w = shared_seq(p.b, s);
+        const SharedSeq w = shared_seq(p.b, s, lane);
         if constexpr (MR) {
             cg = split % p.col_groups;
             split /= p.col_groups;
         }
         if (w.state == SEQ_BAD && split == 0 && cg == 0 && g == 0 && threadIdx.x == 0) flag(ST_BAD_LEN);
+        if (p.out16 && w.state == SEQ_EMPTY && cg == 0)
+            for (int i = threadIdx.x; i < w.n * p.group * D; i += THREADS) {
+                const int r = i / (p.group * D), rem = i % (p.group * D);
+                p.out16[((size_t)(w.row0 + r) * p.hq + g * p.group) * D + rem] = __float2bfloat16(0.f);
+            }
         if (w.state != SEQ_OK || cg * CW >= w.n * p.group) return;
         nq = w.n;
         row = w.row0;
-        L = w.L - w.P;
-        skip = w.P / BS;
+        L = w.L;
+        if (p.whole) {
+            shared_blocks = w.P / BS;
+            first = w.first;
+        } else {
+            L -= w.P;
+            skip = w.P / BS;
+        }
     } else if constexpr (MR) {
         cg = split % p.col_groups;
         split /= p.col_groups;
@@ -258,7 +276,10 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // the 128-sequence shared-prefix batch: 3.5% less time, the prefix's
     // re-reads no longer reaching DRAM).
     uint64_t l2pol;
-    if (TAIL || split > 0) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
+    // (a tail is read once from its first key on)
+    bool once = split > 0;
+    if constexpr (TAIL) once = !p.whole;
+    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
     else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(l2pol));
     const uint32_t ring = smem_u32(smem + warp * GE::RING);
     const uint32_t bar0 = smem_u32(bars + warp * GE::STAGES);
@@ -271,6 +292,11 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // block ids of this warp, 32 at a time: lane i holds the id of block k0 + i
     auto load_ids = [&](int k0) -> int32_t {
         int k = k0 + lane;
+        if constexpr (TAIL) {
+            const int j = b0 + warp + k * WARPS;
+            const int32_t *from = j < shared_blocks ? p.block_tables + (size_t)first * p.max_blocks : bt;
+            return k < count ? __ldg(from + j) : -1;
+        }
         return k < count ? __ldg(bt + b0 + warp + k * WARPS) : -1;
     };
     int32_t ids_cur = load_ids(0), ids_nxt = load_ids(32);
@@ -590,6 +616,10 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
         const int orow = MR ? row + gc / G : row, owi = MR ? orow : wi;
         const int h = g * G + (MR ? gc % G : hl);
         if constexpr (TAIL) {
+            if (p.out16) {
+                p.out16[((size_t)orow * p.hq + h) * D + d] = __float2bfloat16(Ls == 0.f ? 0.f : O * vsc / Ls);
+                continue;
+            }
             const size_t pi = ((size_t)orow * p.hq + h) * p.part_stride + p.part_off + split;
             p.part_o[pi * D + d] = O * vsc;
             if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(Ls > 0.f ? M : -INFINITY, Ls);
@@ -852,6 +882,8 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.b = c.b;
     p.part_stride = c.prefix_splits + c.tail_splits;
     p.part_off = c.prefix_splits;
+    p.whole = c.whole ? 1 : 0;
+    p.out16 = c.whole && c.tail_splits == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
     CUtensorMap km, vm;
     if (!make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, c.fp8 ? KV_FP8_E4M3 : KV_BF16, &km, &vm))
         return cudaErrorInvalidValue;

@@ -65,6 +65,7 @@
 #include "trace.h"
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -212,6 +213,7 @@ struct PrefillParams {
 // nearly equal and each CTA finds its own, without a list (see SharedItems).
 struct PrefixParams : PrefillParams {
     SharedBatch b;
+    int one_wave;        // at most one item a CTA
 };
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
@@ -637,18 +639,22 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(PrefillParams p)
     }
 }
 
+// what a work item of the shared mode costs beside its tiles, in tile-times: the Q
+// load, the first products, the last ones and the stores
+constexpr float SHARED_ITEM_TILES = 3.f;
+
 // Which work items the CTAs of the shared mode take.  The groups' items lie end to
 // end in the order (group, part, KV head, query item), the last fastest, so that
 // CTAs next to each other read the same keys; CTA c of the C that take items takes
 // items c, c + C, ...  One warp walks over the groups, 32 at a time.
 struct SharedItems {
     int w0, x, total;                          // the window's first group; the next item's place in it; its items
-    int incl, nq, ns, KT, row0, rows, P, s0;   // this lane's group: items up to it, query items, parts, ...
+    int incl, nq, ns, KT, row0, rows, P, s0, seqs;   // this lane's group: items up to it, query items, parts, ...
 };
 __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &w, int tpt, int lane)
 {
     const int gi = w.w0 + lane;
-    w.nq = w.ns = w.KT = w.row0 = w.rows = w.P = w.s0 = 0;
+    w.nq = w.ns = w.KT = w.row0 = w.rows = w.P = w.s0 = w.seqs = 0;
     if (gi < p.b.num_groups) {
         const SharedGroup gr = shared_group(p.b, gi);
         if (gr.ok && gr.rows > 0 && gr.P > 0) {
@@ -659,6 +665,7 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
             w.rows = gr.rows;
             w.P = gr.P;
             w.s0 = gr.s0;
+            w.seqs = gr.s1 - gr.s0;
         }
     }
     w.incl = w.nq * w.ns * p.hkv;
@@ -670,25 +677,31 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
     w.total = __shfl_sync(0xffffffffu, w.incl, 31);
 }
 
-// How many CTAs take items (C above; the same in every CTA).  The others leave their
-// SMs to the tails, which the decode kernel reads meanwhile: an SM without a CTA of
-// this kernel reads decode_sm_bytes of K/V in one KV tile's time, all together at
-// most bytes_per_tile, and what is left afterwards is read at that rate.  Items are
-// nearly equal, so only the least C for each number of waves is a candidate: a lane
-// each.
-__device__ __forceinline__ int shared_ctas(const PrefixParams &p, int tpt, int lane)
+// How many CTAs take items (C above; the same in every CTA); `w` gets the first
+// window.  The others leave their SMs to the tails, which the decode kernel reads
+// meanwhile: an SM without a CTA of this kernel reads decode_sm_bytes of K/V in one
+// KV tile's time, all together at most bytes_per_tile, and what is left afterwards
+// is read at that rate.  Items are nearly equal, so only the least C for each number
+// of waves is a candidate: a lane each.
+__device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w, int tpt, int lane)
 {
-    float items = 0.f, tiles = 0.f, tail = 0.f;
-    for (int g = lane; g < p.b.num_groups; g += 32) {
-        const SharedGroup gr = shared_group(p.b, g);
-        if (!gr.ok || gr.rows == 0 || gr.P == 0) continue;
-        const int nq = ((gr.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
-        const int KT = (gr.P + p.tile_keys - 1) / p.tile_keys, ns = (KT + p.tiles_per_split - 1) / p.tiles_per_split;
-        items += (float)nq * ns * p.hkv;
-        tiles += (float)nq * KT * p.hkv;
-        tail -= (float)gr.P * (gr.s1 - gr.s0);
-    }
+    // (asked for before anything waits for the groups)
+    float tail = 0.f;
+#pragma unroll 4
     for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, __ldg(p.b.context_lens + s));
+    load_window(p, w, tpt, lane);
+    // (items at most one a CTA: the host's plan stands)
+    if (p.one_wave) return p.grid_ctas;
+    float items = 0.f, tiles = 0.f;
+    SharedItems x = w;
+    for (;;) {
+        items += (float)(x.nq * x.ns) * p.hkv;
+        tiles += (float)x.nq * x.KT * p.hkv;
+        tail -= (float)x.P * x.seqs;
+        if (x.w0 + 32 >= p.b.num_groups) break;
+        x.w0 += 32;
+        load_window(p, x, tpt, lane);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         items += __shfl_xor_sync(0xffffffffu, items, o);
@@ -696,11 +709,11 @@ __device__ __forceinline__ int shared_ctas(const PrefixParams &p, int tpt, int l
         tail += __shfl_xor_sync(0xffffffffu, tail, o);
     }
     if (items < 1.f) return 0;
-    const float bytes = fmaxf(tail, 0.f) * p.decode_key_bytes, each = tiles / items + 2.f * ITEM_TILES;
+    const float bytes = fmaxf(tail, 0.f) * p.decode_key_bytes, each = tiles / items + SHARED_ITEM_TILES;
     const float waves = ceilf(items / (float)p.grid_ctas) + (float)lane;
     const float c = ceilf(items / waves), chunk = waves * each;
     const float beside = fminf((float)(p.num_sms - c) * p.decode_sm_bytes, p.bytes_per_tile);
-    float t = chunk + fmaxf(0.f, bytes - chunk * beside) / p.bytes_per_tile;
+    const float t = chunk + fmaxf(0.f, bytes - chunk * beside) / p.bytes_per_tile;
     float best = t;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -870,8 +883,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
         int ctas = 0;
         if constexpr (SHARED) {
             if (role == 0) {
-                ctas = shared_ctas(p, tpt, lane);
-                load_window(p, win, tpt, lane);
+                ctas = shared_ctas(p, win, tpt, lane);
                 win.x = (int)blockIdx.x;
             }
         }
@@ -1427,6 +1439,34 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 const size_t rh = (size_t)(row0 + (row_valid ? i : i0)) * p.hq + head;
                 const size_t pi = rh * p.max_splits + split;
                 const bool whole = !SHARED && nsplit == 1;
+                if constexpr (SHARED) {
+                    // Eight lanes exchange their rows' 16-byte pieces, so that they store
+                    // one row's 128 bytes together.  (A lane storing its own row's pieces
+                    // touches 32 rows with each instruction: an item's two tiles, 128
+                    // KiB, took 7 us that way.)
+                    float *const to = p.part_o + (((size_t)(row0 + i0) * p.hq + g * G) * p.max_splits + split) * D + (lane & 7) * 4;
+                    const int rows = (i1 - i0) * G, lg = __ffs(G) - 1;   // (G is a power of two)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        tmem_ld32(tO(gi) + lane_base + c * 32, o);
+                        uint32_t v[8][4];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(o[e] * vsc);
+                        oct_transpose(v, lane);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int rj = (r & ~7) + j;
+                            if (rj < rows)
+                                *reinterpret_cast<uint4 *>(to + ((size_t)(rj >> lg) * p.hq + (rj & (G - 1))) * p.max_splits * D + c * 32) =
+                                    make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+                        }
+                    }
+                    if (row_valid) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
+                    cs += T;
+                    ++kg;
+                    continue;
+                }
                 const float inv = ((whole && l > 0.f) ? 1.f / l : (whole ? 0.f : 1.f)) * vsc;
                 float4 *dst = reinterpret_cast<float4 *>(whole ? p.out + rh * D : p.part_o + pi * D);
 #pragma unroll
@@ -1663,38 +1703,44 @@ cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret
 
 // The layout and the parts of shared prefixes.  One query tile a CTA (128-key tiles)
 // when the groups' rows x heads fill one tile on average, over a bf16 cache.  The
-// number of parts minimises a makespan: waves of equal items over the SMs, each with
-// a fixed cost, and the partial results' write and read.
-void plan_prefixes(SharedCall &c)
+// number of parts minimises the modelled end of prefixes, tails and merge (the terms
+// of shared_ctas, from the caller's bounds): with several groups their prefixes are
+// taken to be ragged, half as long as the longest.
+void plan_prefixes(SharedCall &c, double tail_keys)
 {
     const int G = c.hq / c.hkv, ng = std::max(1, c.b.num_groups);
     c.big = !c.fp8 && (int64_t)c.b.total_rows * G <= (int64_t)BM * ng;
     const int tile_keys = c.big ? 128 : 64, item_rows = (BM / G) * (c.big ? 1 : 2);
     const int W = (c.b.max_prefix + tile_keys - 1) / tile_keys;
-    if (W == 0 || c.b.num_groups == 0) {
-        c.prefix_splits = c.prefix_tiles = 0;
-        c.prefix_items = 0;
-        return;
-    }
+    c.prefix_splits = c.prefix_tiles = 0;
+    c.prefix_items = 0;
+    if (W == 0 || c.b.num_groups == 0) return;
     const int64_t rows = ((int64_t)c.b.total_rows + ng - 1) / ng;
-    const int64_t problems = ng * ((rows + item_rows - 1) / item_rows) * c.hkv;
-    const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / (BYTES_PER_TILE_TIME * tile_keys / 64.0);
-    const double fixed = CTA_FIXED_TILES * 64.0 / tile_keys;
+    const double problems = (double)ng * ((rows + item_rows - 1) / item_rows) * c.hkv;
+    const double per_tile = BYTES_PER_TILE_TIME * tile_keys / 64.0, per_sm = DECODE_SM_BYTES_PER_TILE_TIME * tile_keys / 64.0;
+    const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / per_tile;
+    const double tail = tail_keys * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+    const double sms = (double)NUM_SMS, mean = ng > 1 ? 0.5 : 1.0;
     double best = 0;
     int pick = 0;
-    for (int s = 1; s <= std::min(W, 256); ++s) {
+    for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
         const int len = (W + s - 1) / s, parts = (W + len - 1) / len;
-        const int64_t waves = (problems * parts + NUM_SMS - 1) / NUM_SMS;
-        const double cost = (double)waves * (len + fixed) + parts * merge;
-        if (pick == 0 || cost < best) {
-            best = cost;
-            pick = s;
+        const double items = problems * (1.0 + mean * (parts - 1)), each = std::min<double>(len, mean * W) + SHARED_ITEM_TILES;
+        const double least = std::ceil(items / sms);
+        for (int w = 0; w < 4; ++w) {
+            const double ctas = std::ceil(items / (least + w)), chunk = (least + w) * each;
+            const double beside = std::min((sms - ctas) * per_sm, per_tile);
+            const double cost = chunk + std::max(0.0, tail - chunk * beside) / per_tile + parts * merge;
+            if (pick == 0 || cost < best) {
+                best = cost;
+                pick = s;
+            }
         }
     }
     c.prefix_tiles = (W + pick - 1) / pick;
     c.prefix_splits = (W + c.prefix_tiles - 1) / c.prefix_tiles;
-    // at most: every group's rows in tiles of their own
-    c.prefix_items = ((int64_t)c.b.total_rows / item_rows + c.b.num_groups) * c.hkv * c.prefix_splits;
+    // at most: every group's rows in tiles of their own, each group's last tile of one row
+    c.prefix_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_groups * (item_rows - 1)) / item_rows * c.hkv * c.prefix_splits;
 }
 
 cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
@@ -1726,6 +1772,7 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.decode_sm_bytes = (float)(DECODE_SM_BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
     p.q_box_bytes = tpt * G * 128;
     p.grid_ctas = (int)std::min<int64_t>(c.prefix_items, p.num_sms);
+    p.one_wave = c.prefix_items <= p.num_sms;
     CUtensorMap qm, km, vm;
     if (!pkv_host::encode_tmap_3d(&qm, c.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, c.hq, c.b.total_rows, (uint64_t)D * 2,
                                   (uint64_t)c.hq * D * 2, 64, G, tpt, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -23,7 +23,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     const float *part_o, *part_ml;
     int hq, prefix_splits, splits;         // splits: of prefix and tail together
-    int tile_keys, prefix_tiles, tail_part_blocks;
+    int tile_keys, prefix_tiles, tail_part_blocks, whole;
 };
 
 // Joins a row's parts, those of its group's prefix and those of its own tail, by the
@@ -33,8 +33,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 {
     const int row = blockIdx.x, h = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     // (what describes the batch was written before the kernels of the parts began)
-    const int s = p.b.cu_q_lens ? last_at_most(p.b.cu_q_lens, p.b.num_seqs, row) : row;
-    const SharedSeq w = shared_seq(p.b, s);
+    const int s = p.b.cu_q_lens ? last_at_most(p.b.cu_q_lens, p.b.num_seqs, row, lane) : row;
+    const SharedSeq w = shared_seq(p.b, s, lane);
     griddep_wait();
     griddep_launch_dependents();
     if (h >= p.hq || w.state == SEQ_BAD || row < w.row0 || row >= w.row0 + w.n) return;
@@ -43,48 +43,87 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
         *out = make_uint2(0u, 0u);
         return;
     }
-    const int KT = (w.P + p.tile_keys - 1) / p.tile_keys, np = KT ? (KT + p.prefix_tiles - 1) / p.prefix_tiles : 0;
-    const int blocks = (w.L - w.P + BS - 1) / BS, nt = (blocks + p.tail_part_blocks - 1) / p.tail_part_blocks;
+    const int P = p.whole ? 0 : w.P;          // keys that have parts of their own
+    const int KT = (P + p.tile_keys - 1) / p.tile_keys, np = KT ? (KT + p.prefix_tiles - 1) / p.prefix_tiles : 0;
+    const int blocks = (w.L - P + BS - 1) / BS, nt = (blocks + p.tail_part_blocks - 1) / p.tail_part_blocks;
     const size_t base = ((size_t)row * p.hq + h) * p.splits;
     auto at = [&](int i) { return base + (i < np ? i : p.prefix_splits + i - np); };
     const int n = np + nt;
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[2 * at(i)]);
+    // the first 32 parts' (max, sum), a part a lane, and the first parts' rows are asked
+    // for together, before anything depends on them
+    constexpr int AHEAD = 8;
+    float2 e0 = make_float2(-INFINITY, 0.f);
+    if (lane < n) e0 = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at(lane));
+    float4 v[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        if (u < n) v[u] = reinterpret_cast<const float4 *>(p.part_o + at(u) * D)[lane];
+    float M = e0.x;
+    for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.part_ml[2 * at(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     // (no finite maximum: a row whose sums are not numbers stays one)
     const float R = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int i = 0; i < n; ++i) {
-        const float2 e = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at(i));
-        const float f = ex2(e.x - R);
-        sum += f * e.y;
-        const float4 o = reinterpret_cast<const float4 *>(p.part_o + at(i) * D)[lane];
-        acc.x += f * o.x;
-        acc.y += f * o.y;
-        acc.z += f * o.z;
-        acc.w += f * o.w;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        if (i0 > 0) e0 = i0 + lane < n ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * at(i0 + lane)) : make_float2(-INFINITY, 0.f);
+        const float weight = ex2(e0.x - R), part = weight * e0.y;
+        for (int k0 = 0; k0 < min(32, n - i0); k0 += AHEAD) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = i0 + k0 + u;
+                const float f = __shfl_sync(0xffffffffu, weight, k0 + u), l = __shfl_sync(0xffffffffu, part, k0 + u);
+                if (i < n) {
+                    sum += l;
+                    acc.x += f * v[u].x;
+                    acc.y += f * v[u].y;
+                    acc.z += f * v[u].z;
+                    acc.w += f * v[u].w;
+                }
+                if (i + AHEAD < n) v[u] = reinterpret_cast<const float4 *>(p.part_o + at(i + AHEAD) * D)[lane];
+            }
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
-// The parts of prefixes and tails, from the call's sizes and bounds.
+// How a call is done, from its sizes and bounds.
+//
+// whole: no kernel for the prefixes.  The tails' kernel then attends whole contexts
+// and reads a prefix once a sequence, from L2, which for small batches takes less
+// time than a second kernel and a merge.
+//
+// Tails: partitions of 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, shorter
+// ones (down to 16 blocks) where the grid would hold fewer than TAIL_CTAS.
+constexpr int64_t WHOLE_BYTES = 64ll << 20, TAIL_CTAS = 2 * 3 * 152;
 void plan(SharedCall &c, int32_t max_tail_len)
 {
-    pkv_prefill::plan_prefixes(c);
-    pkv_decode::plan_splits(std::max(1, (max_tail_len + BS - 1) / BS), 0, c.b.num_seqs, c.hq, &c.tail_part_blocks,
-                            &c.tail_splits);
+    const int64_t key_bytes = (int64_t)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+    c.whole = (int64_t)c.b.num_seqs * c.b.max_prefix <= WHOLE_BYTES / key_bytes;
+    c.prefix_splits = 0;
+    c.prefix_items = 0;
+    if (!c.whole) pkv_prefill::plan_prefixes(c, 0.5 * c.b.num_seqs * max_tail_len);
+    const int64_t keys = (int64_t)max_tail_len + (c.whole ? c.b.max_prefix : 0);
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
+    const int64_t most = blocks <= 512 ? 64 : blocks <= 4096 ? 128 : 256;
+    const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
+    const int64_t part = std::min(blocks, std::min(most, std::max<int64_t>(16, want)));
+    c.tail_splits = (int)((blocks + part - 1) / part);
+    c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+// (none where the only kernel writes the output itself)
 size_t part_o_bytes(const SharedCall &c)
 {
+    if (c.whole && c.tail_splits == 1) return 0;
     return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * D * sizeof(float));
 }
 size_t part_ml_bytes(const SharedCall &c)
 {
+    if (c.whole && c.tail_splits == 1) return 0;
     return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * 2 * sizeof(float));
 }
 
@@ -153,6 +192,7 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     SharedCall c{};
     c.b = {cu_groups, prefix_lens, cu_q_lens, context_lens, num_groups, num_seqs, total_q_tokens, max_q_len,
            max_prefix_len / BS * BS, max_tail_len, max_blocks_per_seq};
+    c.out = out;
     c.q = static_cast<const uint16_t *>(q);
     c.k_cache = k_cache;
     c.v_cache = v_cache;
@@ -174,7 +214,7 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     c.b.max_prefix = std::min(c.b.max_prefix, max_blocks_per_seq * BS);
     c.b.max_tail = std::min(c.b.max_tail, max_blocks_per_seq * BS);
     const size_t o_bytes = part_o_bytes(c);
-    if (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < o_bytes + part_ml_bytes(c))
+    if (o_bytes && (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < o_bytes + part_ml_bytes(c)))
         return KV_ERR_INVALID;
     c.part_o = static_cast<float *>(workspace);
     c.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
@@ -182,8 +222,10 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     const bool prefixes = c.prefix_splits > 0;
     if (prefixes && pkv_prefill::launch_prefixes(c, st) != cudaSuccess) return KV_ERR_CUDA;
     if (pkv_decode::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
+    if (!o_bytes) return KV_OK;
     const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
-                           c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks};
+                           c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,
+                           c.whole ? 1 : 0};
     const dim3 grid(total_q_tokens, (num_q_heads + MERGE_WARPS - 1) / MERGE_WARPS);
     return pkv_host::launch_ex(shared_merge_kernel, grid, dim3(32 * MERGE_WARPS), 0, st, true, m) == cudaSuccess
                ? KV_OK : KV_ERR_CUDA;

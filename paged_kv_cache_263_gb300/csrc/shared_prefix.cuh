@@ -23,14 +23,17 @@ struct SharedBatch {
 };
 
 #if defined(__CUDACC__)
-// the last i in [0, n) with v[i] <= x, or 0 (bounded whatever v holds)
-__device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x)
+// the last i in [0, n) with v[i] <= x, or 0 (bounded whatever v holds; v non-decreasing):
+// by the whole warp, a memory round trip for every factor of 32
+__device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x, int lane)
 {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(v + mid) <= x) lo = mid;
-        else hi = mid;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) >> 5, i = lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, i < n && __ldg(v + lo + min(i, n - 1)) <= x);
+        const int at = m ? 31 - __clz(m) : 0;
+        lo += at * step;
+        n = min(step, n - at * step);
     }
     return lo;
 }
@@ -65,27 +68,28 @@ struct SharedSeq {
     int L, P;         // context, and how much of it is its group's prefix
     int first;        // the sequence whose table row the prefix is read through
 };
-__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s)
+// (by the whole warp: the sequence is the same in all lanes)
+__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int lane)
 {
     SharedSeq r;
     r.state = SEQ_BAD;
+    // what does not depend on the group is asked for together with it
     r.row0 = b.cu_q_lens ? __ldg(b.cu_q_lens + s) : s;
-    r.n = b.cu_q_lens ? __ldg(b.cu_q_lens + s + 1) - r.row0 : 1;
+    r.n = (b.cu_q_lens ? __ldg(b.cu_q_lens + s + 1) : s + 1) - r.row0;
     r.L = __ldg(b.context_lens + s);
     r.P = 0;
     r.first = s;
-    if (r.row0 < 0 || r.n < 0 || r.row0 > b.total_rows - r.n || r.n > b.max_q_len) return r;
     bool ok = true;
     if (b.num_groups > 0) {
-        const int g = last_at_most(b.cu_groups, b.num_groups, s);
-        const int s0 = __ldg(b.cu_groups + g), s1 = __ldg(b.cu_groups + g + 1);
-        if (s >= s0 && s < s1) {
-            const SharedGroup gr = shared_group(b, g);
+        const int g = b.num_groups > 1 ? last_at_most(b.cu_groups, b.num_groups, s, lane) : 0;
+        const SharedGroup gr = shared_group(b, g);
+        if (s >= gr.s0 && s < gr.s1) {
             ok = gr.ok && r.row0 >= gr.row0 && r.row0 + r.n <= gr.row0 + gr.rows;
             r.P = gr.P;
-            r.first = s0;
+            r.first = gr.s0;
         }
     }
+    if (r.row0 < 0 || r.n < 0 || r.row0 > b.total_rows - r.n || r.n > b.max_q_len) return r;
     if (r.L == 0) {
         r.state = SEQ_EMPTY;
         return r;

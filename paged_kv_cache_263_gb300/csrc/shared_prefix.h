@@ -8,6 +8,7 @@
 
 struct SharedCall {
     pkv::SharedBatch b;
+    void *out;                        // bf16
     const uint16_t *q;
     const void *k_cache, *v_cache;
     const int32_t *block_tables;
@@ -15,6 +16,7 @@ struct SharedCall {
     float *part_o, *part_ml;          // [rows][hq][prefix_splits + tail_splits][128], [..][2] (max, sum)
     int hq, hkv, num_blocks;
     bool fp8, big;                    // big: one query tile a CTA, 128-key tiles
+    bool whole;                       // no kernel for the prefixes: the tails' attends whole contexts
     int prefix_splits, prefix_tiles;  // parts of a prefix at most, and KV tiles a part
     int64_t prefix_items;             // work items of the prefixes at most
     int tail_splits, tail_part_blocks;
@@ -23,11 +25,10 @@ struct SharedCall {
 
 namespace pkv_decode {
 cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st);
-void plan_splits(int32_t max_blocks, int32_t num_splits, int32_t num_seqs, int32_t hq, int32_t *part_blocks,
-                 int32_t *splits);
 }  // namespace pkv_decode
 namespace pkv_prefill {
-// the parts that prefixes are cut into (fields big and prefix_*)
-void plan_prefixes(SharedCall &c);
+// the parts that prefixes are cut into (fields big and prefix_*); tail_keys: what the
+// tails of the batch hold together, about
+void plan_prefixes(SharedCall &c, double tail_keys);
 cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st);
 }  // namespace pkv_prefill

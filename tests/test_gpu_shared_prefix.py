@@ -95,12 +95,19 @@ class Batch:
         return osp.shared(f64(self.q), self.k64, self.v64, self.tables, self.lens, self.groups, self.prefix, self.scale,
                           cu=self.cu, fp8=self.fp8, **kw)
 
+    def apart(self):
+        """A bound on the prefixes from which on a kernel of its own attends them (a batch
+        with less to read does without)."""
+        return max(int(max([0, *self.prefix])), 16 + (64 << 20) // (self.B * self.hkv * D * (2 if self.fp8 else 4)))
+
     def check(self, flags=0, got=None, ref=None, **kw):
+        exp, tol, f = ref or self.reference()
+        assert f == flags
+        if got is None and "max_prefix_len" not in kw:
+            self.check(flags, ref=(exp, tol, f), max_prefix_len=self.apart(), **kw)
         got = self.call(**kw) if got is None else got
         assert pkv.kv_last_device_status() == (5 if flags else 0)
         assert pkv.kv_last_device_status_flags() == flags
-        exp, tol, f = ref or self.reference()
-        assert f == flags
         compare(f64(got), exp, tol)
         return got
 
@@ -173,6 +180,7 @@ def test_long_prefix_of_many_parts():
     b = Batch([20], [40000], np.arange(1, 21), hq=8, hkv=1, seed=3)
     b.check()
     b.check(max_prefix_len=65536)
+    Batch([1, 20], [40000, 9000], np.arange(1, 22), hq=16, hkv=2, seed=4).check()
 
 
 def test_sharp_scores():
@@ -213,10 +221,10 @@ def test_padded_and_bad_sequences():
     groups = b.groups
     for bad in ([0, 4, 8, 12], [-1, 4, 8, 11], [0, 4, 99, 11]):
         b.groups = np.array(bad)
-        got = b.call()
-        assert pkv.kv_last_device_status_flags() in (0, 4) and pkv.kv_last_device_status() == 5
-        rows = f64(got)
-        assert (np.isfinite(rows)).all()
+        for bound in (100, b.apart()):
+            got = b.call(max_prefix_len=bound)
+            assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 4
+            assert np.isfinite(f64(got)).all()
     b.groups = groups
     b.check()
 
@@ -232,10 +240,11 @@ def test_blocks_outside_the_pool():
         b = Batch([3, 3], [200, 150], [20, 30, 40, 50, 60, 70], hq=8, hkv=2)
         exp, tol, _ = b.reference()
         b.tables[0, 3 if where == "prefix" else 13] = b.nb + 5
-        got = b.call()
-        assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 1
-        first = 3 if where == "prefix" else 1
-        compare(f64(got)[first:], exp[first:], tol[first:])
+        for bound in (200, b.apart()):
+            got = b.call(max_prefix_len=bound)
+            assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 1
+            first = 3 if where == "prefix" else 1
+            compare(f64(got)[first:], exp[first:], tol[first:])
 
 
 @pytest.mark.parametrize("where", [0, 5])
@@ -245,28 +254,31 @@ def test_queries_that_are_not_finite(bad, where):
     b = Batch([4, 3], [200, 90], [20, 30, 40, 5, 7, 9, 11], hq=8, hkv=2)
     exp, tol, _ = b.reference()
     b.q[where, 3, 17] = bad
-    got = f64(b.call())
-    assert pkv.kv_last_device_status() == 0
-    assert np.isnan(got[where, 3]).all()
-    got[where, 3] = exp[where, 3]
-    compare(got, exp, tol)
+    for bound in (200, b.apart()):
+        got = f64(b.call(max_prefix_len=bound))
+        assert pkv.kv_last_device_status() == 0
+        assert np.isnan(got[where, 3]).all()
+        got[where, 3] = exp[where, 3]
+        compare(got, exp, tol)
 
 
 def test_any_placement_and_workspace_gives_the_same_bits():
-    args = dict(sizes=[20, 7], prefix=[3000, 800], tails=np.arange(1, 28) * 11, hq=16, hkv=2)
-    b = Batch(**args)
-    need = pkv.paged_attention_shared_prefix_workspace_size(b.B, b.B, 1, 2, 16, 2, 3000, b.width * BS)
+    args = dict(sizes=[20, 7], prefix=[3000, 800], tails=np.arange(1, 28) * 11, hq=16, hkv=4)
+    b = Batch(**args, width=300)
+    need = pkv.paged_attention_shared_prefix_workspace_size(b.B, b.B, 1, 2, 16, 4, 3000, b.width * BS)
     ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
     ws = ws[-ws.data_ptr() % 256:][:need]
-    first = b.check(workspace=ws if need else None).view(torch.int16).clone()
+    assert need > 0
+    exact = dict(max_prefix_len=3000)
+    first = b.check(workspace=ws, **exact).view(torch.int16).clone()
     ws.fill_(0x7F)
-    assert torch.equal(b.call(workspace=ws if need else None).view(torch.int16), first)
+    assert torch.equal(b.call(workspace=ws, **exact).view(torch.int16), first)
     # another order of the blocks
     perm = np.random.default_rng(8).permutation(b.nb)
     inv = torch.tensor(np.argsort(perm), device="cuda")
     b.k, b.v = b.k[inv].contiguous(), b.v[inv].contiguous()
     b.tables = np.where(b.tables >= 0, perm[b.tables.clip(0)], b.tables)
-    assert torch.equal(b.call().view(torch.int16), first)
+    assert torch.equal(b.call(**exact).view(torch.int16), first)
     assert pkv.kv_last_device_status() == 0
 
 
