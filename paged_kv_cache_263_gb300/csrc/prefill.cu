@@ -1447,7 +1447,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     float *const to = p.part_o + (((size_t)(row0 + i0) * p.hq + g * G) * p.max_splits + split) * D + (lane & 7) * 4;
                     const int rows = (i1 - i0) * G, lg = __ffs(G) - 1;   // (G is a power of two)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 4 && (r & ~31) < rows; ++c) {   // (a warp without rows stores nothing)
                         float o[32];
                         tmem_ld32(tO(gi) + lane_base + c * 32, o);
                         uint32_t v[8][4];

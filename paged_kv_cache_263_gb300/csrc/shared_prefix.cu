@@ -92,16 +92,22 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // How a call is done, from its sizes and bounds.
 //
 // whole: no kernel for the prefixes.  The tails' kernel then attends whole contexts
-// and reads a prefix once a sequence, from L2, which for small batches takes less
-// time than a second kernel and a merge.
+// and reads a prefix once a sequence, from L2.  That takes 5 to 25 us, and a second
+// kernel and a merge 15 to 18 at least, so it pays up to WHOLE_KEYS keys x KV heads of
+// prefix, counted once a sequence: 16 sequences of 512 tokens, 8 KV heads, take 9.4 us
+// against 15.1, of 1,024 tokens 15.8 against 15.3, of 4,096 tokens 26.9 against 17.6
+// (bf16); 32 of 1,024, 2 KV heads, 11.1 against 16.3, of 2,048 18.0 against 18.2.  With
+// fewer than three sequences a group there is little to save, and it pays up to four
+// times that: 8 sequences in 4 groups of 8,192 tokens take 37.5 us against 48.8 (bf16),
+// of 16,384 tokens 60.4 against 83.6 (fp8).
 //
 // Tails: partitions of 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, shorter
 // ones (down to 16 blocks) where the grid would hold fewer than TAIL_CTAS.
-constexpr int64_t WHOLE_BYTES = 64ll << 20, TAIL_CTAS = 2 * 3 * 152;
+constexpr int64_t WHOLE_KEYS = 128ll << 10, TAIL_CTAS = 2 * 3 * 152;
 void plan(SharedCall &c, int32_t max_tail_len)
 {
-    const int64_t key_bytes = (int64_t)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
-    c.whole = (int64_t)c.b.num_seqs * c.b.max_prefix <= WHOLE_BYTES / key_bytes;
+    c.whole = (int64_t)c.b.num_seqs * c.b.max_prefix <=
+              WHOLE_KEYS / c.hkv * (c.b.num_seqs < 3ll * c.b.num_groups ? 4 : 1);
     c.prefix_splits = 0;
     c.prefix_items = 0;
     if (!c.whole) pkv_prefill::plan_prefixes(c, 0.5 * c.b.num_seqs * max_tail_len);
@@ -109,7 +115,9 @@ void plan(SharedCall &c, int32_t max_tail_len)
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
     const int64_t most = blocks <= 512 ? 64 : blocks <= 4096 ? 128 : 256;
     const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
-    const int64_t part = std::min(blocks, std::min(most, std::max<int64_t>(16, want)));
+    // (whole contexts that fit 32 blocks are written by the only kernel: no merge)
+    const int64_t least = c.whole && blocks <= 32 ? 32 : 16;
+    const int64_t part = std::min(blocks, std::min(most, std::max(least, want)));
     c.tail_splits = (int)((blocks + part - 1) / part);
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
 }

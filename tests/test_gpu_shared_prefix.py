@@ -98,7 +98,7 @@ class Batch:
     def apart(self):
         """A bound on the prefixes from which on a kernel of its own attends them (a batch
         with less to read does without)."""
-        return max(int(max([0, *self.prefix])), 16 + (64 << 20) // (self.B * self.hkv * D * (2 if self.fp8 else 4)))
+        return max(int(max([0, *self.prefix])), 16 + 4 * (128 << 10) // (self.B * self.hkv))
 
     def check(self, flags=0, got=None, ref=None, **kw):
         exp, tol, f = ref or self.reference()
