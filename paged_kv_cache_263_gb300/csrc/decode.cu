@@ -146,7 +146,18 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-template <bool FP8>
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y,
+                                                 int32_t z, uint32_t bar, uint64_t pol)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
+        : "memory");
+}
+
+// BOX: a tile's two 64-dim halves in one 3-D box (the maps are made for it)
+template <bool FP8, bool BOX>
 __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CUtensorMap *km,
                                             const CUtensorMap *vm, int32_t y, uint64_t pol)
 {
@@ -154,6 +165,9 @@ __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CU
     if constexpr (FP8) {
         tma_load_2d_hint(dst, km, 0, y, bar, pol);
         tma_load_2d_hint(dst + Geo<FP8>::TILE, vm, 0, y, bar, pol);
+    } else if constexpr (BOX) {
+        tma_load_3d_hint(dst, km, 0, y, 0, bar, pol);
+        tma_load_3d_hint(dst + 4096, vm, 0, y, 0, bar, pol);
     } else {
         tma_load_2d_hint(dst, km, 0, y, bar, pol);
         tma_load_2d_hint(dst + 2048, km, 64, y, bar, pol);
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
             const uint32_t bar = bar0 + 8 * st;
             if (phys >= 0 && phys < p.num_blocks) {
                 fence_proxy_async_smem();
-                issue_stage<FP8>(ring + st * GE::STAGE, bar, &kmap, &vmap, (phys * p.hkv + g) * BS, l2pol);
+                issue_stage<FP8, TAIL>(ring + st * GE::STAGE, bar, &kmap, &vmap, (phys * p.hkv + g) * BS, l2pol);
             } else {
                 flag(ST_BAD_BLOCK);
                 mbar_arrive(bar);  // completes the phase without data
@@ -885,7 +899,14 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.whole = c.whole ? 1 : 0;
     p.out16 = c.whole && c.tail_splits == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
     CUtensorMap km, vm;
-    if (!make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, c.fp8 ? KV_FP8_E4M3 : KV_BF16, &km, &vm))
+    // (bf16: dims (64 dims, rows, halves), strides (row 256 B, half 128 B))
+    const uint64_t rows = (uint64_t)c.num_blocks * c.hkv * BS;
+    auto halves = [&](CUtensorMap *m, const void *cache) {
+        return pkv_host::encode_tmap_3d(m, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, rows, 2, D * 2, 128, 64, BS, 2,
+                                        CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!(c.fp8 ? make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, KV_FP8_E4M3, &km, &vm)
+                : halves(&km, c.k_cache) && halves(&vm, c.v_cache)))
         return cudaErrorInvalidValue;
     const int64_t cols = (int64_t)c.b.max_q_len * p.group;
     const bool two = cols > 8;

@@ -155,7 +155,9 @@ enum {
 };
 // a work item as the producer hands it to the other warps (valid = 0: no more)
 struct ItemSlot {
-    int s, row0, n, L, t0q, has1, j0, T, nsplit, g, split, valid, pad[4];
+    int s, row0, n, L, t0q, has1, j0, T, nsplit, g, split, valid;
+    int skip, causal;    // shared mode: key 0 is in the table row's block `skip`; the rows see keys up to their own
+    int pad[2];
 };
 constexpr uint32_t SLOT_OFF = 512;   // within the barrier area
 static_assert(NBAR * 8 + 8 <= SLOT_OFF && SLOT_OFF + NSLOT * sizeof(ItemSlot) <= 1024, "barrier area");
@@ -211,8 +213,13 @@ struct PrefillParams {
 // sees every key, and every result is a partial one, at ((row x hq + head) x
 // max_splits + part).  The parts are tiles_per_split KV tiles, so the items are
 // nearly equal and each CTA finds its own, without a list (see SharedItems).
+// joined: the sequences' own tails are items too, causal, in parts of tail_tiles tiles
+// and with results from part tail_at on; else the decode kernel attends them.
 struct PrefixParams : PrefillParams {
     SharedBatch b;
+    int sources;         // groups, then sequences if joined
+    int groups;          // of them
+    int joined, tail_tiles, tail_at;
     int one_wave;        // at most one item a CTA
 };
 
@@ -643,30 +650,46 @@ __global__ void __launch_bounds__(1024) tile_prefix_kernel(PrefillParams p)
 // load, the first products, the last ones and the stores
 constexpr float SHARED_ITEM_TILES = 3.f;
 
-// Which work items the CTAs of the shared mode take.  The groups' items lie end to
-// end in the order (group, part, KV head, query item), the last fastest, so that
-// CTAs next to each other read the same keys; CTA c of the C that take items takes
-// items c, c + C, ...  One warp walks over the groups, 32 at a time.
+// Which work items the CTAs of the shared mode take.  The items of the sources (the
+// groups, then the sequences if they are joined) lie end to end in the order (source,
+// part, KV head, query item), the last fastest, so that CTAs next to each other read
+// the same keys; CTA c of the C that take items takes items c, c + C, ...  One warp
+// walks over the sources, 32 at a time.
 struct SharedItems {
-    int w0, x, total;                          // the window's first group; the next item's place in it; its items
-    int incl, nq, ns, KT, row0, rows, P, s0, seqs;   // this lane's group: items up to it, query items, parts, ...
+    int w0, x, total;                     // the window's first source; the next item's place in it; its items
+    int incl;                             // this lane's source: items up to it,
+    int nq, ns, KT, row0, rows, L;        // query items, parts, KV tiles, rows and keys,
+    int s, skip, seqs;                    // its table row, the block of key 0; the group's sequences
 };
 __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &w, int tpt, int lane)
 {
-    const int gi = w.w0 + lane;
-    w.nq = w.ns = w.KT = w.row0 = w.rows = w.P = w.s0 = w.seqs = 0;
-    if (gi < p.b.num_groups) {
-        const SharedGroup gr = shared_group(p.b, gi);
-        if (gr.ok && gr.rows > 0 && gr.P > 0) {
-            w.nq = ((gr.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
-            w.KT = (gr.P + p.tile_keys - 1) / p.tile_keys;
-            w.ns = (w.KT + p.tiles_per_split - 1) / p.tiles_per_split;
+    const int u = w.w0 + lane;
+    w.nq = w.ns = w.KT = w.row0 = w.rows = w.L = w.s = w.skip = w.seqs = 0;
+    if (u < p.groups) {
+        const SharedGroup gr = shared_group(p.b, u);
+        if (gr.ok) {
             w.row0 = gr.row0;
             w.rows = gr.rows;
-            w.P = gr.P;
-            w.s0 = gr.s0;
+            w.L = gr.P;
+            w.s = gr.s0;
             w.seqs = gr.s1 - gr.s0;
         }
+    } else if (u < p.sources) {
+        const SharedSeq q = shared_seq(p.b, u - p.groups);
+        if (q.state == SEQ_BAD) flag(ST_BAD_LEN);
+        if (q.state == SEQ_OK) {
+            w.row0 = q.row0;
+            w.rows = q.n;
+            w.L = q.L - q.P;
+            w.s = u - p.groups;
+            w.skip = q.P / BS;
+        }
+    }
+    if (w.rows > 0 && w.L > 0) {
+        const int len = u < p.groups ? p.tiles_per_split : p.tail_tiles;
+        w.nq = ((w.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
+        w.KT = (w.L + p.tile_keys - 1) / p.tile_keys;
+        w.ns = (w.KT + len - 1) / len;
     }
     w.incl = w.nq * w.ns * p.hkv;
 #pragma unroll
@@ -690,15 +713,15 @@ __device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w
 #pragma unroll 4
     for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, __ldg(p.b.context_lens + s));
     load_window(p, w, tpt, lane);
-    // (items at most one a CTA: the host's plan stands)
-    if (p.one_wave) return p.grid_ctas;
+    // (no tails beside this kernel, or at most one item a CTA: the host's plan stands)
+    if (p.joined || p.one_wave) return p.grid_ctas;
     float items = 0.f, tiles = 0.f;
     SharedItems x = w;
     for (;;) {
         items += (float)(x.nq * x.ns) * p.hkv;
         tiles += (float)x.nq * x.KT * p.hkv;
-        tail -= (float)x.P * x.seqs;
-        if (x.w0 + 32 >= p.b.num_groups) break;
+        tail -= (float)x.L * x.seqs;
+        if (x.w0 + 32 >= p.sources) break;
         x.w0 += 32;
         load_window(p, x, tpt, lane);
     }
@@ -833,6 +856,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
         it.g = slots[sl].g;
         it.split = slots[sl].split;
         it.valid = slots[sl].valid;
+        if constexpr (SHARED) {
+            it.skip = slots[sl].skip;
+            it.causal = slots[sl].causal;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + sl));
         return it.valid != 0;
@@ -899,7 +926,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 // CTAs past the work list's count leave their SMs to the decode rows
                 if constexpr (SHARED) {
                     if ((int)blockIdx.x < ctas) {
-                        while (win.x >= win.total && win.w0 + 32 < p.b.num_groups) {
+                        while (win.x >= win.total && win.w0 + 32 < p.sources) {
                             win.x -= win.total;
                             win.w0 += 32;
                             load_window(p, win, tpt, lane);
@@ -911,16 +938,19 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                             const int nq = __shfl_sync(0xffffffffu, win.nq, at), ns = __shfl_sync(0xffffffffu, win.ns, at);
                             const int r = x - (__shfl_sync(0xffffffffu, win.incl, at) - nq * ns * p.hkv);
                             const int KT = __shfl_sync(0xffffffffu, win.KT, at), part_tiles = (KT + ns - 1) / ns;
-                            it.s = __shfl_sync(0xffffffffu, win.s0, at);
+                            it.s = __shfl_sync(0xffffffffu, win.s, at);
                             it.row0 = __shfl_sync(0xffffffffu, win.row0, at);
                             it.n = __shfl_sync(0xffffffffu, win.rows, at);
-                            it.L = __shfl_sync(0xffffffffu, win.P, at);
+                            it.L = __shfl_sync(0xffffffffu, win.L, at);
+                            it.skip = __shfl_sync(0xffffffffu, win.skip, at);
+                            it.causal = win.w0 + at >= p.groups;
                             it.t0q = p.item_tiles * (r % nq);
                             it.has1 = p.item_tiles == 2 && (it.t0q + 1) * tpt < it.n;
                             it.g = (r / nq) % p.hkv;
-                            it.split = r / nq / p.hkv;
+                            const int part = r / nq / p.hkv;
+                            it.split = it.causal ? p.tail_at + part : part;
                             it.nsplit = ns;
-                            it.j0 = it.split * part_tiles;
+                            it.j0 = part * part_tiles;
                             it.T = min(KT, it.j0 + part_tiles) - it.j0;
                             it.valid = it.T > 0;    // (always: (ns - 1) x part_tiles < KT)
                         }
@@ -964,6 +994,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     slots[sl].g = it.g;
                     slots[sl].split = it.split;
                     slots[sl].valid = it.valid;
+                    if constexpr (SHARED) {
+                        slots[sl].skip = it.skip;
+                        slots[sl].causal = it.causal;
+                    }
                     mbar_arrive(bar(B_IFULL + sl));
                 }
                 __syncwarp();
@@ -982,7 +1016,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             } else if (!read_item(k, it)) {
                 break;
             }
-            const int32_t *bt = p.block_tables + (size_t)it.s * p.max_blocks;
+            const int32_t *bt = p.block_tables + (size_t)it.s * p.max_blocks + (SHARED ? it.skip : 0);
             const int nblk = (it.L + BS - 1) / BS;
             const int j0 = it.j0, T = it.T;
             if constexpr (FP8) {
@@ -1248,7 +1282,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             for (int k = 0; !failed; ++k) {
                 ItemSlot it;
                 if (!read_item(k, it)) break;
-                const int32_t *bt = p.block_tables + (size_t)it.s * p.max_blocks;
+                const int32_t *bt = p.block_tables + (size_t)it.s * p.max_blocks + (SHARED ? it.skip : 0);
                 const int j0 = it.j0, T = it.T, L = it.L;
                 // the row's key of tile jj lies inside the context and its block in the
                 // pool (read one tile ahead, during the waits)
@@ -1325,9 +1359,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             // last key this row may attend; rows past the chunk (computed only to fill
             // the tile, never stored) take the tile's last valid row, so no row ever
             // sees a key at or beyond L
-            // (SHARED: every row attends every key of the prefix)
-            const int pos = SHARED ? L - 1 : row_valid ? L - n + i : L - n + i1 - 1;
-            const int pos_min = SHARED ? L - 1 : L - n + i0;
+            // (SHARED: every row attends every key of a prefix)
+            const bool all = SHARED && !it.causal;
+            const int pos = all ? L - 1 : row_valid ? L - n + i : L - n + i1 - 1;
+            const int pos_min = all ? L - 1 : L - n + i0;
             float m_ref = -INFINITY, l = 0.f;
             // fp8 cache: the k scale folds into the softmax scale, the v scale into O
             const float sl = FP8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
@@ -1444,22 +1479,24 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     // one row's 128 bytes together.  (A lane storing its own row's pieces
                     // touches 32 rows with each instruction: an item's two tiles, 128
                     // KiB, took 7 us that way.)
-                    float *const to = p.part_o + (((size_t)(row0 + i0) * p.hq + g * G) * p.max_splits + split) * D + (lane & 7) * 4;
-                    const int rows = (i1 - i0) * G, lg = __ffs(G) - 1;   // (G is a power of two)
+                    const int rows = (i1 - i0) * G, r8 = r & ~7, lg = __ffs(G) - 1;   // (G is a power of two)
+                    const size_t head_step = (size_t)p.max_splits * D, row_step = head_step * p.hq;
+                    float *const to = p.part_o + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * head_step +
+                                      (size_t)split * D + (lane & 7) * 4;
+                    if ((r & ~31) < rows) {      // (a warp without rows stores nothing)
 #pragma unroll
-                    for (int c = 0; c < 4 && (r & ~31) < rows; ++c) {   // (a warp without rows stores nothing)
-                        float o[32];
-                        tmem_ld32(tO(gi) + lane_base + c * 32, o);
-                        uint32_t v[8][4];
+                        for (int c = 0; c < 4; ++c) {
+                            float o[32];
+                            tmem_ld32(tO(gi) + lane_base + c * 32, o);
+                            uint32_t v[8][4];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(o[e] * vsc);
-                        oct_transpose(v, lane);
+                            for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(FP8 ? o[e] * vsc : o[e]);
+                            oct_transpose(v, lane);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int rj = (r & ~7) + j;
-                            if (rj < rows)
-                                *reinterpret_cast<uint4 *>(to + ((size_t)(rj >> lg) * p.hq + (rj & (G - 1))) * p.max_splits * D + c * 32) =
-                                    make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+                            for (int j = 0; j < 8; ++j)
+                                if (r8 + j < rows)
+                                    *reinterpret_cast<uint4 *>(to + (j >> lg) * row_step + (j & (G - 1)) * head_step + c * 32) =
+                                        make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
                         }
                     }
                     if (row_valid) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
@@ -1701,43 +1738,62 @@ Trace *trace_for_call()
 namespace pkv_prefill {
 cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
 
-// The layout and the parts of shared prefixes.  One query tile a CTA (128-key tiles)
-// when the groups' rows x heads fill one tile on average, over a bf16 cache.  The
-// number of parts minimises the modelled end of prefixes, tails and merge (the terms
-// of shared_ctas, from the caller's bounds): with several groups their prefixes are
-// taken to be ragged, half as long as the longest.
-void plan_prefixes(SharedCall &c, double tail_keys)
+// The layout and the parts of shared prefixes, and of the tails where they are joined.
+// One query tile a CTA (128-key tiles) when the rows x heads of a group, or without
+// groups of a sequence, fill one tile on average, over a bf16 cache.
+//
+// The tails apart: the number of parts minimises the modelled end of prefixes, tails
+// and merge (the terms of shared_ctas, from the caller's bounds): with several groups
+// their prefixes are taken to be ragged, half as long as the longest.
+// Joined: parts of a third of what an SM gets of all tiles, tails taken to be half as
+// long as the longest.
+void plan_prefixes(SharedCall &c, int64_t max_tail)
 {
     const int G = c.hq / c.hkv, ng = std::max(1, c.b.num_groups);
-    c.big = !c.fp8 && (int64_t)c.b.total_rows * G <= (int64_t)BM * ng;
+    const bool prefixes = c.b.max_prefix > 0 && c.b.num_groups > 0;
+    const int64_t each_of = prefixes ? ng : c.b.num_seqs;
+    c.big = !c.fp8 && (int64_t)c.b.total_rows * G <= (int64_t)BM * each_of && (!c.joined || (int64_t)c.b.max_q_len * G <= BM);
     const int tile_keys = c.big ? 128 : 64, item_rows = (BM / G) * (c.big ? 1 : 2);
-    const int W = (c.b.max_prefix + tile_keys - 1) / tile_keys;
-    c.prefix_splits = c.prefix_tiles = 0;
-    c.prefix_items = 0;
-    if (W == 0 || c.b.num_groups == 0) return;
+    const int W = prefixes ? (c.b.max_prefix + tile_keys - 1) / tile_keys : 0;
     const int64_t rows = ((int64_t)c.b.total_rows + ng - 1) / ng;
-    const double problems = (double)ng * ((rows + item_rows - 1) / item_rows) * c.hkv;
-    const double per_tile = BYTES_PER_TILE_TIME * tile_keys / 64.0, per_sm = DECODE_SM_BYTES_PER_TILE_TIME * tile_keys / 64.0;
-    const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / per_tile;
-    const double tail = tail_keys * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
-    const double sms = (double)NUM_SMS, mean = ng > 1 ? 0.5 : 1.0;
-    double best = 0;
-    int pick = 0;
-    for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
-        const int len = (W + s - 1) / s, parts = (W + len - 1) / len;
-        const double items = problems * (1.0 + mean * (parts - 1)), each = std::min<double>(len, mean * W) + SHARED_ITEM_TILES;
-        const double least = std::ceil(items / sms);
-        for (int w = 0; w < 4; ++w) {
-            const double ctas = std::ceil(items / (least + w)), chunk = (least + w) * each;
-            const double beside = std::min((sms - ctas) * per_sm, per_tile);
-            const double cost = chunk + std::max(0.0, tail - chunk * beside) / per_tile + parts * merge;
-            if (pick == 0 || cost < best) {
-                best = cost;
-                pick = s;
+    const double problems = (double)ng * ((rows + item_rows - 1) / item_rows) * c.hkv, sms = (double)NUM_SMS;
+    c.prefix_splits = c.prefix_tiles = 0;
+    c.prefix_items = c.tail_items = 0;
+    if (c.joined) {
+        const int64_t Wt = std::max<int64_t>(1, (max_tail + tile_keys - 1) / tile_keys);
+        const int64_t mine = ((int64_t)c.b.max_q_len + item_rows - 1) / item_rows;      // query items of a sequence
+        const double tiles = problems * W * (ng > 1 ? 0.5 : 1.0) + 0.5 * c.b.num_seqs * mine * c.hkv * Wt;
+        const int64_t len = std::max<int64_t>({4, (int64_t)(tiles / sms / 3.0), (W + 127) / 128, (Wt + 127) / 128});
+        c.tail_splits = (int)((Wt + len - 1) / len);
+        c.tail_part_blocks = (int)(std::min(len, Wt) * (tile_keys / BS));
+        c.tail_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_seqs * (item_rows - 1)) / item_rows * c.hkv * c.tail_splits;
+        if (W) c.prefix_tiles = (int)std::min<int64_t>(len, W);
+    } else if (W) {
+        const double per_tile = BYTES_PER_TILE_TIME * tile_keys / 64.0;
+        const double per_sm = DECODE_SM_BYTES_PER_TILE_TIME * tile_keys / 64.0;
+        // (and the merge's trips to memory: eight parts a trip)
+        const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / per_tile + 0.12 * 64.0 / tile_keys;
+        const double tail = 0.5 * c.b.num_seqs * (double)max_tail * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+        const double mean = ng > 1 ? 0.5 : 1.0;
+        double best = 0;
+        int pick = 0;
+        for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
+            const int len = (W + s - 1) / s, parts = (W + len - 1) / len;
+            const double items = problems * (1.0 + mean * (parts - 1));
+            const double each = std::min<double>(len, mean * W) + SHARED_ITEM_TILES, least = std::ceil(items / sms);
+            for (int w = 0; w < 4; ++w) {
+                const double ctas = std::ceil(items / (least + w)), chunk = (least + w) * each;
+                const double beside = std::min((sms - ctas) * per_sm, per_tile);
+                const double cost = chunk + std::max(0.0, tail - chunk * beside) / per_tile + parts * merge;
+                if (pick == 0 || cost < best) {
+                    best = cost;
+                    pick = s;
+                }
             }
         }
+        c.prefix_tiles = (W + pick - 1) / pick;
     }
-    c.prefix_tiles = (W + pick - 1) / pick;
+    if (!W) return;
     c.prefix_splits = (W + c.prefix_tiles - 1) / c.prefix_tiles;
     // at most: every group's rows in tiles of their own, each group's last tile of one row
     c.prefix_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_groups * (item_rows - 1)) / item_rows * c.hkv * c.prefix_splits;
@@ -1771,8 +1827,13 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.decode_key_bytes = (float)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
     p.decode_sm_bytes = (float)(DECODE_SM_BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
     p.q_box_bytes = tpt * G * 128;
-    p.grid_ctas = (int)std::min<int64_t>(c.prefix_items, p.num_sms);
+    p.grid_ctas = (int)std::min<int64_t>(c.prefix_items + c.tail_items, p.num_sms);
     p.one_wave = c.prefix_items <= p.num_sms;
+    p.groups = c.prefix_splits > 0 ? c.b.num_groups : 0;
+    p.joined = c.joined ? 1 : 0;
+    p.sources = p.groups + (c.joined ? c.b.num_seqs : 0);
+    p.tail_tiles = c.joined ? c.tail_part_blocks / (p.tile_keys / BS) : 0;
+    p.tail_at = c.prefix_splits;
     CUtensorMap qm, km, vm;
     if (!pkv_host::encode_tmap_3d(&qm, c.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, c.hq, c.b.total_rows, (uint64_t)D * 2,
                                   (uint64_t)c.hq * D * 2, 64, G, tpt, CU_TENSOR_MAP_SWIZZLE_128B) ||

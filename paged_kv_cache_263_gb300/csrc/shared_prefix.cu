@@ -92,26 +92,35 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // How a call is done, from its sizes and bounds.
 //
 // whole: no kernel for the prefixes.  The tails' kernel then attends whole contexts
-// and reads a prefix once a sequence, from L2.  That takes 5 to 25 us, and a second
-// kernel and a merge 15 to 18 at least, so it pays up to WHOLE_KEYS keys x KV heads of
-// prefix, counted once a sequence: 16 sequences of 512 tokens, 8 KV heads, take 9.4 us
-// against 15.1, of 1,024 tokens 15.8 against 15.3, of 4,096 tokens 26.9 against 17.6
-// (bf16); 32 of 1,024, 2 KV heads, 11.1 against 16.3, of 2,048 18.0 against 18.2.  With
-// fewer than three sequences a group there is little to save, and it pays up to four
-// times that: 8 sequences in 4 groups of 8,192 tokens take 37.5 us against 48.8 (bf16),
-// of 16,384 tokens 60.4 against 83.6 (fp8).
+// and reads a prefix once a sequence, from L2 where it fits.  It reads 13 to 18 keys a
+// KV head in a ns (bf16; fp8 27) and the prefixes' kernel 13 (fp8 7 to 10), so with few
+// sequences a group the latter never pays: 2 of 24,576 tokens, 8 KV heads, 16 groups:
+// 236 us against 263 (bf16), 200 against 347 (fp8; 3: 289 against 346).  With more it
+// has to save what it and the merge add, 10 us: that takes about WHOLE_KEYS +
+// WHOLE_FEW / (sequences a group) keys x KV heads of prefix, counted once a sequence.
+//   sequences a group       4            6            8            16
+//   K keys x KV heads   512   1024   384    768   256    512   64     192
+//   whole, us           26.6  46.3   24.2   34.8  19.5   26.8  9.4    17.7
+//   prefixes apart      30.4  39.9   25.7   30.9  25.0   25.7  15.1   15.9   (bf16)
 //
 // Tails: partitions of 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, shorter
 // ones (down to 16 blocks) where the grid would hold fewer than TAIL_CTAS.
-constexpr int64_t WHOLE_KEYS = 128ll << 10, TAIL_CTAS = 2 * 3 * 152;
+//
+// joined: rows x heads of a sequence that are more than the columns of the decode
+// kernel (16) are attended in the chunk kernel's tiles, which hold 128, tails and all.
+constexpr int64_t TAIL_COLS = 16;
+constexpr int64_t WHOLE_KEYS = 64ll << 10, WHOLE_FEW = 1536ll << 10, TAIL_CTAS = 2 * 3 * 152;
 void plan(SharedCall &c, int32_t max_tail_len)
 {
-    c.whole = (int64_t)c.b.num_seqs * c.b.max_prefix <=
-              WHOLE_KEYS / c.hkv * (c.b.num_seqs < 3ll * c.b.num_groups ? 4 : 1);
+    c.joined = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > TAIL_COLS && c.b.max_q_len > 1;
+    const int64_t seqs = std::max(1, c.b.num_seqs), groups = c.b.num_groups;
+    c.whole = !c.joined && (seqs < (c.fp8 ? 4 : 3) * groups || groups == 0 ||
+                            seqs * c.b.max_prefix <= (WHOLE_KEYS + WHOLE_FEW * groups / seqs) / c.hkv);
     c.prefix_splits = 0;
-    c.prefix_items = 0;
-    if (!c.whole) pkv_prefill::plan_prefixes(c, 0.5 * c.b.num_seqs * max_tail_len);
-    const int64_t keys = (int64_t)max_tail_len + (c.whole ? c.b.max_prefix : 0);
+    c.prefix_items = c.tail_items = 0;
+    if (!c.whole) pkv_prefill::plan_prefixes(c, max_tail_len);
+    if (c.joined) return;
+    const int64_t keys = (int64_t)max_tail_len + (c.whole && groups ? c.b.max_prefix : 0);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
     const int64_t most = blocks <= 512 ? 64 : blocks <= 4096 ? 128 : 256;
     const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
@@ -156,6 +165,7 @@ size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t to
         SharedCall c{};
         c.b.num_seqs = num_seqs;
         c.b.total_rows = total_q_tokens;
+        c.b.max_q_len = max_q_len;
         c.b.num_groups = num_groups;
         c.b.max_prefix = max_prefix_len / BS * BS;
         c.hq = num_q_heads;
@@ -214,7 +224,9 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     c.scale_log2 = scale * LOG2E;
     plan(c, max_tail_len);
     // (32 groups that claim all rows, as malformed data may, still count their items in 32 bits)
-    if (c.prefix_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
+    if (c.prefix_items > INT32_MAX / 64 || c.tail_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
+    if (c.joined && ((int64_t)max_q_len * G / 128 + 1) * num_kv_heads * c.tail_splits > INT32_MAX / 64)
+        return KV_ERR_UNSUPPORTED;
     if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)c.tail_splits * ((int64_t)max_q_len * G / 8 + 1) > INT32_MAX)
         return KV_ERR_UNSUPPORTED;
     // (the plan goes by the bounds as given, which the workspace's size goes by; no
@@ -227,9 +239,9 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     c.part_o = static_cast<float *>(workspace);
     c.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool prefixes = c.prefix_splits > 0;
+    const bool prefixes = c.prefix_splits > 0 || c.joined;
     if (prefixes && pkv_prefill::launch_prefixes(c, st) != cudaSuccess) return KV_ERR_CUDA;
-    if (pkv_decode::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
+    if (!c.joined && pkv_decode::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
     if (!o_bytes) return KV_OK;
     const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
                            c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,

@@ -68,8 +68,8 @@ struct SharedSeq {
     int L, P;         // context, and how much of it is its group's prefix
     int first;        // the sequence whose table row the prefix is read through
 };
-// (by the whole warp: the sequence is the same in all lanes)
-__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int lane)
+// (g: the last group that begins at or before s; any number if there is none)
+__device__ __forceinline__ SharedSeq shared_seq_in(const SharedBatch &b, int s, int g)
 {
     SharedSeq r;
     r.state = SEQ_BAD;
@@ -81,7 +81,6 @@ __device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int
     r.first = s;
     bool ok = true;
     if (b.num_groups > 0) {
-        const int g = b.num_groups > 1 ? last_at_most(b.cu_groups, b.num_groups, s, lane) : 0;
         const SharedGroup gr = shared_group(b, g);
         if (s >= gr.s0 && s < gr.s1) {
             ok = gr.ok && r.row0 >= gr.row0 && r.row0 + r.n <= gr.row0 + gr.rows;
@@ -98,6 +97,22 @@ __device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int
     if (!ok || r.L < 0 || r.L > b.max_blocks * BS || r.L - r.n < r.P || r.L - r.P > b.max_tail) return r;
     r.state = SEQ_OK;
     return r;
+}
+// by the whole warp, for a sequence that is the same in all lanes
+__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int lane)
+{
+    return shared_seq_in(b, s, b.num_groups > 1 ? last_at_most(b.cu_groups, b.num_groups, s, lane) : 0);
+}
+// by a lane, for a sequence of its own
+__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s)
+{
+    int lo = 0, hi = b.num_groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(b.cu_groups + mid) <= s) lo = mid;
+        else hi = mid;
+    }
+    return shared_seq_in(b, s, lo);
 }
 #endif  // __CUDACC__
 

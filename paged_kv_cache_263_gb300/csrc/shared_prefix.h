@@ -1,7 +1,7 @@
 // shared_prefix.h -- what the host side of attention over shared prefixes
 // (shared_prefix.cu) hands to the two kernels that do its products: the chunk
 // kernel's shared mode (prefill.cu) for the prefixes, the decode kernel's tail mode
-// (decode.cu) for each sequence's own keys.
+// (decode.cu) for each sequence's own keys, or the former for both.
 #pragma once
 
 #include "shared_prefix.cuh"
@@ -16,9 +16,10 @@ struct SharedCall {
     float *part_o, *part_ml;          // [rows][hq][prefix_splits + tail_splits][128], [..][2] (max, sum)
     int hq, hkv, num_blocks;
     bool fp8, big;                    // big: one query tile a CTA, 128-key tiles
+    bool joined;                      // the kernel of the prefixes attends the tails as well
     bool whole;                       // no kernel for the prefixes: the tails' attends whole contexts
     int prefix_splits, prefix_tiles;  // parts of a prefix at most, and KV tiles a part
-    int64_t prefix_items;             // work items of the prefixes at most
+    int64_t prefix_items, tail_items; // work items of prefixes, and of joined tails, at most
     int tail_splits, tail_part_blocks;
     float scale_log2;
 };
@@ -27,8 +28,8 @@ namespace pkv_decode {
 cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st);
 }  // namespace pkv_decode
 namespace pkv_prefill {
-// the parts that prefixes are cut into (fields big and prefix_*); tail_keys: what the
-// tails of the batch hold together, about
-void plan_prefixes(SharedCall &c, double tail_keys);
+// the parts that prefixes are cut into (fields big and prefix_*), and tails where they
+// are joined (tail_*)
+void plan_prefixes(SharedCall &c, int64_t max_tail);
 cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st);
 }  // namespace pkv_prefill

@@ -97,8 +97,9 @@ class Batch:
 
     def apart(self):
         """A bound on the prefixes from which on a kernel of its own attends them (a batch
-        with less to read does without)."""
-        return max(int(max([0, *self.prefix])), 16 + 4 * (128 << 10) // (self.B * self.hkv))
+        with less to read does without, as do groups of few sequences)."""
+        few = (1536 << 10) * len(self.prefix) // max(1, self.B)
+        return max(int(max([0, *self.prefix])), 16 + ((64 << 10) + few) // (self.B * self.hkv))
 
     def check(self, flags=0, got=None, ref=None, **kw):
         exp, tol, f = ref or self.reference()
@@ -135,7 +136,7 @@ def test_prefix_lengths(p, fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("tail", [1, 2, 15, 16, 17, 64, 65, 333, 1024, 1025, 4100])
 def test_tail_lengths(tail, fp8):
-    Batch([2, 1], [48, 200], [tail, 5, tail], hq=8, hkv=1, fp8=fp8, seed=tail).check()
+    Batch([5, 3], [48, 200], [tail, 5, tail, 1, 16, 40, tail, 9], hq=8, hkv=1, fp8=fp8, seed=tail).check()
 
 
 @pytest.mark.parametrize("size", [1, 2, 7, 8, 15, 16, 17, 31, 33, 64, 130, 300])
@@ -148,7 +149,7 @@ def test_group_sizes(size):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_many_groups_of_all_sizes(fp8):
     rng = np.random.default_rng(5)
-    sizes = [0, 1, 9, 0, 0, 40, 2, 17, 1, 1, 3, 0] + [2] * 40
+    sizes = [0, 1, 9, 0, 0, 40, 2, 17, 1, 1, 3, 0] + [5] * 40
     n = sum(sizes) + 4
     Batch(sizes, rng.integers(0, 700, len(sizes)), rng.integers(1, 90, n), hq=8, hkv=2, fp8=fp8, loose=3, before=1).check()
 
@@ -156,7 +157,8 @@ def test_many_groups_of_all_sizes(fp8):
 @pytest.mark.parametrize("ng", [31, 32, 33, 100, 1025])
 def test_numbers_of_groups(ng):
     rng = np.random.default_rng(ng)
-    sizes = rng.integers(0, 3, ng)
+    sizes = rng.integers(1, 9, ng)
+    sizes[ng // 2] = 0
     Batch(list(sizes), rng.integers(0, 100, ng), rng.integers(1, 20, int(sizes.sum()) + 1), hq=2, hkv=1, loose=1).check()
 
 
@@ -298,31 +300,35 @@ def test_agrees_with_decode_over_the_whole_context():
 
 def test_on_another_stream_and_twice_at_once():
     b, c = Batch([9], [900], np.arange(1, 10) * 30, seed=1), Batch([5, 5], [300, 2000], np.arange(1, 11), seed=2)
+    far = {"max_prefix_len": b.apart()}
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     for _ in range(3):
         with torch.cuda.stream(s1):
-            x = b.call()
+            x = b.call(**far)
         with torch.cuda.stream(s2):
-            y = c.call()
-        z = b.call(stream=s2, out=torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device="cuda"))
+            y = c.call(max_prefix_len=c.apart())
+            y2 = c.call()
+        z = b.call(stream=s2, out=torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device="cuda"), **far)
         torch.cuda.synchronize()
+        c.check(got=y2)
         b.check(got=x)
         c.check(got=y)
         b.check(got=z)
 
 
-def test_captured_and_replayed_with_other_lengths():
+@pytest.mark.parametrize("bound", [1024, 20000])
+def test_captured_and_replayed_with_other_lengths(bound):
     """One graph, padded to its size, replayed over batches with other groups, prefixes and tails."""
     big = Batch([8, 8, 4], [900, 400, 200], np.arange(1, 21) * 9, hq=8, hkv=2, loose=0)
     tables, lens = i32(big.tables), i32(big.lens)
     groups, prefix, q = i32(big.groups), i32(big.prefix), big.q.clone()
     out = torch.full(q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
-    ws = torch.empty(pkv.paged_attention_shared_prefix_workspace_size(20, 20, 1, 3, 8, 2, 1024, 256), dtype=torch.uint8,
+    ws = torch.empty(pkv.paged_attention_shared_prefix_workspace_size(20, 20, 1, 3, 8, 2, bound, 256), dtype=torch.uint8,
                      device="cuda")
 
     def call():
-        pkv.paged_attention_shared_prefix(out, q, big.k, big.v, tables, lens, groups, prefix, max_prefix_len=1024,
+        pkv.paged_attention_shared_prefix(out, q, big.k, big.v, tables, lens, groups, prefix, max_prefix_len=bound,
                                           max_tail_len=256, scale=big.scale, workspace=ws)
 
     side = torch.cuda.Stream()
