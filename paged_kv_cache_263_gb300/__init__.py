@@ -730,8 +730,8 @@ def kv_copy_blocks(caches, src, dst, stream=None):
     if len(shape) < 2 or shape[0] < 1:
         raise ValueError("caches must be [num_blocks][...]")
     at = (ctypes.c_void_p * len(caches))(*[_at("caches", t, dev, dtype, shape) for t in caches])
-    _check(_call_on(dev, stream, lib().kv_copy_blocks, at, len(caches), caches[0].stride(0) * caches[0].element_size(),
-                    shape[0], s, d, n), "kv_copy_blocks")
+    _check(_call_on(dev, stream, lib().kv_copy_blocks, at, len(caches), caches[0].nbytes // shape[0], shape[0], s, d, n),
+           "kv_copy_blocks")
 
 
 def kv_fork_tables(block_tables, context_lens, parents, free_blocks, child_tables, child_lens, copy_src, copy_dst, taken,

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256)
 
 // Takes the flags out of all status words at once.  (A blocking copy of each word
 // took 10 us: 79 us a call with eight of them, 23 with this.)
-constexpr int STATUS_WORDS = 10;
+constexpr int STATUS_WORDS = 11;
 struct StatusWords {
     uint32_t *at[STATUS_WORDS];
 };
@@ -164,6 +164,7 @@ namespace pkv_latent { cudaError_t status_word(uint32_t **at); }
 namespace pkv_latent_small { cudaError_t status_word(uint32_t **at); }
 namespace pkv_latent_prefill { cudaError_t status_word(uint32_t **at); }
 namespace pkv_shared { cudaError_t status_word(uint32_t **at); }
+namespace pkv_shared_tail { cudaError_t status_word(uint32_t **at); }
 namespace pkv_pages { cudaError_t status_word(uint32_t **at); }
 
 static cudaError_t status_word_cache(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
@@ -248,7 +249,7 @@ kv_status kv_last_device_status(void *stream)
     cudaError_t (*const words[])(uint32_t **) = {
         status_word_cache, pkv_decode::status_word, pkv_prefill::status_word, pkv_swap::status_word,
         pkv_step::status_word, pkv_latent::status_word, pkv_latent_small::status_word, pkv_latent_prefill::status_word,
-        pkv_shared::status_word, pkv_pages::status_word};
+        pkv_shared::status_word, pkv_shared_tail::status_word, pkv_pages::status_word};
     static_assert(sizeof words / sizeof *words == STATUS_WORDS, "a word a source file");
     for (int i = 0; i < STATUS_WORDS; ++i)
         if (words[i](&w.at[i]) != cudaSuccess) return KV_ERR_CUDA;

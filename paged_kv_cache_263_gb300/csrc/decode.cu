@@ -33,15 +33,11 @@
 //    writes its partial (max, sum, O) and a second kernel merges the
 //    partitions with the log-sum-exp rule in fixed order -- no atomics, so the
 //    result is bitwise independent of physical placement.
-#include "shared_prefix.cuh"
-#include "shared_prefix.h"
+#include "common.cuh"
 #include "trace.h"
-
-#include <cuda_bf16.h>
 
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 // ---- device code begin (hashed with the ncu counters of profiles/)
 namespace {
@@ -80,18 +76,6 @@ struct DecodeParams {
     // kernel, so only the first CTA waits for the chunk kernel (the grid then
     // completes after it, and the kernels behind it see both grids' results)
     int corun;
-};
-
-// TAIL: the sequences' own keys behind a prefix that another kernel attends for
-// whole groups.  Every result is a partial one, of row r and head h at
-// ((r x hq + h) x part_stride + part_off + split), or with a single partition and
-// nothing to join it to (out16) the output.  whole: there is no other kernel, and a
-// sequence's keys begin with its prefix, read through the group's first row.
-struct TailParams : DecodeParams {
-    SharedBatch b;
-    __nv_bfloat16 *out16;
-    int part_stride, part_off;
-    int whole;
 };
 
 // Ring depth per warp and CTAs per SM (compile-time).  Measured on GB300:
@@ -146,18 +130,7 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y,
-                                                 int32_t z, uint32_t bar, uint64_t pol)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
-        : "memory");
-}
-
-// BOX: a tile's two 64-dim halves in one 3-D box (the maps are made for it)
-template <bool FP8, bool BOX>
+template <bool FP8>
 __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CUtensorMap *km,
                                             const CUtensorMap *vm, int32_t y, uint64_t pol)
 {
@@ -165,9 +138,6 @@ __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CU
     if constexpr (FP8) {
         tma_load_2d_hint(dst, km, 0, y, bar, pol);
         tma_load_2d_hint(dst + Geo<FP8>::TILE, vm, 0, y, bar, pol);
-    } else if constexpr (BOX) {
-        tma_load_3d_hint(dst, km, 0, y, 0, bar, pol);
-        tma_load_3d_hint(dst + 4096, vm, 0, y, 0, bar, pol);
     } else {
         tma_load_2d_hint(dst, km, 0, y, bar, pol);
         tma_load_2d_hint(dst + 2048, km, 64, y, bar, pol);
@@ -182,10 +152,10 @@ __device__ __forceinline__ void issue_stage(uint32_t dst, uint32_t bar, const CU
 // speculative draft being verified) reads each K/V tile once for all its
 // rows.  Row i of the chunk sees keys 0 .. L-n+i; longer chunks take several
 // column groups (CTAs next to each other in the grid, sharing tiles in L2).
-template <bool FP8, int NT, bool MR, bool TAIL>
+template <bool FP8, int NT, bool MR>
 __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const std::conditional_t<TAIL, TailParams, DecodeParams> p)
+                  const DecodeParams p)
 {
     using GE = Geo<FP8>;
     extern __shared__ uint8_t smem_raw[];
@@ -205,32 +175,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // s: sequence (block table); row: (first) row of q/out; wi: index of the
     // partials; nq: query rows of the sequence this CTA covers
     int s = blockIdx.z, row = s, wi = s, L, nq = 1;
-    [[maybe_unused]] int skip = 0, shared_blocks = 0, first = 0;
-    if constexpr (TAIL) {
-        // from here on key 0 is the first one behind the prefix
-        const SharedSeq w = shared_seq(p.b, s, lane);
-        if constexpr (MR) {
-            cg = split % p.col_groups;
-            split /= p.col_groups;
-        }
-        if (w.state == SEQ_BAD && split == 0 && cg == 0 && g == 0 && threadIdx.x == 0) flag(ST_BAD_LEN);
-        if (p.out16 && w.state == SEQ_EMPTY && cg == 0)
-            for (int i = threadIdx.x; i < w.n * p.group * D; i += THREADS) {
-                const int r = i / (p.group * D), rem = i % (p.group * D);
-                p.out16[((size_t)(w.row0 + r) * p.hq + g * p.group) * D + rem] = __float2bfloat16(0.f);
-            }
-        if (w.state != SEQ_OK || cg * CW >= w.n * p.group) return;
-        nq = w.n;
-        row = w.row0;
-        L = w.L;
-        if (p.whole) {
-            shared_blocks = w.P / BS;
-            first = w.first;
-        } else {
-            L -= w.P;
-            skip = w.P / BS;
-        }
-    } else if constexpr (MR) {
+    if constexpr (MR) {
         cg = split % p.col_groups;
         split /= p.col_groups;
         const int a = p.cu_q_lens[s], b = p.cu_q_lens[s + 1];
@@ -277,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     if (b0 >= nblk) return;
     const int b1 = min(nblk, b0 + p.part_blocks);
     const int nsplit_s = (nblk + p.part_blocks - 1) / p.part_blocks;
-    const int32_t *bt = p.block_tables + (size_t)s * p.max_blocks + skip;
+    const int32_t *bt = p.block_tables + (size_t)s * p.max_blocks;
     // blocks of this warp: b0 + warp + k * WARPS, k < count
     // (b1 - b0 >= 1 and warp <= 3, so the numerator is never negative)
     const int count = (b1 - b0 - warp + WARPS - 1) / WARPS;
@@ -290,10 +235,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // the 128-sequence shared-prefix batch: 3.5% less time, the prefix's
     // re-reads no longer reaching DRAM).
     uint64_t l2pol;
-    // (a tail is read once from its first key on)
-    bool once = split > 0;
-    if constexpr (TAIL) once = !p.whole;
-    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
+    if (split > 0) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(l2pol));
     else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(l2pol));
     const uint32_t ring = smem_u32(smem + warp * GE::RING);
     const uint32_t bar0 = smem_u32(bars + warp * GE::STAGES);
@@ -306,11 +248,6 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // block ids of this warp, 32 at a time: lane i holds the id of block k0 + i
     auto load_ids = [&](int k0) -> int32_t {
         int k = k0 + lane;
-        if constexpr (TAIL) {
-            const int j = b0 + warp + k * WARPS;
-            const int32_t *from = j < shared_blocks ? p.block_tables + (size_t)first * p.max_blocks : bt;
-            return k < count ? __ldg(from + j) : -1;
-        }
         return k < count ? __ldg(bt + b0 + warp + k * WARPS) : -1;
     };
     int32_t ids_cur = load_ids(0), ids_nxt = load_ids(32);
@@ -329,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
             const uint32_t bar = bar0 + 8 * st;
             if (phys >= 0 && phys < p.num_blocks) {
                 fence_proxy_async_smem();
-                issue_stage<FP8, TAIL>(ring + st * GE::STAGE, bar, &kmap, &vmap, (phys * p.hkv + g) * BS, l2pol);
+                issue_stage<FP8>(ring + st * GE::STAGE, bar, &kmap, &vmap, (phys * p.hkv + g) * BS, l2pol);
             } else {
                 flag(ST_BAD_BLOCK);
                 mbar_arrive(bar);  // completes the phase without data
@@ -621,23 +558,11 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
                 O += f * sm_o[(w * HL + hl) * D + d];
             }
         }
-        // (a query that is not finite may leave no score to be the largest: its sums
-        // are NaN then, and stay so)
-        if (TAIL && M == -INFINITY && !any_to)
-            Ls = sm_l[hl] + sm_l[HL + hl] + sm_l[2 * HL + hl] + sm_l[3 * HL + hl];
         // MR: column -> (row of the chunk, head); partials are per row
         const int gc = cg * CW + hl;
         const int orow = MR ? row + gc / G : row, owi = MR ? orow : wi;
         const int h = g * G + (MR ? gc % G : hl);
-        if constexpr (TAIL) {
-            if (p.out16) {
-                p.out16[((size_t)orow * p.hq + h) * D + d] = __float2bfloat16(Ls == 0.f ? 0.f : O * vsc / Ls);
-                continue;
-            }
-            const size_t pi = ((size_t)orow * p.hq + h) * p.part_stride + p.part_off + split;
-            p.part_o[pi * D + d] = O * vsc;
-            if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(Ls > 0.f ? M : -INFINITY, Ls);
-        } else if (nsplit_s == 1) {
+        if (nsplit_s == 1) {
             p.out[((size_t)orow * p.hq + h) * D + d] = Ls > 0.f ? O * vsc / Ls : 0.f;
         } else {
             const size_t pi = ((size_t)owi * p.hq + h) * p.num_splits + split;
@@ -688,11 +613,10 @@ template <bool FP8, int NT, bool MR>
 cudaError_t launch_one(const CUtensorMap &km, const CUtensorMap &vm, const DecodeParams &p,
                        cudaStream_t st, bool pdl)
 {
-    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR, false>>(Geo<FP8>::SMEM);
+    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR>>(Geo<FP8>::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(p.num_splits * (MR ? p.col_groups : 1), p.hkv, p.num_seqs);
-    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR, false>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, pdl, km, vm,
-                               p);
+    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, pdl, km, vm, p);
 }
 
 template <bool FP8>
@@ -702,16 +626,6 @@ cudaError_t launch_for(const CUtensorMap &km, const CUtensorMap &vm, const Decod
     if (p.col_groups > 0)
         return nt == 2 ? launch_one<FP8, 2, true>(km, vm, p, st, pdl) : launch_one<FP8, 1, true>(km, vm, p, st, pdl);
     return nt == 2 ? launch_one<FP8, 2, false>(km, vm, p, st, pdl) : launch_one<FP8, 1, false>(km, vm, p, st, pdl);
-}
-
-template <bool FP8, int NT, bool MR>
-cudaError_t launch_tails_as(const CUtensorMap &km, const CUtensorMap &vm, const TailParams &p, cudaStream_t st)
-{
-    const cudaError_t e = pkv_host::ensure_dynamic_smem<decode_kernel<FP8, NT, MR, true>>(Geo<FP8>::SMEM);
-    if (e != cudaSuccess) return e;
-    dim3 grid(p.num_splits * (MR ? p.col_groups : 1), p.hkv, p.num_seqs);
-    return pkv_host::launch_ex(decode_kernel<FP8, NT, MR, true>, grid, dim3(THREADS), Geo<FP8>::SMEM, st, true, km, vm,
-                               p);
 }
 
 }  // namespace
@@ -870,54 +784,6 @@ kv_status run(float *out, const void *q, const void *k_cache, const void *v_cach
 }
 
 cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret_cast<void **>(at), g_status); }
-
-// The tails of a batch in groups (see TailParams), launched programmatically; beside:
-// behind the kernel of the prefixes, to run beside it (see DecodeParams::corun).
-cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
-{
-    TailParams p{};
-    p.q = c.q;
-    p.block_tables = c.block_tables;
-    p.k_scale = c.k_scale;
-    p.v_scale = c.v_scale;
-    p.part_o = c.part_o;
-    p.part_ml = c.part_ml;
-    p.max_blocks = c.b.max_blocks;
-    p.num_seqs = c.b.num_seqs;
-    p.total_rows = c.b.total_rows;
-    p.hq = c.hq;
-    p.hkv = c.hkv;
-    p.group = c.hq / c.hkv;
-    p.num_blocks = c.num_blocks;
-    p.part_blocks = c.tail_part_blocks;
-    p.num_splits = c.tail_splits;
-    p.scale_log2 = c.scale_log2;
-    p.corun = beside ? 1 : 0;
-    p.b = c.b;
-    p.part_stride = c.prefix_splits + c.tail_splits;
-    p.part_off = c.prefix_splits;
-    p.whole = c.whole ? 1 : 0;
-    p.out16 = c.whole && c.tail_splits == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
-    CUtensorMap km, vm;
-    // (bf16: dims (64 dims, rows, halves), strides (row 256 B, half 128 B))
-    const uint64_t rows = (uint64_t)c.num_blocks * c.hkv * BS;
-    auto halves = [&](CUtensorMap *m, const void *cache) {
-        return pkv_host::encode_tmap_3d(m, cache, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, rows, 2, D * 2, 128, 64, BS, 2,
-                                        CU_TENSOR_MAP_SWIZZLE_128B);
-    };
-    if (!(c.fp8 ? make_maps(c.k_cache, c.v_cache, c.num_blocks, c.hkv, KV_FP8_E4M3, &km, &vm)
-                : halves(&km, c.k_cache) && halves(&vm, c.v_cache)))
-        return cudaErrorInvalidValue;
-    const int64_t cols = (int64_t)c.b.max_q_len * p.group;
-    const bool two = cols > 8;
-    if (c.b.max_q_len > 1) {
-        p.col_groups = (int)((cols + (two ? 15 : 7)) / (two ? 16 : 8));
-        if (c.fp8) return two ? launch_tails_as<true, 2, true>(km, vm, p, st) : launch_tails_as<true, 1, true>(km, vm, p, st);
-        return two ? launch_tails_as<false, 2, true>(km, vm, p, st) : launch_tails_as<false, 1, true>(km, vm, p, st);
-    }
-    if (c.fp8) return two ? launch_tails_as<true, 2, false>(km, vm, p, st) : launch_tails_as<true, 1, false>(km, vm, p, st);
-    return two ? launch_tails_as<false, 2, false>(km, vm, p, st) : launch_tails_as<false, 1, false>(km, vm, p, st);
-}
 
 }  // namespace pkv_decode
 

@@ -217,10 +217,10 @@ struct PrefillParams {
 // and with results from part tail_at on; else the decode kernel attends them.
 struct PrefixParams : PrefillParams {
     SharedBatch b;
-    int sources;         // groups, then sequences if joined
-    int groups;          // of them
+    int groups, seq0, sources;   // the groups, from seq0 (a multiple of 32) on the sequences if joined; in all
     int joined, tail_tiles, tail_at;
     int one_wave;        // at most one item a CTA
+    int *tail_counter;   // of the kernel that attends the tails beside this one
 };
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
@@ -674,19 +674,20 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
             w.s = gr.s0;
             w.seqs = gr.s1 - gr.s0;
         }
-    } else if (u < p.sources) {
-        const SharedSeq q = shared_seq(p.b, u - p.groups);
-        if (q.state == SEQ_BAD) flag(ST_BAD_LEN);
+    }
+    if (w.w0 >= p.seq0) {       // (all lanes: sequences begin with a window of their own)
+        const SharedSeq q = shared_seq_window(p.b, w.w0 - p.seq0, lane);
+        if (q.state == SEQ_BAD && u < p.sources) flag(ST_BAD_LEN);
         if (q.state == SEQ_OK) {
             w.row0 = q.row0;
             w.rows = q.n;
             w.L = q.L - q.P;
-            w.s = u - p.groups;
+            w.s = u - p.seq0;
             w.skip = q.P / BS;
         }
     }
     if (w.rows > 0 && w.L > 0) {
-        const int len = u < p.groups ? p.tiles_per_split : p.tail_tiles;
+        const int len = w.w0 < p.seq0 ? p.tiles_per_split : p.tail_tiles;
         w.nq = ((w.rows + tpt - 1) / tpt + p.item_tiles - 1) / p.item_tiles;
         w.KT = (w.L + p.tile_keys - 1) / p.tile_keys;
         w.ns = (w.KT + len - 1) / len;
@@ -831,7 +832,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
     tc_fence_after();
     if constexpr (SHARED) {
         griddep_wait();
-        griddep_launch_dependents();
+        // (by one thread: what it wrote is there when the kernel behind starts)
+        if (threadIdx.x == 0) {
+            if (blockIdx.x == 0 && p.tail_counter) {
+                *p.tail_counter = 0;
+                __threadfence();
+            }
+            griddep_launch_dependents();
+        }
     }
     const uint32_t tmem = *tmem_slot;
     // TMEM columns per query tile gi: two S buffers of BN fp32 columns at
@@ -943,7 +951,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                             it.n = __shfl_sync(0xffffffffu, win.rows, at);
                             it.L = __shfl_sync(0xffffffffu, win.L, at);
                             it.skip = __shfl_sync(0xffffffffu, win.skip, at);
-                            it.causal = win.w0 + at >= p.groups;
+                            it.causal = win.w0 >= p.seq0;
                             it.t0q = p.item_tiles * (r % nq);
                             it.has1 = p.item_tiles == 2 && (it.t0q + 1) * tpt < it.n;
                             it.g = (r / nq) % p.hkv;
@@ -1831,9 +1839,11 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.one_wave = c.prefix_items <= p.num_sms;
     p.groups = c.prefix_splits > 0 ? c.b.num_groups : 0;
     p.joined = c.joined ? 1 : 0;
-    p.sources = p.groups + (c.joined ? c.b.num_seqs : 0);
+    p.seq0 = (p.groups + 31) / 32 * 32;
+    p.sources = c.joined ? p.seq0 + c.b.num_seqs : p.groups;
     p.tail_tiles = c.joined ? c.tail_part_blocks / (p.tile_keys / BS) : 0;
     p.tail_at = c.prefix_splits;
+    p.tail_counter = c.joined ? nullptr : c.counter;
     CUtensorMap qm, km, vm;
     if (!pkv_host::encode_tmap_3d(&qm, c.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, c.hq, c.b.total_rows, (uint64_t)D * 2,
                                   (uint64_t)c.hq * D * 2, 64, G, tpt, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -103,8 +103,13 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 //   whole, us           26.6  46.3   24.2   34.8  19.5   26.8  9.4    17.7
 //   prefixes apart      30.4  39.9   25.7   30.9  25.0   25.7  15.1   15.9   (bf16)
 //
-// Tails: partitions of 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, shorter
-// ones (down to 16 blocks) where the grid would hold fewer than TAIL_CTAS.
+// Tails: parts of at most 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, and
+// shorter ones where there would be fewer than TAIL_CTAS: down to 16 blocks for whole
+// contexts, whose CTAs all start together, and two fifths of that, but no fewer than
+// about 22, beside the prefixes, where SMs come free one after another (48 sequences
+// of 100 to 2,500 tokens beside two prefixes, fp8: 57.3 us with parts of 16 blocks,
+// 54.8 of 22, 58.1 of 32, 66 of 53; 64 of 20 to 1,000 beside one, bf16: 92 of 16, 86
+// of 32, 84 of 63).
 //
 // joined: rows x heads of a sequence that are more than the columns of the decode
 // kernel (16) are attended in the chunk kernel's tiles, which hold 128, tails and all.
@@ -124,10 +129,14 @@ void plan(SharedCall &c, int32_t max_tail_len)
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
     const int64_t most = blocks <= 512 ? 64 : blocks <= 4096 ? 128 : 256;
     const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
-    // (whole contexts that fit 32 blocks are written by the only kernel: no merge)
-    const int64_t least = c.whole && blocks <= 32 ? 32 : 16;
-    const int64_t part = std::min(blocks, std::min(most, std::max(least, want)));
-    c.tail_splits = (int)((blocks + part - 1) / part);
+    if (c.whole) {
+        // (whole contexts that fit 32 blocks are written by the only kernel: no merge)
+        const int64_t part = std::min(most, std::max<int64_t>(blocks <= 32 ? 32 : 16, want));
+        c.tail_splits = (int)((blocks + part - 1) / part);
+    } else {
+        const int64_t part = std::max<int64_t>(22, want * 2 / 5);
+        c.tail_splits = (int)(part >= most ? (blocks + most - 1) / most : std::max<int64_t>(1, blocks / part));
+    }
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
 }
 
@@ -142,6 +151,12 @@ size_t part_ml_bytes(const SharedCall &c)
 {
     if (c.whole && c.tail_splits == 1) return 0;
     return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * 2 * sizeof(float));
+}
+
+size_t scratch_bytes(const SharedCall &c)
+{
+    const size_t o = part_o_bytes(c);
+    return o ? o + part_ml_bytes(c) + 256 : 0;      // and the counter
 }
 
 }  // namespace
@@ -172,7 +187,7 @@ size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t to
         c.hkv = num_kv_heads;
         c.fp8 = fp8;
         plan(c, max_tail_len);
-        most = std::max(most, part_o_bytes(c) + part_ml_bytes(c));
+        most = std::max(most, scratch_bytes(c));
     }
     return most;
 }
@@ -227,21 +242,22 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (c.prefix_items > INT32_MAX / 64 || c.tail_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
     if (c.joined && ((int64_t)max_q_len * G / 128 + 1) * num_kv_heads * c.tail_splits > INT32_MAX / 64)
         return KV_ERR_UNSUPPORTED;
-    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)c.tail_splits * ((int64_t)max_q_len * G / 8 + 1) > INT32_MAX)
+    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)num_seqs * num_kv_heads * c.tail_splits > INT32_MAX / 2)
         return KV_ERR_UNSUPPORTED;
     // (the plan goes by the bounds as given, which the workspace's size goes by; no
     // length passes what a table row holds)
     c.b.max_prefix = std::min(c.b.max_prefix, max_blocks_per_seq * BS);
     c.b.max_tail = std::min(c.b.max_tail, max_blocks_per_seq * BS);
     const size_t o_bytes = part_o_bytes(c);
-    if (o_bytes && (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < o_bytes + part_ml_bytes(c)))
+    if (o_bytes && (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < scratch_bytes(c)))
         return KV_ERR_INVALID;
     c.part_o = static_cast<float *>(workspace);
     c.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
+    c.counter = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + o_bytes + part_ml_bytes(c));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool prefixes = c.prefix_splits > 0 || c.joined;
     if (prefixes && pkv_prefill::launch_prefixes(c, st) != cudaSuccess) return KV_ERR_CUDA;
-    if (!c.joined && pkv_decode::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
+    if (!c.joined && pkv_shared_tail::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
     if (!o_bytes) return KV_OK;
     const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
                            c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,

@@ -103,16 +103,28 @@ __device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s, int
 {
     return shared_seq_in(b, s, b.num_groups > 1 ? last_at_most(b.cu_groups, b.num_groups, s, lane) : 0);
 }
-// by a lane, for a sequence of its own
-__device__ __forceinline__ SharedSeq shared_seq(const SharedBatch &b, int s)
+// by the whole warp, sequence s0 + lane for each lane (SEQ_BAD past the batch)
+__device__ __forceinline__ SharedSeq shared_seq_window(const SharedBatch &b, int s0, int lane)
 {
-    int lo = 0, hi = b.num_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(b.cu_groups + mid) <= s) lo = mid;
-        else hi = mid;
+    const int s = s0 + lane;
+    int g = 0;
+    if (b.num_groups > 1) {
+        // the first sequence's group, then the 32 groups' beginnings behind it, counted
+        g = last_at_most(b.cu_groups, b.num_groups, s0, lane);
+        const int mine = g + 1 + lane < b.num_groups ? __ldg(b.cu_groups + g + 1 + lane) : INT_MAX;
+        int more = 0;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) more += __shfl_sync(0xffffffffu, mine, i) <= s;
+        g += more;
+        // (empty groups among them: a lane may have further to go)
+        while (more == 32 && g + 1 < b.num_groups && __ldg(b.cu_groups + g + 1) <= s) ++g;
     }
-    return shared_seq_in(b, s, lo);
+    if (s >= b.num_seqs) {
+        SharedSeq r = {};
+        r.state = SEQ_BAD;
+        return r;
+    }
+    return shared_seq_in(b, s, g);
 }
 #endif  // __CUDACC__
 

@@ -1,7 +1,7 @@
 // shared_prefix.h -- what the host side of attention over shared prefixes
 // (shared_prefix.cu) hands to the two kernels that do its products: the chunk
-// kernel's shared mode (prefill.cu) for the prefixes, the decode kernel's tail mode
-// (decode.cu) for each sequence's own keys, or the former for both.
+// kernel's shared mode (prefill.cu) for the prefixes, shared_tail.cu for each
+// sequence's own keys, or the former for both.
 #pragma once
 
 #include "shared_prefix.cuh"
@@ -14,6 +14,7 @@ struct SharedCall {
     const int32_t *block_tables;
     const float *k_scale, *v_scale;   // fp8 cache
     float *part_o, *part_ml;          // [rows][hq][prefix_splits + tail_splits][128], [..][2] (max, sum)
+    int *counter;                     // of the tails' items: the kernel of the prefixes sets it to 0
     int hq, hkv, num_blocks;
     bool fp8, big;                    // big: one query tile a CTA, 128-key tiles
     bool joined;                      // the kernel of the prefixes attends the tails as well
@@ -24,9 +25,10 @@ struct SharedCall {
     float scale_log2;
 };
 
-namespace pkv_decode {
+namespace pkv_shared_tail {
+// beside: behind the kernel of the prefixes, to run beside it
 cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st);
-}  // namespace pkv_decode
+}  // namespace pkv_shared_tail
 namespace pkv_prefill {
 // the parts that prefixes are cut into (fields big and prefix_*), and tails where they
 // are joined (tail_*)
