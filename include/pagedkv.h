@@ -466,7 +466,7 @@ PAGEDKV_API kv_status kv_build_step_tables(int32_t *block_tables, int32_t max_bl
  *  Latent cache: [num_blocks][16][576] bf16, one row a token (latent, then
  *  rotary key), in the same blocks and tables as the K/V cache.  (A kv_pool
  *  serves it as well; kv_copy_on_write takes NULL caches then, and the caller
- *  copies the block's 18,432 bytes.)
+ *  copies the block's 18,432 bytes, as kv_copy_blocks does.)
  *
  * reshape_and_cache_latent writes new tokens' rows:
  *  latent         device bf16, row t at latent + t x latent_stride, 512 values
@@ -608,6 +608,8 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
  *                 outside the pool are not read, and the rows that see it are then
  *                 unspecified (flag 1).  Keys 0 .. L-1 have to be finite; what lies
  *                 past key L-1 does not matter.
+ *  sizes          num_seqs and num_groups at most 65,535 (KV_ERR_INVALID above),
+ *                 max_blocks_per_seq at most 2^27 - 16 (KV_ERR_UNSUPPORTED above)
  *  workspace      device scratch of paged_attention_shared_prefix_workspace_size()
  *                 bytes, 256-byte aligned.  Calls that may overlap on the GPU need
  *                 one each.

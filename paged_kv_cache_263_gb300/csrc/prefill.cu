@@ -1762,7 +1762,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
     const int64_t each_of = prefixes ? ng : c.b.num_seqs;
     c.big = !c.fp8 && (int64_t)c.b.total_rows * G <= (int64_t)BM * each_of && (!c.joined || (int64_t)c.b.max_q_len * G <= BM);
     const int tile_keys = c.big ? 128 : 64, item_rows = (BM / G) * (c.big ? 1 : 2);
-    const int W = prefixes ? (c.b.max_prefix + tile_keys - 1) / tile_keys : 0;
+    const int W = prefixes ? (int)(((int64_t)c.b.max_prefix + tile_keys - 1) / tile_keys) : 0;
     const int64_t rows = ((int64_t)c.b.total_rows + ng - 1) / ng;
     const double problems = (double)ng * ((rows + item_rows - 1) / item_rows) * c.hkv, sms = (double)NUM_SMS;
     c.prefix_splits = c.prefix_tiles = 0;
@@ -1786,7 +1786,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
         double best = 0;
         int pick = 0;
         for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
-            const int len = (W + s - 1) / s, parts = (W + len - 1) / len;
+            const int len = (W - 1) / s + 1, parts = (W - 1) / len + 1;
             const double items = problems * (1.0 + mean * (parts - 1));
             const double each = std::min<double>(len, mean * W) + SHARED_ITEM_TILES, least = std::ceil(items / sms);
             for (int w = 0; w < 4; ++w) {
@@ -1799,10 +1799,10 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
                 }
             }
         }
-        c.prefix_tiles = (W + pick - 1) / pick;
+        c.prefix_tiles = (W - 1) / pick + 1;
     }
     if (!W) return;
-    c.prefix_splits = (W + c.prefix_tiles - 1) / c.prefix_tiles;
+    c.prefix_splits = (W - 1) / c.prefix_tiles + 1;
     // at most: every group's rows in tiles of their own, each group's last tile of one row
     c.prefix_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_groups * (item_rows - 1)) / item_rows * c.hkv * c.prefix_splits;
 }

@@ -205,7 +205,8 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (num_seqs < 0 || total_q_tokens < 0 || num_groups < 0 || max_q_len < 1 || max_prefix_len < 0 || max_tail_len < 0 ||
         num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 || max_blocks_per_seq < 1 || num_q_heads % num_kv_heads)
         return KV_ERR_INVALID;
-    if (max_blocks_per_seq > INT32_MAX / BS) return KV_ERR_UNSUPPORTED;
+    // (keys and a tile more are counted in 32 bits)
+    if (max_blocks_per_seq > (INT32_MAX - 255) / BS || num_q_heads > 65535 * MERGE_WARPS) return KV_ERR_UNSUPPORTED;
     const int G = num_q_heads / num_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return KV_ERR_UNSUPPORTED;
     if (dtype != KV_BF16 && dtype != KV_FP8_E4M3) return KV_ERR_UNSUPPORTED;

@@ -185,6 +185,41 @@ def test_long_prefix_of_many_parts():
     Batch([1, 20], [40000, 9000], np.arange(1, 22), hq=16, hkv=2, seed=4).check()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv,rows", [(8, 4, 1), (32, 2, 1), (16, 4, 4), (16, 4, 3), (16, 2, 5)])
+def test_many_items_a_cta(hq, hkv, rows, fp8):
+    """Hundreds of sequences and parts: every CTA goes through many items, some of one block."""
+    rng = np.random.default_rng(hq + rows)
+    n = 330 // rows
+    tails = rng.integers(rows, 1100, n)
+    tails[::7] = rows
+    b = Batch([n // 3, 0, n - n // 3 - 2], [330, 40, 97], tails, rows=rows, hq=hq, hkv=hkv, fp8=fp8, loose=2, seed=rows)
+    first = b.check(max_prefix_len=b.apart()).view(torch.int16).clone()
+    for _ in range(3):
+        assert torch.equal(b.call(max_prefix_len=b.apart()).view(torch.int16), first)
+    b.check(max_prefix_len=330)
+
+
+def test_more_parts_than_lanes():
+    """A prefix and a tail of more parts than the merge's warp has lanes."""
+    b = Batch([12], [30000], [4000, 70000, 3] + [20] * 9, hq=4, hkv=1, seed=12)
+    b.check()
+
+
+def test_caches_past_four_gigabytes():
+    """Blocks at the end of caches of 4.6 GB."""
+    b = Batch([4, 3], [600, 90], [20, 30, 400, 5, 7, 9, 11], hq=16, hkv=8)
+    ref, nb = b.reference(), 140000
+    for name in ("k", "v"):
+        small, big = getattr(b, name), torch.empty(nb, 8, BS, D, dtype=torch.bfloat16, device="cuda")
+        big[-small.shape[0]:] = small
+        setattr(b, name, big)
+    b.tables = np.where(b.tables >= 0, b.tables + nb - b.nb, b.tables)
+    b.nb = nb
+    b.check(ref=ref, max_prefix_len=600)
+    b.check(ref=ref, max_prefix_len=b.apart())
+
+
 def test_sharp_scores():
     """Scores spread so far that the running maximum moves often and most weights vanish."""
     Batch([6, 6], [700, 320], [3, 90, 200, 16, 1, 33] * 2, hq=16, hkv=2, spread=30.0).check()

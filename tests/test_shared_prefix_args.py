@@ -38,8 +38,8 @@ ATT = dict(out=A, q=2 * A, cu=3 * A, lens=4 * A, B=4, R=8, nq=2, groups=5 * A, p
     (dict(hq=30), INVALID), (dict(hq=24), UNSUPPORTED), (dict(hq=256), UNSUPPORTED), (dict(dt=2), UNSUPPORTED),
     (dict(dt=1), INVALID), (dict(dt=1, ks=A), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(cu=None), INVALID),
-    (dict(cu=None, R=4), INVALID), (dict(B=65536), INVALID), (dict(G=65536), INVALID), (dict(mb=1 << 28), UNSUPPORTED),
-    (dict(nb=1 << 27), UNSUPPORTED), (dict(out=None), INVALID), (dict(q=None), INVALID), (dict(lens=None), INVALID),
+    (dict(cu=None, R=4), INVALID), (dict(B=65536), INVALID), (dict(G=65536), INVALID), (dict(mb=1 << 28), UNSUPPORTED), (dict(mb=(1 << 27) - 15), UNSUPPORTED),
+    (dict(hq=16 * 65535, hkv=65535), UNSUPPORTED), (dict(nb=1 << 27), UNSUPPORTED), (dict(out=None), INVALID), (dict(q=None), INVALID), (dict(lens=None), INVALID),
     (dict(groups=None), INVALID), (dict(prefix=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(tables=None), INVALID), (dict(out=A + 8), INVALID), (dict(q=2 * A + 4), INVALID), (dict(k=7 * A + 8), INVALID),
     (dict(v=8 * A + 2), INVALID), (dict(cu=3 * A + 1), INVALID), (dict(lens=4 * A + 2), INVALID),
@@ -54,6 +54,19 @@ def test_attention_refuses_a_workspace(change):
     assert need > 0
     change = dict(change, nbytes=need - 1) if change.get("nbytes") == -1 else change
     assert _call("paged_attention_shared_prefix", ATT, **change) == INVALID
+
+
+@pytest.mark.parametrize("fp8", [0, 1])
+@pytest.mark.parametrize("nq", [1, 2, 3, 17, 4000])
+@pytest.mark.parametrize("mp,mt", [(0, 0), (15, 1), (640, 4096), (BIG, BIG), (BIG, 0), (5, BIG)])
+def test_attention_sizes_its_workspace_for_any_bounds(mp, mt, nq, fp8):
+    """No bound makes the call ask for more than the size that it was told, or for less than nothing."""
+    need = pkv.paged_attention_shared_prefix_workspace_size(4, 4 * nq, nq, 2, 32, 8, mp, mt)
+    assert 0 <= need < 1 << 45
+    if need:
+        st = _call("paged_attention_shared_prefix", ATT, mp=mp, mt=mt, nq=nq, R=4 * nq, dt=fp8, ks=A, vs=A, nbytes=0)
+        assert st == INVALID
+    assert pkv.paged_attention_shared_prefix_workspace_size(4, 4 * nq, nq, 2, 24, 7, mp, mt) == 0
 
 
 @pytest.mark.parametrize("change", [dict(B=0), dict(R=0)])
