@@ -1,7 +1,9 @@
 """Builds libpagedkv.so in place: every CUDA/C++ source of csrc/ compiled for
 sm_103a only, in parallel, then linked into one shared library with a plain C
 ABI (static CUDA runtime; the driver's tensor-map encoder is resolved at run
-time, so the library loads on a machine without a GPU)."""
+time, so the library loads on a machine without a GPU).  Beside it, _fastcall.so:
+direct Python entries of the shortest calls (csrc/fastcall.c), linked to the
+library."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -9,10 +11,12 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libpagedkv.so")
+FAST, FAST_SRC = os.path.join(HERE, "_fastcall.so"), os.path.join(CSRC, "fastcall.c")
 BUILD = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -27,10 +31,10 @@ def _sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(OUT):
+    if not os.path.exists(OUT) or not os.path.exists(FAST):
         return True
-    t = os.path.getmtime(OUT)
-    deps = _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
+    t = min(os.path.getmtime(OUT), os.path.getmtime(FAST))
+    deps = _sources() + [FAST_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
         os.path.join(os.path.dirname(HERE), "include", "pagedkv.h"), __file__]
     return any(os.path.getmtime(f) > t for f in deps)
 
@@ -65,6 +69,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", sysconfig.get_paths()["include"], FAST_SRC, "-o", tmp, "-L", HERE, "-lpagedkv",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {FAST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST)
     return OUT
 
 

@@ -21,6 +21,15 @@ using namespace pkv;
 
 __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits); }
 
+// These kernels are short, and their launches follow one another (a fork, its copies,
+// the attention): each is launched programmatically, and waits here before its first
+// access to memory.
+__device__ __forceinline__ void begin()
+{
+    griddep_launch_dependents();
+    griddep_wait();
+}
+
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
@@ -44,6 +53,7 @@ struct CopyParams {
 // with the caches varying fastest 162 us.
 __global__ void __launch_bounds__(COPY_THREADS) copy_blocks_kernel(const __grid_constant__ CopyParams p)
 {
+    begin();
     const int i = blockIdx.x / p.pieces, piece = blockIdx.x - i * p.pieces;
     const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
     if (d < 0 && s < 0) return;          // no pair
@@ -86,6 +96,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_tables_kernel(const ForkPar
     int32_t *first = sh, *len = sh + p.num_parents;
     int16_t *parent = reinterpret_cast<int16_t *>(len + p.num_children), *place = parent + p.num_children;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    begin();
     // lengths and parents of all children; -1: the child is refused
     for (int c = tid; c < p.num_children; c += FORK_THREADS) {
         const int a = __ldg(p.parents + c);
@@ -163,6 +174,7 @@ __global__ void __launch_bounds__(REMAP_THREADS)
     remap_tables_kernel(int32_t *__restrict__ tables, int max_blocks, const int32_t *__restrict__ lens, int num_seqs,
                         const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n, int pieces)
 {
+    begin();
     const int lowest = __ldg(src), highest = __ldg(src + n - 1);
     for (int64_t x = blockIdx.x; x < (int64_t)num_seqs * pieces; x += gridDim.x) {
         const int s = (int)(x / pieces), piece = (int)(x - (int64_t)s * pieces);
@@ -222,9 +234,9 @@ kv_status kv_copy_blocks(void *const *caches, int32_t num_caches, int64_t block_
     for (int at = 0; at < num_caches; at += COPY_CACHES) {
         const int count = std::min(num_caches - at, COPY_CACHES);
         for (int i = 0; i < count; ++i) p.cache[i] = static_cast<uint4 *>(caches[at + i]);
-        copy_blocks_kernel<<<dim3((unsigned)(n * pieces), (unsigned)count), COPY_THREADS, 0,
-                             static_cast<cudaStream_t>(stream)>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return KV_ERR_CUDA;
+        if (pkv_host::launch_ex(copy_blocks_kernel, dim3((unsigned)(n * pieces), (unsigned)count), dim3(COPY_THREADS), 0,
+                                static_cast<cudaStream_t>(stream), true, p) != cudaSuccess)
+            return KV_ERR_CUDA;
     }
     return KV_OK;
 }
@@ -258,8 +270,8 @@ kv_status kv_fork_tables(const int32_t *block_tables, int32_t max_blocks_per_seq
     if (pkv_host::ensure_dynamic_smem<fork_tables_kernel>(fork_smem(FORK_MAX, FORK_MAX)) != cudaSuccess) return KV_ERR_CUDA;
     const int warps = FORK_THREADS / 32;
     const int grid = std::max(1, std::min((num_children + warps - 1) / warps, 152));
-    fork_tables_kernel<<<grid, FORK_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    return pkv_host::launch_ex(fork_tables_kernel, dim3(grid), dim3(FORK_THREADS), smem, static_cast<cudaStream_t>(stream),
+                               true, p) == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
 kv_status kv_remap_tables(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
@@ -276,9 +288,9 @@ kv_status kv_remap_tables(int32_t *block_tables, int32_t max_blocks_per_seq, con
         if (!pkv_host::aligned(x.p, 4) || overlap(block_tables, t, x.p, x.n)) return KV_ERR_INVALID;
     const int pieces = (max_blocks_per_seq + REMAP_PIECE - 1) / REMAP_PIECE;
     const int grid = (int)std::min<int64_t>((int64_t)num_seqs * pieces, 152 * 8);
-    remap_tables_kernel<<<grid, REMAP_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-        block_tables, max_blocks_per_seq, context_lens, num_seqs, src, dst, n, pieces);
-    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+    return pkv_host::launch_ex(remap_tables_kernel, dim3(grid), dim3(REMAP_THREADS), 0, static_cast<cudaStream_t>(stream),
+                               true, block_tables, max_blocks_per_seq, context_lens, num_seqs, src, dst, n, pieces) ==
+                   cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
 }  // extern "C"
