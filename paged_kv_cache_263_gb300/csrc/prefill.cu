@@ -64,6 +64,8 @@
 #include "shared_prefix.h"
 #include "trace.h"
 
+#include <cuda_bf16.h>
+
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -219,6 +221,7 @@ struct PrefixParams : PrefillParams {
     SharedBatch b;
     int groups, seq0, sources;   // the groups, from seq0 (a multiple of 32) on the sequences if joined; in all
     int joined, tail_tiles, tail_at;
+    __nv_bfloat16 *out16;        // the output, where one part is all that a row has; else null
     int one_wave;        // at most one item a CTA
     int *tail_counter;   // of the kernel that attends the tails beside this one
 };
@@ -685,6 +688,8 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
             w.s = u - p.seq0;
             w.skip = q.P / BS;
         }
+        // rows of sequences without a context, where no merge kernel writes them
+        if (p.out16 && blockIdx.x == 0) zero_rows(p.out16, p.hq, u < p.sources && q.state == SEQ_EMPTY, q.row0, q.n, lane);
     }
     if (w.rows > 0 && w.L > 0) {
         const int len = w.w0 < p.seq0 ? p.tiles_per_split : p.tail_tiles;
@@ -1491,15 +1496,29 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     const size_t head_step = (size_t)p.max_splits * D, row_step = head_step * p.hq;
                     float *const to = p.part_o + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * head_step +
                                       (size_t)split * D + (lane & 7) * 4;
+                    const float by = p.out16 ? (l == 0.f ? 0.f : vsc / l) : vsc;
+                    __nv_bfloat16 *const to16 = p.out16 + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * D +
+                                                (lane & 7) * 4;
                     if ((r & ~31) < rows) {      // (a warp without rows stores nothing)
-#pragma unroll
+// (one copy of the code: it runs once an item, and fetching four takes longer
+                        // than running them)
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             float o[32];
                             tmem_ld32(tO(gi) + lane_base + c * 32, o);
                             uint32_t v[8][4];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(FP8 ? o[e] * vsc : o[e]);
+                            for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(o[e] * by);
                             oct_transpose(v, lane);
+                            if (p.out16) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (r8 + j < rows)
+                                        *reinterpret_cast<uint2 *>(to16 + ((size_t)(j >> lg) * p.hq + (j & (G - 1))) * D + c * 32) =
+                                            make_uint2(pack_bf16(__uint_as_float(v[j][0]), __uint_as_float(v[j][1])),
+                                                       pack_bf16(__uint_as_float(v[j][2]), __uint_as_float(v[j][3])));
+                                continue;
+                            }
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 if (r8 + j < rows)
@@ -1507,7 +1526,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                                         make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
                         }
                     }
-                    if (row_valid) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
+                    if (row_valid && !p.out16) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
                     cs += T;
                     ++kg;
                     continue;
@@ -1824,7 +1843,7 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.num_blocks = c.num_blocks;
     p.total_rows = c.b.total_rows;
     p.tiles_per_split = c.prefix_tiles;
-    p.max_splits = c.prefix_splits + c.tail_splits;
+    p.max_splits = shared_parts(c);
     p.scale_log2 = c.scale_log2;
     p.k_scale = c.k_scale;
     p.v_scale = c.v_scale;
@@ -1844,6 +1863,7 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.tail_tiles = c.joined ? c.tail_part_blocks / (p.tile_keys / BS) : 0;
     p.tail_at = c.prefix_splits;
     p.tail_counter = c.joined ? nullptr : c.counter;
+    p.out16 = shared_parts(c) == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
     CUtensorMap qm, km, vm;
     if (!pkv_host::encode_tmap_3d(&qm, c.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, c.hq, c.b.total_rows, (uint64_t)D * 2,
                                   (uint64_t)c.hq * D * 2, 64, G, tpt, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -141,16 +141,16 @@ void plan(SharedCall &c, int32_t max_tail_len)
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
-// (none where the only kernel writes the output itself)
+// (none where the only part is the output)
 size_t part_o_bytes(const SharedCall &c)
 {
-    if (c.whole && c.tail_splits == 1) return 0;
-    return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * D * sizeof(float));
+    if (shared_parts(c) == 1) return 0;
+    return up((size_t)c.b.total_rows * c.hq * shared_parts(c) * D * sizeof(float));
 }
 size_t part_ml_bytes(const SharedCall &c)
 {
-    if (c.whole && c.tail_splits == 1) return 0;
-    return up((size_t)c.b.total_rows * c.hq * (c.prefix_splits + c.tail_splits) * 2 * sizeof(float));
+    if (shared_parts(c) == 1) return 0;
+    return up((size_t)c.b.total_rows * c.hq * shared_parts(c) * 2 * sizeof(float));
 }
 
 size_t scratch_bytes(const SharedCall &c)
@@ -261,7 +261,7 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (!c.joined && pkv_shared_tail::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
     if (!o_bytes) return KV_OK;
     const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
-                           c.prefix_splits + c.tail_splits, c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,
+                           shared_parts(c), c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,
                            c.whole ? 1 : 0};
     const dim3 grid(total_q_tokens, (num_q_heads + MERGE_WARPS - 1) / MERGE_WARPS);
     return pkv_host::launch_ex(shared_merge_kernel, grid, dim3(32 * MERGE_WARPS), 0, st, true, m) == cudaSuccess

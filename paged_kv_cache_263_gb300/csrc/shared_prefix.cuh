@@ -11,6 +11,8 @@
 
 #include "common.cuh"
 
+#include <cuda_bf16.h>
+
 namespace pkv {
 
 struct SharedBatch {
@@ -125,6 +127,15 @@ __device__ __forceinline__ SharedSeq shared_seq_window(const SharedBatch &b, int
         return r;
     }
     return shared_seq_in(b, s, g);
+}
+// zeros in the rows of each lane's sequence that is marked (by the whole warp)
+__device__ __forceinline__ void zero_rows(__nv_bfloat16 *out, int hq, bool marked, int row0, int n, int lane)
+{
+    for (unsigned m = __ballot_sync(0xffffffffu, marked); m; m &= m - 1) {
+        const int at = __ffs(m) - 1, first = __shfl_sync(0xffffffffu, row0, at), rows = __shfl_sync(0xffffffffu, n, at);
+        uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)first * hq * D);
+        for (int64_t i = lane; i < (int64_t)rows * hq * (D / 8); i += 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
 }
 #endif  // __CUDACC__
 

@@ -25,6 +25,9 @@ struct SharedCall {
     float scale_log2;
 };
 
+// partial results of a row and head; the only one is the output itself
+inline int shared_parts(const SharedCall &c) { return c.prefix_splits + c.tail_splits; }
+
 namespace pkv_shared_tail {
 // beside: behind the kernel of the prefixes, to run beside it
 cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st);

@@ -23,8 +23,6 @@
 #include "shared_prefix.h"
 #include "trace.h"
 
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
 namespace {
@@ -124,14 +122,8 @@ __device__ __forceinline__ void load_window(const TailParams &p, TailWindow &w, 
     }
     w.total = __shfl_sync(0xffffffffu, w.incl, 31);
     // rows of sequences without a context, where no merge kernel writes them
-    if (p.out16 && blockIdx.x == 0) {
-        unsigned m = __ballot_sync(0xffffffffu, s < p.b.num_seqs && w.q.state == SEQ_EMPTY);
-        for (; m; m &= m - 1) {
-            const int at = __ffs(m) - 1, row0 = __shfl_sync(0xffffffffu, w.q.row0, at), n = __shfl_sync(0xffffffffu, w.q.n, at);
-            uint4 *to = reinterpret_cast<uint4 *>(p.out16 + (size_t)row0 * p.hq * D);
-            for (int i = lane; i < n * p.hq * (D / 8); i += 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
+    if (p.out16 && blockIdx.x == 0)
+        zero_rows(p.out16, p.hq, s < p.b.num_seqs && w.q.state == SEQ_EMPTY, w.q.row0, w.q.n, lane);
 }
 
 template <bool FP8, int NT>
@@ -580,7 +572,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
 {
     TailParams p{};
     p.b = c.b;
-    p.out16 = c.whole && c.tail_splits == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
+    p.out16 = shared_parts(c) == 1 ? static_cast<__nv_bfloat16 *>(c.out) : nullptr;
     p.q = c.q;
     p.block_tables = c.block_tables;
     p.k_scale = c.k_scale;
@@ -593,7 +585,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.group = c.hq / c.hkv;
     p.num_blocks = c.num_blocks;
     p.part_blocks = c.tail_part_blocks;
-    p.part_stride = c.prefix_splits + c.tail_splits;
+    p.part_stride = shared_parts(c);
     p.part_off = c.prefix_splits;
     p.whole = c.whole ? 1 : 0;
     p.beside = beside ? 1 : 0;

@@ -231,9 +231,15 @@ def test_default_bounds():
     b.check(got=b.call(cu_q_lens=i32(b.cu), max_q_len=None))
 
 
-def test_without_groups():
-    b = Batch([], [], [20, 9, 1, 400], loose=0, before=4)
-    b.check()
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (1, 16, 1), (2, 8, 1), (5, 16, 1), (20, 8, 1), (40, 16, 2)])
+def test_without_groups(rows, hq, hkv, fp8):
+    """Nothing shared: one part a sequence, written by the only kernel, or several; padded entries."""
+    for tails in ([rows, 2 * rows, 40, 41, 130, 250], [rows, 40, 700, 1500, 9000, 41]):
+        b = Batch([], [], tails, before=6, rows=rows, hq=hq, hkv=hkv, fp8=fp8, seed=rows)
+        b.lens[2] = 0
+        b.check(max_tail_len=max(tails))
+        b.check()
 
 
 def test_padded_and_bad_sequences():
