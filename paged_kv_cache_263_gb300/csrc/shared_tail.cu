@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
         TailWindow w = {};
         load_window(p, w, lane);
-        int u = 0, k = 0;        // blocks handed to this lane's consumer warp (lanes 0 .. 3), and items
+        int u = 0, k = 0;        // blocks handed to this lane's consumer warp, and items
+        int asked = 0;           // items whose queries were asked for
         bool ok = true;
         int idx = blockIdx.x;
         if (p.counter) idx = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(p.counter, 1) : 0, 0);
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
             }
             __syncwarp();
             if (!it.valid) break;
+            asked = k + 1;
             fence_proxy_async_smem();
             if (lane < cols)
                 bulk_load(sbase + LY::S_Q + (sl * LY::COLS + lane) * QROW,
@@ -276,7 +278,8 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                 for (int uu = max(0, u - LY::RING); uu < u; ++uu)
                     (void)mbar_wait_bounded(b_full + 8 * (lane * LY::RING + uu % LY::RING), (uu / LY::RING) & 1);
             __syncwarp();
-            if (k > 0) (void)mbar_wait_bounded(b_item + 8 * ((k - 1) % SLOTS), ((k - 1) / SLOTS) & 1);
+            for (int kk = max(0, asked - SLOTS); kk < asked; ++kk)
+                (void)mbar_wait_bounded(b_item + 8 * (kk % SLOTS), (kk / SLOTS) & 1);
         }
         griddep_launch_dependents();
         // the grid completes after the kernel it ran beside: what waits for it sees both
