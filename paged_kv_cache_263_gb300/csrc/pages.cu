@@ -23,7 +23,8 @@ __device__ __forceinline__ void flag(uint32_t bits) { atomicOr(&g_status, bits);
 
 // These kernels are short, and their launches follow one another (a fork, its copies,
 // the attention): each is launched programmatically, and waits here before its first
-// access to memory.
+// access to memory.  (Plain loads behind it: what a kernel before wrote is not constant
+// for as long as this one is resident.)
 __device__ __forceinline__ void begin()
 {
     griddep_launch_dependents();
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_blocks_kernel(const __grid_
 {
     begin();
     const int i = blockIdx.x / p.pieces, piece = blockIdx.x - i * p.pieces;
-    const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
+    const int s = p.src[i], d = p.dst[i];
     if (d < 0 && s < 0) return;          // no pair
     if (s < 0 || d < 0 || s >= p.num_blocks || d >= p.num_blocks) {
         if (threadIdx.x == 0) flag(ST_BAD_BLOCK);
@@ -99,9 +100,9 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_tables_kernel(const ForkPar
     begin();
     // lengths and parents of all children; -1: the child is refused
     for (int c = tid; c < p.num_children; c += FORK_THREADS) {
-        const int a = __ldg(p.parents + c);
+        const int a = p.parents[c];
         int L = -1;
-        if (a >= 0 && a < p.num_parents) L = __ldg(p.lens + a);
+        if (a >= 0 && a < p.num_parents) L = p.lens[a];
         if (L < 0 || L > p.max_blocks * BS) L = -1;
         parent[c] = (int16_t)(L < 0 ? 0 : a);
         len[c] = L;
@@ -143,15 +144,15 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_tables_kernel(const ForkPar
         int32_t *to = p.child_tables + (size_t)c * p.max_blocks;
         int s = -1, d = -1;
         if (lane == 0 && ok && at >= 0) {
-            s = __ldg(from + n - 1);
-            d = __ldg(p.free_ids + at);
+            s = from[n - 1];
+            d = p.free_ids[at];
         }
         // (eight entries a lane in flight)
         for (int j0 = lane; j0 < kept; j0 += 256) {
             int32_t e[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (j0 + 32 * u < kept) e[u] = __ldg(from + j0 + 32 * u);
+                if (j0 + 32 * u < kept) e[u] = from[j0 + 32 * u];
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 if (j0 + 32 * u < kept) to[j0 + 32 * u] = e[u];
@@ -171,15 +172,15 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_tables_kernel(const ForkPar
 // end, so nearly all of them -- and the others look their id up in the list.
 constexpr int REMAP_THREADS = 256, REMAP_UNROLL = 4, REMAP_PIECE = REMAP_THREADS * REMAP_UNROLL;
 __global__ void __launch_bounds__(REMAP_THREADS)
-    remap_tables_kernel(int32_t *__restrict__ tables, int max_blocks, const int32_t *__restrict__ lens, int num_seqs,
-                        const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n, int pieces)
+    remap_tables_kernel(int32_t *tables, int max_blocks, const int32_t *lens, int num_seqs, const int32_t *src,
+                        const int32_t *dst, int n, int pieces)
 {
     begin();
-    const int lowest = __ldg(src), highest = __ldg(src + n - 1);
+    const int lowest = *src, highest = src[n - 1];
     for (int64_t x = blockIdx.x; x < (int64_t)num_seqs * pieces; x += gridDim.x) {
         const int s = (int)(x / pieces), piece = (int)(x - (int64_t)s * pieces);
         int32_t *row = tables + (size_t)s * max_blocks;
-        const int L = __ldg(lens + s), j0 = piece * REMAP_PIECE + threadIdx.x;
+        const int L = lens[s], j0 = piece * REMAP_PIECE + threadIdx.x;
         int32_t id[REMAP_UNROLL];
         // (asked for together with the length: entries past it are not used)
 #pragma unroll
@@ -197,10 +198,10 @@ __global__ void __launch_bounds__(REMAP_THREADS)
             int lo = 0, hi = n;
             while (hi - lo > 1) {
                 const int mid = lo + ((hi - lo) >> 1);
-                if (__ldg(src + mid) <= id[u]) lo = mid;
+                if (src[mid] <= id[u]) lo = mid;
                 else hi = mid;
             }
-            if (__ldg(src + lo) == id[u]) row[j] = __ldg(dst + lo);
+            if (src[lo] == id[u]) row[j] = dst[lo];
         }
     }
 }
