@@ -260,9 +260,9 @@ PAGEDKV_API kv_status kv_prefix_alloc(kv_prefix_cache *cache, int32_t n, int32_t
 PAGEDKV_API kv_status kv_prefix_stats(const kv_prefix_cache *cache, kv_prefix_stats_t *out);
 
 /* After kv_pool_compact on the cache's pool: every cached block src[i] is block
- * dst[i] from now on (src strictly ascending, host int32 [n]; KV_ERR_INVALID and
- * nothing changes otherwise).  What the cache holds, its order of eviction and its
- * statistics stay as they are. */
+ * dst[i] from now on (host int32 [n], src strictly ascending, dst ids of the pool;
+ * KV_ERR_INVALID and nothing changes otherwise).  What the cache holds, its order of
+ * eviction and its statistics stay as they are. */
 PAGEDKV_API kv_status kv_prefix_remap(kv_prefix_cache *cache, const int32_t *src, const int32_t *dst, int32_t n);
 
 /* ------------------------------------------------------------------------

@@ -290,8 +290,10 @@ kv_status kv_prefix_alloc(kv_prefix_cache *c, int32_t n, int32_t *out_ids)
 kv_status kv_prefix_remap(kv_prefix_cache *cache, const int32_t *src, const int32_t *dst, int32_t n)
 {
     if (!cache || n < 0 || (n > 0 && (!src || !dst))) return KV_ERR_INVALID;
-    for (int32_t i = 1; i < n; ++i)
-        if (src[i] <= src[i - 1]) return KV_ERR_INVALID;
+    kv_pool_stats_t pool;
+    if (kv_pool_stats(cache->pool, &pool) != KV_OK) return KV_ERR_INVALID;
+    for (int32_t i = 0; i < n; ++i)
+        if ((i > 0 && src[i] <= src[i - 1]) || dst[i] < 0 || dst[i] >= pool.num_blocks) return KV_ERR_INVALID;
     std::lock_guard<std::mutex> g(cache->mu);
     for (Node &x : cache->nodes) {
         if (!x.live) continue;

@@ -131,6 +131,59 @@ def test_binding_refuses_cpu_tensors(name):
         getattr(pkv, name)(*args)
 
 
+DIRECT = {"paged_attention_shared_prefix": ATT, "kv_copy_blocks": dict(COPY, caches=[A, 2 * A], count=None),
+          "kv_fork_tables": FORK, "kv_remap_tables": REMAP}
+SIZES = dict(B=4, R=8, nq=2, G=2, hq=32, hkv=8, mp=640, mt=4096)
+
+
+def _direct(name, **change):
+    return getattr(pkv._fast(), name)(*[v for k, v in dict(DIRECT[name], **change).items() if k != "count"])
+
+
+@pytest.mark.parametrize("name,change,status", [
+    ("paged_attention_shared_prefix", dict(nq=0), INVALID), ("paged_attention_shared_prefix", dict(hq=24), UNSUPPORTED),
+    ("paged_attention_shared_prefix", dict(dt=1), INVALID), ("paged_attention_shared_prefix", dict(scale=-1.0), INVALID),
+    ("paged_attention_shared_prefix", dict(scale=float("nan")), INVALID), ("paged_attention_shared_prefix", dict(nbytes=0), INVALID),
+    ("paged_attention_shared_prefix", dict(tables=9 * A + 3), INVALID), ("paged_attention_shared_prefix", dict(B=0), OK),
+    ("paged_attention_shared_prefix", dict(v=None), INVALID), ("paged_attention_shared_prefix", dict(nb=1 << 27), UNSUPPORTED),
+    ("kv_copy_blocks", dict(bytes=4104), INVALID), ("kv_copy_blocks", dict(caches=[A, None]), INVALID),
+    ("kv_copy_blocks", dict(caches=[A] * 129 + [A + 8]), INVALID), ("kv_copy_blocks", dict(caches=[]), OK),
+    ("kv_copy_blocks", dict(dst=None), INVALID), ("kv_copy_blocks", dict(n=0), OK),
+    ("kv_fork_tables", dict(taken=4 * A + 4), INVALID), ("kv_fork_tables", dict(C=16385), UNSUPPORTED),
+    ("kv_fork_tables", dict(free=None), INVALID), ("kv_remap_tables", dict(dst=A), INVALID),
+    ("kv_remap_tables", dict(lens=A + 64), INVALID), ("kv_remap_tables", dict(B=0), OK)])
+def test_direct_entries_refuse_alike(name, change, status):
+    assert _direct(name, **change) == status
+
+
+@pytest.mark.parametrize("name", DIRECT)
+def test_direct_entries_check_their_arguments(name):
+    values = [v for k, v in DIRECT[name].items() if k != "count"]
+    entry = getattr(pkv._fast(), name)
+    for wrong in (values[:-1], values + [0], []):
+        with pytest.raises(TypeError, match="arguments"):
+            entry(*wrong)
+    for i, v in enumerate(values):
+        with pytest.raises(TypeError):
+            entry(*values[:i], "1", *values[i + 1:])
+    for key, v in DIRECT[name].items():
+        if key in ("B", "R", "mb", "nb", "n", "P", "C", "nfree", "hq"):
+            for far in (1 << 31, -(1 << 31) - 1, 1 << 80):
+                with pytest.raises(OverflowError):
+                    _direct(name, **{key: far})
+    with pytest.raises(TypeError):
+        pkv._fast().kv_copy_blocks((A, 2 * A), *[v for k, v in COPY.items() if k not in ("caches", "count")])
+    with pytest.raises(TypeError):
+        pkv._fast().kv_copy_blocks([A, "2"], *[v for k, v in COPY.items() if k not in ("caches", "count")])
+
+
+@pytest.mark.parametrize("change", [dict(), dict(B=0), dict(nq=17), dict(hq=24, hkv=7), dict(mp=BIG, mt=BIG), dict(G=0), dict(mt=-1)])
+def test_direct_size_agrees(change):
+    args = list(dict(SIZES, **change).values())
+    assert pkv._fast().paged_attention_shared_prefix_workspace_size(*args) == \
+        pkv.lib().paged_attention_shared_prefix_workspace_size(*args)
+
+
 # ------------------------------------------------------------------ compaction
 def _busy_pool(seed, nb):
     rng = np.random.default_rng(seed)
@@ -217,8 +270,12 @@ def test_prefix_cache_follows_a_compaction():
         cache.remap([3, 3], [1, 2])
     with pytest.raises(pkv.KVError):
         cache.remap([3, 2], [1, 4])
+    for bad in (-1, nb):
+        with pytest.raises(pkv.KVError):
+            cache.remap([3, 5], [1, bad])
     with pytest.raises(ValueError):
         cache.remap([3], [1, 4])
+    assert [cache.match(t).tolist() for t in prompts] == [[to.get(b, b) for b in model.match(t, 0)] for t in prompts]
     # everything can be given back under the new ids
     free = pool.stats()["free"]
     evicted = cache.evict(nb)
