@@ -1500,8 +1500,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     __nv_bfloat16 *const to16 = p.out16 + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * D +
                                                 (lane & 7) * 4;
                     if ((r & ~31) < rows) {      // (a warp without rows stores nothing)
-// (one copy of the code: it runs once an item, and fetching four takes longer
-                        // than running them)
+                        // (one copy of the code, which runs once an item: unrolled, its fetch
+                        // took longer, 75 us against 60 for 73 sequences x 4 rows x 8 heads)
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             float o[32];
