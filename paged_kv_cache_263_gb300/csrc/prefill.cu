@@ -717,7 +717,7 @@ __device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w
     // (asked for before anything waits for the groups)
     float tail = 0.f;
 #pragma unroll 4
-    for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, __ldg(p.b.context_lens + s));
+    for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, p.b.context_lens[s]);
     load_window(p, w, tpt, lane);
     // (no tails beside this kernel, or at most one item a CTA: the host's plan stands)
     if (p.joined || p.one_wave) return p.grid_ctas;

@@ -32,7 +32,7 @@ __device__ __forceinline__ int last_at_most(const int32_t *v, int n, int x, int 
     int lo = 0;
     while (n > 1) {
         const int step = (n + 31) >> 5, i = lane * step;
-        const unsigned m = __ballot_sync(0xffffffffu, i < n && __ldg(v + lo + min(i, n - 1)) <= x);
+        const unsigned m = __ballot_sync(0xffffffffu, i < n && v[lo + min(i, n - 1)] <= x);
         const int at = m ? 31 - __clz(m) : 0;
         lo += at * step;
         n = min(step, n - at * step);
@@ -47,15 +47,15 @@ struct SharedGroup {
 __device__ __forceinline__ SharedGroup shared_group(const SharedBatch &b, int g)
 {
     SharedGroup r;
-    r.s0 = __ldg(b.cu_groups + g);
-    r.s1 = __ldg(b.cu_groups + g + 1);
-    const int p = __ldg(b.prefix_lens + g);
+    r.s0 = b.cu_groups[g];
+    r.s1 = b.cu_groups[g + 1];
+    const int p = b.prefix_lens[g];
     r.P = p & ~(BS - 1);
     r.ok = r.s0 >= 0 && r.s0 <= r.s1 && r.s1 <= b.num_seqs && p >= 0 && r.P <= b.max_prefix;
     r.row0 = r.rows = 0;
     if (r.ok && r.s0 < r.s1) {
-        const int a = b.cu_q_lens ? __ldg(b.cu_q_lens + r.s0) : r.s0;
-        const int e = b.cu_q_lens ? __ldg(b.cu_q_lens + r.s1) : r.s1;
+        const int a = b.cu_q_lens ? b.cu_q_lens[r.s0] : r.s0;
+        const int e = b.cu_q_lens ? b.cu_q_lens[r.s1] : r.s1;
         r.ok = a >= 0 && a <= e && e <= b.total_rows;
         r.row0 = a;
         r.rows = r.ok ? e - a : 0;
@@ -76,9 +76,9 @@ __device__ __forceinline__ SharedSeq shared_seq_in(const SharedBatch &b, int s, 
     SharedSeq r;
     r.state = SEQ_BAD;
     // what does not depend on the group is asked for together with it
-    r.row0 = b.cu_q_lens ? __ldg(b.cu_q_lens + s) : s;
-    r.n = (b.cu_q_lens ? __ldg(b.cu_q_lens + s + 1) : s + 1) - r.row0;
-    r.L = __ldg(b.context_lens + s);
+    r.row0 = b.cu_q_lens ? b.cu_q_lens[s] : s;
+    r.n = (b.cu_q_lens ? b.cu_q_lens[s + 1] : s + 1) - r.row0;
+    r.L = b.context_lens[s];
     r.P = 0;
     r.first = s;
     bool ok = true;
@@ -113,13 +113,13 @@ __device__ __forceinline__ SharedSeq shared_seq_window(const SharedBatch &b, int
     if (b.num_groups > 1) {
         // the first sequence's group, then the 32 groups' beginnings behind it, counted
         g = last_at_most(b.cu_groups, b.num_groups, s0, lane);
-        const int mine = g + 1 + lane < b.num_groups ? __ldg(b.cu_groups + g + 1 + lane) : INT_MAX;
+        const int mine = g + 1 + lane < b.num_groups ? b.cu_groups[g + 1 + lane] : INT_MAX;
         int more = 0;
 #pragma unroll 8
         for (int i = 0; i < 32; ++i) more += __shfl_sync(0xffffffffu, mine, i) <= s;
         g += more;
         // (empty groups among them: a lane may have further to go)
-        while (more == 32 && g + 1 < b.num_groups && __ldg(b.cu_groups + g + 1) <= s) ++g;
+        while (more == 32 && g + 1 < b.num_groups && b.cu_groups[g + 1] <= s) ++g;
     }
     if (s >= b.num_seqs) {
         SharedSeq r = {};

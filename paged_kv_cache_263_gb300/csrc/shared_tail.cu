@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
             const int32_t *own = p.block_tables + (size_t)s * p.b.max_blocks + (p.whole ? 0 : pb) + it.b0;
             const int32_t *shared = p.block_tables + (size_t)first * p.b.max_blocks + it.b0;
             const int from_shared = p.whole ? pb - it.b0 : 0;
-            auto load_ids = [&](int j) -> int { return j < it.nb ? __ldg((j < from_shared ? shared : own) + j) : -1; };
+            auto load_ids = [&](int j) -> int { return j < it.nb ? (j < from_shared ? shared : own)[j] : -1; };
             // a block for each consumer warp at a time, from the lane of the warp's number
             int ids = load_ids(lane), ahead = load_ids(32 + lane), base = 0;   // ids of blocks base + lane, base + 32 + lane
             for (int j0 = 0; j0 < it.nb; j0 += CONSUMERS) {
@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         if (lane == 0) mbar_arrive(b_taken + 8 * sl);
         float sl2 = p.scale_log2, vsc = 1.f;
         if constexpr (FP8) {
-            sl2 *= __ldg(p.k_scale + it.g);
-            vsc = __ldg(p.v_scale + it.g);
+            sl2 *= p.k_scale[it.g];
+            vsc = p.v_scale[it.g];
         }
         float o[NT][8][4], m[NT][2], l[NT][2];
 #pragma unroll
