@@ -33,6 +33,7 @@ using namespace pkv;
 
 constexpr int QROW = 272;          // bytes of a column's query in shared memory: 256, kept off one bank
 constexpr int SLOTS = 2;           // items ahead
+constexpr int ASK_BLOCKS = 12;     // the next item is asked for when so many blocks of one are left to ask for
 
 template <bool FP8, int NT>
 struct TailLay {
@@ -63,7 +64,9 @@ struct TailParams {
     const int32_t *block_tables;
     const float *k_scale, *v_scale;
     float *part_o, *part_ml;
-    int *counter;                    // items taken (the kernel of the prefixes set it to 0); null: every grid-th
+    int *counter;                    // the next item, set by the kernel before; null: a CTA takes every grid-th
+    int first;                       // ... and its first item is its own number
+    int direct;                      // one part a sequence
     int hq, hkv, group, num_blocks, part_blocks, part_stride, part_off;
     int whole;                       // contexts from their first key on, the prefix through the group's first row
     int beside;                      // launched to run beside the kernel before, whose inputs were complete too
@@ -121,9 +124,6 @@ __device__ __forceinline__ void load_window(const TailParams &p, TailWindow &w, 
         if (lane >= o) w.incl += t;
     }
     w.total = __shfl_sync(0xffffffffu, w.incl, 31);
-    // rows of sequences without a context, where no merge kernel writes them
-    if (p.out16 && blockIdx.x == 0)
-        zero_rows(p.out16, p.hq, s < p.b.num_seqs && w.q.state == SEQ_EMPTY, w.q.row0, w.q.n, lane);
 }
 
 template <bool FP8, int NT>
@@ -170,28 +170,57 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         if (p.whole) asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
         else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
         TailWindow w = {};
-        load_window(p, w, lane);
+        if (p.direct) w.w0 = -1;       // none
+        else load_window(p, w, lane);
         int u = 0, k = 0;        // blocks handed to this lane's consumer warp, and items
         int asked = 0;           // items whose queries were asked for
         bool ok = true;
-        int idx = blockIdx.x;
-        if (p.counter) idx = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(p.counter, 1) : 0, 0);
+        // (in lane 0; its answer is waited for where it is used)
+        auto ask = [&](int idx) -> int {
+            return !p.counter ? idx + (int)gridDim.x : lane == 0 ? atomicAdd(p.counter, 1) : 0;
+        };
+        int idx = p.first ? (int)blockIdx.x : __shfl_sync(0xffffffffu, ask(0), 0);
         for (;; ++k) {
-            // (the one after this is asked for now)
-            int next = idx + gridDim.x;
-            if (p.counter && lane == 0) next = atomicAdd(p.counter, 1);
-            while (idx - w.base >= w.total && w.w0 + 32 < p.b.num_seqs) {
-                w.base += w.total;
-                w.w0 += 32;
-                load_window(p, w, lane);
+            int at = 32, r = 0;      // the item's sequence in the window (32: no more), its place there
+            if (p.direct) {
+                // sequence and head from the number; sequences with nothing to attend are passed over
+                for (; idx < p.b.num_seqs * p.hkv; idx = __shfl_sync(0xffffffffu, ask(idx), 0)) {
+                    const int in = idx / p.hkv;
+                    r = idx - in * p.hkv;
+                    if ((in & ~31) != w.w0) {
+                        w.w0 = in & ~31;
+                        load_window(p, w, lane);
+                    }
+                    if (__shfl_sync(0xffffffffu, w.ns, in & 31)) {
+                        at = in & 31;
+                        break;
+                    }
+                    // (rows without a context, where no merge kernel writes them)
+                    const int n = __shfl_sync(0xffffffffu, w.q.state == SEQ_EMPTY ? w.q.n : 0, in & 31);
+                    const int row0 = __shfl_sync(0xffffffffu, w.q.row0, in & 31);
+                    if (p.out16)
+                        for (int64_t i = lane; i < (int64_t)n * p.group * (D / 8); i += 32) {
+                            const int64_t row = row0 + i / (p.group * (D / 8));
+                            reinterpret_cast<uint4 *>(p.out16 + (row * p.hq + r * p.group) * D)[i % (p.group * (D / 8))] =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                }
+            } else {
+                while (idx - w.base >= w.total && w.w0 + 32 < p.b.num_seqs) {
+                    w.base += w.total;
+                    w.w0 += 32;
+                    load_window(p, w, lane);
+                }
+                const int x = idx - w.base;
+                if (x < w.total) {
+                    at = __ffs(__ballot_sync(0xffffffffu, w.incl > x)) - 1;
+                    r = x - (__shfl_sync(0xffffffffu, w.incl, at) - __shfl_sync(0xffffffffu, w.ns, at) * p.hkv);
+                }
             }
-            const int x = idx - w.base;
             TailItem it = {};
             int s = 0, P = 0, first = 0;
-            if (x < w.total) {
-                const int at = __ffs(__ballot_sync(0xffffffffu, w.incl > x)) - 1;
-                const int ns = __shfl_sync(0xffffffffu, w.ns, at);
-                const int r = x - (__shfl_sync(0xffffffffu, w.incl, at) - ns * p.hkv), part = r / p.hkv;
+            if (at < 32) {
+                const int part = r / p.hkv;
                 s = w.w0 + at;
                 P = __shfl_sync(0xffffffffu, w.q.P, at);
                 first = __shfl_sync(0xffffffffu, w.q.first, at);
@@ -227,8 +256,15 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
             const int from_shared = p.whole ? pb - it.b0 : 0;
             auto load_ids = [&](int j) -> int { return j < it.nb ? (j < from_shared ? shared : own)[j] : -1; };
             // a block for each consumer warp at a time, from the lane of the warp's number
+            int next = 0;
+            bool asked_next = false;
             int ids = load_ids(lane), ahead = load_ids(32 + lane), base = 0;   // ids of blocks base + lane, base + 32 + lane
             for (int j0 = 0; j0 < it.nb; j0 += CONSUMERS) {
+                // (late: an item that waits behind a long one could be another CTA's)
+                if (!asked_next && it.nb - j0 <= ASK_BLOCKS) {
+                    next = ask(idx);
+                    asked_next = true;
+                }
                 if (j0 - base >= 32) {
                     base += 32;
                     ids = ahead;
@@ -556,13 +592,26 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
     }
 }
 
+__global__ void set_counter_kernel(int *counter, int to)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    if (threadIdx.x == 0) *counter = to;
+}
+
 template <bool FP8, int NT>
-cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const TailParams &p, int64_t items, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, TailParams p, int *counter, int64_t items, cudaStream_t st)
 {
     using LY = TailLay<FP8, NT>;
     const cudaError_t e = pkv_host::ensure_dynamic_smem<shared_tail_kernel<FP8, NT>>(LY::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(items, 152 * LY::CTAS));
+    if (p.beside) p.counter = counter;       // (set by the kernel of the prefixes)
+    else if (counter && items > grid) {
+        const cudaError_t set = pkv_host::launch_ex(set_counter_kernel, dim3(1), dim3(32), 0, st, true, counter, grid);
+        if (set != cudaSuccess) return set;
+        p.counter = counter;
+    }
     return pkv_host::launch_ex(shared_tail_kernel<FP8, NT>, dim3(grid), dim3(LY::THREADS), LY::SMEM, st, true, km, vm, p);
 }
 
@@ -582,7 +631,8 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.v_scale = c.v_scale;
     p.part_o = c.part_o;
     p.part_ml = c.part_ml;
-    p.counter = beside ? c.counter : nullptr;
+    p.direct = c.tail_splits == 1 ? 1 : 0;
+    p.first = beside ? 0 : 1;
     p.hq = c.hq;
     p.hkv = c.hkv;
     p.group = c.hq / c.hkv;
@@ -606,9 +656,12 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
             return cudaErrorInvalidValue;
     }
     const int64_t items = (int64_t)c.b.num_seqs * c.hkv * c.tail_splits;
+    int *const counter = p.out16 ? nullptr : c.counter;     // (no workspace where the only part is the output)
     if ((int64_t)c.b.max_q_len * p.group > 8)
-        return c.fp8 ? launch<true, 2>(map[0], map[1], p, items, st) : launch<false, 2>(map[0], map[1], p, items, st);
-    return c.fp8 ? launch<true, 1>(map[0], map[1], p, items, st) : launch<false, 1>(map[0], map[1], p, items, st);
+        return c.fp8 ? launch<true, 2>(map[0], map[1], p, counter, items, st)
+                     : launch<false, 2>(map[0], map[1], p, counter, items, st);
+    return c.fp8 ? launch<true, 1>(map[0], map[1], p, counter, items, st)
+                 : launch<false, 1>(map[0], map[1], p, counter, items, st);
 }
 
 }  // namespace pkv_shared_tail
