@@ -103,18 +103,26 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 //   whole, us           26.6  46.3   24.2   34.8  19.5   26.8  9.4    17.7
 //   prefixes apart      30.4  39.9   25.7   30.9  25.0   25.7  15.1   15.9   (bf16)
 //
-// Tails: parts of at most 64 blocks up to 8K tokens, 128 up to 64K, 256 beyond, and
-// shorter ones where there would be fewer than TAIL_CTAS: down to 16 blocks for whole
-// contexts, whose CTAs all start together, and two fifths of that, but no fewer than
-// about 22, beside the prefixes, where SMs come free one after another (48 sequences
-// of 100 to 2,500 tokens beside two prefixes, fp8: 57.3 us with parts of 16 blocks,
-// 54.8 of 22, 58.1 of 32, 66 of 53; 64 of 20 to 1,000 beside one, bf16: 92 of 16, 86
-// of 32, 84 of 63).
+// Whole contexts are cut into the number of parts whose cost is the least, in us: what an
+// item takes to begin and to end, ITEM_US times the items a CTA; what the last items
+// take alone, BLOCK_US a block; a row's parts in the merge, PART_US each; the merge
+// itself, and a counter of items where there are more than CTAs.  (Blocks a part,
+// measured, us; 8 items a part, 1,094 blocks: 16 26.4, 28 25.8, 36 19.2, 64 20.6, 100 25.6;
+// 31 of 464: 16 17.8, 24 14.3, 36 14.2, 64 16.8; 672 of 91, fp8: 46 46.0, 91 41.2; 252 of
+// 1,056, fp8: 36 136.9, 64 128.5, 118 128.4.  Over 46 drawn batches the choice is 2 % off
+// the best of 12 lengths, and a fixed one of 16 blocks or two items a CTA 7 %.)
+//
+// Tails beside the prefixes run on few SMs at first, 10 items or more a CTA: parts of at
+// least 36 blocks (48 sequences of 100 to 2,500 tokens beside two prefixes, fp8: 55.3 us
+// with 24, 53.1 with 40, 56.0 with 64, 63.5 with 100; 64 of 20 to 1,000 beside one, bf16:
+// 88.5 with 24, 84.1 with 32, 82.6 with 40, 81.0 whole), of two fifths of what gives two
+// items a CTA, and of at most 96 up to 8K tokens, 128 up to 64K, 256 beyond.
 //
 // joined: rows x heads of a sequence that are more than the columns of the decode
 // kernel (16) are attended in the chunk kernel's tiles, which hold 128, tails and all.
 constexpr int64_t TAIL_COLS = 16;
 constexpr int64_t WHOLE_KEYS = 64ll << 10, WHOLE_FEW = 1536ll << 10, TAIL_CTAS = 2 * 3 * 152;
+constexpr double ITEM_US = 1.5, BLOCK_US = 0.15, PART_US = 0.15, MERGE_US = 4, COUNTER_US = 1.2;
 void plan(SharedCall &c, int32_t max_tail_len)
 {
     c.joined = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > TAIL_COLS && c.b.max_q_len > 1;
@@ -127,14 +135,22 @@ void plan(SharedCall &c, int32_t max_tail_len)
     if (c.joined) return;
     const int64_t keys = (int64_t)max_tail_len + (c.whole && groups ? c.b.max_prefix : 0);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
-    const int64_t most = blocks <= 512 ? 64 : blocks <= 4096 ? 128 : 256;
-    const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
     if (c.whole) {
-        // (whole contexts that fit 32 blocks are written by the only kernel: no merge)
-        const int64_t part = std::min(most, std::max<int64_t>(blocks <= 32 ? 32 : 16, want));
-        c.tail_splits = (int)((blocks + part - 1) / part);
+        const int64_t each = (int64_t)c.b.num_seqs * c.hkv, ctas = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
+        const int64_t most = std::min<int64_t>(256, (blocks + 11) / 12);
+        double best = 0;
+        for (int64_t n = 1; n <= most; n += 1 + n / 16) {
+            const double us = ITEM_US * (double)(n * each) / (double)ctas + BLOCK_US * (double)((blocks + n - 1) / n) +
+                              PART_US * (double)n + (n > 1 ? MERGE_US + (n * each > ctas ? COUNTER_US : 0) : 0);
+            if (n == 1 || us < best) {
+                best = us;
+                c.tail_splits = (int)n;
+            }
+        }
     } else {
-        const int64_t part = std::max<int64_t>(22, want * 2 / 5);
+        const int64_t most = blocks <= 512 ? 96 : blocks <= 4096 ? 128 : 256;
+        const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
+        const int64_t part = std::max<int64_t>(36, want * 2 / 5);
         c.tail_splits = (int)(part >= most ? (blocks + most - 1) / most : std::max<int64_t>(1, blocks / part));
     }
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);

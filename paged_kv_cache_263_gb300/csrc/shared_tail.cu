@@ -169,9 +169,6 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         uint64_t pol;
         if (p.whole) asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
         else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-        TailWindow w = {};
-        if (p.direct) w.w0 = -1;       // none
-        else load_window(p, w, lane);
         int u = 0, k = 0;        // blocks handed to this lane's consumer warp, and items
         int asked = 0;           // items whose queries were asked for
         bool ok = true;
@@ -179,7 +176,12 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         auto ask = [&](int idx) -> int {
             return !p.counter ? idx + (int)gridDim.x : lane == 0 ? atomicAdd(p.counter, 1) : 0;
         };
-        int idx = p.first ? (int)blockIdx.x : __shfl_sync(0xffffffffu, ask(0), 0);
+        int idx = p.first ? (int)blockIdx.x : ask(0);
+        // (direct: the window of the item that is likely to be its first)
+        TailWindow w = {};
+        if (p.direct) w.w0 = min((int)blockIdx.x / p.hkv, p.b.num_seqs - 1) & ~31;
+        load_window(p, w, lane);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
         for (;; ++k) {
             int at = 32, r = 0;      // the item's sequence in the window (32: no more), its place there
             if (p.direct) {
