@@ -623,6 +623,13 @@ PAGEDKV_API size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs
                                                                 int32_t max_q_len, int32_t num_groups,
                                                                 int32_t num_q_heads, int32_t num_kv_heads,
                                                                 int32_t max_prefix_len, int32_t max_tail_len);
+/* How such a call is done: 0 whole contexts in one kernel, 1 the prefixes in a kernel of
+ * their own beside the tails', 2 prefixes and tails in one kernel of 128-row tiles (rows x
+ * heads of a sequence above 16 only); -1 for sizes that no call takes.  The choice is by
+ * what each would take, from the sizes and the two bounds. */
+PAGEDKV_API int32_t paged_attention_shared_prefix_way(int32_t num_seqs, int32_t total_q_tokens, int32_t max_q_len,
+                                                      int32_t num_groups, int32_t num_q_heads, int32_t num_kv_heads,
+                                                      int32_t max_prefix_len, int32_t max_tail_len, kv_dtype dtype);
 PAGEDKV_API kv_status paged_attention_shared_prefix(
     void *out, const void *q, const int32_t *cu_q_lens, const int32_t *context_lens, int32_t num_seqs,
     int32_t total_q_tokens, int32_t max_q_len, const int32_t *cu_groups, const int32_t *prefix_lens,

@@ -24,8 +24,8 @@ __all__ = [
     "kv_build_step_tables", "reshape_and_cache_latent", "paged_latent_attention",
     "paged_latent_attention_workspace_size", "latent_prefill_attention",
     "latent_prefill_attention_workspace_size", "LATENT_DIM", "LATENT_ROPE_DIM", "LATENT_MAX_HEADS",
-    "paged_attention_shared_prefix", "paged_attention_shared_prefix_workspace_size", "kv_copy_blocks",
-    "kv_fork_tables", "kv_remap_tables",
+    "paged_attention_shared_prefix", "paged_attention_shared_prefix_workspace_size",
+    "paged_attention_shared_prefix_way", "kv_copy_blocks", "kv_fork_tables", "kv_remap_tables",
 ]
 
 HEAD_DIM = 128
@@ -115,6 +115,7 @@ def lib():
             "kv_pool_compact": (c.c_int, [P, I, P, P, c.POINTER(I)]),
             "kv_prefix_remap": (c.c_int, [P, P, P, I]),
             "paged_attention_shared_prefix_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
+            "paged_attention_shared_prefix_way": (I, [I, I, I, I, I, I, I, I, c.c_int]),
             "paged_attention_shared_prefix": (c.c_int, [P, P, P, P, I, I, I, P, P, I, I, I, P, P, P, I, I, I, I, F,
                                                         c.c_int, P, P, P, SZ, P]),
             "kv_copy_blocks": (c.c_int, [P, I, I64, I, P, P, I, P]),
@@ -677,6 +678,13 @@ def paged_attention_shared_prefix_workspace_size(num_seqs, total_q_tokens, max_q
                                                  num_kv_heads, max_prefix_len, max_tail_len) -> int:
     return _fast().paged_attention_shared_prefix_workspace_size(
         num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len, max_tail_len)
+
+
+def paged_attention_shared_prefix_way(num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads,
+                                      max_prefix_len, max_tail_len, fp8=False) -> int:
+    """How a call of these sizes and bounds is done: 0 whole contexts, 1 prefixes apart, 2 joined."""
+    return lib().paged_attention_shared_prefix_way(num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads,
+                                                   num_kv_heads, max_prefix_len, max_tail_len, 1 if fp8 else 0)
 
 
 def paged_attention_shared_prefix(out, q, k_cache, v_cache, block_tables, context_lens, cu_groups, prefix_lens,

@@ -1800,7 +1800,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
         const double per_sm = DECODE_SM_BYTES_PER_TILE_TIME * tile_keys / 64.0;
         // (and the merge's trips to memory: eight parts a trip)
         const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / per_tile + 0.12 * 64.0 / tile_keys;
-        const double tail = 0.5 * c.b.num_seqs * (double)max_tail * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+        const double tail = 0.5 * c.b.num_seqs * (double)max_tail * c.mean_sets * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
         const double mean = ng > 1 ? 0.5 : 1.0;
         double best = 0;
         int pick = 0;
@@ -1851,7 +1851,7 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.tile_keys = c.big ? 128 : 64;
     p.num_sms = num_sms();
     p.bytes_per_tile = (float)(BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
-    p.decode_key_bytes = (float)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
+    p.decode_key_bytes = (float)c.mean_sets * (float)c.hkv * D * 2 * (c.fp8 ? 1 : 2);
     p.decode_sm_bytes = (float)(DECODE_SM_BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
     p.q_box_bytes = tpt * G * 128;
     p.grid_ctas = (int)std::min<int64_t>(c.prefix_items + c.tail_items, p.num_sms);

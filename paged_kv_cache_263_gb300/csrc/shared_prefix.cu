@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace {
 
@@ -89,19 +90,33 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
     *out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
-// How a call is done, from its sizes and bounds.
+// How a call is done, from its sizes and bounds: the way that these costs say is the
+// shortest, in us of the 152 SMs, for blocks of 16 keys.
 //
-// whole: no kernel for the prefixes.  The tails' kernel then attends whole contexts
-// and reads a prefix once a sequence, from L2 where it fits.  It reads 13 to 18 keys a
-// KV head in a ns (bf16; fp8 27) and the prefixes' kernel 13 (fp8 7 to 10), so with few
-// sequences a group the latter never pays: 2 of 24,576 tokens, 8 KV heads, 16 groups:
-// 236 us against 263 (bf16), 200 against 347 (fp8; 3: 289 against 346).  With more it
-// has to save what it and the merge add, 10 us: that takes about WHOLE_KEYS +
-// WHOLE_FEW / (sequences a group) keys x KV heads of prefix, counted once a sequence.
-//   sequences a group       4            6            8            16
-//   K keys x KV heads   512   1024   384    768   256    512   64     192
-//   whole, us           26.6  46.3   24.2   34.8  19.5   26.8  9.4    17.7
-//   prefixes apart      30.4  39.9   25.7   30.9  25.0   25.7  15.1   15.9   (bf16)
+// whole: one kernel attends whole contexts, at most 16 rows x heads an item (a set of a
+// sequence's rows), and reads a prefix once a set, from L2 where it fits.  A set takes
+// SET_US, a block FIRST_US where it comes from memory and AGAIN_US for each further set
+// that reads it (fp8: FIRST8_US, AGAIN8_US).
+// apart: the prefixes in the chunk kernel's tiles, the tails beside it as above.  A block
+// of a prefix takes TILE_US for a query item (256 rows x heads; BIG_US for 128 where a
+// group has no more, over a bf16 cache; fp8 TILE8_US): twice the tiles' own time, as the
+// items and the prefixes are unequal.
+// joined: the chunk kernel takes the tails as well, JOIN_US an item and less a block than
+// for prefixes, as each tail is read once.  Only for rows x heads of a sequence that are
+// more than 16: at 16 it lost (32 sequences x 4 rows: 62.5 us against 52.5).
+// ROOT_US: the last parts and the merge of long contexts, which are cut into about the
+// root of their blocks.
+//
+// Measured on 284 drawn batches, each way forced in turn: the costs' choice takes 2 % more
+// than the best way (fitted on one half of them, 3.5 % on the other); rules by sequences a
+// group and keys of prefix, with joined for all wide rows, took 3 % more for narrow rows
+// and 16 % for wide ones.  Some of them, us (rows x heads of a sequence):
+//                                                        whole   apart   joined
+//   152 sequences x 32, prefixes to 600, tails to 200    27.6    47.3    47.2
+//   51 x 56, one prefix of 12K, tails to 180, fp8        205     45.2    62.1
+//   49 x 56, tails of 7K to 11K                          205     243     125
+//   16 groups of 2 x 4, 24,576 of prefix                 236     263
+//   8 groups of 16 x 4, 1,500 of prefix                  17.7    15.9
 //
 // Whole contexts are cut into the number of parts whose cost is the least, in us: what an
 // item takes to begin and to end, ITEM_US times the items a CTA; what the last items
@@ -118,17 +133,54 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // 88.5 with 24, 84.1 with 32, 82.6 with 40, 81.0 whole), of two fifths of what gives two
 // items a CTA, and of at most 96 up to 8K tokens, 128 up to 64K, 256 beyond.
 //
-// joined: rows x heads of a sequence that are more than the columns of the decode
-// kernel (16) are attended in the chunk kernel's tiles, which hold 128, tails and all.
-constexpr int64_t TAIL_COLS = 16;
-constexpr int64_t WHOLE_KEYS = 64ll << 10, WHOLE_FEW = 1536ll << 10, TAIL_CTAS = 2 * 3 * 152;
+constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
+constexpr double SET_US = 1.5, FIRST_US = 0.14, AGAIN_US = 0.09, FIRST8_US = 0.17, AGAIN8_US = 0.06;
+constexpr double TILE_US = 0.38, BIG_US = 0.34, TILE8_US = 0.47;
+constexpr double JOIN_US = 5.8, JOIN_TILE_US = 0.20, JOIN_BIG_US = 0.125, JOIN_TILE8_US = 0.27;
+constexpr double WHOLE_START_US = 5.6, APART_START_US = 12, JOINED_START_US = 13.7, ROOT_US = 0.13;
 constexpr double ITEM_US = 1.5, BLOCK_US = 0.15, PART_US = 0.15, MERGE_US = 4, COUNTER_US = 1.2;
+
+void choose(SharedCall &c, int32_t max_tail_len)
+{
+    const int G = c.hq / c.hkv;
+    const int64_t groups = c.b.num_groups, rows = c.b.total_rows;
+    const double seqs = std::max(1, c.b.num_seqs), sms = 152;
+    const double P = groups ? (double)(c.b.max_prefix / BS) : 0, T = ((double)max_tail_len + BS - 1) / BS;
+    const double mean = std::max(1.0, (double)rows / seqs);          // rows of a sequence
+    const double sets = c.mean_sets;
+    const double first = c.fp8 ? FIRST8_US : FIRST_US, again = c.fp8 ? AGAIN8_US : AGAIN_US;
+    const double tails = seqs * c.hkv * (SET_US * sets + (first + (sets - 1) * again) * T) / sms;
+    const double readers = std::min((double)groups, seqs);
+    auto big = [&](bool joined) {
+        const double of = P > 0 ? (double)groups : seqs;
+        return !c.fp8 && (double)rows * G <= 128 * of && (!joined || (int64_t)c.b.max_q_len * G <= 128);
+    };
+    auto prefix = [&](bool is_big) {
+        if (P == 0) return 0.0;
+        const double items = std::ceil((double)rows / groups / ((is_big ? 128 : 256) / G));
+        return groups * items * c.hkv * P * (c.fp8 ? TILE8_US : is_big ? BIG_US : TILE_US) / sms;
+    };
+    const double whole = WHOLE_START_US + tails + c.hkv * P * (first * readers + again * (seqs * sets - readers)) / sms +
+                         ROOT_US * std::sqrt(P + T);
+    const double apart = P > 0 ? APART_START_US + prefix(big(false)) + tails + ROOT_US * std::sqrt(T) : INFINITY;
+    double joined = INFINITY;
+    if (c.b.max_q_len > 1 && (int64_t)c.b.max_q_len * G > TAIL_COLS) {
+        const bool is_big = big(true);
+        const double items = seqs * std::ceil(mean / ((is_big ? 128 : 256) / G)) * c.hkv;
+        joined = JOINED_START_US + prefix(is_big) +
+                 items * (JOIN_US + T * (c.fp8 ? JOIN_TILE8_US : is_big ? JOIN_BIG_US : JOIN_TILE_US)) / sms;
+    }
+    c.joined = joined < std::min(whole, apart);
+    c.whole = !c.joined && whole <= apart;
+}
+
 void plan(SharedCall &c, int32_t max_tail_len)
 {
-    c.joined = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > TAIL_COLS && c.b.max_q_len > 1;
-    const int64_t seqs = std::max(1, c.b.num_seqs), groups = c.b.num_groups;
-    c.whole = !c.joined && (seqs < (c.fp8 ? 4 : 3) * groups || groups == 0 ||
-                            seqs * c.b.max_prefix <= (WHOLE_KEYS + WHOLE_FEW * groups / seqs) / c.hkv);
+    const int64_t groups = c.b.num_groups;
+    c.set_rows = (int)std::min<int64_t>(c.b.max_q_len, TAIL_COLS / (c.hq / c.hkv));
+    c.sets = (c.b.max_q_len - 1) / c.set_rows + 1;
+    c.mean_sets = std::ceil(std::max(1.0, (double)c.b.total_rows / std::max(1, c.b.num_seqs)) / c.set_rows);
+    choose(c, max_tail_len);
     c.prefix_splits = 0;
     c.prefix_items = c.tail_items = 0;
     if (!c.whole) pkv_prefill::plan_prefixes(c, max_tail_len);
@@ -136,11 +188,12 @@ void plan(SharedCall &c, int32_t max_tail_len)
     const int64_t keys = (int64_t)max_tail_len + (c.whole && groups ? c.b.max_prefix : 0);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
     if (c.whole) {
-        const int64_t each = (int64_t)c.b.num_seqs * c.hkv, ctas = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
+        const double each = (double)c.b.num_seqs * c.hkv * c.mean_sets;
+        const double ctas = c.set_rows * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
         const int64_t most = std::min<int64_t>(256, (blocks + 11) / 12);
         double best = 0;
         for (int64_t n = 1; n <= most; n += 1 + n / 16) {
-            const double us = ITEM_US * (double)(n * each) / (double)ctas + BLOCK_US * (double)((blocks + n - 1) / n) +
+            const double us = ITEM_US * n * each / ctas + BLOCK_US * (double)((blocks + n - 1) / n) +
                               PART_US * (double)n + (n > 1 ? MERGE_US + (n * each > ctas ? COUNTER_US : 0) : 0);
             if (n == 1 || us < best) {
                 best = us;
@@ -175,6 +228,25 @@ size_t scratch_bytes(const SharedCall &c)
     return o ? o + part_ml_bytes(c) + 256 : 0;      // and the counter
 }
 
+// the description that sizes and bounds alone make (false: sizes that no call takes)
+bool describe(SharedCall &c, int32_t num_seqs, int32_t total_q_tokens, int32_t max_q_len, int32_t num_groups,
+              int32_t num_q_heads, int32_t num_kv_heads, int32_t max_prefix_len, int32_t max_tail_len, bool fp8)
+{
+    if (num_seqs < 1 || total_q_tokens < 1 || max_q_len < 1 || num_groups < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
+        max_prefix_len < 0 || max_tail_len < 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16)
+        return false;
+    c.b.num_seqs = num_seqs;
+    c.b.total_rows = total_q_tokens;
+    c.b.max_q_len = max_q_len;
+    c.b.num_groups = num_groups;
+    c.b.max_prefix = max_prefix_len / BS * BS;
+    c.hq = num_q_heads;
+    c.hkv = num_kv_heads;
+    c.fp8 = fp8;
+    plan(c, max_tail_len);
+    return true;
+}
+
 }  // namespace
 
 namespace pkv_shared {
@@ -188,24 +260,27 @@ size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t to
                                                     int32_t max_prefix_len, int32_t max_tail_len)
 {
     // (the caches' type is not given: room for the plan of either)
-    if (num_seqs < 1 || total_q_tokens < 1 || max_q_len < 1 || num_groups < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
-        max_prefix_len < 0 || max_tail_len < 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16)
-        return 0;
     size_t most = 0;
     for (const bool fp8 : {false, true}) {
         SharedCall c{};
-        c.b.num_seqs = num_seqs;
-        c.b.total_rows = total_q_tokens;
-        c.b.max_q_len = max_q_len;
-        c.b.num_groups = num_groups;
-        c.b.max_prefix = max_prefix_len / BS * BS;
-        c.hq = num_q_heads;
-        c.hkv = num_kv_heads;
-        c.fp8 = fp8;
-        plan(c, max_tail_len);
+        if (!describe(c, num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
+                      max_tail_len, fp8))
+            return 0;
         most = std::max(most, scratch_bytes(c));
     }
     return most;
+}
+
+int32_t paged_attention_shared_prefix_way(int32_t num_seqs, int32_t total_q_tokens, int32_t max_q_len, int32_t num_groups,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t max_prefix_len,
+                                          int32_t max_tail_len, kv_dtype dtype)
+{
+    SharedCall c{};
+    if ((dtype != KV_BF16 && dtype != KV_FP8_E4M3) ||
+        !describe(c, num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
+                  max_tail_len, dtype == KV_FP8_E4M3))
+        return -1;
+    return c.whole ? 0 : c.joined ? 2 : 1;
 }
 
 kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t *cu_q_lens,
@@ -259,7 +334,7 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (c.prefix_items > INT32_MAX / 64 || c.tail_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
     if (c.joined && ((int64_t)max_q_len * G / 128 + 1) * num_kv_heads * c.tail_splits > INT32_MAX / 64)
         return KV_ERR_UNSUPPORTED;
-    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)num_seqs * num_kv_heads * c.tail_splits > INT32_MAX / 2)
+    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)num_seqs * num_kv_heads * c.tail_splits > INT32_MAX / 2 / c.sets)
         return KV_ERR_UNSUPPORTED;
     // (the plan goes by the bounds as given, which the workspace's size goes by; no
     // length passes what a table row holds)

@@ -66,7 +66,8 @@ struct TailParams {
     float *part_o, *part_ml;
     int *counter;                    // the next item, set by the kernel before; null: a CTA takes every grid-th
     int first;                       // ... and its first item is its own number
-    int direct;                      // one part a sequence
+    int direct;                      // one part and one set of rows a sequence: its items are found without a walk
+    int set_rows;                    // rows of a sequence in an item
     int hq, hkv, group, num_blocks, part_blocks, part_stride, part_off;
     int whole;                       // contexts from their first key on, the prefix through the group's first row
     int beside;                      // launched to run beside the kernel before, whose inputs were complete too
@@ -102,28 +103,33 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // end in the order (sequence, part, KV head), the last fastest
 struct TailWindow {
     int w0, base, total;             // first sequence, items before it, items in it
-    int incl, ns;                    // this lane's sequence: items up to it, parts
+    int incl, ns, sets;              // this lane's sequence: items up to it, parts, sets of rows
     SharedSeq q;
 };
 __device__ __forceinline__ void load_window(const TailParams &p, TailWindow &w, int lane)
 {
     const int s = w.w0 + lane;
     w.q = shared_seq_window(p.b, w.w0, lane);
-    w.ns = 0;
+    w.ns = w.sets = 0;
     if (s < p.b.num_seqs) {
         if (w.q.state == SEQ_BAD) flag(ST_BAD_LEN);
         if (w.q.state == SEQ_OK && w.q.n > 0) {
             const int blocks = (w.q.L - (p.whole ? 0 : w.q.P) + BS - 1) / BS;
             w.ns = (blocks + p.part_blocks - 1) / p.part_blocks;
+            w.sets = (w.q.n + p.set_rows - 1) / p.set_rows;
         }
     }
-    w.incl = w.ns * p.hkv;
+    w.incl = w.ns * p.hkv * w.sets;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, w.incl, o);
         if (lane >= o) w.incl += t;
     }
     w.total = __shfl_sync(0xffffffffu, w.incl, 31);
+    // rows of sequences without a context, where no merge kernel writes them (this CTA goes
+    // through all windows; else the CTAs that come upon them do)
+    if (p.out16 && !p.direct && blockIdx.x == 0)
+        zero_rows(p.out16, p.hq, s < p.b.num_seqs && w.q.state == SEQ_EMPTY, w.q.row0, w.q.n, lane);
 }
 
 template <bool FP8, int NT>
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
         load_window(p, w, lane);
         idx = __shfl_sync(0xffffffffu, idx, 0);
         for (;; ++k) {
-            int at = 32, r = 0;      // the item's sequence in the window (32: no more), its place there
+            int at = 32, part = 0, r = 0;    // the item's sequence in the window (32: no more), its head and set
             if (p.direct) {
                 // sequence and head from the number; sequences with nothing to attend are passed over
                 for (; idx < p.b.num_seqs * p.hkv; idx = __shfl_sync(0xffffffffu, ask(idx), 0)) {
@@ -197,15 +203,12 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                         at = in & 31;
                         break;
                     }
-                    // (rows without a context, where no merge kernel writes them)
                     const int n = __shfl_sync(0xffffffffu, w.q.state == SEQ_EMPTY ? w.q.n : 0, in & 31);
-                    const int row0 = __shfl_sync(0xffffffffu, w.q.row0, in & 31);
+                    const int row0 = __shfl_sync(0xffffffffu, w.q.row0, in & 31), width = p.group * (D / 8);
                     if (p.out16)
-                        for (int64_t i = lane; i < (int64_t)n * p.group * (D / 8); i += 32) {
-                            const int64_t row = row0 + i / (p.group * (D / 8));
-                            reinterpret_cast<uint4 *>(p.out16 + (row * p.hq + r * p.group) * D)[i % (p.group * (D / 8))] =
+                        for (int i = lane; i < n * width; i += 32)
+                            reinterpret_cast<uint4 *>(p.out16 + ((size_t)(row0 + i / width) * p.hq + r * p.group) * D)[i % width] =
                                 make_uint4(0u, 0u, 0u, 0u);
-                        }
                 }
             } else {
                 while (idx - w.base >= w.total && w.w0 + 32 < p.b.num_seqs) {
@@ -216,22 +219,28 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                 const int x = idx - w.base;
                 if (x < w.total) {
                     at = __ffs(__ballot_sync(0xffffffffu, w.incl > x)) - 1;
-                    r = x - (__shfl_sync(0xffffffffu, w.incl, at) - __shfl_sync(0xffffffffu, w.ns, at) * p.hkv);
+                    const int of = p.hkv * __shfl_sync(0xffffffffu, w.sets, at);
+                    r = x - (__shfl_sync(0xffffffffu, w.incl, at) - __shfl_sync(0xffffffffu, w.ns, at) * of);
+                    part = r / of;
+                    r -= part * of;
                 }
             }
             TailItem it = {};
             int s = 0, P = 0, first = 0;
             if (at < 32) {
-                const int part = r / p.hkv;
                 s = w.w0 + at;
                 P = __shfl_sync(0xffffffffu, w.q.P, at);
                 first = __shfl_sync(0xffffffffu, w.q.first, at);
-                it.row0 = __shfl_sync(0xffffffffu, w.q.row0, at);
-                it.n = __shfl_sync(0xffffffffu, w.q.n, at);
-                it.L = __shfl_sync(0xffffffffu, w.q.L, at) - (p.whole ? 0 : P);
-                it.g = r % p.hkv;
+                // (set i of a sequence's rows: rows i x set_rows on, whose keys end where those of
+                // its last row do; the parts are those of the whole sequence)
+                const int n = __shfl_sync(0xffffffffu, w.q.n, at), sets = __shfl_sync(0xffffffffu, w.sets, at);
+                const int i0 = r % sets * p.set_rows, keys = __shfl_sync(0xffffffffu, w.q.L, at) - (p.whole ? 0 : P);
+                it.row0 = __shfl_sync(0xffffffffu, w.q.row0, at) + i0;
+                it.n = min(p.set_rows, n - i0);
+                it.L = keys - n + i0 + it.n;
+                it.g = r / sets;
                 it.b0 = part * p.part_blocks;
-                it.nb = min((it.L + BS - 1) / BS, it.b0 + p.part_blocks) - it.b0;
+                it.nb = min((keys + BS - 1) / BS, it.b0 + p.part_blocks) - it.b0;
                 it.slot = p.part_off + part;
                 it.valid = 1;
             }
@@ -633,7 +642,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.v_scale = c.v_scale;
     p.part_o = c.part_o;
     p.part_ml = c.part_ml;
-    p.direct = c.tail_splits == 1 ? 1 : 0;
+    p.direct = c.tail_splits == 1 && c.sets == 1 ? 1 : 0;
     p.first = beside ? 0 : 1;
     p.hq = c.hq;
     p.hkv = c.hkv;
@@ -643,6 +652,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.part_stride = shared_parts(c);
     p.part_off = c.prefix_splits;
     p.whole = c.whole ? 1 : 0;
+    p.set_rows = c.set_rows;
     p.beside = beside ? 1 : 0;
     p.scale_log2 = c.scale_log2;
     // bf16: a tile's two 64-dim halves as one box: dims (64 dims, rows, halves), strides
@@ -657,9 +667,9 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
                                                BS, 2, CU_TENSOR_MAP_SWIZZLE_128B)))
             return cudaErrorInvalidValue;
     }
-    const int64_t items = (int64_t)c.b.num_seqs * c.hkv * c.tail_splits;
+    const int64_t items = (int64_t)c.b.num_seqs * c.hkv * c.tail_splits * c.sets;
     int *const counter = p.out16 ? nullptr : c.counter;     // (no workspace where the only part is the output)
-    if ((int64_t)c.b.max_q_len * p.group > 8)
+    if (p.set_rows * p.group > 8)
         return c.fp8 ? launch<true, 2>(map[0], map[1], p, counter, items, st)
                      : launch<false, 2>(map[0], map[1], p, counter, items, st);
     return c.fp8 ? launch<true, 1>(map[0], map[1], p, counter, items, st)

@@ -80,37 +80,56 @@ class Batch:
                     x[self.tables[s, (self.lens[s] - 1) // BS], :, self.lens[s] % BS:] = nan
         self.scale = D ** -0.5
 
-    def call(self, out=None, **kw):
+    def call(self, out=None, pad=0, **kw):
+        """pad: entries without rows or context behind the batch."""
         if out is None:
             out = torch.full(self.q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
-        args = dict(cu_q_lens=None if (self.rows == 1).all() else i32(self.cu), max_q_len=int(max(self.rows.max(), 1)),
+        cu, lens = np.append(self.cu, [self.cu[-1]] * pad), np.append(self.lens, [0] * pad)
+        tables = np.concatenate([self.tables.reshape(self.B, self.width), np.full((pad, self.width), -7)])
+        args = dict(cu_q_lens=None if pad == 0 and (self.rows == 1).all() else i32(cu), max_q_len=int(max(self.rows.max(), 1)),
                     scale=self.scale, k_scale=self.ks, v_scale=self.vs, max_prefix_len=int(max([0, *self.prefix])),
                     max_tail_len=self.width * BS)
         args.update(kw)
-        pkv.paged_attention_shared_prefix(out, self.q, self.k, self.v, i32(self.tables).reshape(self.B, self.width),
-                                          i32(self.lens), i32(self.groups), i32(self.prefix), **args)
+        pkv.paged_attention_shared_prefix(out, self.q, self.k, self.v, i32(tables), i32(lens), i32(self.groups),
+                                          i32(self.prefix), **args)
         return out
 
     def reference(self, **kw):
         return osp.shared(f64(self.q), self.k64, self.v64, self.tables, self.lens, self.groups, self.prefix, self.scale,
                           cu=self.cu, fp8=self.fp8, **kw)
 
+    def ways(self, rows=None):
+        """Bounds and padding with which the call goes each of its ways."""
+        return ways_of(self.B, len(self.q), rows or int(max(self.rows.max(), 1)), len(self.prefix), self.hq, self.hkv,
+                       int(max([0, *self.prefix])), self.width * BS, self.fp8)
+
     def apart(self):
-        """A bound on the prefixes from which on a kernel of its own attends them (a batch
-        with less to read does without, as do groups of few sequences)."""
-        few = (1536 << 10) * len(self.prefix) // max(1, self.B)
-        return max(int(max([0, *self.prefix])), 16 + ((64 << 10) + few) // (self.B * self.hkv))
+        """Bounds with which a kernel of its own attends the prefixes."""
+        return self.ways()[1]
 
     def check(self, flags=0, got=None, ref=None, **kw):
         exp, tol, f = ref or self.reference()
         assert f == flags
-        if got is None and "max_prefix_len" not in kw:
-            self.check(flags, ref=(exp, tol, f), max_prefix_len=self.apart(), **kw)
+        if got is None and "max_prefix_len" not in kw and "max_tail_len" not in kw:
+            for bounds in self.ways(kw.get("max_q_len")).values():
+                self.check(flags, ref=(exp, tol, f), **bounds, **kw)
         got = self.call(**kw) if got is None else got
         assert pkv.kv_last_device_status() == (5 if flags else 0)
         assert pkv.kv_last_device_status_flags() == flags
         compare(f64(got), exp, tol)
         return got
+
+
+def ways_of(B, R, n, groups, hq, hkv, prefix, tail, fp8):
+    found = {}
+    for pad in (0, 60, 600):
+        for t in (tail, 1 << 15, 1 << 18):
+            for p in (prefix, 1 << 12, 1 << 14, 1 << 16, 1 << 18):
+                sizes = (B + pad, R, n, groups, hq, hkv, max(p, prefix), max(t, tail))
+                if pkv.paged_attention_shared_prefix_workspace_size(*sizes) < 1 << 30:
+                    found.setdefault(pkv.paged_attention_shared_prefix_way(*sizes, fp8),
+                                     dict(max_prefix_len=sizes[6], max_tail_len=sizes[7], **({"pad": pad} if pad else {})))
+    return found
 
 
 def compare(got, exp, tol):
@@ -178,6 +197,15 @@ def test_rows_of_all_lengths():
     Batch([4, 3], [95, 260], [9, 1, 5, 20, 30, 77, 1, 4], rows=rows, hq=8, hkv=2, loose=1, fp8=True).check(max_q_len=9)
 
 
+def test_every_way_is_gone():
+    """The batches of the tests above reach whole contexts, prefixes apart, and both joined."""
+    for fp8 in (False, True):
+        for hq, hkv in ((1, 1), (8, 8), (16, 1), (64, 8)):
+            assert set(ways_of(8, 8, 1, 2, hq, hkv, 100, 208, fp8)) == {0, 1}
+        for n, hq, hkv in ((20, 8, 2), (3, 16, 1)):
+            assert set(ways_of(7, 7 * n, n, 2, hq, hkv, 500, 700, fp8)) == {0, 1, 2}
+
+
 def test_long_prefix_of_many_parts():
     b = Batch([20], [40000], np.arange(1, 21), hq=8, hkv=1, seed=3)
     b.check()
@@ -194,15 +222,19 @@ def test_many_items_a_cta(hq, hkv, rows, fp8):
     tails = rng.integers(rows, 1100, n)
     tails[::7] = rows
     b = Batch([n // 3, 0, n - n // 3 - 2], [330, 40, 97], tails, rows=rows, hq=hq, hkv=hkv, fp8=fp8, loose=2, seed=rows)
-    first = b.check(max_prefix_len=b.apart()).view(torch.int16).clone()
-    for _ in range(3):
-        assert torch.equal(b.call(max_prefix_len=b.apart()).view(torch.int16), first)
-    b.check(max_prefix_len=330)
+    ref = b.reference()
+    for bounds in b.ways().values():
+        first = b.check(ref=ref, **bounds).view(torch.int16).clone()
+        for _ in range(3):
+            assert torch.equal(b.call(**bounds).view(torch.int16), first)
 
 
 def test_more_parts_than_lanes():
     """A prefix and a tail of more parts than the merge's warp has lanes."""
     b = Batch([12], [30000], [4000, 70000, 3] + [20] * 9, hq=4, hkv=1, seed=12)
+    b.check()
+    b = Batch([1], [30000], [900], hq=4, hkv=1, seed=13)
+    assert 0 in b.ways()
     b.check()
 
 
@@ -217,7 +249,7 @@ def test_caches_past_four_gigabytes():
     b.tables = np.where(b.tables >= 0, b.tables + nb - b.nb, b.tables)
     b.nb = nb
     b.check(ref=ref, max_prefix_len=600)
-    b.check(ref=ref, max_prefix_len=b.apart())
+    b.check(ref=ref, **b.apart())
 
 
 def test_sharp_scores():
@@ -239,6 +271,17 @@ def test_without_groups(rows, hq, hkv, fp8):
         b = Batch([], [], tails, before=6, rows=rows, hq=hq, hkv=hkv, fp8=fp8, seed=rows)
         b.lens[2] = 0
         b.check(max_tail_len=max(tails))
+        b.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (2, 8, 1), (3, 16, 2), (9, 8, 1)])
+def test_many_padded_entries(rows, hq, hkv, fp8):
+    """Every third of 200 sequences without a context: zeros, whichever CTA comes upon it."""
+    tails = np.random.default_rng(rows).integers(rows, 300, 200)
+    for groups in (([], []), ([50, 60], [40, 100])):
+        b = Batch(*groups, tails, before=200 - sum(groups[0]), rows=rows, hq=hq, hkv=hkv, fp8=fp8, seed=rows)
+        b.lens[::3] = 0
         b.check()
 
 
@@ -264,8 +307,8 @@ def test_padded_and_bad_sequences():
     groups = b.groups
     for bad in ([0, 4, 8, 12], [-1, 4, 8, 11], [0, 4, 99, 11]):
         b.groups = np.array(bad)
-        for bound in (100, b.apart()):
-            got = b.call(max_prefix_len=bound)
+        for bounds in b.ways().values():
+            got = b.call(**bounds)
             assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 4
             assert np.isfinite(f64(got)).all()
     b.groups = groups
@@ -283,8 +326,8 @@ def test_blocks_outside_the_pool():
         b = Batch([3, 3], [200, 150], [20, 30, 40, 50, 60, 70], hq=8, hkv=2)
         exp, tol, _ = b.reference()
         b.tables[0, 3 if where == "prefix" else 13] = b.nb + 5
-        for bound in (200, b.apart()):
-            got = b.call(max_prefix_len=bound)
+        for bounds in b.ways().values():
+            got = b.call(**bounds)
             assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 1
             first = 3 if where == "prefix" else 1
             compare(f64(got)[first:], exp[first:], tol[first:])
@@ -297,8 +340,8 @@ def test_queries_that_are_not_finite(bad, where):
     b = Batch([4, 3], [200, 90], [20, 30, 40, 5, 7, 9, 11], hq=8, hkv=2)
     exp, tol, _ = b.reference()
     b.q[where, 3, 17] = bad
-    for bound in (200, b.apart()):
-        got = f64(b.call(max_prefix_len=bound))
+    for bounds in b.ways().values():
+        got = f64(b.call(**bounds))
         assert pkv.kv_last_device_status() == 0
         assert np.isnan(got[where, 3]).all()
         got[where, 3] = exp[where, 3]
@@ -341,14 +384,14 @@ def test_agrees_with_decode_over_the_whole_context():
 
 def test_on_another_stream_and_twice_at_once():
     b, c = Batch([9], [900], np.arange(1, 10) * 30, seed=1), Batch([5, 5], [300, 2000], np.arange(1, 11), seed=2)
-    far = {"max_prefix_len": b.apart()}
+    far = b.apart()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
     for _ in range(3):
         with torch.cuda.stream(s1):
             x = b.call(**far)
         with torch.cuda.stream(s2):
-            y = c.call(max_prefix_len=c.apart())
+            y = c.call(**c.apart())
             y2 = c.call()
         z = b.call(stream=s2, out=torch.full(b.q.shape, 77.0, dtype=torch.bfloat16, device="cuda"), **far)
         torch.cuda.synchronize()
