@@ -177,7 +177,7 @@ void choose(SharedCall &c, int32_t max_tail_len)
 void plan(SharedCall &c, int32_t max_tail_len)
 {
     const int64_t groups = c.b.num_groups;
-    c.set_rows = (int)std::min<int64_t>(c.b.max_q_len, TAIL_COLS / (c.hq / c.hkv));
+    c.set_rows = (int)(TAIL_COLS / (c.hq / c.hkv));
     c.sets = (c.b.max_q_len - 1) / c.set_rows + 1;
     c.mean_sets = std::ceil(std::max(1.0, (double)c.b.total_rows / std::max(1, c.b.num_seqs)) / c.set_rows);
     choose(c, max_tail_len);
@@ -189,7 +189,7 @@ void plan(SharedCall &c, int32_t max_tail_len)
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((keys + BS - 1) / BS, INT32_MAX / BS));
     if (c.whole) {
         const double each = (double)c.b.num_seqs * c.hkv * c.mean_sets;
-        const double ctas = c.set_rows * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
+        const double ctas = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
         const int64_t most = std::min<int64_t>(256, (blocks + 11) / 12);
         double best = 0;
         for (int64_t n = 1; n <= most; n += 1 + n / 16) {

@@ -67,7 +67,7 @@ struct TailParams {
     int *counter;                    // the next item, set by the kernel before; null: a CTA takes every grid-th
     int first;                       // ... and its first item is its own number
     int direct;                      // one part and one set of rows a sequence: its items are found without a walk
-    int set_rows;                    // rows of a sequence in an item
+    int set_log2;                    // rows of a sequence in an item, a power of two
     int hq, hkv, group, num_blocks, part_blocks, part_stride, part_off;
     int whole;                       // contexts from their first key on, the prefix through the group's first row
     int beside;                      // launched to run beside the kernel before, whose inputs were complete too
@@ -116,7 +116,7 @@ __device__ __forceinline__ void load_window(const TailParams &p, TailWindow &w, 
         if (w.q.state == SEQ_OK && w.q.n > 0) {
             const int blocks = (w.q.L - (p.whole ? 0 : w.q.P) + BS - 1) / BS;
             w.ns = (blocks + p.part_blocks - 1) / p.part_blocks;
-            w.sets = (w.q.n + p.set_rows - 1) / p.set_rows;
+            w.sets = (w.q.n + (1 << p.set_log2) - 1) >> p.set_log2;
         }
     }
     w.incl = w.ns * p.hkv * w.sets;
@@ -231,14 +231,14 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                 s = w.w0 + at;
                 P = __shfl_sync(0xffffffffu, w.q.P, at);
                 first = __shfl_sync(0xffffffffu, w.q.first, at);
-                // (set i of a sequence's rows: rows i x set_rows on, whose keys end where those of
-                // its last row do; the parts are those of the whole sequence)
+                // (the rows of set i of a sequence begin at i << set_log2, and their keys end where
+                // those of the last one do; the parts are those of the whole sequence)
                 const int n = __shfl_sync(0xffffffffu, w.q.n, at), sets = __shfl_sync(0xffffffffu, w.sets, at);
-                const int i0 = r % sets * p.set_rows, keys = __shfl_sync(0xffffffffu, w.q.L, at) - (p.whole ? 0 : P);
+                it.g = sets == 1 ? r : r / sets;
+                const int i0 = (r - it.g * sets) << p.set_log2, keys = __shfl_sync(0xffffffffu, w.q.L, at) - (p.whole ? 0 : P);
                 it.row0 = __shfl_sync(0xffffffffu, w.q.row0, at) + i0;
-                it.n = min(p.set_rows, n - i0);
+                it.n = min(1 << p.set_log2, n - i0);
                 it.L = keys - n + i0 + it.n;
-                it.g = r / sets;
                 it.b0 = part * p.part_blocks;
                 it.nb = min((keys + BS - 1) / BS, it.b0 + p.part_blocks) - it.b0;
                 it.slot = p.part_off + part;
@@ -652,7 +652,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.part_stride = shared_parts(c);
     p.part_off = c.prefix_splits;
     p.whole = c.whole ? 1 : 0;
-    p.set_rows = c.set_rows;
+    for (p.set_log2 = 0; 1 << p.set_log2 < c.set_rows;) ++p.set_log2;
     p.beside = beside ? 1 : 0;
     p.scale_log2 = c.scale_log2;
     // bf16: a tile's two 64-dim halves as one box: dims (64 dims, rows, halves), strides
@@ -669,7 +669,7 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     }
     const int64_t items = (int64_t)c.b.num_seqs * c.hkv * c.tail_splits * c.sets;
     int *const counter = p.out16 ? nullptr : c.counter;     // (no workspace where the only part is the output)
-    if (p.set_rows * p.group > 8)
+    if (std::min(c.b.max_q_len, c.set_rows) * p.group > 8)
         return c.fp8 ? launch<true, 2>(map[0], map[1], p, counter, items, st)
                      : launch<false, 2>(map[0], map[1], p, counter, items, st);
     return c.fp8 ? launch<true, 1>(map[0], map[1], p, counter, items, st)

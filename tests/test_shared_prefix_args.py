@@ -69,6 +69,22 @@ def test_attention_sizes_its_workspace_for_any_bounds(mp, mt, nq, fp8):
     assert pkv.paged_attention_shared_prefix_workspace_size(4, 4 * nq, nq, 2, 24, 7, mp, mt) == 0
 
 
+@pytest.mark.parametrize("sizes,fp8,way", [
+    ((4, 4, 1, 1, 8, 2, 256, 64), False, 0), ((64, 64, 1, 1, 64, 8, 32768, 1000), False, 1),
+    ((64, 64, 1, 1, 64, 8, 32768, 1000), True, 1), ((52, 364, 7, 1, 16, 2, 29, 11260), False, 2),
+    ((152, 608, 4, 2, 32, 4, 38, 210), False, 0), ((6, 6, 1, 0, 8, 2, 4096, 4096), False, 0), ((6, 6, 1, 2, 8, 2, 15, BIG), True, 0),
+    ((65535, BIG, BIG, 65535, 16, 1, BIG, BIG), False, None), ((0, 4, 1, 1, 8, 2, 256, 64), False, -1),
+    ((4, 4, 0, 1, 8, 2, 256, 64), False, -1), ((4, 4, 1, 1, 9, 2, 256, 64), False, -1), ((4, 4, 1, 1, 8, 2, -1, 64), False, -1),
+    ((4, 4, 1, 1, 34, 2, 256, 64), False, -1)])
+def test_way(sizes, fp8, way):
+    got = pkv.paged_attention_shared_prefix_way(*sizes, fp8)
+    assert got == way if way is not None else got in (0, 1, 2)
+
+
+def test_way_refuses_a_type():
+    assert pkv.lib().paged_attention_shared_prefix_way(4, 4, 1, 1, 8, 2, 256, 64, 2) == -1
+
+
 @pytest.mark.parametrize("change", [dict(B=0), dict(R=0)])
 def test_attention_of_nothing(change):
     assert _call("paged_attention_shared_prefix", ATT, **change) == OK
