@@ -597,26 +597,6 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&v)[4][4], int lane)
     }
 }
 
-// Lane i of eight holds the 16-byte pieces v[0..7] of row i; afterwards v[j] is
-// piece i of row j.
-__device__ __forceinline__ void oct_transpose(uint32_t (&v)[8][4], int lane)
-{
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-        const bool up = lane & d;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j & d) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j][e] : v[j + d][e], d);
-                if (up) v[j][e] = got;
-                else v[j + d][e] = got;
-            }
-        }
-    }
-}
-
 // max of three fp32 values
 __device__ __forceinline__ float max3(float a, float b, float c)
 {

@@ -1488,42 +1488,38 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 const size_t pi = rh * p.max_splits + split;
                 const bool whole = !SHARED && nsplit == 1;
                 if constexpr (SHARED) {
-                    // Eight lanes exchange their rows' 16-byte pieces, so that they store
-                    // one row's 128 bytes together.  (A lane storing its own row's pieces
-                    // touches 32 rows with each instruction: an item's two tiles, 128
-                    // KiB, took 7 us that way.)
-                    const int rows = (i1 - i0) * G, r8 = r & ~7, lg = __ffs(G) - 1;   // (G is a power of two)
+                    // Four lanes exchange their rows' 16-byte pieces, so that they store one
+                    // row's 64 bytes together.  (A lane storing its own row's pieces touches
+                    // 32 rows with each instruction: an item's two tiles, 128 KiB, took 7 us
+                    // that way.)
+                    const int rows = (i1 - i0) * G, r4 = r & ~3, lg = __ffs(G) - 1;   // (G is a power of two)
                     const size_t head_step = (size_t)p.max_splits * D, row_step = head_step * p.hq;
-                    float *const to = p.part_o + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * head_step +
-                                      (size_t)split * D + (lane & 7) * 4;
+                    const size_t rh4 = (size_t)(row0 + i0 + (r4 >> lg)) * p.hq + g * G + (r4 & (G - 1));
+                    float *to = p.part_o + rh4 * head_step + (size_t)split * D + (lane & 3) * 4;
                     const float by = p.out16 ? (l == 0.f ? 0.f : vsc / l) : vsc;
-                    __nv_bfloat16 *const to16 = p.out16 + ((size_t)(row0 + i0 + (r8 >> lg)) * p.hq + g * G + (r8 & (G - 1))) * D +
-                                                (lane & 7) * 4;
+                    __nv_bfloat16 *to16 = p.out16 + rh4 * D + (lane & 3) * 4;
                     if ((r & ~31) < rows) {      // (a warp without rows stores nothing)
                         // (one copy of the code, which runs once an item: unrolled, its fetch
                         // took longer, 75 us against 60 for 73 sequences x 4 rows x 8 heads)
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float o[32];
-                            tmem_ld32(tO(gi) + lane_base + c * 32, o);
-                            uint32_t v[8][4];
+                        for (int c = 0; c < 8; ++c, to += 16, to16 += 16) {
+                            float o[16];
+                            tmem_ld16(tO(gi) + lane_base + c * 16, o);
+                            uint32_t v[4][4];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e >> 2][e & 3] = __float_as_uint(o[e] * by);
-                            oct_transpose(v, lane);
-                            if (p.out16) {
+                            for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = __float_as_uint(o[e] * by);
+                            quad_transpose(v, lane);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    if (r8 + j < rows)
-                                        *reinterpret_cast<uint2 *>(to16 + ((size_t)(j >> lg) * p.hq + (j & (G - 1))) * D + c * 32) =
-                                            make_uint2(pack_bf16(__uint_as_float(v[j][0]), __uint_as_float(v[j][1])),
-                                                       pack_bf16(__uint_as_float(v[j][2]), __uint_as_float(v[j][3])));
-                                continue;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (r8 + j < rows)
-                                    *reinterpret_cast<uint4 *>(to + (j >> lg) * row_step + (j & (G - 1)) * head_step + c * 32) =
+                            for (int j = 0; j < 4; ++j) {
+                                if (r4 + j >= rows) continue;
+                                if (p.out16)
+                                    *reinterpret_cast<uint2 *>(to16 + ((size_t)(j >> lg) * p.hq + (j & (G - 1))) * D) =
+                                        make_uint2(pack_bf16(__uint_as_float(v[j][0]), __uint_as_float(v[j][1])),
+                                                   pack_bf16(__uint_as_float(v[j][2]), __uint_as_float(v[j][3])));
+                                else
+                                    *reinterpret_cast<uint4 *>(to + (j >> lg) * row_step + (j & (G - 1)) * head_step) =
                                         make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+                            }
                         }
                     }
                     if (row_valid && !p.out16) *reinterpret_cast<float2 *>(p.part_ml + pi * 2) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
