@@ -216,7 +216,7 @@ struct PrefillParams {
 // max_splits + part).  The parts are tiles_per_split KV tiles, so the items are
 // nearly equal and each CTA finds its own, without a list (see SharedItems).
 // joined: the sequences' own tails are items too, causal, in parts of tail_tiles tiles
-// and with results from part tail_at on; else the decode kernel attends them.
+// and with results from part tail_at on; else a kernel of their own attends them.
 struct PrefixParams : PrefillParams {
     SharedBatch b;
     int groups, seq0, sources;   // the groups, from seq0 (a multiple of 32) on the sequences if joined; in all
@@ -707,7 +707,7 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
 }
 
 // How many CTAs take items (C above; the same in every CTA); `w` gets the first
-// window.  The others leave their SMs to the tails, which the decode kernel reads
+// window.  The others leave their SMs to the tails, which a kernel of their own reads
 // meanwhile: an SM without a CTA of this kernel reads decode_sm_bytes of K/V in one
 // KV tile's time, all together at most bytes_per_tile, and what is left afterwards
 // is read at that rate.  Items are nearly equal, so only the least C for each number

@@ -1,10 +1,10 @@
 // shared_tail.cu -- each sequence's own keys behind a prefix that a group shares, or
 // whole contexts where no kernel of its own attends the prefixes (sm_103a).
 //
-// A work item is (sequence, part of its keys, KV head).  Its n rows x G heads, at most
-// 16 columns, are attended as in the decode kernel: S^T[16 tokens][columns] = K Q^T and
-// O^T[128][columns] += V^T P^T with mma.sync, one 16-token block a warp at a time, the
-// softmax online.  What differs is how the work reaches the SM.  This kernel runs
+// A work item is (sequence, set of its rows, part of its keys, KV head).  A set's rows x G
+// heads, at most 16 columns, are attended as in the decode kernel: S^T[16 tokens][columns]
+// = K Q^T and O^T[128][columns] += V^T P^T with mma.sync, one 16-token block a warp at a
+// time, the softmax online.  What differs is how the work reaches the SM.  This kernel runs
 // beside the one that attends the prefixes, on the few SMs that one leaves free, and
 // an SM takes in at most 64 bytes a clock, 130 GB/s: so it must never stop loading.  A
 // kernel with a CTA an item had its place in the batch, its block ids and its first
@@ -17,6 +17,13 @@
 //    that runs on across items: the next item's first blocks are there when the last
 //    one's end.  (A ring of its own for each warp: a barrier's phases alternate between
 //    two parities, so a warp has to see every phase of the stages that it waits for.)
+//  * The next item is asked for when ASK_BLOCKS of the current one's blocks are left, not
+//    at its start: an item that waits behind a long one could be another CTA's.  With items
+//    of one part and one set, their sequence follows from their number; else the producer
+//    walks over the batch, 32 sequences a step, 0.9 us each.  (Together: 48 sequences of 100
+//    to 2,500 tokens beside two prefixes, fp8, 56.6 to 53.8 us for the call; 193 of one KV
+//    head 30.3 to 26.9.  The counter for whole contexts too, where there are more items than
+//    CTAs: 101 sequences of up to 12,356 tokens, fp8, 129 to 104.)
 //  * The consumers' states are joined one after another through shared memory,
 //    signalled by mbarriers, while warps that are done begin the next item.
 //  * Results are partial ones, joined by the merge kernel, or the output itself.
