@@ -747,7 +747,7 @@ __device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
     const int at = __ffs(__ballot_sync(0xffffffffu, t <= best)) - 1;
-    return max(1, min(p.grid_ctas, (int)__shfl_sync(0xffffffffu, c, at)));
+    return min(p.grid_ctas, ((int)__shfl_sync(0xffffffffu, c, at) + 1) & ~1);
 }
 
 // (the fp8 variant declares 512 threads so that registers stay <= 128, which 15
@@ -1851,6 +1851,11 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     p.decode_sm_bytes = (float)(DECODE_SM_BYTES_PER_TILE_TIME * p.tile_keys / 64.0);
     p.q_box_bytes = tpt * G * 128;
     p.grid_ctas = (int)std::min<int64_t>(c.prefix_items + c.tail_items, p.num_sms);
+    // (in pairs, which share a TPC: the SMs that are left to the tails are then neighbours of
+    // one another.  The tails take all that a TPC takes in: a CTA of this kernel beside them
+    // ended 5 us of 65 late; 122 sequences of 600 to 4,300 tokens in three groups, fp8: 163
+    // to 156 us)
+    p.grid_ctas += p.grid_ctas & 1;
     p.one_wave = c.prefix_items <= p.num_sms;
     p.groups = c.prefix_splits > 0 ? c.b.num_groups : 0;
     p.joined = c.joined ? 1 : 0;
@@ -1872,7 +1877,7 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
         return cudaErrorInvalidValue;
     auto launch = [&](auto kernel, cudaError_t smem_ok, int threads, int smem) {
         if (smem_ok != cudaSuccess) return smem_ok;
-        return pkv_host::launch_ex(kernel, dim3((unsigned)p.grid_ctas), dim3(threads), smem, st, true, qm, km, vm, p);
+        return pkv_host::launch_clusters(kernel, dim3((unsigned)p.grid_ctas), dim3(threads), smem, st, true, 2, qm, km, vm, p);
     };
     if (c.fp8)
         return launch(prefill_kernel<true, false, true>,
