@@ -24,7 +24,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     const float *part_o, *part_ml;
     int hq, prefix_splits, splits;         // splits: of prefix and tail together
-    int tile_keys, prefix_tiles, tail_part_blocks, whole;
+    int tile_keys, prefix_tiles, tail_part_blocks, fine_from, fine_blocks, whole;
 };
 
 // Joins a row's parts, those of its group's prefix and those of its own tail, by the
@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
     }
     const int P = p.whole ? 0 : w.P;          // keys that have parts of their own
     const int KT = (P + p.tile_keys - 1) / p.tile_keys, np = KT ? (KT + p.prefix_tiles - 1) / p.prefix_tiles : 0;
-    const int blocks = (w.L - P + BS - 1) / BS, nt = (blocks + p.tail_part_blocks - 1) / p.tail_part_blocks;
+    const int blocks = (w.L - P + BS - 1) / BS, part = s < p.fine_from ? p.tail_part_blocks : p.fine_blocks;
+    const int nt = (blocks + part - 1) / part;
     const size_t base = ((size_t)row * p.hq + h) * p.splits;
     auto at = [&](int i) { return base + (i < np ? i : p.prefix_splits + i - np); };
     const int n = np + nt;
@@ -131,7 +132,11 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // least 36 blocks (48 sequences of 100 to 2,500 tokens beside two prefixes, fp8: 55.3 us
 // with 24, 53.1 with 40, 56.0 with 64, 63.5 with 100; 64 of 20 to 1,000 beside one, bf16:
 // 88.5 with 24, 84.1 with 32, 82.6 with 40, 81.0 whole), of two fifths of what gives two
-// items a CTA, and of at most 96 up to 8K tokens, 128 up to 64K, 256 beyond.
+// items a CTA, and of at most 96 up to 8K tokens, 128 up to 64K, 256 beyond.  The last
+// fifth of the sequences has parts of half the length, so that the last items are short
+// (that batch in fp8: 52.6 to 51.7 us, 32 sequences x 4 rows 49.2 to 47.8; a third or half
+// of the sequences gain less; contexts that are one part lose 1 us by it, and so do whole
+// contexts, up to 4 us of 15).
 //
 constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
 constexpr double SET_US = 1.5, FIRST_US = 0.14, AGAIN_US = 0.09, FIRST8_US = 0.17, AGAIN8_US = 0.06;
@@ -181,6 +186,8 @@ void plan(SharedCall &c, int32_t max_tail_len)
     c.sets = (c.b.max_q_len - 1) / c.set_rows + 1;
     c.mean_sets = std::ceil(std::max(1.0, (double)c.b.total_rows / std::max(1, c.b.num_seqs)) / c.set_rows);
     choose(c, max_tail_len);
+    c.fine_from = INT32_MAX;
+    c.fine_blocks = 1;
     c.prefix_splits = 0;
     c.prefix_items = c.tail_items = 0;
     if (!c.whole) pkv_prefill::plan_prefixes(c, max_tail_len);
@@ -207,6 +214,11 @@ void plan(SharedCall &c, int32_t max_tail_len)
         c.tail_splits = (int)(part >= most ? (blocks + most - 1) / most : std::max<int64_t>(1, blocks / part));
     }
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
+    if (!c.whole && c.tail_splits > 1) {
+        c.fine_from = (int)((int64_t)c.b.num_seqs * 4 / 5);
+        c.fine_blocks = (c.tail_part_blocks + 1) / 2;
+        c.tail_splits = (int)((blocks + c.fine_blocks - 1) / c.fine_blocks);
+    }
 }
 
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
@@ -352,8 +364,8 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (!c.joined && pkv_shared_tail::launch_tails(c, prefixes, st) != cudaSuccess) return KV_ERR_CUDA;
     if (!o_bytes) return KV_OK;
     const MergeParams m = {c.b, static_cast<__nv_bfloat16 *>(out), c.part_o, c.part_ml, num_q_heads, c.prefix_splits,
-                           shared_parts(c), c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks,
-                           c.whole ? 1 : 0};
+                           shared_parts(c), c.big ? 128 : 64, c.prefix_tiles, c.tail_part_blocks, c.fine_from,
+                           c.fine_blocks, c.whole ? 1 : 0};
     const dim3 grid(total_q_tokens, (num_q_heads + MERGE_WARPS - 1) / MERGE_WARPS);
     return pkv_host::launch_ex(shared_merge_kernel, grid, dim3(32 * MERGE_WARPS), 0, st, true, m) == cudaSuccess
                ? KV_OK : KV_ERR_CUDA;

@@ -22,6 +22,7 @@ struct SharedCall {
     int prefix_splits, prefix_tiles;  // parts of a prefix at most, and KV tiles a part
     int64_t prefix_items, tail_items; // work items of prefixes, and of joined tails, at most
     int tail_splits, tail_part_blocks;
+    int fine_from, fine_blocks;       // sequences from fine_from on have shorter parts, of fine_blocks
     int sets, set_rows;               // the tails' kernel takes a sequence's rows in sets: how many at most
     double mean_sets;                 // ... and for a sequence of as many rows as there are on average
     float scale_log2;

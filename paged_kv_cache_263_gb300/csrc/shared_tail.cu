@@ -75,7 +75,7 @@ struct TailParams {
     int first;                       // ... and its first item is its own number
     int direct;                      // one part and one set of rows a sequence: its items are found without a walk
     int set_log2;                    // rows of a sequence in an item, a power of two
-    int hq, hkv, group, num_blocks, part_blocks, part_stride, part_off;
+    int hq, hkv, group, num_blocks, part_blocks, fine_from, fine_blocks, part_stride, part_off;
     int whole;                       // contexts from their first key on, the prefix through the group's first row
     int beside;                      // launched to run beside the kernel before, whose inputs were complete too
     float scale_log2;
@@ -122,7 +122,8 @@ __device__ __forceinline__ void load_window(const TailParams &p, TailWindow &w, 
         if (w.q.state == SEQ_BAD) flag(ST_BAD_LEN);
         if (w.q.state == SEQ_OK && w.q.n > 0) {
             const int blocks = (w.q.L - (p.whole ? 0 : w.q.P) + BS - 1) / BS;
-            w.ns = (blocks + p.part_blocks - 1) / p.part_blocks;
+            const int part = s < p.fine_from ? p.part_blocks : p.fine_blocks;
+            w.ns = (blocks + part - 1) / part;
             w.sets = (w.q.n + (1 << p.set_log2) - 1) >> p.set_log2;
         }
     }
@@ -246,8 +247,9 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                 it.row0 = __shfl_sync(0xffffffffu, w.q.row0, at) + i0;
                 it.n = min(1 << p.set_log2, n - i0);
                 it.L = keys - n + i0 + it.n;
-                it.b0 = part * p.part_blocks;
-                it.nb = min((keys + BS - 1) / BS, it.b0 + p.part_blocks) - it.b0;
+                const int part_blocks = s < p.fine_from ? p.part_blocks : p.fine_blocks;
+                it.b0 = part * part_blocks;
+                it.nb = min((keys + BS - 1) / BS, it.b0 + part_blocks) - it.b0;
                 it.slot = p.part_off + part;
                 it.valid = 1;
             }
@@ -656,6 +658,8 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
     p.group = c.hq / c.hkv;
     p.num_blocks = c.num_blocks;
     p.part_blocks = c.tail_part_blocks;
+    p.fine_from = c.fine_from;
+    p.fine_blocks = c.fine_blocks;
     p.part_stride = shared_parts(c);
     p.part_off = c.prefix_splits;
     p.whole = c.whole ? 1 : 0;
