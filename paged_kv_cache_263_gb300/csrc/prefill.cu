@@ -1765,11 +1765,23 @@ cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret
 // One query tile a CTA (128-key tiles) when the rows x heads of a group, or without
 // groups of a sequence, fill one tile on average, over a bf16 cache.
 //
-// The tails apart: the number of parts minimises the modelled end of prefixes, tails
-// and merge (the terms of shared_ctas, from the caller's bounds): with several groups
-// their prefixes are taken to be ragged, half as long as the longest.
+// The tails apart: the number of parts minimises the modelled end of prefixes and tails, in
+// us, prefixes taken to be nearly as long as the bound and tails PART_TAIL of it.  Items run
+// in waves over the CTAs, PART_TILE_US a tile (PART_BIG_US, PART_TILE8_US) and PART_ITEM_US
+// beside; the tails meanwhile on the other SMs, PART_SM_MB a us each, from PART_START_US on.
+// What they have left is read at PART_ALL_MB a us, but begins anew on every SM and ends
+// unevenly: PART_LEFT_US.  So a call is the shortest whose tails end with the prefixes.
+// Each part costs the merge.
+// (Measured with 15 numbers of parts each, 80 drawn batches: the choice is 1.8 % off the
+// best number -- fitted on one half, 3 % on the other -- and the terms of shared_ctas, which
+// leave out PART_LEFT_US, 12 %: 48 sequences of 100 to 2,500 tokens beside two prefixes to
+// 8,192, fp8, 46.0 us with 4 parts, 51.9 with 7; 107 of 6 groups to 10,996, fp8, 59.9 with
+// 4, 87.8 with 8.)
 // Joined: parts of a third of what an SM gets of all tiles, tails taken to be half as
 // long as the longest.
+constexpr double PART_TILE_US = 1.03, PART_BIG_US = 0.9, PART_TILE8_US = 1.02, PART_ITEM_US = 7, PART_ITEM8_US = 4.2;
+constexpr double PART_SM_MB = 0.08, PART_SM8_MB = 0.06, PART_ALL_MB = 5.9, PART_ALL8_MB = 6.5, PART_START_US = 9,
+                 PART_LEFT_US = 10.4, PART_MEAN = 0.957, PART_MEAN_ONE = 0.917, PART_TAIL = 0.56;
 void plan_prefixes(SharedCall &c, int64_t max_tail)
 {
     const int G = c.hq / c.hkv, ng = std::max(1, c.b.num_groups);
@@ -1792,22 +1804,22 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
         c.tail_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_seqs * (item_rows - 1)) / item_rows * c.hkv * c.tail_splits;
         if (W) c.prefix_tiles = (int)std::min<int64_t>(len, W);
     } else if (W) {
-        const double per_tile = BYTES_PER_TILE_TIME * tile_keys / 64.0;
-        const double per_sm = DECODE_SM_BYTES_PER_TILE_TIME * tile_keys / 64.0;
-        // (and the merge's trips to memory: eight parts a trip)
-        const double merge = (double)c.b.total_rows * c.hq * (D + 2) * 4.0 * 2.0 / per_tile + 0.12 * 64.0 / tile_keys;
-        const double tail = 0.5 * c.b.num_seqs * (double)max_tail * c.mean_sets * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
-        const double mean = ng > 1 ? 0.5 : 1.0;
+        const double tile = c.fp8 ? PART_TILE8_US : c.big ? PART_BIG_US : PART_TILE_US;
+        const double item = c.fp8 ? PART_ITEM8_US : PART_ITEM_US, mean = W * (ng > 1 ? PART_MEAN : PART_MEAN_ONE);
+        const double per_sm = c.fp8 ? PART_SM8_MB : PART_SM_MB, all = c.fp8 ? PART_ALL8_MB : PART_ALL_MB;
+        const double tail = PART_TAIL * 1e-6 * c.b.num_seqs * (double)max_tail * c.mean_sets * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
         double best = 0;
         int pick = 0;
         for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
             const int len = (W - 1) / s + 1, parts = (W - 1) / len + 1;
-            const double items = problems * (1.0 + mean * (parts - 1));
-            const double each = std::min<double>(len, mean * W) + SHARED_ITEM_TILES, least = std::ceil(items / sms);
+            const double items = problems * std::max(1.0, mean / len), least = std::ceil(items / sms);
+            const double each = (ng > 1 ? std::min((double)len, std::max(1.0, mean)) : len) * tile + item;
             for (int w = 0; w < 4; ++w) {
                 const double ctas = std::ceil(items / (least + w)), chunk = (least + w) * each;
-                const double beside = std::min((sms - ctas) * per_sm, per_tile);
-                const double cost = chunk + std::max(0.0, tail - chunk * beside) / per_tile + parts * merge;
+                const double beside = std::min((sms - ctas) * per_sm, all);
+                const double left = std::max(0.0, tail - std::max(0.0, chunk - PART_START_US) * beside);
+                const double cost = chunk + (left > 0 ? PART_LEFT_US + left / all : 0) +
+                                    parts * (0.17 + 0.365e-4 * (double)c.b.total_rows * c.hq);
                 if (pick == 0 || cost < best) {
                     best = cost;
                     pick = s;
