@@ -1777,11 +1777,17 @@ cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret
 // leave out PART_LEFT_US, 12 %: 48 sequences of 100 to 2,500 tokens beside two prefixes to
 // 8,192, fp8, 46.0 us with 4 parts, 51.9 with 7; 107 of 6 groups to 10,996, fp8, 59.9 with
 // 4, 87.8 with 8.)
-// Joined: parts of a third of what an SM gets of all tiles, tails taken to be half as
-// long as the longest.
+// Joined: parts of so many tiles, of prefixes and tails alike, that the modelled end is the
+// earliest: the work of all items shared by the SMs and JOIN_LAST of the longest one, as
+// the last items end unevenly; and the merge of the parts.  (90 drawn batches with 10
+// lengths each: 3.3 % off the best length, 4.5 % when fitted on the other half, where a
+// third of an SM's tiles was 12 % off: 77 sequences x 7 rows x 16 heads with tails of 340
+// to 952 tokens 103 us with parts of 4 tiles, 56.5 with 12.)
 constexpr double PART_TILE_US = 1.03, PART_BIG_US = 0.9, PART_TILE8_US = 1.02, PART_ITEM_US = 7, PART_ITEM8_US = 4.2;
 constexpr double PART_SM_MB = 0.08, PART_SM8_MB = 0.06, PART_ALL_MB = 5.9, PART_ALL8_MB = 6.5, PART_START_US = 9,
                  PART_LEFT_US = 10.4, PART_MEAN = 0.957, PART_MEAN_ONE = 0.917, PART_TAIL = 0.56;
+constexpr double JOIN_TILE_US = 1.03, JOIN_BIG_US = 0.99, JOIN_TILE8_US = 1.22, JOIN_ITEM_US = 4, JOIN_LAST = 0.6,
+                 JOIN_PREFIX = 0.88, JOIN_TAIL = 0.61;
 void plan_prefixes(SharedCall &c, int64_t max_tail)
 {
     const int G = c.hq / c.hkv, ng = std::max(1, c.b.num_groups);
@@ -1797,8 +1803,25 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
     if (c.joined) {
         const int64_t Wt = std::max<int64_t>(1, (max_tail + tile_keys - 1) / tile_keys);
         const int64_t mine = ((int64_t)c.b.max_q_len + item_rows - 1) / item_rows;      // query items of a sequence
-        const double tiles = problems * W * (ng > 1 ? 0.5 : 1.0) + 0.5 * c.b.num_seqs * mine * c.hkv * Wt;
-        const int64_t len = std::max<int64_t>({4, (int64_t)(tiles / sms / 3.0), (W + 127) / 128, (Wt + 127) / 128});
+        const double tile = c.fp8 ? JOIN_TILE8_US : c.big ? JOIN_BIG_US : JOIN_TILE_US;
+        const double mean = std::max(1.0, JOIN_PREFIX * W), mean_tail = std::max(1.0, JOIN_TAIL * (double)Wt);
+        const double before = W ? problems : 0, behind = (double)c.b.num_seqs * mine * c.hkv;
+        const int64_t most = std::max<int64_t>(W, Wt), least = std::max<int64_t>((W + 127) / 128, (Wt + 127) / 128);
+        double best = 0;
+        int64_t len = 0;
+        for (int64_t n = least; n < most + most / 8 + 1; n += 1 + n / 8) {
+            const double p = (double)std::min<int64_t>(n, std::max(1, W)), t = (double)std::min(n, Wt);
+            const double items = before * std::max(1.0, mean / p) + behind * std::max(1.0, mean_tail / t);
+            const double work = (before * mean + behind * mean_tail) * tile + items * JOIN_ITEM_US;
+            const double longest = std::min((double)n, std::max(W ? mean : 0.0, mean_tail)) * tile + JOIN_ITEM_US;
+            const double parts = (W ? std::ceil(W / p) : 0.0) + std::ceil((double)Wt / t);
+            const double cost = std::max(work / sms + JOIN_LAST * longest, longest) +
+                                parts * (0.14 + 0.09e-4 * (double)c.b.total_rows * c.hq);
+            if (len == 0 || cost < best) {
+                best = cost;
+                len = n;
+            }
+        }
         c.tail_splits = (int)((Wt + len - 1) / len);
         c.tail_part_blocks = (int)(std::min(len, Wt) * (tile_keys / BS));
         c.tail_items = ((int64_t)c.b.total_rows + (int64_t)c.b.num_seqs * (item_rows - 1)) / item_rows * c.hkv * c.tail_splits;

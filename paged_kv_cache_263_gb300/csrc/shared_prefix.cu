@@ -100,18 +100,18 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // that reads it (fp8: FIRST8_US, AGAIN8_US).
 // apart: the prefixes in the chunk kernel's tiles, the tails beside it as above.  A block
 // of a prefix takes TILE_US for a query item (256 rows x heads; BIG_US for 128 where a
-// group has no more, over a bf16 cache; fp8 TILE8_US): twice the tiles' own time, as the
-// items and the prefixes are unequal.
+// group has no more, over a bf16 cache; fp8 TILE8_US): more than the tiles' own time, as
+// the items and the prefixes are unequal.
 // joined: the chunk kernel takes the tails as well, JOIN_US an item and less a block than
 // for prefixes, as each tail is read once.  Only for rows x heads of a sequence that are
 // more than 16: at 16 it lost (32 sequences x 4 rows: 62.5 us against 52.5).
 // ROOT_US: the last parts and the merge of long contexts, which are cut into about the
 // root of their blocks.
 //
-// Measured on 284 drawn batches, each way forced in turn: the costs' choice takes 2 % more
-// than the best way (fitted on one half of them, 3.5 % on the other); rules by sequences a
-// group and keys of prefix, with joined for all wide rows, took 3 % more for narrow rows
-// and 16 % for wide ones.  Some of them, us (rows x heads of a sequence):
+// Measured on 180 drawn batches, each way forced in turn: the costs' choice takes 1 % more
+// than the best way (2 % when fitted on the other half); rules by sequences a group and keys
+// of prefix, with joined for all wide rows, took 3 % more for narrow rows and 16 % for wide
+// ones.  Some of them, us (rows x heads of a sequence):
 //                                                        whole   apart   joined
 //   152 sequences x 32, prefixes to 600, tails to 200    27.6    47.3    47.2
 //   51 x 56, one prefix of 12K, tails to 180, fp8        205     45.2    62.1
@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // contexts, up to 4 us of 15).
 //
 constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
-constexpr double SET_US = 1.5, FIRST_US = 0.14, AGAIN_US = 0.09, FIRST8_US = 0.17, AGAIN8_US = 0.06;
-constexpr double TILE_US = 0.38, BIG_US = 0.34, TILE8_US = 0.47;
-constexpr double JOIN_US = 5.8, JOIN_TILE_US = 0.20, JOIN_BIG_US = 0.125, JOIN_TILE8_US = 0.27;
-constexpr double WHOLE_START_US = 5.6, APART_START_US = 12, JOINED_START_US = 13.7, ROOT_US = 0.13;
+constexpr double SET_US = 1.5, FIRST_US = 0.133, AGAIN_US = 0.077, FIRST8_US = 0.153, AGAIN8_US = 0.055;
+constexpr double TILE_US = 0.295, BIG_US = 0.215, TILE8_US = 0.32;
+constexpr double JOIN_US = 7.2, JOIN_TILE_US = 0.183, JOIN_BIG_US = 0.158, JOIN_TILE8_US = 0.227;
+constexpr double WHOLE_START_US = 6, APART_START_US = 11.7, JOINED_START_US = 9.2, ROOT_US = 0.157;
 constexpr double ITEM_US = 1.5, BLOCK_US = 0.15, PART_US = 0.15, MERGE_US = 4, COUNTER_US = 1.2;
 
 void choose(SharedCall &c, int32_t max_tail_len)
