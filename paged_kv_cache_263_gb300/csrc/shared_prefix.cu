@@ -128,17 +128,18 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // 1,056, fp8: 36 136.9, 64 128.5, 118 128.4.  Over 46 drawn batches the choice is 2 % off
 // the best of 12 lengths, and a fixed one of 16 blocks or two items a CTA 7 %.)
 //
-// Tails beside the prefixes run on few SMs at first, 10 items or more a CTA: parts of at
-// least 36 blocks (48 sequences of 100 to 2,500 tokens beside two prefixes, fp8: 55.3 us
-// with 24, 53.1 with 40, 56.0 with 64, 63.5 with 100; 64 of 20 to 1,000 beside one, bf16:
-// 88.5 with 24, 84.1 with 32, 82.6 with 40, 81.0 whole), of two fifths of what gives two
-// items a CTA, and of at most 96 up to 8K tokens, 128 up to 64K, 256 beyond.  The last
+// Tails beside the prefixes: parts of TAIL_ROOT times the root of their blocks, or of
+// TAIL_WANT of what gives TAIL_CTAS items where that is more, and of at most 256 (75 drawn
+// batches with 13 lengths each: 2 % off the best length; 48 sequences of 100 to 2,500 tokens
+// beside two prefixes, fp8: 55.3 us with 24 blocks, 53.1 with 40, 63.5 with 100; 64 of 20 to
+// 1,000 beside one, bf16: 88.5 with 24, 82.6 with 40, 81.0 whole).  The last
 // fifth of the sequences has parts of half the length, so that the last items are short
 // (that batch in fp8: 52.6 to 51.7 us, 32 sequences x 4 rows 49.2 to 47.8; a third or half
 // of the sequences gain less; contexts that are one part lose 1 us by it, and so do whole
 // contexts, up to 4 us of 15).
 //
 constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
+constexpr double TAIL_ROOT = 2.6, TAIL_WANT = 0.9;
 constexpr double SET_US = 1.5, FIRST_US = 0.133, AGAIN_US = 0.077, FIRST8_US = 0.153, AGAIN8_US = 0.055;
 constexpr double TILE_US = 0.295, BIG_US = 0.215, TILE8_US = 0.32;
 constexpr double JOIN_US = 7.2, JOIN_TILE_US = 0.183, JOIN_BIG_US = 0.158, JOIN_TILE8_US = 0.227;
@@ -208,10 +209,9 @@ void plan(SharedCall &c, int32_t max_tail_len)
             }
         }
     } else {
-        const int64_t most = blocks <= 512 ? 96 : blocks <= 4096 ? 128 : 256;
-        const int64_t want = (blocks * c.b.num_seqs * c.hkv + TAIL_CTAS - 1) / TAIL_CTAS;
-        const int64_t part = std::max<int64_t>(36, want * 2 / 5);
-        c.tail_splits = (int)(part >= most ? (blocks + most - 1) / most : std::max<int64_t>(1, blocks / part));
+        const double want = (double)blocks * c.b.num_seqs * c.hkv / TAIL_CTAS;
+        const double part = std::max(TAIL_ROOT * std::sqrt((double)blocks), TAIL_WANT * want);
+        c.tail_splits = (int)std::max<int64_t>({1, (int64_t)((double)blocks / part), (blocks + 255) / 256});
     }
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
     if (!c.whole && c.tail_splits > 1) {
