@@ -132,11 +132,10 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // TAIL_WANT of what gives TAIL_CTAS items where that is more, and of at most 256 (75 drawn
 // batches with 13 lengths each: 2 % off the best length; 48 sequences of 100 to 2,500 tokens
 // beside two prefixes, fp8: 55.3 us with 24 blocks, 53.1 with 40, 63.5 with 100; 64 of 20 to
-// 1,000 beside one, bf16: 88.5 with 24, 82.6 with 40, 81.0 whole).  The last
-// fifth of the sequences has parts of half the length, so that the last items are short
-// (that batch in fp8: 52.6 to 51.7 us, 32 sequences x 4 rows 49.2 to 47.8; a third or half
-// of the sequences gain less; contexts that are one part lose 1 us by it, and so do whole
-// contexts, up to 4 us of 15).
+// 1,000 beside one, bf16: 88.5 with 24, 82.6 with 40, 81.0 whole).  The last fifth of the
+// sequences has parts of half the length, so that the last items are short (the batch in
+// fp8: 52.6 to 51.7 us, 32 sequences x 4 rows 49.2 to 47.8; a third or half of the sequences
+// gain less; contexts that are one part lose 1 us by it, whole contexts up to 4 us of 15).
 //
 constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
 constexpr double TAIL_ROOT = 2.6, TAIL_WANT = 0.9;
