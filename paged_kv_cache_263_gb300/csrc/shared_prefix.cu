@@ -345,7 +345,9 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if (c.prefix_items > INT32_MAX / 64 || c.tail_items > INT32_MAX / 64) return KV_ERR_UNSUPPORTED;
     if (c.joined && ((int64_t)max_q_len * G / 128 + 1) * num_kv_heads * c.tail_splits > INT32_MAX / 64)
         return KV_ERR_UNSUPPORTED;
-    if ((int64_t)max_q_len * G > INT32_MAX / 32 || (int64_t)num_seqs * num_kv_heads * c.tail_splits > INT32_MAX / 2 / c.sets)
+    // (and 32 sequences in the tails' kernel, of which each may claim all rows)
+    if ((int64_t)max_q_len * G > INT32_MAX / 32 || tail_kernel_items(c) > INT32_MAX / 2 ||
+        (int64_t)std::min(max_q_len, total_q_tokens) / c.set_rows + 1 > INT32_MAX / 64 / num_kv_heads / c.tail_splits)
         return KV_ERR_UNSUPPORTED;
     // (the plan goes by the bounds as given, which the workspace's size goes by; no
     // length passes what a table row holds)

@@ -28,6 +28,13 @@ struct SharedCall {
     float scale_log2;
 };
 
+// items of the tails' kernel at most
+inline int64_t tail_kernel_items(const SharedCall &c)
+{
+    const int64_t sets = (int64_t)c.b.num_seqs * c.sets, by_rows = c.b.total_rows / c.set_rows + (int64_t)c.b.num_seqs;
+    return (sets < by_rows || c.sets == 1 ? sets : by_rows) * c.hkv * c.tail_splits;
+}
+
 // partial results of a row and head; the only one is the output itself
 inline int shared_parts(const SharedCall &c) { return c.prefix_splits + c.tail_splits; }
 

@@ -75,6 +75,7 @@ struct TailParams {
     int first;                       // ... and its first item is its own number
     int direct;                      // one part and one set of rows a sequence: its items are found without a walk
     int set_log2;                    // rows of a sequence in an item, a power of two
+    int most;                        // items at most, of a batch that keeps the rules
     int hq, hkv, group, num_blocks, part_blocks, fine_from, fine_blocks, part_stride, part_off;
     int whole;                       // contexts from their first key on, the prefix through the group's first row
     int beside;                      // launched to run beside the kernel before, whose inputs were complete too
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                                 make_uint4(0u, 0u, 0u, 0u);
                 }
             } else {
-                while (idx - w.base >= w.total && w.w0 + 32 < p.b.num_seqs) {
+                while (idx - w.base >= w.total && w.w0 + 32 < p.b.num_seqs && w.base + w.total <= p.most) {
                     w.base += w.total;
                     w.w0 += 32;
                     load_window(p, w, lane);
@@ -678,7 +679,8 @@ cudaError_t launch_tails(const SharedCall &c, bool beside, cudaStream_t st)
                                                BS, 2, CU_TENSOR_MAP_SWIZZLE_128B)))
             return cudaErrorInvalidValue;
     }
-    const int64_t items = (int64_t)c.b.num_seqs * c.hkv * c.tail_splits * c.sets;
+    const int64_t items = tail_kernel_items(c);
+    p.most = (int)items;
     int *const counter = p.out16 ? nullptr : c.counter;     // (no workspace where the only part is the output)
     if (std::min(c.b.max_q_len, c.set_rows) * p.group > 8)
         return c.fp8 ? launch<true, 2>(map[0], map[1], p, counter, items, st)

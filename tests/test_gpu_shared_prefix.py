@@ -197,6 +197,17 @@ def test_rows_of_all_lengths():
     Batch([4, 3], [95, 260], [9, 1, 5, 20, 30, 77, 1, 4], rows=rows, hq=8, hkv=2, loose=1, fp8=True).check(max_q_len=9)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (3, 16, 2), (5, 16, 1)])
+def test_rows_bound_far_above_their_number(rows, hq, hkv, fp8):
+    """max_q_len as loose as the number of all rows."""
+    tails = np.random.default_rng(rows).integers(rows, 400, 150)
+    b = Batch([60, 0, 70], [330, 40, 97], tails, rows=rows, hq=hq, hkv=hkv, fp8=fp8, loose=20, seed=rows)
+    b.lens[[5, 70, 149]] = 0
+    b.check(cu_q_lens=i32(b.cu), max_q_len=150 * rows, max_prefix_len=330, max_tail_len=b.width * BS)
+    b.check(max_q_len=40 * rows) if rows > 1 else None
+
+
 def test_every_way_is_gone():
     """The batches of the tests above reach whole contexts, prefixes apart, and both joined."""
     for fp8 in (False, True):

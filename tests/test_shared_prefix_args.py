@@ -85,6 +85,17 @@ def test_way_refuses_a_type():
     assert pkv.lib().paged_attention_shared_prefix_way(4, 4, 1, 1, 8, 2, 256, 64, 2) == -1
 
 
+@pytest.mark.parametrize("fp8", [0, 1])
+@pytest.mark.parametrize("hq,hkv,mp,mt", [(64, 8, 20000, 2000), (64, 8, 30000, 9000), (8, 8, 30000, 100), (16, 1, 30000, 16384)])
+def test_rows_bound_far_above_their_number(hq, hkv, mp, mt, fp8):
+    """max_q_len as loose as the number of all rows is no reason to refuse a batch."""
+    # (a prefix and a tail: at least two parts, so that a workspace is asked for)
+    assert pkv.paged_attention_shared_prefix_way(4096, 8192, 8192, 64, hq, hkv, mp, mt, fp8) in (1, 2)
+    st = _call("paged_attention_shared_prefix", ATT, B=4096, R=8192, nq=8192, G=64, hq=hq, hkv=hkv, mp=mp, mt=mt, mb=2000, nb=4096,
+               dt=fp8, ks=A, vs=A, ws=A + 16)
+    assert st == INVALID       # (the workspace's alignment)
+
+
 @pytest.mark.parametrize("change", [dict(B=0), dict(R=0)])
 def test_attention_of_nothing(change):
     assert _call("paged_attention_shared_prefix", ATT, **change) == OK
