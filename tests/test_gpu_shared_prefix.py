@@ -331,6 +331,24 @@ def test_more_rows_than_announced():
     b.check(flags=4, max_q_len=2, ref=b.reference(max_q=2))
 
 
+def test_rows_out_of_order():
+    """Offsets of rows that go back and forth: flagged, and the rows of a sequence that keeps the rules are right."""
+    rows, n = 4, 7
+    b = Batch([4, 3], [95, 260], [40, 33, 64, 29, 50, 31, 77], rows=rows, hq=8, hkv=2)
+    exp, tol, _ = b.reference()
+    back = b.cu.copy()
+    back[3] = back[2] - 2          # sequence 2 has -2 rows, sequence 3 six of which two are sequence 1's
+    claim = np.array([0, n * rows] * (n // 2 + 1))[:n + 1]
+    for cu, kept in ((back, range(0, rows)), (claim, ())):
+        for bounds in b.ways(n * rows).values():
+            if "pad" in bounds:
+                continue
+            got = f64(b.call(cu_q_lens=i32(cu), max_q_len=n * rows, **bounds))
+            assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 4
+            for r in kept:
+                compare(got[r], exp[r], tol[r])
+
+
 def test_blocks_outside_the_pool():
     """Flagged and not read; the other groups' rows are as ever."""
     for where in ("prefix", "tail"):
