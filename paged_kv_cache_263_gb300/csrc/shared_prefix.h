@@ -14,7 +14,7 @@ struct SharedCall {
     const int32_t *block_tables;
     const float *k_scale, *v_scale;   // fp8 cache
     float *part_o, *part_ml;          // [rows][hq][prefix_splits + tail_splits][128], [..][2] (max, sum)
-    int *counter;                     // of the tails' items: the kernel of the prefixes sets it to 0
+    int *counter;                     // of the tails' items, set by the kernel before theirs
     int hq, hkv, num_blocks;
     bool fp8, big;                    // big: one query tile a CTA, 128-key tiles
     bool joined;                      // the kernel of the prefixes attends the tails as well
