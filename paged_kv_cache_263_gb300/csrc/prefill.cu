@@ -1772,7 +1772,7 @@ cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret
 // What they have left is read at PART_ALL_MB a us, but begins anew on every SM and ends
 // unevenly: PART_LEFT_US.  So a call is the shortest whose tails end with the prefixes.
 // Each part costs the merge.
-// (Measured with 15 numbers of parts each, 80 drawn batches: the choice is 1.8 % off the
+// (Measured with 10 to 15 numbers of parts each, 95 drawn batches: the choice is 2 % off the
 // best number -- fitted on one half, 3 % on the other -- and the terms of shared_ctas, which
 // leave out PART_LEFT_US, 12 %: 48 sequences of 100 to 2,500 tokens beside two prefixes to
 // 8,192, fp8, 46.0 us with 4 parts, 51.9 with 7; 107 of 6 groups to 10,996, fp8, 59.9 with
@@ -1783,9 +1783,9 @@ cudaError_t status_word(uint32_t **at) { return cudaGetSymbolAddress(reinterpret
 // lengths each: 3.3 % off the best length, 4.5 % when fitted on the other half, where a
 // third of an SM's tiles was 12 % off: 77 sequences x 7 rows x 16 heads with tails of 340
 // to 952 tokens 103 us with parts of 4 tiles, 56.5 with 12.)
-constexpr double PART_TILE_US = 1.03, PART_BIG_US = 0.9, PART_TILE8_US = 1.02, PART_ITEM_US = 7, PART_ITEM8_US = 4.2;
-constexpr double PART_SM_MB = 0.08, PART_SM8_MB = 0.06, PART_ALL_MB = 5.9, PART_ALL8_MB = 6.5, PART_START_US = 9,
-                 PART_LEFT_US = 10.4, PART_MEAN = 0.957, PART_MEAN_ONE = 0.917, PART_TAIL = 0.56;
+constexpr double PART_TILE_US = 1.06, PART_BIG_US = 0.9, PART_TILE8_US = 1.03, PART_ITEM_US = 7.9, PART_ITEM8_US = 4.25;
+constexpr double PART_SM_MB = 0.081, PART_SM8_MB = 0.058, PART_ALL_MB = 6.5, PART_ALL8_MB = 5.5, PART_START_US = 9,
+                 PART_LEFT_US = 13.6, PART_MEAN = 0.956, PART_MEAN_ONE = 0.932, PART_TAIL = 0.58;
 constexpr double JOIN_TILE_US = 1.03, JOIN_BIG_US = 0.99, JOIN_TILE8_US = 1.22, JOIN_ITEM_US = 4, JOIN_LAST = 0.6,
                  JOIN_PREFIX = 0.88, JOIN_TAIL = 0.61;
 void plan_prefixes(SharedCall &c, int64_t max_tail)
@@ -1842,7 +1842,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
                 const double beside = std::min((sms - ctas) * per_sm, all);
                 const double left = std::max(0.0, tail - std::max(0.0, chunk - PART_START_US) * beside);
                 const double cost = chunk + (left > 0 ? PART_LEFT_US + left / all : 0) +
-                                    parts * (0.17 + 0.365e-4 * (double)c.b.total_rows * c.hq);
+                                    parts * (0.165 + 0.54e-4 * (double)c.b.total_rows * c.hq);
                 if (pick == 0 || cost < best) {
                     best = cost;
                     pick = s;
