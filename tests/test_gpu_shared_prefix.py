@@ -349,6 +349,27 @@ def test_rows_out_of_order():
                 compare(got[r], exp[r], tol[r])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_groups_that_claim_the_same_rows(rows, fp8):
+    """Offsets of groups that go back and forth, so that 33 groups of 65 have all rows: flagged, and no more is
+    done than a batch of so many groups and rows can need."""
+    n, ng = 300, 65
+    b = Batch([n], [330], np.random.default_rng(rows).integers(rows, 90, n), rows=rows, hq=64, hkv=4, fp8=fp8, seed=rows)
+    b.tables[:, :20] = b.tables[0, :20]      # (whichever group a sequence is taken for, its row holds the prefix)
+    groups, prefix = b.groups, b.prefix
+    b.groups, b.prefix = np.array([0, n] * (ng // 2 + 1)), np.full(ng, 330)
+    ways = b.ways()
+    assert 1 in ways or rows > 1 and 2 in ways
+    for way in (1, 2):
+        if way in ways:
+            got = b.call(**ways[way])
+            assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() == 4
+            assert np.isfinite(f64(got)).all()
+    b.groups, b.prefix = groups, prefix
+    b.check()
+
+
 def test_blocks_outside_the_pool():
     """Flagged and not read; the other groups' rows are as ever."""
     for where in ("prefix", "tail"):
