@@ -368,6 +368,9 @@ namespace pkv {
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation may start while the previous kernel on the stream is still
 // running; it must wait here before reading anything an earlier kernel wrote.
+// What such a kernel writes -- block tables, lengths, offsets, slots -- is not constant
+// while this one is resident, so it is read by plain loads, never by read-only ones
+// (__ldg), which this wait does not order.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // lets the next kernel on the stream (if launched with that attribute) start
 __device__ __forceinline__ void griddep_launch_dependents()
@@ -534,8 +537,7 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
 // Lane i reads the (max, sum) of partitions i, i + 32, ... together, so the
 // whole merge costs a few memory round trips instead of a chain per
 // partition; the order of every sum is fixed, so the result is deterministic.
-__device__ __forceinline__ float4 lse_merge_warp(const float *__restrict__ ml, const float *__restrict__ o, int ns,
-                                                 int lane)
+__device__ __forceinline__ float4 lse_merge_warp(const float *ml, const float *o, int ns, int lane)
 {
     // the first 32 partitions' (max, sum) and the first four partitions' rows are
     // requested together, before anything depends on them

@@ -111,12 +111,12 @@ __device__ __forceinline__ int row_seq_len(const DecodeParams &p, int r)
     int lo = 0, hi = p.num_seqs;                 // cu[lo] <= r < cu[hi] if well formed
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= r) lo = mid;
+        if (cu[mid] <= r) lo = mid;
         else hi = mid;
     }
-    const int a = __ldg(cu + lo), b = __ldg(cu + lo + 1);
+    const int a = cu[lo], b = cu[lo + 1];
     if (r < a || r >= b) return 0;
-    const int len = __ldg(p.context_lens + lo);
+    const int len = p.context_lens[lo];
     return (b - a > len || len > p.max_blocks * BS) ? 0 : len;
 }
 
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     // block ids of this warp, 32 at a time: lane i holds the id of block k0 + i
     auto load_ids = [&](int k0) -> int32_t {
         int k = k0 + lane;
-        return k < count ? __ldg(bt + b0 + warp + k * WARPS) : -1;
+        return k < count ? bt[b0 + warp + k * WARPS] : -1;
     };
     int32_t ids_cur = load_ids(0), ids_nxt = load_ids(32);
     int win = 0;  // window base of ids_cur
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(THREADS, PKV_DECODE_MIN_CTAS)
     float sl = p.scale_log2;
     float vsc = 1.f;
     if constexpr (FP8) {
-        sl *= __ldg(p.k_scale + g);
-        vsc = __ldg(p.v_scale + g);
+        sl *= p.k_scale[g];
+        vsc = p.v_scale[g];
     }
 
     // ---- prologue

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             auto block_id = [&](int j) -> int32_t {
                 const int b = j * (TK / BS) + blk;
-                return (j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
+                return (j < it.j1 && b < nblk) ? bt[b] : -1;
             };
             int32_t next_id = block_id(it.j0);
             for (int j = it.j0; j < it.j1; ++j, ++u) {
@@ -397,6 +397,9 @@ __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
             const int rows = q.rows;
             const uint16_t *src = p.q + ((size_t)q.q.a * p.heads + q.r0 + w * 32) * LKD;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            // (read-only loads, unlike those of tables and lengths: queries are whole before a kernel
+            // that lets this one start early begins, as no kernel that does so writes queries.  Plain
+            // ones need more registers than there are, 98 bytes of spills)
             const int lr = lane >> 3, le = lane & 7;      // row within four, piece
             const uint32_t qt = sbase + SQ + w * 4096;
             uint4 y[2][8];

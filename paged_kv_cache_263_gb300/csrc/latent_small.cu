@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int nblk = (it.q.L + BS - 1) / BS;
             auto block_id = [&](int j) -> int32_t {
                 const int b = j * (TK / BS) + blk;
-                return (j < it.j1 && b < nblk) ? __ldg(bt + b) : -1;
+                return (j < it.j1 && b < nblk) ? bt[b] : -1;
             };
             int32_t next_id = block_id(it.j0);
             auto queries = [&]() {

@@ -80,10 +80,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ Seq read_seq(const LatentParams &p, int s, bool flagging)
 {
     Seq q;
-    q.a = p.cu ? __ldg(p.cu + s) : s;
-    const int b = p.cu ? __ldg(p.cu + s + 1) : s + 1;
+    q.a = p.cu ? p.cu[s] : s;
+    const int b = p.cu ? p.cu[s + 1] : s + 1;
     q.n = b - q.a;
-    q.L = __ldg(p.lens + s);
+    q.L = p.lens[s];
     if (q.n == 0) return q;
     if (q.a < 0 || b < q.a || b > p.rows || q.L < 0 || q.L > p.max_blocks * BS || (q.L != 0 && q.L < q.n)) {
         if (flagging) flag(ST_BAD_LEN);

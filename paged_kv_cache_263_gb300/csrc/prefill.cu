@@ -1045,7 +1045,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 // the next tile are read during the wait for a free stage.
                 auto block_id8 = [&](int jj) -> int32_t {
                     const int b = (j0 + jj) * (BN / BS) + blk8;
-                    return (lane < 8 && jj < T && b < nblk) ? __ldg(bt + b) : -1;
+                    return (lane < 8 && jj < T && b < nblk) ? bt[b] : -1;
                 };
                 int32_t next_id = block_id8(0);
                 for (int jj = 0; jj < T; ++jj, ++u) {
@@ -1075,7 +1075,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             } else {
                 auto block_id = [&](int jj) -> int32_t {
                     const int b = (j0 + jj) * (BN / BS) + blk;
-                    return (lane < BOX_LANES && jj < T && b < nblk) ? __ldg(bt + b) : -1;
+                    return (lane < BOX_LANES && jj < T && b < nblk) ? bt[b] : -1;
                 };
                 int32_t next_id = block_id(0);
                 for (int jj = 0; jj < T; ++jj, ++u) {
@@ -1309,7 +1309,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 auto row_ok = [&](int jj) -> bool {
                     const int key = (j0 + jj) * BN + row;
                     if (jj >= T || key >= L) return false;
-                    const int32_t id = __ldg(bt + key / BS);
+                    const int32_t id = bt[key / BS];
                     return id >= 0 && id < p.num_blocks;
                 };
                 bool next_ok = row_ok(0);
@@ -1385,8 +1385,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
             const int pos_min = all ? L - 1 : L - n + i0;
             float m_ref = -INFINITY, l = 0.f;
             // fp8 cache: the k scale folds into the softmax scale, the v scale into O
-            const float sl = FP8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
-            const float vsc = FP8 ? __ldg(p.v_scale + g) : 1.f;
+            const float sl = FP8 ? p.scale_log2 * p.k_scale[g] : p.scale_log2;
+            const float vsc = FP8 ? p.v_scale[g] : 1.f;
             if constexpr (FP8) {
                 // the group's Q tile, bf16 -> f16 in place (exact for these values'
                 // range but the smallest subnormals), before its first product
