@@ -223,7 +223,7 @@ struct PrefixParams : PrefillParams {
     int joined, tail_tiles, tail_at;
     __nv_bfloat16 *out16;        // the output, where one part is all that a row has; else null
     int one_wave;        // at most one item a CTA
-    int most;            // items at most, of a batch that keeps the rules
+    int most, most_tails;   // items at most, of a batch that keeps the rules: prefixes', joined tails'
     int *tail_counter;   // of the kernel that attends the tails beside this one
 };
 
@@ -661,7 +661,7 @@ constexpr float SHARED_ITEM_TILES = 3.f;
 // walks over the sources, 32 at a time.
 struct SharedItems {
     int w0, x, total;                     // the window's first source; the next item's place in it; its items
-    int base;                             // items before the window
+    int left;                             // items that the groups, or the sequences, behind it may still have
     int incl;                             // this lane's source: items up to it,
     int nq, ns, KT, row0, rows, L;        // query items, parts, KV tiles, rows and keys,
     int s, skip, seqs;                    // its table row, the block of key 0; the group's sequences
@@ -706,6 +706,15 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
         if (lane >= o) w.incl += t;
     }
     w.total = __shfl_sync(0xffffffffu, w.incl, 31);
+    // (groups or sequences that claim the same rows, as offsets out of order do, could have
+    // any number of items: no more are done than a valid batch has)
+    if (w.w0 == p.seq0) w.left = p.most_tails;
+    else if (w.w0 == 0) w.left = p.most;
+    if (w.total > w.left) {
+        if (lane == 0) flag(ST_BAD_LEN);
+        w.total = w.left;
+    }
+    w.left -= w.total;
 }
 
 // How many CTAs take items (C above; the same in every CTA); `w` gets the first
@@ -941,19 +950,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                 // CTAs past the work list's count leave their SMs to the decode rows
                 if constexpr (SHARED) {
                     if ((int)blockIdx.x < ctas) {
-                        while (win.x >= win.total && win.w0 + 32 < p.sources && win.base + win.total <= p.most) {
-                            win.base += win.total;
+                        while (win.x >= win.total && win.w0 + 32 < p.sources) {
                             win.x -= win.total;
                             win.w0 += 32;
                             load_window(p, win, tpt, lane);
                         }
                         const int x = win.x;
                         win.x += ctas;
-                        // (groups or sequences that claim the same rows, as offsets out of order do,
-                        // could have any number of items: no more are done than a valid batch has)
-                        if (win.base + win.total > p.most && win.base + x >= p.most) {
-                            if (lane == 0) flag(ST_BAD_LEN);
-                        } else if (x < win.total) {
+                        if (x < win.total) {
                             const int at = __ffs(__ballot_sync(0xffffffffu, win.incl > x)) - 1;
                             const int nq = __shfl_sync(0xffffffffu, win.nq, at), ns = __shfl_sync(0xffffffffu, win.ns, at);
                             const int r = x - (__shfl_sync(0xffffffffu, win.incl, at) - nq * ns * p.hkv);
@@ -1899,7 +1903,8 @@ cudaError_t launch_prefixes(const SharedCall &c, cudaStream_t st)
     // to 156 us)
     p.grid_ctas += p.grid_ctas & 1;
     p.one_wave = c.prefix_items <= p.num_sms;
-    p.most = (int)(c.prefix_items + c.tail_items);
+    p.most = (int)c.prefix_items;
+    p.most_tails = (int)c.tail_items;
     p.groups = c.prefix_splits > 0 ? c.b.num_groups : 0;
     p.joined = c.joined ? 1 : 0;
     p.seq0 = (p.groups + 31) / 32 * 32;
