@@ -611,8 +611,11 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
  *  sizes          num_seqs and num_groups at most 65,535 (KV_ERR_INVALID above),
  *                 max_blocks_per_seq at most 2^27 - 16 (KV_ERR_UNSUPPORTED above)
  *  workspace      device scratch of paged_attention_shared_prefix_workspace_size()
- *                 bytes, 256-byte aligned.  Calls that may overlap on the GPU need
- *                 one each.
+ *                 bytes, 256-byte aligned.  The size grows with each argument of that
+ *                 function: with the same heads, a workspace for the largest batch and
+ *                 bounds serves all smaller ones.  At most 128 MiB, or two partial
+ *                 results (520 bytes) for each row and head where that is more.  Calls
+ *                 that may overlap on the GPU need one each.
  * Scores, softmax statistics, sums and partial outputs are fp32; probabilities are
  * rounded to bf16 (f16 over an fp8 cache) for the second product, and the output
  * once at the end.  Split points depend on the call's sizes and bounds and on each

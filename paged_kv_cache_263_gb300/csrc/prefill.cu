@@ -1826,6 +1826,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
             const double work = (before * mean + behind * mean_tail) * tile + items * JOIN_ITEM_US;
             const double longest = std::min((double)n, std::max(W ? mean : 0.0, mean_tail)) * tile + JOIN_ITEM_US;
             const double parts = (W ? std::ceil(W / p) : 0.0) + std::ceil((double)Wt / t);
+            if (parts > c.most_parts && n < most) continue;
             const double cost = std::max(work / sms + JOIN_LAST * longest, longest) +
                                 parts * (0.14 + 0.09e-4 * (double)c.b.total_rows * c.hq);
             if (len == 0 || cost < best) {
@@ -1844,7 +1845,7 @@ void plan_prefixes(SharedCall &c, int64_t max_tail)
         const double tail = PART_TAIL * 1e-6 * c.b.num_seqs * (double)max_tail * c.mean_sets * c.hkv * D * 2 * (c.fp8 ? 1 : 2);
         double best = 0;
         int pick = 0;
-        for (int s = 1; s <= std::min(W, 128); s += 1 + s / 8) {
+        for (int s = 1; s <= std::min({W, 128, c.most_parts / 2}); s += 1 + s / 8) {
             const int len = (W - 1) / s + 1, parts = (W - 1) / len + 1;
             const double items = problems * std::max(1.0, mean / len), least = std::ceil(items / sms);
             const double each = (ng > 1 ? std::min((double)len, std::max(1.0, mean)) : len) * tile + item;

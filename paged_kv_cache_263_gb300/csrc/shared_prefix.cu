@@ -179,9 +179,37 @@ void choose(SharedCall &c, int32_t max_tail_len)
     c.whole = !c.joined && whole <= apart;
 }
 
+// A call's partial results are at most those that PART_BYTES hold, or two parts a row where
+// that is more: so the workspace's size grows with every argument, and the one for the
+// largest batch serves all.  No drawn batch with bounds of its own has more (2,333, up to
+// 256 sequences; 24 with bounds 16 times its tails).
+constexpr int64_t PART_EACH = D * 4 + 8, PART_BYTES = 128 << 20;
+int64_t room_for(const SharedCall &c)       // partial results of one row and head
+{
+    return std::max<int64_t>(2 * (int64_t)c.b.total_rows * c.hq, PART_BYTES / PART_EACH);
+}
+int64_t whole_parts(int64_t blocks) { return std::min<int64_t>(256, (blocks + 11) / 12); }
+// the most parts that a row has with these bounds or lower ones, whichever way the call goes
+// (plan below and plan_prefixes)
+int64_t parts_at_most(const SharedCall &c, int32_t max_tail_len)
+{
+    const int64_t P = c.b.num_groups > 0 ? c.b.max_prefix / BS : 0, T = ((int64_t)max_tail_len + BS - 1) / BS;
+    const int64_t tiles = std::min<int64_t>(128, (P * BS + 63) / 64);
+    int64_t most = std::max<int64_t>(1, whole_parts(P + T));
+    if (P > 0) {
+        const int64_t cut = std::max<int64_t>({1, (int64_t)((double)T / (TAIL_ROOT * std::sqrt(std::max(1.0, (double)T)))),
+                                               (T + 255) / 256});
+        most = std::max(most, tiles + (cut > 1 ? 2 * cut : 1));
+    }
+    if (c.b.max_q_len > 1 && (int64_t)c.b.max_q_len * (c.hq / c.hkv) > TAIL_COLS)
+        most = std::max(most, tiles + std::max<int64_t>(1, std::min<int64_t>(128, ((int64_t)max_tail_len + 63) / 64)));
+    return most;
+}
+
 void plan(SharedCall &c, int32_t max_tail_len)
 {
     const int64_t groups = c.b.num_groups;
+    c.most_parts = (int)std::min<int64_t>(room_for(c) / ((int64_t)c.b.total_rows * c.hq), INT32_MAX);
     c.set_rows = (int)(TAIL_COLS / (c.hq / c.hkv));
     c.sets = (c.b.max_q_len - 1) / c.set_rows + 1;
     c.mean_sets = std::ceil(std::max(1.0, (double)c.b.total_rows / std::max(1, c.b.num_seqs)) / c.set_rows);
@@ -197,7 +225,7 @@ void plan(SharedCall &c, int32_t max_tail_len)
     if (c.whole) {
         const double each = (double)c.b.num_seqs * c.hkv * c.mean_sets;
         const double ctas = (int64_t)c.b.max_q_len * (c.hq / c.hkv) > 8 ? 2 * 152 : 3 * 152;
-        const int64_t most = std::min<int64_t>(256, (blocks + 11) / 12);
+        const int64_t most = std::min<int64_t>(c.most_parts, whole_parts(blocks));
         double best = 0;
         for (int64_t n = 1; n <= most; n += 1 + n / 16) {
             const double us = ITEM_US * n * each / ctas + BLOCK_US * (double)((blocks + n - 1) / n) +
@@ -210,7 +238,9 @@ void plan(SharedCall &c, int32_t max_tail_len)
     } else {
         const double want = (double)blocks * c.b.num_seqs * c.hkv / TAIL_CTAS;
         const double part = std::max(TAIL_ROOT * std::sqrt((double)blocks), TAIL_WANT * want);
-        c.tail_splits = (int)std::max<int64_t>({1, (int64_t)((double)blocks / part), (blocks + 255) / 256});
+        const int64_t cut = std::max<int64_t>({1, (int64_t)((double)blocks / part), (blocks + 255) / 256});
+        // (twice as many with the shorter parts at the end)
+        c.tail_splits = (int)std::min<int64_t>(cut, std::max(1, (c.most_parts - c.prefix_splits) / 2));
     }
     c.tail_part_blocks = (int)((blocks + c.tail_splits - 1) / c.tail_splits);
     if (!c.whole && c.tail_splits > 1) {
@@ -233,10 +263,13 @@ size_t part_ml_bytes(const SharedCall &c)
     return up((size_t)c.b.total_rows * c.hq * shared_parts(c) * 2 * sizeof(float));
 }
 
-size_t scratch_bytes(const SharedCall &c)
+// what the caller provides: room for the parts of this call's plan and of any smaller call's
+size_t scratch_bytes(const SharedCall &c, int32_t max_tail_len)
 {
-    const size_t o = part_o_bytes(c);
-    return o ? o + part_ml_bytes(c) + 256 : 0;      // and the counter
+    const int64_t parts = parts_at_most(c, max_tail_len), rh = (int64_t)c.b.total_rows * c.hq;
+    if (parts == 1) return 0;
+    const int64_t n = rh > INT64_MAX / parts ? room_for(c) : std::min(rh * parts, room_for(c));
+    return up((size_t)n * D * sizeof(float)) + up((size_t)n * 2 * sizeof(float)) + 256;      // and the counter
 }
 
 // the description that sizes and bounds alone make (false: sizes that no call takes)
@@ -244,7 +277,8 @@ bool describe(SharedCall &c, int32_t num_seqs, int32_t total_q_tokens, int32_t m
               int32_t num_q_heads, int32_t num_kv_heads, int32_t max_prefix_len, int32_t max_tail_len, bool fp8)
 {
     if (num_seqs < 1 || total_q_tokens < 1 || max_q_len < 1 || num_groups < 0 || num_q_heads < 1 || num_kv_heads < 1 ||
-        max_prefix_len < 0 || max_tail_len < 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16)
+        max_prefix_len < 0 || max_tail_len < 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 ||
+        num_q_heads > 65535 * MERGE_WARPS)
         return false;
     c.b.num_seqs = num_seqs;
     c.b.total_rows = total_q_tokens;
@@ -254,7 +288,6 @@ bool describe(SharedCall &c, int32_t num_seqs, int32_t total_q_tokens, int32_t m
     c.hq = num_q_heads;
     c.hkv = num_kv_heads;
     c.fp8 = fp8;
-    plan(c, max_tail_len);
     return true;
 }
 
@@ -270,16 +303,11 @@ size_t paged_attention_shared_prefix_workspace_size(int32_t num_seqs, int32_t to
                                                     int32_t num_groups, int32_t num_q_heads, int32_t num_kv_heads,
                                                     int32_t max_prefix_len, int32_t max_tail_len)
 {
-    // (the caches' type is not given: room for the plan of either)
-    size_t most = 0;
-    for (const bool fp8 : {false, true}) {
-        SharedCall c{};
-        if (!describe(c, num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
-                      max_tail_len, fp8))
-            return 0;
-        most = std::max(most, scratch_bytes(c));
-    }
-    return most;
+    SharedCall c{};
+    if (!describe(c, num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
+                  max_tail_len, false))
+        return 0;
+    return scratch_bytes(c, max_tail_len);
 }
 
 int32_t paged_attention_shared_prefix_way(int32_t num_seqs, int32_t total_q_tokens, int32_t max_q_len, int32_t num_groups,
@@ -291,6 +319,7 @@ int32_t paged_attention_shared_prefix_way(int32_t num_seqs, int32_t total_q_toke
         !describe(c, num_seqs, total_q_tokens, max_q_len, num_groups, num_q_heads, num_kv_heads, max_prefix_len,
                   max_tail_len, dtype == KV_FP8_E4M3))
         return -1;
+    plan(c, max_tail_len);
     return c.whole ? 0 : c.joined ? 2 : 1;
 }
 
@@ -349,13 +378,13 @@ kv_status paged_attention_shared_prefix(void *out, const void *q, const int32_t 
     if ((int64_t)max_q_len * G > INT32_MAX / 32 || tail_kernel_items(c) > INT32_MAX / 2 ||
         (int64_t)std::min(max_q_len, total_q_tokens) / c.set_rows + 1 > INT32_MAX / 64 / num_kv_heads / c.tail_splits)
         return KV_ERR_UNSUPPORTED;
-    // (the plan goes by the bounds as given, which the workspace's size goes by; no
-    // length passes what a table row holds)
+    // (the plan and the workspace's size go by the bounds as given; no length passes what a
+    // table row holds)
+    const size_t need = scratch_bytes(c, max_tail_len);
     c.b.max_prefix = std::min(c.b.max_prefix, max_blocks_per_seq * BS);
     c.b.max_tail = std::min(c.b.max_tail, max_blocks_per_seq * BS);
     const size_t o_bytes = part_o_bytes(c);
-    if (o_bytes && (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < scratch_bytes(c)))
-        return KV_ERR_INVALID;
+    if (need && (!workspace || !pkv_host::aligned(workspace, 256) || workspace_bytes < need)) return KV_ERR_INVALID;
     c.part_o = static_cast<float *>(workspace);
     c.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o_bytes);
     c.counter = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + o_bytes + part_ml_bytes(c));

@@ -20,6 +20,7 @@ struct SharedCall {
     bool joined;                      // the kernel of the prefixes attends the tails as well
     bool whole;                       // no kernel for the prefixes: the tails' attends whole contexts
     int prefix_splits, prefix_tiles;  // parts of a prefix at most, and KV tiles a part
+    int most_parts;                   // parts of a row at most, that the workspace has room for (two or more)
     int64_t prefix_items, tail_items; // work items of prefixes, and of joined tails, at most
     int tail_splits, tail_part_blocks;
     int fine_from, fine_blocks;       // sequences from fine_from on have shorter parts, of fine_blocks

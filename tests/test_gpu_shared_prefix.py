@@ -418,6 +418,31 @@ def test_any_placement_and_workspace_gives_the_same_bits():
     assert pkv.kv_last_device_status() == 0
 
 
+@pytest.mark.parametrize("rows", [1, 3])
+def test_one_workspace_for_smaller_batches_and_bounds(rows):
+    """Kept from call to call, as a server does: asked for once, for the largest batch and the loosest bounds."""
+    most = (256, 256 * rows, rows, 4, 64, 8, 4096, 4096)
+    ws = torch.full((pkv.paged_attention_shared_prefix_workspace_size(*most),), 0xFF, dtype=torch.uint8, device="cuda")
+    for n in (38, 32, 16, 5, 1):
+        b = Batch([n], [4000 - n], np.random.default_rng(n).integers(rows, 500, n), rows=rows, hq=64, hkv=8, width=300, seed=n)
+        ref = b.reference()
+        for bounds in (dict(max_prefix_len=4096, max_tail_len=4096), dict(max_prefix_len=4000, max_tail_len=500),
+                       dict(max_prefix_len=4000, max_tail_len=4096), dict(max_prefix_len=4096, max_tail_len=600)):
+            b.check(ref=ref, workspace=ws, **bounds)
+
+
+@pytest.mark.parametrize("rows,fp8", [(1, False), (1, True), (3, False)])
+def test_fewer_parts_where_the_workspace_ends(rows, fp8):
+    """Bounds so far above the lengths that parts by them alone would not fit what partial results may take."""
+    tails = np.random.default_rng(5).integers(rows, 60, 40)
+    tails[7] = 9000
+    b = Batch([40], [2000], tails, rows=rows, hq=128, hkv=8, fp8=fp8, seed=5)
+    ref = b.reference()
+    for tail in (1 << 14, 1 << 18, 1 << 22):
+        for prefix in (2000, 1 << 18):
+            b.check(ref=ref, max_prefix_len=prefix, max_tail_len=tail)
+
+
 def test_agrees_with_decode_over_the_whole_context():
     """The same rows through paged_attention_decode with the prefix in every table row."""
     b = Batch([16, 9], [2000, 512], np.arange(1, 26) * 13, hq=16, hkv=2)

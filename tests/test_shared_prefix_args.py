@@ -69,6 +69,22 @@ def test_attention_sizes_its_workspace_for_any_bounds(mp, mt, nq, fp8):
     assert pkv.paged_attention_shared_prefix_workspace_size(4, 4 * nq, nq, 2, 24, 7, mp, mt) == 0
 
 
+def test_a_workspace_serves_every_smaller_call():
+    """The size grows with every argument, so that the one for the largest batch and bounds can be kept."""
+    size = pkv.paged_attention_shared_prefix_workspace_size
+    falling = [size(n, n, 1, 1, 64, 8, 4096, 4096) for n in (256, 128, 64, 38, 32, 16, 8, 1)]
+    assert falling == sorted(falling, reverse=True) and falling[-1] > 0
+    rng = np.random.default_rng(3)
+    for _ in range(4000):
+        kv, per, rows = rng.choice([1, 2, 8, 16]), rng.choice([1, 2, 4, 8, 16]), rng.choice([1, 1, 2, 4, 7, 30])
+        seqs = int(np.exp(rng.uniform(0, 9)))
+        heads = [int(kv * per), int(kv)]
+        large = [seqs, seqs * int(rows), int(rows), int(rng.integers(0, seqs + 1)), *(int(np.exp(rng.uniform(0, 13))) for _ in range(2))]
+        small = [max(1, int(x * rng.choice([1, 1, rng.random()]))) for x in large[:3]] + [
+            int(x * rng.choice([1, 1, rng.random()])) for x in large[3:]]
+        assert size(*small[:4], *heads, *small[4:]) <= size(*large[:4], *heads, *large[4:]), (small, large, heads)
+
+
 @pytest.mark.parametrize("sizes,fp8,way", [
     ((4, 4, 1, 1, 8, 2, 256, 64), False, 0), ((64, 64, 1, 1, 64, 8, 32768, 1000), False, 1),
     ((64, 64, 1, 1, 64, 8, 32768, 1000), True, 1), ((52, 364, 7, 1, 16, 2, 29, 11260), False, 2),
