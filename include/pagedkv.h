@@ -587,8 +587,8 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
  *
  *  out            device bf16 [total_q_tokens][num_q_heads][128]
  *  q              device bf16 [total_q_tokens][num_q_heads][128]; scores that are
- *                 NaN or +inf (a query that is not finite) make their own row of
- *                 that head NaN.  KV_FP8_E4M3: the query range of
+ *                 NaN or +inf, or all -inf (a query that is not finite), make their
+ *                 own row of that head NaN.  KV_FP8_E4M3: the query range of
  *                 paged_attention_decode
  *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
  *                 sequence (total_q_tokens = num_seqs, max_q_len = 1)

@@ -1507,7 +1507,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                     const size_t head_step = (size_t)p.max_splits * D, row_step = head_step * p.hq;
                     const size_t rh4 = (size_t)(row0 + i0 + (r4 >> lg)) * p.hq + g * G + (r4 & (G - 1));
                     float *to = p.part_o + rh4 * head_step + (size_t)split * D + (lane & 3) * 4;
-                    const float by = p.out16 ? (l == 0.f ? 0.f : vsc / l) : vsc;
+                    const float by = p.out16 ? vsc / l : vsc;     // (a sum of 0: scores that are all -inf, NaN)
                     __nv_bfloat16 *to16 = p.out16 + rh4 * D + (lane & 3) * 4;
                     if ((r & ~31) < rows) {      // (a warp without rows stores nothing)
                         // (one copy of the code, which runs once an item: unrolled, its fetch

@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
             }
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    // (every row sees a key: a sum of 0 is scores that are all -inf, whose softmax is NaN)
+    const float inv = 1.f / sum;
     *out = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 

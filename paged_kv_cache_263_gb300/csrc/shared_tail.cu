@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
                 if (c >= cols) continue;
                 const size_t rh = (size_t)(it.row0 + c / p.group) * p.hq + it.g * p.group + c % p.group;
                 if (p.out16) {
-                    const float inv = l[nt][e] == 0.f ? 0.f : vsc / l[nt][e];
+                    const float inv = vsc / l[nt][e];     // (a sum of 0: scores that are all -inf, NaN)
                     __nv_bfloat16 *to = p.out16 + rh * D;
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj)

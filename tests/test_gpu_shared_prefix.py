@@ -398,6 +398,30 @@ def test_queries_that_are_not_finite(bad, where):
         compare(got, exp, tol)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [1, 5])
+@pytest.mark.parametrize("groups", [True, False])
+def test_scores_that_are_all_minus_infinity(rows, groups, fp8):
+    """Their softmax is NaN, in their own row of that head; where one key has another score, it is a softmax as any."""
+    b = Batch(*(([4, 3], [200, 90]) if groups else ([], [])), [20, 30, 40, 5, 7, 9, 11], before=0 if groups else 7, rows=rows,
+              hq=8, hkv=2, fp8=fp8)
+    if fp8:
+        b.k[..., 17] = b.k[..., 17] & 0x7F | 1
+        b.k64[..., 17] = f64(b.k.view(torch.float8_e4m3fn))[..., 17] * f64(b.ks)[:, None]
+    else:
+        b.k[..., 17] = b.k[..., 17].abs() + 0.5
+        b.k64 = f64(b.k)
+    exp, tol, _ = b.reference()
+    some = [0, rows + rows // 2, 6 * rows]
+    b.q[some, 3, 17] = -float("inf")
+    for bounds in b.ways().values():
+        got = f64(b.call(**bounds))
+        assert pkv.kv_last_device_status() == 0
+        assert np.isnan(got[some, 3]).all()
+        got[some, 3] = exp[some, 3]
+        compare(got, exp, tol)
+
+
 def test_any_placement_and_workspace_gives_the_same_bits():
     args = dict(sizes=[20, 7], prefix=[3000, 800], tails=np.arange(1, 28) * 11, hq=16, hkv=4)
     b = Batch(**args, width=300)
