@@ -593,7 +593,7 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
  *  cu_q_lens      device int32 [num_seqs + 1], non-decreasing; NULL: one row a
  *                 sequence (total_q_tokens = num_seqs, max_q_len = 1)
  *  context_lens   device int32 [num_seqs]; L = 0 (a padded entry): the sequence's
- *                 rows are zeros.
+ *                 rows are zeros.  The prefix of a group of such entries is not read.
  *  max_q_len      host int: an upper bound on every n
  *  cu_groups      device int32 [num_groups + 1], non-decreasing; prefix_lens device
  *                 int32 [num_groups].  Groups may be empty.

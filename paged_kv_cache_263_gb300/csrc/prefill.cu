@@ -665,20 +665,48 @@ struct SharedItems {
     int incl;                             // this lane's source: items up to it,
     int nq, ns, KT, row0, rows, L;        // query items, parts, KV tiles, rows and keys,
     int s, skip, seqs;                    // its table row, the block of key 0; the group's sequences
+    unsigned alive;                       // bit i: runs of sequences with a context, from run 32 lane on
 };
-__device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &w, int tpt, int lane)
+__device__ __forceinline__ SharedGroup window_group(const PrefixParams &p, int u)
+{
+    SharedGroup gr = {};
+    if (u < p.groups) gr = shared_group(p.b, u);
+    return gr;
+}
+// Whether a sequence of each lane's group (where `ask`) has a context: a prefix that only
+// padded entries share is not read.  By 1,024 bits, one for a run of 1 << alive_log2
+// sequences; where that is more than one, the sequences of a run that has any are looked
+// at one by one.
+__device__ __forceinline__ int alive_log2(const PrefixParams &p) { return max(0, 22 - __clz(p.b.num_seqs - 1)); }
+__device__ __forceinline__ bool any_alive(const PrefixParams &p, const SharedItems &w, const SharedGroup &gr, bool ask, int lane)
+{
+    const int of = alive_log2(p);
+    int s = gr.s0;
+    // (mostly the first one.  In the loop alone: 0.6 us of 62 more, 133 sequences in 16 groups)
+    bool any = of == 0 && (__shfl_sync(0xffffffffu, w.alive, s >> 5) >> (s & 31) & 1);
+    while (__any_sync(0xffffffffu, ask && !any && s < gr.s1)) {
+        const int run = s >> of;
+        const unsigned rest = __shfl_sync(0xffffffffu, w.alive, run >> 5) >> (run & 31);
+        if (rest == 0) {
+            s = ((run | 31) + 1) << of;
+        } else {
+            s = max(s, (run + __ffs(rest) - 1) << of);
+            any = any || (s < gr.s1 && (of == 0 || p.b.context_lens[s] > 0));
+            ++s;
+        }
+    }
+    return ask && any;
+}
+__device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &w, const SharedGroup &gr, int tpt, int lane)
 {
     const int u = w.w0 + lane;
     w.nq = w.ns = w.KT = w.row0 = w.rows = w.L = w.s = w.skip = w.seqs = 0;
-    if (u < p.groups) {
-        const SharedGroup gr = shared_group(p.b, u);
-        if (gr.ok) {
-            w.row0 = gr.row0;
-            w.rows = gr.rows;
-            w.L = gr.P;
-            w.s = gr.s0;
-            w.seqs = gr.s1 - gr.s0;
-        }
+    if (w.w0 < p.groups && any_alive(p, w, gr, gr.ok && gr.rows > 0 && gr.P > 0, lane)) {
+        w.row0 = gr.row0;
+        w.rows = gr.rows;
+        w.L = gr.P;
+        w.s = gr.s0;
+        w.seqs = gr.s1 - gr.s0;
     }
     if (w.w0 >= p.seq0) {       // (all lanes: sequences begin with a window of their own)
         const SharedSeq q = shared_seq_window(p.b, w.w0 - p.seq0, lane);
@@ -726,10 +754,22 @@ __device__ __forceinline__ void load_window(const PrefixParams &p, SharedItems &
 __device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w, int tpt, int lane)
 {
     // (asked for before anything waits for the groups)
+    int len[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) len[i] = 32 * i + lane < p.b.num_seqs ? p.b.context_lens[32 * i + lane] : 0;
+    const SharedGroup gr = window_group(p, w.w0 + lane);
     float tail = 0.f;
+    const int of = alive_log2(p);
+    auto count = [&](int s, int L) {
+        tail += (float)max(0, L);
+        const unsigned bits = __reduce_or_sync(0xffffffffu, L > 0 ? 1u << ((s + lane) >> of & 31) : 0u);
+        if (lane == s >> (of + 5)) w.alive |= bits;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count(32 * i, len[i]);
 #pragma unroll 4
-    for (int s = lane; s < p.b.num_seqs; s += 32) tail += (float)max(0, p.b.context_lens[s]);
-    load_window(p, w, tpt, lane);
+    for (int s = 128; s < p.b.num_seqs; s += 32) count(s, s + lane < p.b.num_seqs ? p.b.context_lens[s + lane] : 0);
+    load_window(p, w, gr, tpt, lane);
     // (no tails beside this kernel, or at most one item a CTA: the host's plan stands)
     if (p.joined || p.one_wave) return p.grid_ctas;
     float items = 0.f, tiles = 0.f;
@@ -740,7 +780,7 @@ __device__ __forceinline__ int shared_ctas(const PrefixParams &p, SharedItems &w
         tail -= (float)x.L * x.seqs;
         if (x.w0 + 32 >= p.sources) break;
         x.w0 += 32;
-        load_window(p, x, tpt, lane);
+        load_window(p, x, window_group(p, x.w0 + lane), tpt, lane);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -953,7 +993,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : Lay<FP8, BIG>::THREADS, 1)
                         while (win.x >= win.total && win.w0 + 32 < p.sources) {
                             win.x -= win.total;
                             win.w0 += 32;
-                            load_window(p, win, tpt, lane);
+                            load_window(p, win, window_group(p, win.w0 + lane), tpt, lane);
                         }
                         const int x = win.x;
                         win.x += ctas;

@@ -326,6 +326,39 @@ def test_padded_and_bad_sequences():
     b.check()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (3, 16, 2), (5, 16, 1)])
+def test_padded_groups(rows, hq, hkv, fp8):
+    """A group of padded entries reads nothing, whatever its prefix length and table rows hold; one entry that
+    is not padded, wherever it is, attends its group's prefix."""
+    sizes = [5, 200, 40, 3, 150, 1] if rows > 1 else [5, 1100, 40, 3, 700, 1]
+    n = sum(sizes)
+    b = Batch(sizes, [130, 500, 77, 90, 260, 400], np.random.default_rng(rows).integers(rows, 90, n), rows=rows, hq=hq, hkv=hkv,
+              fp8=fp8, seed=rows)
+    lens, tables = b.lens, b.tables
+    for alive in ((2, 3), (0, 5), (1,), (4,), ()):
+        for kept in ("last", "all", "middle"):
+            b.lens, b.tables = np.zeros_like(lens), np.full_like(tables, -1)
+            for g in alive:
+                a, e = b.groups[g], b.groups[g + 1]
+                on = {"last": [e - 1], "all": range(a, e), "middle": [(a + e) // 2]}[kept]
+                b.lens[on] = lens[on]
+                b.tables[on] = tables[on]
+                b.tables[a, :b.prefix[g] // BS] = tables[a, :b.prefix[g] // BS]
+            b.check()
+    # a group of sequences that break a rule: flagged and left as they were, the others as ever
+    # (its prefix may be read, and its blocks be flagged)
+    b.lens, b.tables = lens.copy(), tables.copy()
+    b.lens[b.groups[1]:b.groups[2]] = 7
+    b.tables[b.groups[1]:b.groups[2]] = -1
+    exp, tol, f = b.reference()
+    assert f == 4
+    for bounds in b.ways().values():
+        got = b.call(**bounds)
+        assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() in (4, 5)
+        compare(f64(got), exp, tol)
+
+
 def test_more_rows_than_announced():
     b = Batch([2, 2], [40, 50], [9, 9, 9, 9], rows=[3, 1, 2, 3], hq=4, hkv=1)
     b.check(flags=4, max_q_len=2, ref=b.reference(max_q=2))
