@@ -9,6 +9,7 @@ a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -140,13 +141,29 @@ def lib():
 _fast_module = None
 
 
+class _ByCtypes:
+    """The entries of the module _fastcall through ctypes, where it was not built (no
+    Python headers) or not for this interpreter."""
+
+    def __init__(self, L):
+        for name in ("paged_attention_shared_prefix", "paged_attention_shared_prefix_workspace_size", "kv_fork_tables",
+                     "kv_remap_tables"):
+            setattr(self, name, getattr(L, name))
+        self._copy = L.kv_copy_blocks
+
+    def kv_copy_blocks(self, caches, *args):
+        return self._copy((ctypes.c_void_p * len(caches))(*caches), len(caches), *args)
+
+
 def _fast():
     """The library's shortest calls without ctypes, which takes 0.15 us an argument."""
     global _fast_module
     if _fast_module is None:
-        lib()
-        from . import _fastcall
-        _fast_module = _fastcall
+        L = lib()
+        try:
+            _fast_module = importlib.import_module("._fastcall", __name__)
+        except ModuleNotFoundError:
+            _fast_module = _ByCtypes(L)
     return _fast_module
 
 

@@ -1,9 +1,10 @@
 """Builds libpagedkv.so in place: every CUDA/C++ source of csrc/ compiled for
 sm_103a only, in parallel, then linked into one shared library with a plain C
 ABI (static CUDA runtime; the driver's tensor-map encoder is resolved at run
-time, so the library loads on a machine without a GPU).  Beside it, _fastcall.so:
-direct Python entries of the shortest calls (csrc/fastcall.c), linked to the
-library."""
+time, so the library loads on a machine without a GPU).  Beside it, where Python's
+headers are installed, the module _fastcall: direct Python entries of the shortest
+calls (csrc/fastcall.c), linked to the library.  Its name holds the interpreter's
+tag, so that no other one loads it; without it those calls go through ctypes."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libpagedkv.so")
-FAST, FAST_SRC = os.path.join(HERE, "_fastcall.so"), os.path.join(CSRC, "fastcall.c")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "pagedkv.h")
+FAST = os.path.join(HERE, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+FAST_SRC = os.path.join(CSRC, "fastcall.c")
 BUILD = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -30,17 +34,30 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(OUT) or not os.path.exists(FAST):
-        return True
-    t = min(os.path.getmtime(OUT), os.path.getmtime(FAST))
-    deps = _sources() + [FAST_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [
-        os.path.join(os.path.dirname(HERE), "include", "pagedkv.h"), __file__]
-    return any(os.path.getmtime(f) > t for f in deps)
+def _stale(out, deps) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out) for f in deps)
+
+
+def _build_fast(force):
+    """The module, where it can be built; the library does not need it."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")) or not (force or _stale(FAST, [FAST_SRC, HEADER, __file__])):
+        return
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-I", include, FAST_SRC, "-o", tmp,
+           "-L", HERE, "-lpagedkv", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        warnings.warn(f"{FAST_SRC} was not compiled, the shortest calls go through ctypes:\n{r.stdout}\n{r.stderr}")
+        return
+    os.replace(tmp, FAST)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
-    if not force and not _stale():
+    sources = _sources()
+    deps = sources + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, __file__]
+    if not force and not _stale(OUT, deps):
+        _build_fast(False)
         return OUT
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -58,7 +75,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         return obj, (r.stdout + r.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        results = list(ex.map(compile_one, _sources()))
+        results = list(ex.map(compile_one, sources))
     if verbose or ptxas_v:
         for obj, log in results:
             if log.strip():
@@ -69,14 +86,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
-    tmp = FAST + f".tmp{os.getpid()}"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-I", sysconfig.get_paths()["include"], FAST_SRC, "-o", tmp, "-L", HERE, "-lpagedkv",
-           "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {FAST_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, FAST)
+    _build_fast(force)
     return OUT
 
 

@@ -1,4 +1,6 @@
 """Block copies, forks and table rewriting against their models, exactly."""
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -153,6 +155,18 @@ def test_remap_of_bad_rows():
 def test_remap_with_ids_in_both_lists():
     """A chain 1 -> 2 -> 3 moves each entry once."""
     run_remap(np.array([[1, 2, 3, 4], [4, 3, 2, 1]]), [64, 49], [1, 2, 3], [2, 3, 9])
+
+
+def test_calls_without_the_module_of_direct_entries(monkeypatch):
+    """As where Python's headers were missing: the same calls through ctypes."""
+    monkeypatch.setitem(sys.modules, "paged_kv_cache_263_gb300._fastcall", None)
+    monkeypatch.setattr(pkv, "_fast_module", None)
+    test_copies((2, 16, 128), torch.bfloat16, 160, 3)
+    test_copies_that_are_skipped()
+    test_forks(300, 513, 20, True)
+    test_remap(16, 256, 9, 4000)
+    test_a_prompt_sampled_searched_and_compacted(False)
+    assert not hasattr(pkv._fast(), "__file__")
 
 
 # ---------------------------------------------------------------------- in use

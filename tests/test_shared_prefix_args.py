@@ -2,6 +2,8 @@
 refusals of the C calls and of the binding, and the pool and the prefix cache
 against their models.  (The addresses below are never read.)"""
 import ctypes
+import sys
+import sysconfig
 
 import numpy as np
 import pytest
@@ -225,6 +227,44 @@ def test_direct_size_agrees(change):
     args = list(dict(SIZES, **change).values())
     assert pkv._fast().paged_attention_shared_prefix_workspace_size(*args) == \
         pkv.lib().paged_attention_shared_prefix_workspace_size(*args)
+
+
+# ------------------------------------------------- without the module of direct entries
+@pytest.fixture
+def no_module(monkeypatch):
+    monkeypatch.setitem(sys.modules, "paged_kv_cache_263_gb300._fastcall", None)     # (its import fails)
+    monkeypatch.setattr(pkv, "_fast_module", None)
+
+
+@pytest.mark.parametrize("name,change,status", [
+    ("paged_attention_shared_prefix", dict(nq=0), INVALID), ("paged_attention_shared_prefix", dict(hq=24), UNSUPPORTED),
+    ("paged_attention_shared_prefix", dict(nbytes=0), INVALID), ("paged_attention_shared_prefix", dict(B=0), OK),
+    ("kv_copy_blocks", dict(bytes=4104), INVALID), ("kv_copy_blocks", dict(caches=[A, None]), INVALID),
+    ("kv_copy_blocks", dict(caches=[A] * 129 + [A + 8]), INVALID), ("kv_copy_blocks", dict(caches=[]), OK),
+    ("kv_fork_tables", dict(taken=4 * A + 4), INVALID), ("kv_fork_tables", dict(C=16385), UNSUPPORTED),
+    ("kv_remap_tables", dict(dst=A), INVALID), ("kv_remap_tables", dict(B=0), OK)])
+def test_calls_without_the_module(no_module, name, change, status):
+    """It takes Python's headers to build, and is one interpreter's: the calls do without it."""
+    assert _direct(name, **change) == status
+    assert not hasattr(pkv._fast(), "__file__")
+
+
+def test_size_without_the_module(no_module):
+    assert pkv.paged_attention_shared_prefix_workspace_size(*SIZES.values()) > 0
+
+
+def test_build_without_python_headers(monkeypatch, tmp_path):
+    """The library is complete, and nothing is built again at the next call."""
+    monkeypatch.setattr(pkv_build, "FAST", str(tmp_path / "none.so"))
+    monkeypatch.setattr(pkv_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    monkeypatch.setattr(pkv_build.subprocess, "run", lambda *a, **k: pytest.fail("compiles"))
+    assert pkv_build.build() == pkv.library_path
+    assert not list(tmp_path.iterdir())
+
+
+def test_the_module_is_one_interpreters():
+    tag = sysconfig.get_config_var("EXT_SUFFIX")
+    assert tag.count(".") > 1 and pkv._fast().__file__.endswith(tag)
 
 
 # ------------------------------------------------------------------ compaction
