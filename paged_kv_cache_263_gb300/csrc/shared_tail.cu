@@ -28,6 +28,7 @@
 //    signalled by mbarriers, while warps that are done begin the next item.
 //  * Results are partial ones, joined by the merge kernel, or the output itself.
 #include "shared_prefix.h"
+#include "tail_loads.h"
 #include "trace.h"
 
 #include <algorithm>
@@ -329,16 +330,13 @@ __global__ void __launch_bounds__(TailLay<FP8, NT>::THREADS, TailLay<FP8, NT>::C
             if (!ok) break;
             idx = __shfl_sync(0xffffffffu, next, 0);
         }
-        if (!ok) {
-            // loads still in flight land before the CTA ends
-            if (lane < CONSUMERS)
-                for (int uu = max(0, u - LY::RING); uu < u; ++uu)
-                    (void)mbar_wait_bounded(b_full + 8 * (lane * LY::RING + uu % LY::RING), (uu / LY::RING) & 1);
-            __syncwarp();
-            for (int kk = max(0, asked - SLOTS); kk < asked; ++kk)
-                (void)mbar_wait_bounded(b_item + 8 * (kk % SLOTS), (kk / SLOTS) & 1);
-        }
         griddep_launch_dependents();
+        // (this lane's consumer warp's blocks, and the items' queries)
+        pkv_tail::drain(
+            lane < CONSUMERS ? u : 0, LY::RING, asked, SLOTS, ok,
+            [&](int i) { (void)mbar_wait_bounded(b_full + 8 * (lane * LY::RING + i % LY::RING), (i / LY::RING) & 1); },
+            [&](int i) { (void)mbar_wait_bounded(b_item + 8 * (i % SLOTS), (i / SLOTS) & 1); });
+        __syncwarp();
         // the grid completes after the kernel it ran beside: what waits for it sees both
         if (p.beside && blockIdx.x == 0) griddep_wait();
         return;
