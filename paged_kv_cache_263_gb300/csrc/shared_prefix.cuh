@@ -118,8 +118,12 @@ __device__ __forceinline__ SharedSeq shared_seq_window(const SharedBatch &b, int
 #pragma unroll 8
         for (int i = 0; i < 32; ++i) more += __shfl_sync(0xffffffffu, mine, i) <= s;
         g += more;
-        // (empty groups among them: a lane may have further to go)
-        while (more == 32 && g + 1 < b.num_groups && b.cu_groups[g + 1] <= s) ++g;
+        // (empty groups among them: a lane may have further to go, past any number of them)
+        for (int end = more == 32 ? b.num_groups : 0; end - g > 1;) {
+            const int mid = g + ((end - g) >> 1);
+            if (b.cu_groups[mid] <= s) g = mid;
+            else end = mid;
+        }
     }
     if (s >= b.num_seqs) {
         SharedSeq r = {};

@@ -181,6 +181,32 @@ def test_numbers_of_groups(ng):
     Batch(list(sizes), rng.integers(0, 100, ng), rng.integers(1, 20, int(sizes.sum()) + 1), hq=2, hkv=1, loose=1).check()
 
 
+@pytest.mark.parametrize("rows", [1, 5])
+@pytest.mark.parametrize("empty", [31, 32, 33, 64, 1000, 65533])
+def test_many_empty_groups(empty, rows):
+    """As a graph has them that is captured for many groups: behind the last, between two or in front, and
+    sequences of no group behind.  They are not gone through one by one."""
+    for sizes, at in (([50], 0), ([20, 30], 1), ([20, 30], 2), ([50], 1)):
+        b = Batch(sizes, [130, 70][:len(sizes)], np.random.default_rng(empty).integers(rows, 60, 55), rows=rows, hq=8, hkv=1,
+                  loose=5, seed=empty)
+        ref = b.reference()
+        b.groups = np.insert(b.groups, at, [b.groups[at]] * empty)
+        b.prefix = np.insert(b.prefix, at, [100] * empty)
+        for bounds in (dict(max_prefix_len=130), dict(max_prefix_len=1 << 14, max_tail_len=64)):
+            b.check(ref=ref, **bounds)
+    out, put = torch.empty_like(b.q), (i32(b.tables), i32(b.lens), i32(b.groups), i32(b.prefix))
+    took = []
+    for _ in range(5):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        pkv.paged_attention_shared_prefix(out, b.q, b.k, b.v, *put, cu_q_lens=i32(b.cu), max_q_len=rows, max_prefix_len=130,
+                                          max_tail_len=64)
+        end.record()
+        torch.cuda.synchronize()
+        took.append(start.elapsed_time(end))
+    assert min(took) < 1      # ms
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("rows", [2, 3, 4, 8, 20])
 @pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (16, 1)])
