@@ -598,8 +598,12 @@ PAGEDKV_API kv_status latent_prefill_attention(void *out, const void *q, const v
  *  cu_groups      device int32 [num_groups + 1], non-decreasing; prefix_lens device
  *                 int32 [num_groups].  Groups may be empty.
  *  max_prefix_len, max_tail_len   host ints: upper bounds on every P and on every
- *                 L - P.  They size the grids and the workspace, so bounds far above
- *                 the lengths cost time.
+ *                 L - P.  With num_groups they size the grids and the workspace, and
+ *                 choose how the call is done, so bounds far above the lengths, and
+ *                 groups that are mostly empty, cost time.  (64 sequences of 64/8
+ *                 heads behind 32,768 tokens: 81 us with exact bounds; 138 with twice
+ *                 and 261 with eight times the prefix bound, 115 with four times the
+ *                 tail bound, 165 with 8 groups given, 537 with 33.)
  *  A sequence is left out, its rows as they were (flag 4), if its rows are outside
  *  the tensors or more than max_q_len, if its group's sequences or rows are, if a
  *  length is negative, above max_blocks_per_seq x 16 or above its bound, or if

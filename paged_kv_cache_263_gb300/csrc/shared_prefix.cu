@@ -103,8 +103,12 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // of a prefix takes TILE_US for a query item (256 rows x heads; BIG_US for 128 where a
 // group has no more, over a bf16 cache; fp8 TILE8_US): more than the tiles' own time, as
 // the items and the prefixes are unequal.
-// joined: the chunk kernel takes the tails as well, JOIN_US an item and less a block than
-// for prefixes, as each tail is read once.  Only for rows x heads of a sequence that are
+// joined: the chunk kernel takes the tails as well, TAIL_ITEM_US an item and less a block
+// than for prefixes, as each tail is read once.  (TAIL_TILE_US and its like are by the block,
+// of whole calls.  The lengths of joined parts go by costs of their own, JOIN_TILE_US and
+// JOIN_ITEM_US in prefill.cu, by the tile and fitted to calls that differ in those lengths
+// alone: there an item is 4 us and a tile of four blocks 1.03, here 7.2 and 0.73, as a
+// whole call's items hold what its start and uneven end take.)  Only for rows x heads of a sequence that are
 // more than 16: at 16 it lost (32 sequences x 4 rows: 62.5 us against 52.5).
 // ROOT_US: the last parts and the merge of long contexts, which are cut into about the
 // root of their blocks.
@@ -132,17 +136,21 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) shared_merge_kernel(const Me
 // Tails beside the prefixes: parts of TAIL_ROOT times the root of their blocks, or of
 // TAIL_WANT of what gives TAIL_CTAS items where that is more, and of at most 256 (75 drawn
 // batches with 13 lengths each: 2 % off the best length; 48 sequences of 100 to 2,500 tokens
-// beside two prefixes, fp8: 55.3 us with 24 blocks, 53.1 with 40, 63.5 with 100; 64 of 20 to
-// 1,000 beside one, bf16: 88.5 with 24, 82.6 with 40, 81.0 whole).  The last fifth of the
-// sequences has parts of half the length, so that the last items are short (the batch in
-// fp8: 52.6 to 51.7 us, 32 sequences x 4 rows 49.2 to 47.8; a third or half of the sequences
-// gain less; contexts that are one part lose 1 us by it, whole contexts up to 4 us of 15).
+// beside two prefixes, fp8: 49.2 us with 24 blocks, 45.4 with 40, 45.1 with 100, 45.0 as
+// chosen; 64 of 20 to 1,000 beside one, bf16: 86.6, 85.2, 81.1 and 81.0; 128 of 1,024 to
+// 16,384: 661, 661, 653 and 645).  The last fifth of the sequences has parts of half the
+// length, so that the last items are short (the first of these batches 47.1 us without, the
+// last 651, 32 sequences x 4 rows 44.0 for 43.5; a third or half of the sequences gain less;
+// contexts that are one part lose 1 us by it, whole contexts up to 4 us of 15).
+//
+// All of these were fitted to batches whose bounds were their own longest prefix and tail,
+// with up to 256 sequences.
 //
 constexpr int64_t TAIL_COLS = 16, TAIL_CTAS = 2 * 3 * 152;
 constexpr double TAIL_ROOT = 2.6, TAIL_WANT = 0.9;
 constexpr double SET_US = 1.5, FIRST_US = 0.133, AGAIN_US = 0.077, FIRST8_US = 0.153, AGAIN8_US = 0.055;
 constexpr double TILE_US = 0.295, BIG_US = 0.215, TILE8_US = 0.32;
-constexpr double JOIN_US = 7.2, JOIN_TILE_US = 0.183, JOIN_BIG_US = 0.158, JOIN_TILE8_US = 0.227;
+constexpr double TAIL_ITEM_US = 7.2, TAIL_TILE_US = 0.183, TAIL_BIG_US = 0.158, TAIL_TILE8_US = 0.227;
 constexpr double WHOLE_START_US = 6, APART_START_US = 11.7, JOINED_START_US = 9.2, ROOT_US = 0.157;
 constexpr double ITEM_US = 1.5, BLOCK_US = 0.15, PART_US = 0.15, MERGE_US = 4, COUNTER_US = 1.2;
 
@@ -174,7 +182,7 @@ void choose(SharedCall &c, int32_t max_tail_len)
         const bool is_big = big(true);
         const double items = seqs * std::ceil(mean / ((is_big ? 128 : 256) / G)) * c.hkv;
         joined = JOINED_START_US + prefix(is_big) +
-                 items * (JOIN_US + T * (c.fp8 ? JOIN_TILE8_US : is_big ? JOIN_BIG_US : JOIN_TILE_US)) / sms;
+                 items * (TAIL_ITEM_US + T * (c.fp8 ? TAIL_TILE8_US : is_big ? TAIL_BIG_US : TAIL_TILE_US)) / sms;
     }
     c.joined = joined < std::min(whole, apart);
     c.whole = !c.joined && whole <= apart;

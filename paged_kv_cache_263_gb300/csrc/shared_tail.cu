@@ -4,7 +4,8 @@
 // A work item is (sequence, set of its rows, part of its keys, KV head).  A set's rows x G
 // heads, at most 16 columns, are attended as in the decode kernel: S^T[16 tokens][columns]
 // = K Q^T and O^T[128][columns] += V^T P^T with mma.sync, one 16-token block a warp at a
-// time, the softmax online.  What differs is how the work reaches the SM.  This kernel runs
+// time, the softmax online (what is repaired in those products' loop belongs in the decode
+// kernel's too, and the other way round).  What differs is how the work reaches the SM.  This kernel runs
 // beside the one that attends the prefixes, on the few SMs that one leaves free, and
 // an SM takes in at most 64 bytes a clock, 130 GB/s: so it must never stop loading.  A
 // kernel with a CTA an item had its place in the batch, its block ids and its first
