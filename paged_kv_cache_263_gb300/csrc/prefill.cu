@@ -691,7 +691,8 @@ __device__ __forceinline__ bool any_alive(const PrefixParams &p, const SharedIte
             s = ((run | 31) + 1) << of;
         } else {
             s = max(s, (run + __ffs(rest) - 1) << of);
-            any = any || (s < gr.s1 && (of == 0 || p.b.context_lens[s] > 0));
+            // (a group that does not ask may be anywhere: nothing is read for it)
+            any = any || (ask && s < gr.s1 && (of == 0 || p.b.context_lens[s] > 0));
             ++s;
         }
     }

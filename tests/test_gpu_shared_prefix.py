@@ -385,6 +385,24 @@ def test_padded_groups(rows, hq, hkv, fp8):
         compare(f64(got), exp, tol)
 
 
+@pytest.mark.parametrize("n", [700, 1024, 1025, 2100])
+def test_bad_groups_in_large_batches(n):
+    """Groups outside the batch are flagged, and no length is read for them; the others are as ever."""
+    b = Batch([10, n - 10], [130, 500], np.random.default_rng(n).integers(1, 90, n), hq=8, hkv=2, seed=n)
+    b.tables[:10, :8], b.tables[10:, :31] = b.tables[0, :8], b.tables[10, :31]
+    b.lens[20:] = 0        # (padded entries, so that the walk goes on)
+    groups, prefix = b.groups, b.prefix
+    far = 2 ** 31 - 1
+    for bad in ([0, 10, far, n], [0, 10, -5, far, 20, n], [-far, far, 10, n, n + 1], [0, 10, n, far, -1, -1, n, n + 7]):
+        b.groups, b.prefix = np.array(bad), np.full(len(bad) - 1, 130)
+        for bounds in b.ways().values():
+            got = b.call(**bounds)
+            assert pkv.kv_last_device_status() == 5 and pkv.kv_last_device_status_flags() in (4, 5)
+            assert np.isfinite(f64(got)).all()
+    b.groups, b.prefix = groups, prefix
+    b.check()
+
+
 def test_more_rows_than_announced():
     b = Batch([2, 2], [40, 50], [9, 9, 9, 9], rows=[3, 1, 2, 3], hq=4, hkv=1)
     b.check(flags=4, max_q_len=2, ref=b.reference(max_q=2))
