@@ -314,7 +314,9 @@ PAGEDKV_API kv_status reshape_and_cache(const void *k, const void *v, void *k_ca
  *  num_splits     maximum partitions per sequence; partition length is
  *                 ceil(max_blocks_per_seq / num_splits) blocks.  0 = choose.
  *  workspace      device scratch of at least paged_attention_workspace_size()
- *                 bytes (256-byte aligned), or NULL when that size is 0.
+ *                 bytes (256-byte aligned), or NULL when that size is 0.  The size is
+ *                 for these arguments: a smaller batch, cut into more partitions, may
+ *                 need more.
  * ---------------------------------------------------------------------- */
 PAGEDKV_API size_t paged_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                       int32_t max_blocks_per_seq, int32_t num_splits);
@@ -394,7 +396,8 @@ PAGEDKV_API kv_status paged_attention_decode_static_scratch(
  *                  plan; a longer query is flagged as out of range and left out)
  *  other arguments as for paged_attention_decode; workspace must be at least
  *  paged_attention_chunked_prefill_workspace_size() bytes (one size serves
- *  both cache dtypes).
+ *  both cache dtypes; it is for these arguments, and a smaller batch may need
+ *  more).
  * ---------------------------------------------------------------------- */
 PAGEDKV_API size_t paged_attention_chunked_prefill_workspace_size(int32_t num_seqs, int32_t total_q_tokens,
                                                       int32_t max_q_len, int32_t num_q_heads,
